@@ -56,7 +56,9 @@ typedef enum {
   PRNN_ERR_TIMEOUT = 6       /* a step wait in the persistent kernel ran out (sticky) */
 } prnn_status_t;
 
-typedef enum { PRNN_F32 = 0, PRNN_F16 = 1 } prnn_dtype_t;
+/* Storage types.  PRNN_BF16 is for the sequence operators (layer norm, dropout,
+ * linear attention); the recurrent layers and stacks take F32 and F16. */
+typedef enum { PRNN_F32 = 0, PRNN_F16 = 1, PRNN_BF16 = 2 } prnn_dtype_t;
 
 typedef enum {
   PRNN_ALGO_PERSISTENT = 0,  /* one persistent launch for all T steps, Wh on chip      */
@@ -586,6 +588,141 @@ prnn_status_t prnn_stack_get_info(prnn_stack_t s, prnn_stack_info_t* info);
 
 /* Free everything the stack owns.  NULL is accepted. */
 prnn_status_t prnn_stack_destroy(prnn_stack_t s);
+
+/* ---- sequence operators -------------------------------------------------
+ *
+ * What stands beside the recurrent layers in a residual block: layer
+ * normalisation, dropout with the residual, and linear attention with a decay
+ * per head, each with its gradient.  They need no handle.  Device pointers
+ * throughout; data in fp32, fp16 or bf16 (`dtype`), arithmetic, statistics and
+ * states in fp32, one rounding at each 16-bit output.  Asynchronous on `stream`;
+ * a call allocates nothing: what scratch it needs is the caller's `workspace`,
+ * 16-byte aligned, of the size its *_workspace query gives, used by the call
+ * on its stream only (give overlapping calls their own).  Results do not depend on the
+ * order in which thread blocks run: equal calls give equal bits.  Errors:
+ * PRNN_ERR_INVALID_ARG (NULL or misaligned pointers, sizes out of range, outputs
+ * that overlap inputs or each other, a workspace too small), PRNN_ERR_UNSUPPORTED
+ * (sizes beyond the stated limits), PRNN_ERR_CUDA.
+ */
+
+/*
+ * Layer norm over the last axis of `rows` rows of `cols` values (rows = T*B of
+ * a sequence):
+ *     mean = sum_c x_c / cols,  rstd = 1 / sqrt(sum_c (x_c - mean)^2 / cols + eps),
+ *     y_c = (x_c - mean) * rstd * gamma_c + beta_c.
+ * x and y hold row r at r*x_stride and r*y_stride (elements, >= cols); y may be
+ * x itself (same stride).  gamma and beta [cols] fp32, each NULL for none (1 and 0).
+ * mean and rstd [rows] fp32 receive the statistics for the backward pass; both may be
+ * NULL.  1 <= cols; rows == 0 is a no-op; eps >= 0.
+ */
+prnn_status_t prnn_layer_norm_forward(prnn_dtype_t dtype, long long rows, int cols, const void* x,
+                                      long long x_stride, const float* gamma, const float* beta,
+                                      float eps, void* y, long long y_stride, float* mean,
+                                      float* rstd, void* stream);
+
+/* Workspace of prnn_layer_norm_backward for this many rows and columns. */
+prnn_status_t prnn_layer_norm_workspace(long long rows, int cols, size_t* bytes);
+
+/*
+ * Its gradient, with xhat = (x - mean) * rstd and g = dy * gamma:
+ *     dx = rstd * (g - sum(g)/cols - xhat * sum(g * xhat)/cols)   (sums over the row),
+ *     dgamma_c = sum_r dy_rc * xhat_rc,   dbeta_c = sum_r dy_rc.
+ * mean and rstd are the forward pass's.  dx [rows], dgamma and dbeta [cols] (fp32) are
+ * overwritten; each may be NULL (not computed).  gamma NULL: 1.  rows == 0 writes zero
+ * dgamma and dbeta.
+ */
+prnn_status_t prnn_layer_norm_backward(prnn_dtype_t dtype, long long rows, int cols,
+                                       const void* dy, long long dy_stride, const void* x,
+                                       long long x_stride, const float* gamma, const float* mean,
+                                       const float* rstd, void* dx, long long dx_stride,
+                                       float* dgamma, float* dbeta, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/*
+ * Dropout of n contiguous values, with an optional residual:
+ *     y_i = (w_i >= p * 2^32 ? x_i / (1 - p) : 0) + residual_i,
+ * w_i = word i mod 4 of the block Philox4x32-10 (Salmon et al., "Parallel random
+ * numbers: as easy as 1, 2, 3", 2011) with the 128-bit counter (i / 4, offset), each
+ * 64 bits with the low word first, and the key `seed`.  The mask is never stored: the
+ * backward pass draws it again from the same seed and offset, so give every use within
+ * a training step its own offset.  0 <= p < 1 (p * 2^32 is rounded to a whole number).  y may be x or
+ * residual itself; residual NULL adds nothing.  n == 0 is a no-op.
+ */
+prnn_status_t prnn_dropout_forward(prnn_dtype_t dtype, long long n, const void* x,
+                                   const void* residual, void* y, double p, uint64_t seed,
+                                   uint64_t offset, void* stream);
+
+/* Its gradient: dx_i = (w_i >= p * 2^32 ? dy_i / (1 - p) : 0); the residual's is dy
+ * itself.  dx may be dy. */
+prnn_status_t prnn_dropout_backward(prnn_dtype_t dtype, long long n, const void* dy, void* dx,
+                                    double p, uint64_t seed, uint64_t offset, void* stream);
+
+/*
+ * Linear attention with a decay per head: a recurrence whose state is a matrix.  For
+ * every sequence b and head h, with l = exp(log_decay[h]),
+ *     S_t = l S_{t-1} + k_t v_t^T  [dk][dv],      o_t = scale * S_t^T q_t,   t = 0 .. len_b - 1.
+ * A tensor of a sequence holds element (t, b, h, d) at t*stride_t + b*stride_b + h*stride_h + d
+ * (elements), so that time-major and packed layouts, and slices of a joint projection, are read in
+ * place.  q and k have qk_heads heads, v and o `heads` (a multiple of qk_heads): head h uses query
+ * and key head h / (heads / qk_heads).
+ */
+typedef struct {
+  void* data;                                /* dtype; outputs are written, inputs only read */
+  long long stride_t, stride_b, stride_h;    /* elements; >= 0                                */
+} prnn_seq_t;
+
+typedef struct {
+  prnn_dtype_t dtype;         /* of q, k, v, o and their gradients                               */
+  int T, B;                   /* steps, sequences                                                */
+  int heads, qk_heads;        /* heads % qk_heads == 0                                           */
+  int dk, dv;                 /* 1 .. 256 each                                                   */
+  float scale;
+  const float* log_decay;     /* [heads] fp32, device; <= 0; a constant of the layer (no gradient) */
+  const int32_t* lens;        /* [B] device: length of each sequence, clamped to 0 .. T;
+                                 NULL: all are T.  Tokens past the length are not read into any
+                                 result: their outputs and gradients are 0                         */
+  prnn_seq_t q, k, v;         /* inputs                                                          */
+  const float* state;         /* [B][heads][dk][dv] S before the first token, NULL: zeros        */
+  prnn_seq_t o;               /* forward: output                                                 */
+  float* state_out;           /* forward: [B][heads][dk][dv] S after the last token; may be NULL;
+                                 may be `state` itself                                           */
+  /* backward only */
+  prnn_seq_t d_o;             /* gradient of o (input)                                           */
+  const float* d_state_out;   /* gradient of state_out (input), NULL: zeros                      */
+  prnn_seq_t d_q, d_k, d_v;   /* gradients of q, k, v; data NULL: not computed                   */
+  float* d_state;             /* gradient of `state`, NULL: not computed                         */
+  void* workspace;
+  size_t workspace_bytes;
+} prnn_linear_attention_t;
+
+/* Workspace of prnn_linear_attention_forward (backward == 0) or _backward (1) for the
+ * sizes, types and layouts in `a` (its pointers are not followed). */
+prnn_status_t prnn_linear_attention_workspace(const prnn_linear_attention_t* a, int backward,
+                                              size_t* bytes);
+
+/* All T tokens.  T == 0 copies the state; B == 0 is a no-op. */
+prnn_status_t prnn_linear_attention_forward(const prnn_linear_attention_t* a, void* stream);
+
+/*
+ * Gradients of the forward call with the same q, k, v, state and lens, for the loss whose
+ * gradient is d_o with respect to o and d_state_out with respect to state_out:
+ *     dq_t = scale S_t do_t;
+ *     R_t = l R_{t+1} + scale q_t do_t^T, with d_state_out in the place of l R_{t+1} at t = len-1;
+ *     dk_t = R_t v_t;  dv_t = R_t^T k_t;  d_state = l R_0 (d_state_out where len is 0),
+ * with dq and dk summed over the heads that share them.  The outputs are d_q, d_k, d_v (each
+ * skipped when its data is NULL) and d_state.
+ */
+prnn_status_t prnn_linear_attention_backward(const prnn_linear_attention_t* a, void* stream);
+
+/*
+ * One token for each of B sequences (decoding): a->T is taken as 1 and stride_t and
+ * lens are not used.  The states lie in `state_pool` [n_slots][heads][dk][dv] fp32 and are updated
+ * in place.  slots [B] int32 (device) gives each sequence's state; NULL: sequence b has
+ * state b.  A slot outside 0 .. n_slots-1 marks a padding row: its o is 0 and no state
+ * changes.  Live slots must differ from one another.  No workspace.
+ */
+prnn_status_t prnn_linear_attention_step(const prnn_linear_attention_t* a, float* state_pool,
+                                         int n_slots, const int32_t* slots, void* stream);
 
 #ifdef __cplusplus
 }

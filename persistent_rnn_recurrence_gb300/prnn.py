@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -23,7 +24,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 # ---- enums (mirror include/prnn.h) ------------------------------------------
 PRNN_OK, PRNN_ERR_INVALID_ARG, PRNN_ERR_UNSUPPORTED, PRNN_ERR_NOT_READY, \
     PRNN_ERR_CUDA, PRNN_ERR_OOM, PRNN_ERR_TIMEOUT = range(7)
-PRNN_F32, PRNN_F16 = 0, 1
+PRNN_F32, PRNN_F16, PRNN_BF16 = 0, 1, 2
 PRNN_ALGO_PERSISTENT, PRNN_ALGO_PER_STEP = 0, 1
 (PRNN_OPT_WAIT_TIMEOUT_US, PRNN_OPT_SYNC_MODE, PRNN_OPT_DEBUG_DROP_CTA,
  PRNN_OPT_DEBUG_DROP_STEP, PRNN_OPT_TIMING, PRNN_OPT_PROJECTION, PRNN_OPT_CTA_GROUPS,
@@ -44,7 +45,11 @@ EXPORTS = ["prnn_create", "prnn_set_weights_dense", "prnn_set_weights_sparse",
            "prnn_set_weights_csr",
            "prnn_stack_create", "prnn_stack_set_layer", "prnn_stack_forward",
            "prnn_stack_get_status", "prnn_stack_set_option", "prnn_stack_get_timing",
-           "prnn_stack_get_info", "prnn_stack_destroy", "prnn_backward"]
+           "prnn_stack_get_info", "prnn_stack_destroy", "prnn_backward",
+           "prnn_layer_norm_forward", "prnn_layer_norm_workspace", "prnn_layer_norm_backward",
+           "prnn_dropout_forward", "prnn_dropout_backward",
+           "prnn_linear_attention_workspace", "prnn_linear_attention_forward",
+           "prnn_linear_attention_backward", "prnn_linear_attention_step"]
 
 
 class prnn_info_t(ctypes.Structure):
@@ -72,8 +77,30 @@ class prnn_stack_info_t(ctypes.Structure):
         return {n: getattr(self, n) for n, _ in self._fields_}
 
 
+class prnn_seq_t(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p)] + [(n, ctypes.c_longlong) for n in (
+        "stride_t", "stride_b", "stride_h")]
+
+
+class prnn_linear_attention_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "dtype", "T", "B", "heads", "qk_heads", "dk", "dv")] + [
+        ("scale", ctypes.c_float), ("log_decay", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+        ("q", prnn_seq_t), ("k", prnn_seq_t), ("v", prnn_seq_t), ("state", ctypes.c_void_p),
+        ("o", prnn_seq_t), ("state_out", ctypes.c_void_p), ("d_o", prnn_seq_t),
+        ("d_state_out", ctypes.c_void_p), ("d_q", prnn_seq_t), ("d_k", prnn_seq_t),
+        ("d_v", prnn_seq_t), ("d_state", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t)]
+
+
+# The same layout for struct.pack, which fills it in one call (a decoding step
+# is short enough for the difference to show).
+_LA_PACK = struct.Struct("=7if40q").pack
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_longlong
+_A = ctypes.c_char_p     # prnn_linear_attention_t as packed bytes
 _sig = {
     "prnn_create": ([ctypes.POINTER(_P), _I, _I, _I, _I, _I], _I),
     "prnn_set_weights_dense": ([_P, _P, _P, _P, _P], _I),
@@ -108,6 +135,19 @@ _sig = {
     "prnn_stack_get_info": ([_P, ctypes.POINTER(prnn_stack_info_t)], _I),
     "prnn_stack_destroy": ([_P], _I),
     "prnn_backward": ([_P, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P], _I),
+    "prnn_layer_norm_forward": ([_I, _L, _I, _P, _L, _P, _P, ctypes.c_float, _P, _L, _P, _P, _P],
+                                _I),
+    "prnn_layer_norm_workspace": ([_L, _I, ctypes.POINTER(ctypes.c_size_t)], _I),
+    "prnn_layer_norm_backward": ([_I, _L, _I, _P, _L, _P, _L, _P, _P, _P, _P, _L, _P, _P, _P,
+                                  ctypes.c_size_t, _P], _I),
+    "prnn_dropout_forward": ([_I, _L, _P, _P, _P, ctypes.c_double, ctypes.c_uint64,
+                              ctypes.c_uint64, _P], _I),
+    "prnn_dropout_backward": ([_I, _L, _P, _P, ctypes.c_double, ctypes.c_uint64, ctypes.c_uint64,
+                               _P], _I),
+    "prnn_linear_attention_workspace": ([_A, _I, ctypes.POINTER(ctypes.c_size_t)], _I),
+    "prnn_linear_attention_forward": ([_A, _P], _I),
+    "prnn_linear_attention_backward": ([_A, _P], _I),
+    "prnn_linear_attention_step": ([_A, _P, _I, _P, _P], _I),
 }
 for _name, (_args, _res) in _sig.items():
     _fn = getattr(_lib, _name)
@@ -353,6 +393,356 @@ def prnn_stack_get_info(s: int) -> dict:
 
 def prnn_stack_destroy(s: int) -> None:
     _check(_lib.prnn_stack_destroy(s), "prnn_stack_destroy")
+
+
+# ---- sequence operators ----------------------------------------------------------
+def prnn_layer_norm_forward(dtype, rows, cols, x, x_stride, gamma, beta, eps, y, y_stride,
+                            mean=None, rstd=None, stream=None) -> None:
+    _check(_lib.prnn_layer_norm_forward(dtype, rows, cols, _ptr(x), x_stride, _ptr(gamma),
+                                        _ptr(beta), eps, _ptr(y), y_stride, _ptr(mean), _ptr(rstd),
+                                        _stream(stream)), "prnn_layer_norm_forward")
+
+
+def prnn_layer_norm_workspace(rows, cols) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.prnn_layer_norm_workspace(rows, cols, ctypes.byref(n)),
+           "prnn_layer_norm_workspace")
+    return n.value
+
+
+def prnn_layer_norm_backward(dtype, rows, cols, dy, dy_stride, x, x_stride, gamma, mean, rstd, dx,
+                             dx_stride, dgamma, dbeta, workspace, workspace_bytes,
+                             stream=None) -> None:
+    _check(_lib.prnn_layer_norm_backward(dtype, rows, cols, _ptr(dy), dy_stride, _ptr(x), x_stride,
+                                         _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dx), dx_stride,
+                                         _ptr(dgamma), _ptr(dbeta), _ptr(workspace),
+                                         workspace_bytes, _stream(stream)),
+           "prnn_layer_norm_backward")
+
+
+def prnn_dropout_forward(dtype, n, x, residual, y, p, seed, offset, stream=None) -> None:
+    _check(_lib.prnn_dropout_forward(dtype, n, _ptr(x), _ptr(residual), _ptr(y), p, seed, offset,
+                                     _stream(stream)), "prnn_dropout_forward")
+
+
+def prnn_dropout_backward(dtype, n, dy, dx, p, seed, offset, stream=None) -> None:
+    _check(_lib.prnn_dropout_backward(dtype, n, _ptr(dy), _ptr(dx), p, seed, offset,
+                                      _stream(stream)), "prnn_dropout_backward")
+
+
+def prnn_linear_attention_workspace(a: bytes, backward: bool) -> int:
+    """`a`: bytes of a prnn_linear_attention_t (``bytes(struct)``)."""
+    n = ctypes.c_size_t()
+    _check(_lib.prnn_linear_attention_workspace(a, int(backward), ctypes.byref(n)),
+           "prnn_linear_attention_workspace")
+    return n.value
+
+
+def prnn_linear_attention_forward(a: bytes, stream=None) -> None:
+    _check(_lib.prnn_linear_attention_forward(a, _stream(stream)), "prnn_linear_attention_forward")
+
+
+def prnn_linear_attention_backward(a: bytes, stream=None) -> None:
+    _check(_lib.prnn_linear_attention_backward(a, _stream(stream)),
+           "prnn_linear_attention_backward")
+
+
+def prnn_linear_attention_step(a: bytes, state_pool, n_slots, slots=None, stream=None) -> None:
+    _check(_lib.prnn_linear_attention_step(a, _ptr(state_pool), n_slots, _ptr(slots),
+                                           _stream(stream)), "prnn_linear_attention_step")
+
+
+# ---- sequence operators on tensors -------------------------------------------------
+# Tensors in, tensors out, on the current stream.  `stream` (a torch stream) runs the call, and
+# allocates its outputs, on that stream instead; the caller orders it after the inputs' producers.
+_dtypes = {}
+
+
+def _dtype(t) -> int:
+    if not _dtypes:
+        import torch
+        _dtypes.update({torch.float32: PRNN_F32, torch.float16: PRNN_F16,
+                        torch.bfloat16: PRNN_BF16})
+    try:
+        return _dtypes[t.dtype]
+    except KeyError:
+        raise ValueError(f"dtype {t.dtype}: float32, float16 or bfloat16 is needed") from None
+
+
+def _like(t, ref, shape, what, dtype=None) -> None:
+    """t is on ref's device, has `dtype` (default ref's) and `shape`, last axis contiguous."""
+    if t.shape != shape or t.dtype != (dtype or ref.dtype) or t.device != ref.device:
+        raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype} on {t.device}, expected "
+                         f"{tuple(shape)} {dtype or ref.dtype} on {ref.device}")
+    if t.ndim and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{what}: the last axis must be contiguous")
+
+
+def _vector(t, ref, n, what, dtype=None):
+    """Address of a contiguous vector of n values (None: NULL)."""
+    if t is None:
+        return None
+    import torch
+    _like(t, ref, (n,), what, dtype or torch.float32)
+    return t.data_ptr()
+
+
+def _decays(t, ref, n, what):
+    """Address of log_decay [n] fp32, contiguous."""
+    if t is None:
+        raise ValueError(f"{what}: log_decay is needed")
+    return _vector(t, ref, n, what)
+
+
+def _device(t, what):
+    """t is a CUDA tensor of the current device; returns the current stream's handle."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError(f"{what}: a CUDA tensor is needed")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: on {t.device}, but the current device is "
+                         f"{torch.cuda.current_device()}")
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _rows(t, what):
+    """(rows, cols, row stride) of t seen as rows of its last axis; copies nothing."""
+    if t.ndim < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{what}: at least one value per row is needed")
+    cols = t.shape[-1]
+    rows = t.numel() // cols
+    if t.is_contiguous():
+        return rows, cols, cols
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what}: the last axis must be contiguous")
+    # the leading axes must step through memory like one axis
+    stride, want = None, None
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if stride is None:
+            stride = st
+        elif st != want:
+            raise ValueError(f"{what}: the leading axes must be evenly spaced rows")
+        want = st * n
+    return rows, cols, cols if stride is None else stride
+
+
+def layer_norm(x, gamma=None, beta=None, eps=1e-5, y=None, stream=None):
+    """Layer norm over x's last axis (prnn_layer_norm_forward): (y, mean, rstd), the
+    statistics fp32 with x's leading shape.  gamma, beta: fp32 [cols] or None.  y may be x."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return layer_norm(x, gamma, beta, eps, y)
+    st = _device(x, "layer_norm: x")
+    dt = _dtype(x)
+    rows, cols, xs = _rows(x, "layer_norm: x")
+    if y is None:
+        y, ys = torch.empty(x.shape, dtype=x.dtype, device=x.device), cols
+    else:
+        _like(y, x, x.shape, "layer_norm: y")
+        ys = _rows(y, "layer_norm: y")[2]
+    stats = torch.empty((2,) + x.shape[:-1], dtype=torch.float32, device=x.device)
+    mean, rstd = stats.unbind(0)
+    p = stats.data_ptr()
+    _check(_lib.prnn_layer_norm_forward(dt, rows, cols, x.data_ptr(), xs,
+                                        _vector(gamma, x, cols, "layer_norm: gamma"),
+                                        _vector(beta, x, cols, "layer_norm: beta"), eps,
+                                        y.data_ptr(), ys, p, p + 4 * rows, st),
+           "prnn_layer_norm_forward")
+    return y, mean, rstd
+
+
+def layer_norm_backward(dy, x, gamma, mean, rstd, stream=None):
+    """Gradients of layer_norm: (dx, dgamma, dbeta), the last two fp32 [cols]."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return layer_norm_backward(dy, x, gamma, mean, rstd)
+    st = _device(x, "layer_norm_backward: x")
+    dt = _dtype(x)
+    rows, cols, xs = _rows(x, "layer_norm_backward: x")
+    _like(dy, x, x.shape, "layer_norm_backward: dy")
+    dys = _rows(dy, "layer_norm_backward: dy")[2]
+    for t, what in ((mean, "mean"), (rstd, "rstd")):
+        _like(t, x, x.shape[:-1], "layer_norm_backward: " + what, torch.float32)
+        if not t.is_contiguous():
+            raise ValueError(f"layer_norm_backward: {what} must be contiguous")
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    need = prnn_layer_norm_workspace(rows, cols)
+    sums = torch.empty(2 * cols, dtype=torch.float32, device=x.device)
+    ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+    p = sums.data_ptr()
+    _check(_lib.prnn_layer_norm_backward(dt, rows, cols, dy.data_ptr(), dys, x.data_ptr(), xs,
+                                         _vector(gamma, x, cols, "layer_norm_backward: gamma"),
+                                         mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), cols,
+                                         p, p + 4 * cols, ws.data_ptr(), need, st),
+           "prnn_layer_norm_backward")
+    return dx, sums[:cols], sums[cols:]
+
+
+def dropout(x, p, seed, offset=0, residual=None, y=None, stream=None):
+    """Dropout of x plus the residual (prnn_dropout_forward); contiguous tensors of one
+    shape.  Give every use in a training step its own offset."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dropout(x, p, seed, offset, residual, y)
+    st = _device(x, "dropout: x")
+    dt = _dtype(x)
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    for t, what in ((x, "x"), (residual, "residual"), (y, "y")):
+        if t is None or t is x and what != "x":
+            continue
+        _like(t, x, x.shape, "dropout: " + what)
+        if not t.is_contiguous():
+            raise ValueError(f"dropout: {what} must be contiguous")
+    _check(_lib.prnn_dropout_forward(dt, x.numel(), x.data_ptr(),
+                                     None if residual is None else residual.data_ptr(),
+                                     y.data_ptr(), p, seed, offset, st), "prnn_dropout_forward")
+    return y
+
+
+def dropout_backward(dy, p, seed, offset=0, dx=None, stream=None):
+    """Gradient of dropout with respect to x for the same seed and offset (the residual's
+    gradient is dy)."""
+    return dropout(dy, p, seed, offset, None, dx, stream)
+
+
+_NO_SEQ = (0, 0, 0, 0)
+
+
+def _seq4(t, ref, shape, what):
+    """(address, strides) of a [T, B, heads, d] tensor, for prnn_seq_t."""
+    _like(t, ref, shape, what)
+    st, sb, sh, _ = t.stride()
+    return t.data_ptr(), st, sb, sh
+
+
+def _attention_shape(q, v):
+    if q.ndim != 4 or v.ndim != 4 or q.shape[:2] != v.shape[:2]:
+        raise ValueError(f"q {tuple(q.shape)} and v {tuple(v.shape)}: expected [T, B, qk_heads, dk] "
+                         "and [T, B, heads, dv]")
+    T, B, H, dv = v.shape
+    return T, B, H, q.shape[2], q.shape[3], dv
+
+
+def _state(t, ref, shape, what):
+    if t is None:
+        return 0
+    import torch
+    _like(t, ref, shape, what, torch.float32)
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def linear_attention(q, k, v, log_decay, scale=1.0, state=None, lens=None, o=None, stream=None):
+    """Linear attention with a decay per head over whole sequences
+    (prnn_linear_attention_forward).  q, k [T, B, qk_heads, dk], v [T, B, heads, dv], any strides
+    with the last axis contiguous; log_decay fp32 [heads]; state fp32 [B, heads, dk, dv] or
+    None (zeros); lens int32 [B] on the device or None.  Returns (o [T, B, heads, dv], the state
+    after the last token)."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear_attention(q, k, v, log_decay, scale, state, lens, o)
+    st = _device(q, "linear_attention: q")
+    T, B, H, Hq, dk, dv = _attention_shape(q, v)
+    if o is None:
+        o = torch.empty((T, B, H, dv), dtype=v.dtype, device=q.device)
+    end = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
+    head = (_dtype(q), T, B, H, Hq, dk, dv, scale,
+            _decays(log_decay, q, H, "linear_attention: log_decay"),
+            _vector(lens, q, B, "linear_attention: lens", torch.int32) or 0,
+            *_seq4(q, q, q.shape, "linear_attention: q"),
+            *_seq4(k, q, q.shape, "linear_attention: k"),
+            *_seq4(v, q, v.shape, "linear_attention: v"),
+            _state(state, q, end.shape, "linear_attention: state"),
+            *_seq4(o, q, v.shape, "linear_attention: o"), end.data_ptr(),
+            *_NO_SEQ, 0, *_NO_SEQ, *_NO_SEQ, *_NO_SEQ, 0)
+    ws, need = _attention_workspace(head, 0, q.device)
+    _check(_lib.prnn_linear_attention_forward(
+        _LA_PACK(*head, 0 if ws is None else ws.data_ptr(), need), st),
+        "prnn_linear_attention_forward")
+    return o, end
+
+
+def _attention_workspace(head, backward, device):
+    n = ctypes.c_size_t()
+    _check(_lib.prnn_linear_attention_workspace(_LA_PACK(*head, 0, 0), backward, ctypes.byref(n)),
+           "prnn_linear_attention_workspace")
+    if n.value == 0:
+        return None, 0
+    import torch
+    return torch.empty(n.value, dtype=torch.uint8, device=device), n.value
+
+
+def linear_attention_backward(do, q, k, v, log_decay, scale=1.0, state=None, lens=None,
+                              dstate=None, stream=None) -> dict:
+    """Gradients of linear_attention for the loss whose gradient is `do` with respect to o and
+    `dstate` (or None) with respect to the returned state: dict of dq, dk, dv and, when a state was
+    given, dstate."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear_attention_backward(do, q, k, v, log_decay, scale, state, lens, dstate)
+    st = _device(q, "linear_attention_backward: q")
+    T, B, H, Hq, dk, dv = _attention_shape(q, v)
+    shape = (B, H, dk, dv)
+    g = {"dq": torch.empty(q.shape, dtype=q.dtype, device=q.device),
+         "dk": torch.empty(q.shape, dtype=q.dtype, device=q.device),
+         "dv": torch.empty(v.shape, dtype=q.dtype, device=q.device)}
+    if state is not None:
+        g["dstate"] = torch.empty(shape, dtype=torch.float32, device=q.device)
+    what = "linear_attention_backward: "
+    head = (_dtype(q), T, B, H, Hq, dk, dv, scale, _decays(log_decay, q, H, what + "log_decay"),
+            _vector(lens, q, B, what + "lens", torch.int32) or 0,
+            *_seq4(q, q, q.shape, what + "q"), *_seq4(k, q, q.shape, what + "k"),
+            *_seq4(v, q, v.shape, what + "v"), _state(state, q, shape, what + "state"),
+            *_NO_SEQ, 0, *_seq4(do, q, v.shape, what + "do"),
+            _state(dstate, q, shape, what + "dstate"), *_seq4(g["dq"], q, q.shape, "dq"),
+            *_seq4(g["dk"], q, q.shape, "dk"), *_seq4(g["dv"], q, v.shape, "dv"),
+            g["dstate"].data_ptr() if state is not None else 0)
+    ws, need = _attention_workspace(head, 1, q.device)
+    _check(_lib.prnn_linear_attention_backward(
+        _LA_PACK(*head, 0 if ws is None else ws.data_ptr(), need), st),
+        "prnn_linear_attention_backward")
+    return g
+
+
+def linear_attention_step(q, k, v, log_decay, state, scale=1.0, slots=None, o=None, stream=None):
+    """One token for each sequence (prnn_linear_attention_step): q, k [B, qk_heads, dk],
+    v [B, heads, dv]; state fp32 [n, heads, dk, dv], updated in place: sequence b's is
+    state[slots[b]] (int32 on the device; outside 0 .. n-1 marks a padding row), or state[b].
+    Returns o [B, heads, dv]."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear_attention_step(q, k, v, log_decay, state, scale, slots, o)
+    st = _device(q, "linear_attention_step: q")
+    if q.ndim != 3 or v.ndim != 3 or q.shape[0] != v.shape[0]:
+        raise ValueError(f"q {tuple(q.shape)} and v {tuple(v.shape)}: expected [B, qk_heads, dk] and "
+                         "[B, heads, dv]")
+    B, H, dv = v.shape
+    Hq, dk = q.shape[1:]
+    if o is None:
+        o = torch.empty((B, H, dv), dtype=q.dtype, device=q.device)
+    for t, shape, n in ((q, q.shape, "q"), (k, q.shape, "k"), (v, v.shape, "v"), (o, v.shape, "o")):
+        _like(t, q, shape, "linear_attention_step: " + n)
+    n_slots = state.shape[0]
+    pool = _state(state, q, (n_slots, H, dk, dv), "linear_attention_step: state")
+    a = _LA_PACK(_dtype(q), 1, B, H, Hq, dk, dv, scale,
+                 _decays(log_decay, q, H, "linear_attention_step: log_decay"), 0,
+                 q.data_ptr(), 0, *q.stride()[:2], k.data_ptr(), 0, *k.stride()[:2],
+                 v.data_ptr(), 0, *v.stride()[:2], 0, o.data_ptr(), 0, *o.stride()[:2], 0,
+                 *_NO_SEQ, 0, *_NO_SEQ, *_NO_SEQ, *_NO_SEQ, 0, 0, 0)
+    _check(_lib.prnn_linear_attention_step(
+        a, pool, n_slots, _vector(slots, q, B, "linear_attention_step: slots", torch.int32), st),
+        "prnn_linear_attention_step")
+    return o
 
 
 # ---- convenience wrapper used by the tests and the benchmark ------------------
