@@ -605,6 +605,12 @@ prnn_status_t prnn_stack_destroy(prnn_stack_t s);
  * (sizes beyond the stated limits), PRNN_ERR_CUDA.
  */
 
+/* Synchronize `stream` and report whether a kernel of these operators on the current
+ * device has given up waiting for one of its own copies or matrix products
+ * (PRNN_ERR_TIMEOUT, sticky until the process ends; that call's outputs are undefined).  No
+ * input does that: it is the report of a defect or of a device that has stopped answering. */
+prnn_status_t prnn_sequence_status(void* stream);
+
 /*
  * Layer norm over the last axis of `rows` rows of `cols` values (rows = T*B of
  * a sequence):

@@ -9,55 +9,103 @@
 namespace prnn {
 namespace {
 
-// One block per (sequence, head), 32 columns of the state per warp row.
-template <typename T>
-__global__ void __launch_bounds__(256) la_step_kernel(LaStepArgs a) {
-  __shared__ float qs[256], ks[256], part[8][33];
+constexpr int kThreads = 256, kInFlight = 8;
+
+// One block: one (sequence, head) and `slice` columns of its state.  TX threads side by side hold
+// V columns each and the 256 / TX rows of threads share the dk rows; every thread keeps kInFlight
+// loads of the state in flight, the first of them issued before q, k and v arrive.
+template <typename T, int V, int TX>
+__global__ void __launch_bounds__(kThreads) la_step_kernel(LaStepArgs a, int slice) {
+  constexpr int TY = kThreads / TX;
+  __shared__ float qs[256], ks[256], part[TY][TX * V + 1];
+  const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
   const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  T* o = static_cast<T*>(a.o) + b * a.ob + h * a.oh;
+  const int c0 = blockIdx.y * slice, c = c0 + tx * V;
+  const int ncol = min(slice, a.dv - c0);
+  T* o = static_cast<T*>(a.o) + b * a.ob + h * a.oh + c0;
   const int slot = a.slots ? a.slots[b] : b;
   if (slot < 0 || slot >= a.n_slots) {
-    for (int c = threadIdx.x; c < a.dv; c += 256) o[c] = from_f32<T>(0.f);
+    for (int i = threadIdx.x; i < ncol; i += kThreads) o[i] = from_f32<T>(0.f);
     return;
+  }
+  float* S = a.state + ((size_t)slot * a.H + h) * a.dk * a.dv + c;
+  const bool mine = tx * V < ncol;  // V divides dv and slice: all V columns or none
+  Pack<float, V> st[kInFlight];
+#pragma unroll
+  for (int u = 0; u < kInFlight; ++u) {
+    const int i = ty + u * TY;
+    if (mine && i < a.dk) st[u] = load_pack<float, V>(S + (size_t)i * a.dv);
   }
   const T* q = static_cast<const T*>(a.q.p) + b * a.q.sb + (h / a.q.share) * a.q.sh;
   const T* k = static_cast<const T*>(a.k.p) + b * a.k.sb + (h / a.k.share) * a.k.sh;
   const T* v = static_cast<const T*>(a.v.p) + b * a.v.sb + (h / a.v.share) * a.v.sh;
-  float* S = a.state + ((size_t)slot * a.H + h) * a.dk * a.dv;
-  for (int i = threadIdx.x; i < a.dk; i += 256) {
+  for (int i = threadIdx.x; i < a.dk; i += kThreads) {
     qs[i] = to_f32(q[i]);
     ks[i] = to_f32(k[i]);
   }
   const float l = expf(a.log_decay[h]);
-  __syncthreads();
-  for (int c0 = 0; c0 < a.dv; c0 += 32) {
-    const int c = c0 + lane;
-    float s = 0.f;
-    if (c < a.dv) {
-      const float vc = to_f32(v[c]);
-      for (int i = warp; i < a.dk; i += 8) {
-        const float n = l * S[(size_t)i * a.dv + c] + ks[i] * vc;
-        S[(size_t)i * a.dv + c] = n;
-        s = fmaf(qs[i], n, s);
-      }
-    }
-    part[warp][lane] = s;
-    __syncthreads();
-    if (warp == 0 && c < a.dv) {
-      s = 0.f;
-      for (int w = 0; w < 8; ++w) s += part[w][lane];
-      o[c] = from_f32<T>(a.scale * s);
-    }
-    __syncthreads();
+  float vc[V], sum[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    vc[j] = mine ? to_f32(v[c + j]) : 0.f;
+    sum[j] = 0.f;
   }
+  __syncthreads();
+  for (int i0 = ty; i0 < a.dk; i0 += kInFlight * TY) {
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) {
+      const int i = i0 + u * TY;
+      if (!mine || i >= a.dk) continue;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        st[u].v[j] = fmaf(l, st[u].v[j], ks[i] * vc[j]);
+        sum[j] = fmaf(qs[i], st[u].v[j], sum[j]);
+      }
+      store_pack<float, V>(S + (size_t)i * a.dv, st[u]);
+      const int next = i + kInFlight * TY;
+      if (next < a.dk) st[u] = load_pack<float, V>(S + (size_t)next * a.dv);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) part[ty][tx * V + j] = sum[j];
+  __syncthreads();
+  for (int i = threadIdx.x; i < ncol; i += kThreads) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < TY; ++w) s += part[w][i];
+    o[i] = from_f32<T>(a.scale * s);
+  }
+}
+
+template <typename T, int V>
+void launch(const LaStepArgs& a, int slice, cudaStream_t s) {
+  const dim3 grid(a.B * a.H, (a.dv + slice - 1) / slice);
+  const int tx = (slice + V - 1) / V;
+  if (tx <= 4)
+    la_step_kernel<T, V, 4><<<grid, kThreads, 0, s>>>(a, slice);
+  else if (tx <= 8)
+    la_step_kernel<T, V, 8><<<grid, kThreads, 0, s>>>(a, slice);
+  else if (tx <= 16)
+    la_step_kernel<T, V, 16><<<grid, kThreads, 0, s>>>(a, slice);
+  else
+    la_step_kernel<T, V, 32><<<grid, kThreads, 0, s>>>(a, slice);
 }
 
 }  // namespace
 
 cudaError_t launch_la_step(const LaStepArgs& a, cudaStream_t s) {
   if (a.B == 0) return cudaSuccess;
-  PRNN_BY_DTYPE(a.dtype, T, (la_step_kernel<T><<<a.B * a.H, 256, 0, s>>>(a)));
+  const bool vec = a.dv % 4 == 0 && (reinterpret_cast<uintptr_t>(a.state) & 15) == 0;
+  // Columns per block: up to 32 threads' worth, narrower while the blocks are too few to fill the SMs.
+  int slice = vec ? 128 : 32;
+  while (slice > a.dv && slice > 16) slice /= 2;
+  if (slice < a.dv && slice * 2 >= a.dv && slice < (vec ? 128 : 32)) slice *= 2;
+  while (slice > 16 && (long long)a.B * a.H * ((a.dv + slice - 1) / slice) < 152) slice /= 2;
+  if (vec) {
+    PRNN_BY_DTYPE(a.dtype, T, (launch<T, 4>(a, slice, s)));
+  } else {
+    PRNN_BY_DTYPE(a.dtype, T, (launch<T, 1>(a, slice, s)));
+  }
   return cudaGetLastError();
 }
 

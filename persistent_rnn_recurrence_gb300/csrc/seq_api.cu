@@ -12,6 +12,25 @@
 
 using namespace prnn;
 
+namespace prnn {
+
+__device__ int g_seq_status;
+
+int* seq_status_word() {
+  void* p = nullptr;
+  return cudaGetSymbolAddress(&p, g_seq_status) == cudaSuccess ? static_cast<int*>(p) : nullptr;
+}
+
+int seq_sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+    n = 1;
+  return n;
+}
+
+}  // namespace prnn
+
 namespace {
 
 size_t elem_size(prnn_dtype_t d) { return d == PRNN_F32 ? 4 : 2; }
@@ -130,6 +149,16 @@ size_t group_bytes(const prnn_linear_attention_t* a) {
 }  // namespace
 
 extern "C" {
+
+prnn_status_t prnn_sequence_status(void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int v = 0;
+  const int* p = seq_status_word();
+  if (!p) return PRNN_ERR_CUDA;
+  PRNN_TRY(cudaMemcpyAsync(&v, p, sizeof(int), cudaMemcpyDeviceToHost, s));
+  PRNN_TRY(cudaStreamSynchronize(s));
+  return v ? PRNN_ERR_TIMEOUT : PRNN_OK;
+}
 
 prnn_status_t prnn_layer_norm_forward(prnn_dtype_t dtype, long long rows, int cols, const void* x,
                                       long long x_stride, const float* gamma, const float* beta,

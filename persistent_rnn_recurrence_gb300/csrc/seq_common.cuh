@@ -3,6 +3,8 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -29,6 +31,87 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// V consecutive elements of T in one access of up to 16 bytes.
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Pack {
+  T v[V];
+};
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> load_pack(const T* p) {
+  return *reinterpret_cast<const Pack<T, V>*>(p);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_pack(T* p, const Pack<T, V>& x) {
+  *reinterpret_cast<Pack<T, V>*>(p) = x;
+}
+// Streaming forms for data that is touched once (read-only path, evict first).
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> load_once(const T* p) {
+  Pack<T, V> r;
+  if constexpr (sizeof(T) * V == 32) {
+    const uint4* u = reinterpret_cast<const uint4*>(p);
+    const uint4 w[2] = {__ldcs(u), __ldcs(u + 1)};
+    r = *reinterpret_cast<const Pack<T, V>*>(w);
+  } else if constexpr (sizeof(T) * V == 16) {
+    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
+    r = *reinterpret_cast<const Pack<T, V>*>(&u);
+  } else {
+    r = load_pack<T, V>(p);
+  }
+  return r;
+}
+
+// Two fp32 values side by side: Blackwell's paired add, multiply and fused multiply-add do both
+// lanes in one instruction, each rounded as the single form rounds it.
+__device__ __forceinline__ uint64_t as_u64(float2 v) {
+  return (uint64_t)__float_as_uint(v.y) << 32 | __float_as_uint(v.x);
+}
+__device__ __forceinline__ float2 as_f2(uint64_t u) {
+  return make_float2(__uint_as_float((uint32_t)u), __uint_as_float((uint32_t)(u >> 32)));
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
+  return as_f2(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
+  return as_f2(d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
+  return as_f2(d);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Elements 2i and 2i + 1 of a pack (i = 0 and a zero for a pack of one).
+template <typename T, int V>
+__device__ __forceinline__ float2 pair_of(const Pack<T, V>& p, int i) {
+  if constexpr (V == 1)
+    return make_float2(to_f32(p.v[0]), 0.f);
+  else if constexpr (sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value)
+    return __bfloat1622float2(reinterpret_cast<const __nv_bfloat162*>(p.v)[i]);
+  else if constexpr (sizeof(T) == 2)
+    return __half22float2(reinterpret_cast<const __half2*>(p.v)[i]);
+  else
+    return make_float2(to_f32(p.v[2 * i]), to_f32(p.v[2 * i + 1]));
+}
+template <typename T, int V>
+__device__ __forceinline__ void set_pair(Pack<T, V>& p, int i, float2 f) {
+  if constexpr (V == 1)
+    p.v[0] = from_f32<T>(f.x);
+  else if constexpr (sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value)
+    reinterpret_cast<__nv_bfloat162*>(p.v)[i] = __float22bfloat162_rn(f);
+  else if constexpr (sizeof(T) == 2)
+    reinterpret_cast<__half2*>(p.v)[i] = __float22half2_rn(f);
+  else {
+    p.v[2 * i] = from_f32<T>(f.x);
+    p.v[2 * i + 1] = from_f32<T>(f.y);
+  }
+}
+
 // Sum over a block of whole warps; `part` holds one float per warp.  Every
 // thread gets the sum, added in the same order.  part may be reused after the next barrier.
 __device__ __forceinline__ float block_sum(float v, float* part) {
@@ -45,6 +128,10 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
 __device__ __forceinline__ float decay_pow(float ld, int n) {
   return n == 0 ? 1.f : expf(ld * (float)n);
 }
+
+// Waits of the sequence operators' kernels for their own copies and matrix products end after
+// this long and set the word that prnn_sequence_status reports.
+constexpr uint64_t kSeqWaitNs = 2000ull * 1000 * 1000;
 
 // Run `f.template operator()<T>()` with the element type of dtype.
 #define PRNN_BY_DTYPE(dtype, T, ...)                 \

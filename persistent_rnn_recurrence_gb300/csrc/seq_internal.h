@@ -10,6 +10,12 @@
 
 namespace prnn {
 
+// The current device's status word of the sequence operators (device int, 0 = no wait has run out);
+// nullptr when it cannot be had.  Looked up at every call, so it survives a device reset.
+int* seq_status_word();
+// SMs of the current device (1 when unknown).
+int seq_sm_count();
+
 // ---- layer norm (layer_norm.cu) -------------------------------------------
 struct LayerNormArgs {
   prnn_dtype_t dtype;

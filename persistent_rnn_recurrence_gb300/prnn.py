@@ -46,7 +46,7 @@ EXPORTS = ["prnn_create", "prnn_set_weights_dense", "prnn_set_weights_sparse",
            "prnn_stack_create", "prnn_stack_set_layer", "prnn_stack_forward",
            "prnn_stack_get_status", "prnn_stack_set_option", "prnn_stack_get_timing",
            "prnn_stack_get_info", "prnn_stack_destroy", "prnn_backward",
-           "prnn_layer_norm_forward", "prnn_layer_norm_workspace", "prnn_layer_norm_backward",
+           "prnn_sequence_status", "prnn_layer_norm_forward", "prnn_layer_norm_workspace", "prnn_layer_norm_backward",
            "prnn_dropout_forward", "prnn_dropout_backward",
            "prnn_linear_attention_workspace", "prnn_linear_attention_forward",
            "prnn_linear_attention_backward", "prnn_linear_attention_step"]
@@ -135,6 +135,7 @@ _sig = {
     "prnn_stack_get_info": ([_P, ctypes.POINTER(prnn_stack_info_t)], _I),
     "prnn_stack_destroy": ([_P], _I),
     "prnn_backward": ([_P, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P], _I),
+    "prnn_sequence_status": ([_P], _I),
     "prnn_layer_norm_forward": ([_I, _L, _I, _P, _L, _P, _P, ctypes.c_float, _P, _L, _P, _P, _P],
                                 _I),
     "prnn_layer_norm_workspace": ([_L, _I, ctypes.POINTER(ctypes.c_size_t)], _I),
@@ -396,6 +397,11 @@ def prnn_stack_destroy(s: int) -> None:
 
 
 # ---- sequence operators ----------------------------------------------------------
+def prnn_sequence_status(stream=None) -> int:
+    """PRNN_OK, or PRNN_ERR_TIMEOUT once a kernel of the sequence operators has given up a wait."""
+    return _lib.prnn_sequence_status(_stream(stream))
+
+
 def prnn_layer_norm_forward(dtype, rows, cols, x, x_stride, gamma, beta, eps, y, y_stride,
                             mean=None, rstd=None, stream=None) -> None:
     _check(_lib.prnn_layer_norm_forward(dtype, rows, cols, _ptr(x), x_stride, _ptr(gamma),
