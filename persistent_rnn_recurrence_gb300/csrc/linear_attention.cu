@@ -139,7 +139,7 @@ size_t mix_smem(int d) {
 
 }  // namespace
 
-cudaError_t launch_la_mix(const LaArgs& a, cudaStream_t s) {
+cudaError_t launch_la_simt(const LaArgs& a, cudaStream_t s) {
   int d = 0, e = 0;
   for (int i = 0; i < a.roles; ++i) {
     d = a.role[i].d > d ? a.role[i].d : d;

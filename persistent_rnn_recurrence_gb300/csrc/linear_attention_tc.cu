@@ -1,0 +1,901 @@
+// linear_attention_tc.cu -- the `mix` operation of seq_internal.h on the 5th-generation tensor
+// cores, for fp16 and bf16 data: linear attention's forward pass and all three products of its
+// backward pass.
+//
+// A CTA walks the chunks of C tokens of one (role, sequence, head) and 64 of the e columns, the
+// state in registers.  With l the decay, per chunk entered with state X:
+//   P  = A B^T            (C x C, scores)             tcgen05, operands K-major
+//   O1 = (P o D) C        D_ij = l^|i-j|, causal      P goes back to TMEM as the A operand
+//   O2 = A X                                          X in shared memory, MN-major
+//   U  = B^T (w C)        w_j the tokens' decays      B is the same tile, MN-major
+//   out_i = s_intra O1_i + s_inter l^(.) O2_i,   X <- l^n X + s_add U.
+// One TMA load of a tile serves both majors, so nothing is transposed.  Every power of l has an
+// exponent >= 0 (D in blocks of 16 columns: l^(i-j) = l^(i-j0-15) l^(15-(j-j0))), so no decay
+// overflows.
+//
+// Rounding.  The products take 16-bit operands.  The data enters as it is; what is computed in
+// between enters as a sum of parts of the data's type: P and X in two (bf16: 16 bits; their error
+// stays far below the output's one rounding), w C in three for bf16 (24 bits) and two for fp16
+// (22), because U sums into the fp32 state.  All products accumulate in fp32.  For fp16, whose range
+// would not hold them, P is scaled by a power of two per row and X and w C per tile, taken back after the
+// product.
+//
+// Warps: 0 loads (TMA), 1 issues the matrix products, 4-7 turn scores into operands and write the
+// output, 8-11 own the state (one row of X per thread), 12-15 make w C.  The order of
+// products is QK(c+1), QS(c), KV(c), PV(c): the scores of the next chunk are being weighted while this
+// chunk's output is finished, and the state's update runs under PV.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "seq_common.cuh"
+#include "seq_internal.h"
+#include "tc_common.cuh"
+
+namespace prnn {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 512, kSlice = 64;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColP = 0, kColO1 = 256, kColO2 = 320, kColU = 384;
+
+template <typename T, int DB>
+struct Cfg {
+  static constexpr int C = DB == 2 ? 112 : 128;  // tokens per chunk: what the rings leave room for
+  static constexpr int kParts = std::is_same<T, __half>::value ? 2 : 3;
+  static constexpr uint32_t kBlock = C * 128;    // one [C][64] tile, 128-byte swizzled
+  static constexpr uint32_t kStage = (2 * DB + 1) * kBlock;
+  static constexpr uint32_t kStateTile = DB * 64 * 128;
+  static constexpr uint32_t oW = 2 * kStage;     // w C, kParts tiles
+  static constexpr uint32_t oX = oW + kParts * kBlock;  // X, two tiles
+  static constexpr uint32_t oTab = oX + 2 * kStateTile;
+};
+
+struct Tables {
+  float pw[132];      // l^n
+  float dec[16];      // l^(15-j), or l^j in reverse
+  float x_scale[2], w_scale[2];  // fp16: powers of two taken back from O2 and U
+  float red[2][4];
+  uint64_t ab_full[2], c_full[2], stage_free[2], p_full[2], p_ready[2];
+  uint64_t o_full, o_free, x_ready, w_ready, u_full, u_free, done;
+  uint32_t tmem;
+};
+
+struct TcRole {
+  int ia, ib, ic;     // tensor maps of a, b, c
+  int sa, sb, sc;     // heads sharing one
+  void* out;
+  long long ot, ob, oh;
+  int out_f32, d, e;
+  const float* x0;
+  float* x_end;
+  int x_t, rev, lead;
+  float s_intra, s_inter, s_add;
+};
+struct TcArgs {
+  TcRole role[3];
+  int T, B, H;
+  const float* log_decay;
+  const int32_t* lens;
+  int* status;
+  // segments: cps chunks each; states of `subs` runs of cpb chunks in part
+  int segs, cps, subs, cpb, slices, states_only;
+  float* part;        // [role][B*H][subs][slices * 64][128]
+};
+struct Maps {
+  CUtensorMap m[4];
+};
+
+// MN-major operand in 128-byte-swizzled tiles: 64 values of the M or N axis side by side, 8 steps of K
+// per 1024 bytes; the next 64 values are `lead` bytes on.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr, uint32_t lead) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(lead >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+constexpr uint32_t kAMn = 1u << 15, kBMn = 1u << 16;
+template <typename T>
+__host__ __device__ constexpr uint32_t idesc(int M, int N) {
+  return std::is_same<T, __half>::value ? f16_idesc(M, N) : bf16_idesc(M, N);
+}
+// A from tensor memory
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
+                                        uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0,
+                                         int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void before_sync() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void after_sync() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void to_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// One arrival for the whole warp, after every lane's work.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15},"
+      " [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(a));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
+      " {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Two values as a packed pair of T, and what the packing left over.
+template <typename T>
+__device__ __forceinline__ uint32_t take(float2& v) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 h = __float22half2_rn(v);
+    const float2 b = __half22float2(h);
+    v = add2(v, make_float2(-b.x, -b.y));
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __float22bfloat162_rn(v);
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
+    v = add2(v, make_float2(-__uint_as_float(u << 16), -__uint_as_float(u & 0xFFFF0000u)));
+    return u;
+  }
+}
+template <typename T>
+__device__ __forceinline__ float2 unpack(uint32_t u) {
+  if constexpr (std::is_same<T, __half>::value)
+    return __half22float2(*reinterpret_cast<const __half2*>(&u));
+  else
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+// 2^k such that max * 2^k lies in [2^13, 2^14), for 0 <= max; and 2^-k.
+__device__ __forceinline__ float2 fit_scale(float max) {
+  int k = 13 + 127 - (int)(__float_as_uint(max) >> 23);
+  k = k > 100 ? 100 : k;
+  return make_float2(__uint_as_float((uint32_t)(127 + k) << 23), __uint_as_float((uint32_t)(127 - k) << 23));
+}
+// The largest of 128 threads' values (warps w = 0..3 of a group with named barrier id).
+__device__ __forceinline__ float group_max(float v, float* red, int w, int id) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
+  if ((threadIdx.x & 31) == 0) red[w] = v;
+  asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
+  return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+}
+
+template <typename T, int DB>
+__global__ void __launch_bounds__(kThreads, 1)
+    la_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g) {
+  using K = Cfg<T, DB>;
+  constexpr int C = K::C;
+  constexpr bool kHalf = std::is_same<T, __half>::value;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  Tables& tab = *reinterpret_cast<Tables*>(smem + K::oTab);
+  const TcRole& r = g.role[blockIdx.y];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int slice = blockIdx.x % g.slices, seg = blockIdx.x / g.slices % (g.states_only ? g.subs : g.segs);
+  const int bh = blockIdx.x / g.slices / (g.states_only ? g.subs : g.segs), b = bh / g.H, h = bh % g.H;
+  const int e0 = slice * kSlice;
+  if (e0 >= r.e) return;
+  int len = g.T;
+  if (g.lens) {
+    len = g.lens[b];
+    len = len < 0 ? 0 : (len > g.T ? g.T : len);
+  }
+  const int chunks = (len + C - 1) / C;
+  // this CTA's run of chunks, in the order of processing
+  const int per = g.states_only ? g.cpb : g.cps;
+  const int from = min(seg * per, chunks), to = min((seg + 1) * per, chunks), nc = to - from;
+  const float ld = g.log_decay[h];
+  const int last = len - (chunks - 1) * C;  // tokens of the last chunk
+  auto chunk_of = [&](int c) { return r.rev ? chunks - 1 - c : c; };
+  auto tokens_of = [&](int c) { return chunk_of(c) == chunks - 1 ? last : C; };
+  // tokens processed before chunk c of the order
+  auto before = [&](int c) {
+    if (c <= 0) return 0;
+    if (c >= chunks) return len;
+    return r.rev ? last + (c - 1) * C : c * C;
+  };
+  const bool writes_end = !g.states_only && r.x_end && (nc > 0 ? to == chunks : (chunks == 0 && seg == 0));
+
+  if (!g.states_only && r.out) {  // zeros past the length
+    const int ncol = min(kSlice, r.e - e0);
+    for (int c = max(seg * per, chunks); c < (seg + 1) * per && c * C < g.T; ++c) {
+      const int rows = min(C, g.T - c * C);
+      for (int i = tid; i < rows * (kSlice / 8); i += kThreads) {
+        const int row = i / (kSlice / 8), q = i % (kSlice / 8) * 8;
+        if (q >= ncol) continue;
+        const long long at = (long long)(c * C + row) * r.ot + b * r.ob + h * r.oh + e0 + q;
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        if (r.out_f32) {
+          uint4* p = reinterpret_cast<uint4*>(static_cast<float*>(r.out) + at);
+          p[0] = z;
+          p[1] = z;
+        } else {
+          *reinterpret_cast<uint4*>(static_cast<T*>(r.out) + at) = z;
+        }
+      }
+    }
+  }
+  if (nc == 0 && !writes_end) return;
+
+  const uint32_t base = smem_u32(smem);
+  if (base & 1023u) {  // the swizzled tiles need it; no static shared memory precedes them
+    if (tid == 0) atomicExch(g.status, 1);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tab.ab_full[i], 1);
+      mbar_init(&tab.c_full[i], 1);
+      mbar_init(&tab.stage_free[i], 1);
+      mbar_init(&tab.p_full[i], 1);
+      mbar_init(&tab.p_ready[i], 4);
+    }
+    mbar_init(&tab.o_full, 1);
+    mbar_init(&tab.o_free, 4);
+    mbar_init(&tab.x_ready, 4);
+    mbar_init(&tab.w_ready, 4);
+    mbar_init(&tab.u_full, 1);
+    mbar_init(&tab.u_free, 4);
+    mbar_init(&tab.done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&tab.tmem)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid < 132) tab.pw[tid] = decay_pow(ld, tid);
+  else if (tid < 148) tab.dec[tid - 132] = decay_pow(ld, r.rev ? tid - 132 : 147 - tid);
+  before_sync();
+  __syncthreads();
+  after_sync();
+  const uint32_t tmem = tab.tmem;
+  const uint64_t deadline = global_ns() + kSeqWaitNs;
+  // a state enters the first chunk unless it is known to be zero
+  const bool enters = r.x0 != nullptr || (seg > 0 && !g.states_only);
+  const bool with_out = !g.states_only;
+  // A wait that runs out is remembered and the work goes on (every later wait then ends at once):
+  // no thread leaves the others waiting, and nothing is left in flight.
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, int turn) { ok = mbar_wait(bar, turn & 1, deadline) && ok; };
+  auto warp_wait = [&](uint64_t* bar, int turn) {
+    wait(bar, turn);
+    __syncwarp();
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---- loads ----
+      const int db = (r.d + 63) / 64;
+      for (int c = 0; c < nc; ++c) {
+        const int s = c & 1, t0 = chunk_of(from + c) * C;
+        if (c >= 2) wait(&tab.stage_free[s], (c >> 1) - 1);
+        const uint32_t at = base + s * K::kStage;
+        mbar_arrive_expect_tx(&tab.ab_full[s], (with_out ? 2 : 1) * db * K::kBlock);
+        for (int k = 0; k < db; ++k) {
+          tma_load(at + (DB + k) * K::kBlock, &maps.m[r.ib], &tab.ab_full[s], k * 64, h / r.sb, b, t0);
+          if (with_out)
+            tma_load(at + k * K::kBlock, &maps.m[r.ia], &tab.ab_full[s], k * 64, h / r.sa, b, t0);
+        }
+        mbar_arrive_expect_tx(&tab.c_full[s], K::kBlock);
+        tma_load(at + 2 * DB * K::kBlock, &maps.m[r.ic], &tab.c_full[s], e0, h / r.sc, b, t0);
+      }
+      for (int c = max(0, nc - 2); c < nc; ++c) {  // every load lands before the CTA leaves
+        const uint64_t limit = deadline + kSeqWaitNs;
+        ok = mbar_wait(&tab.ab_full[c & 1], (c >> 1) & 1, limit) && ok;
+        ok = mbar_wait(&tab.c_full[c & 1], (c >> 1) & 1, limit) && ok;
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---- matrix products ----
+      const int dsteps = (r.d + 15) / 16;
+      auto qk = [&](int c) {
+        wait(&tab.ab_full[c & 1], c >> 1);
+        if (!with_out) return;
+        after_sync();
+        const uint32_t at = base + (c & 1) * K::kStage;
+        for (int k = 0; k < dsteps; ++k) {
+          const uint32_t off = (k / 4) * K::kBlock + (k % 4) * 32;
+          umma_f16(tmem + kColP + (c & 1) * 128, sw128_kmajor_desc(at + off),
+                   sw128_kmajor_desc(at + DB * K::kBlock + off), idesc<T>(128, C), k > 0);
+        }
+        umma_commit(&tab.p_full[c & 1]);
+      };
+      if (nc > 0) qk(0);
+      for (int c = 0; c < nc; ++c) {
+        const uint32_t at = base + (c & 1) * K::kStage;
+        if (c + 1 < nc) qk(c + 1);
+        if (with_out) {
+          if (c > 0) wait(&tab.o_free, c - 1);
+          if (c > 0 || enters) {
+            wait(&tab.x_ready, enters ? c : c - 1);
+            after_sync();
+            for (int p = 0; p < 2; ++p)
+              for (int k = 0; k < dsteps; ++k)
+                umma_f16(tmem + kColO2,
+                         sw128_kmajor_desc(at + (k / 4) * K::kBlock + (k % 4) * 32),
+                         mn_desc(base + K::oX + p * K::kStateTile + k * 2048, 1024),
+                         idesc<T>(128, kSlice) | kBMn, p > 0 || k > 0);
+          }
+        }
+        wait(&tab.c_full[c & 1], c >> 1);
+        wait(&tab.w_ready, c);
+        if (c > 0) wait(&tab.u_free, c - 1);
+        after_sync();
+        for (int p = 0; p < K::kParts; ++p)
+          for (int k = 0; k < C / 16; ++k)
+            umma_f16(tmem + kColU, mn_desc(at + DB * K::kBlock + k * 2048, K::kBlock),
+                     mn_desc(base + K::oW + p * K::kBlock + k * 2048, 1024),
+                     idesc<T>(128, kSlice) | kAMn | kBMn, p > 0 || k > 0);
+        umma_commit(&tab.u_full);
+        if (with_out) {
+          wait(&tab.p_ready[c & 1], c >> 1);
+          after_sync();
+          for (int k = 0; k < C / 16; ++k)
+            for (int p = 0; p < 2; ++p)
+              umma_ts(tmem + kColO1, tmem + kColP + (c & 1) * 128 + 16 * k + 8 * p,
+                      mn_desc(at + 2 * DB * K::kBlock + k * 2048, 1024),
+                      idesc<T>(128, kSlice) | kBMn, k > 0 || p > 0);
+          umma_commit(&tab.o_full);
+        }
+        umma_commit(&tab.stage_free[c & 1]);
+      }
+      // every product has read its operands before the CTA leaves
+      umma_commit(&tab.done);
+      ok = mbar_wait(&tab.done, 0, deadline + kSeqWaitNs) && ok;
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ---- scores to operands; output ----
+    const int w = warp - 4, i = w * 32 + lane;
+    const uint32_t quad = (uint32_t)(w * 32) << 16;
+    float back[2] = {1.f, 1.f};  // fp16: the row's power of two, taken back from O1
+    auto weigh = [&](int c) {
+      warp_wait(&tab.p_full[c & 1], c >> 1);
+      after_sync();
+      const uint32_t at = tmem + quad + kColP + (c & 1) * 128;
+      const int n = tokens_of(from + c);
+      // columns [16 jb, 16 jb + 16) against this warp's rows [32 w, 32 w + 32)
+      auto nothing = [&](int jb) { return r.rev ? jb < 2 * w : jb > 2 * w + 1; };
+      auto weighted = [&](int jb, float2(&v)[8]) {
+        uint32_t raw[16];
+        tmem_ld16(at + 16 * jb, raw);
+        wait_ld();
+        const bool diagonal = jb == 2 * w || jb == 2 * w + 1;
+        if (!diagonal && (n == C || 16 * jb + 16 <= n)) {
+          const float2 f = both(tab.pw[r.rev ? 16 * jb - i : i - 16 * jb - 15]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 d = *reinterpret_cast<const float2*>(tab.dec + 2 * j);
+            v[j] = mul2(make_float2(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1])),
+                        mul2(f, d));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int col = 16 * jb + j, gap = r.rev ? col - i : i - col;
+            const float x = gap >= 0 && col < n ? __uint_as_float(raw[j]) * tab.pw[gap < 0 ? 0 : gap] : 0.f;
+            if (j & 1) v[j / 2].y = x;
+            else v[j / 2].x = x;
+          }
+        }
+      };
+      float2 scale = both(1.f);
+      if constexpr (kHalf) {
+        float top = 0.f;
+#pragma unroll 1
+        for (int jb = 0; jb < C / 16; ++jb) {
+          if (nothing(jb)) continue;
+          float2 v[8];
+          weighted(jb, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top = fmaxf(top, fmaxf(fabsf(v[j].x), fabsf(v[j].y)));
+        }
+        const float2 f = fit_scale(top);
+        scale = both(f.x);
+        back[c & 1] = f.y;
+      }
+#pragma unroll 1
+      for (int jb = 0; jb < C / 16; ++jb) {
+        uint32_t o[16];
+        if (nothing(jb)) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = 0u;
+        } else {
+          float2 v[8];
+          weighted(jb, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (kHalf) v[j] = mul2(v[j], scale);
+            o[j] = take<T>(v[j]);
+            o[8 + j] = take<T>(v[j]);
+          }
+        }
+        tmem_st16(at + 16 * jb, o);
+      }
+      wait_st();
+      before_sync();
+      warp_arrive(&tab.p_ready[c & 1]);
+    };
+    auto output = [&](int c) {
+      warp_wait(&tab.o_full, c);
+      after_sync();
+      const int n = tokens_of(from + c), t0 = chunk_of(from + c) * C;
+      const bool state = c > 0 || enters;
+      const int gap = (r.rev ? n - 1 - i : i) + r.lead;
+      const float2 fi = both(r.s_intra * back[c & 1]);
+      const float2 fx = both(r.s_inter * tab.pw[gap < 0 ? 0 : gap] * (kHalf && state ? tab.x_scale[c & 1] : 1.f));
+      const bool live = i < n, there = i < C && t0 + i < g.T && r.out;
+      const long long at = (long long)(t0 + i) * r.ot + b * r.ob + h * r.oh + e0;
+#pragma unroll
+      for (int q = 0; q < kSlice / 16; ++q) {
+        uint32_t a[16], x[16];
+        tmem_ld16(tmem + quad + kColO1 + 16 * q, a);
+        if (state) tmem_ld16(tmem + quad + kColO2 + 16 * q, x);
+        wait_ld();
+        if (q == kSlice / 16 - 1) {
+          before_sync();
+          warp_arrive(&tab.o_free);
+        }
+        float2 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[j] = mul2(make_float2(__uint_as_float(a[2 * j]), __uint_as_float(a[2 * j + 1])), fi);
+          if (state)
+            v[j] = fma2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), fx, v[j]);
+          if (!live) v[j] = both(0.f);
+        }
+        if (there) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const int col = 16 * q + 8 * s;
+            if (e0 + col < r.e) {  // e is a multiple of 8
+              const float2* u = v + 4 * s;
+              if (r.out_f32) {
+                float4* p = reinterpret_cast<float4*>(static_cast<float*>(r.out) + at + col);
+                p[0] = make_float4(u[0].x, u[0].y, u[1].x, u[1].y);
+                p[1] = make_float4(u[2].x, u[2].y, u[3].x, u[3].y);
+              } else {
+                uint4 p;
+                float2 m[4] = {u[0], u[1], u[2], u[3]};
+                p.x = take<T>(m[0]);
+                p.y = take<T>(m[1]);
+                p.z = take<T>(m[2]);
+                p.w = take<T>(m[3]);
+                *reinterpret_cast<uint4*>(static_cast<T*>(r.out) + at + col) = p;
+              }
+            }
+          }
+        }
+        __syncwarp();
+      }
+    };
+    if (with_out && nc > 0) {
+      weigh(0);
+      for (int c = 0; c < nc; ++c) {
+        if (c + 1 < nc) weigh(c + 1);
+        output(c);
+      }
+    }
+  } else if (warp >= 8 && warp < 12) {
+    // ---- the state: row `row` of X, 64 columns ----
+    const int w = warp - 8, row = w * 32 + lane;
+    const uint32_t quad = (uint32_t)(w * 32) << 16;
+    const int ncol = min(kSlice, r.e - e0);
+    const size_t head = (size_t)bh * r.d * r.e;
+    float2 X[kSlice / 2];
+#pragma unroll
+    for (int j = 0; j < kSlice / 2; ++j) X[j] = both(0.f);
+    const int done_before = before(from);
+    if (r.x0 && !g.states_only && row < r.d) {
+      const float f = decay_pow(ld, done_before);
+#pragma unroll
+      for (int j = 0; j < kSlice; ++j)
+        if (j < ncol) {
+          const float v = f * (r.x_t ? r.x0[head + (size_t)(e0 + j) * r.d + row]
+                                     : r.x0[head + (size_t)row * r.e + e0 + j]);
+          if (j & 1) X[j / 2].y = v;
+          else X[j / 2].x = v;
+        }
+    }
+    float* part = g.part + (((size_t)blockIdx.y * g.B * g.H + bh) * g.subs * g.slices + slice) * kSlice * 128 + row;
+    const size_t sub_size = (size_t)g.slices * kSlice * 128;
+    if (!g.states_only) {
+      const int subs = min(seg * (g.cps / g.cpb), (chunks + g.cpb - 1) / g.cpb);
+      for (int u = 0; u < subs; ++u) {
+        const float f = decay_pow(ld, done_before - before((u + 1) * g.cpb));
+#pragma unroll
+        for (int j = 0; j < kSlice / 2; ++j) {
+          const float* p = part + u * sub_size + 2 * j * 128;
+          X[j] = fma2(make_float2(__ldcg(p), __ldcg(p + 128)), both(f), X[j]);
+        }
+      }
+    }
+    const int db = (r.d + 63) / 64;
+    unsigned char* tile = smem + K::oX + row * 128;
+    auto publish = [&](int turn) {  // X as parts in shared memory, for the chunk of this turn
+      float2 scale = both(1.f);
+      if constexpr (kHalf) {
+        float top = 0.f;
+        if (row < r.d)
+#pragma unroll
+          for (int j = 0; j < kSlice / 2; ++j) top = fmaxf(top, fmaxf(fabsf(X[j].x), fabsf(X[j].y)));
+        const float2 f = fit_scale(group_max(top, tab.red[0], w, 1));
+        scale = both(f.x);
+        if (row == 0) tab.x_scale[turn & 1] = f.y;
+      }
+      if (row < db * 64) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float2 v = X[4 * q + j];
+            if (kHalf) v = mul2(v, scale);
+            hi[j] = take<T>(v);
+            lo[j] = take<T>(v);
+          }
+          const uint32_t at = (uint32_t)((q ^ (row & 7)) << 4);
+          *reinterpret_cast<uint4*>(tile + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(tile + K::kStateTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+      }
+      to_async();
+      warp_arrive(&tab.x_ready);
+    };
+    if (enters && with_out && nc > 0) publish(0);
+    for (int c = 0; c < nc; ++c) {
+      warp_wait(&tab.u_full, c);
+      after_sync();
+      const float2 f = both(tab.pw[min(tokens_of(from + c), 131)]);
+      const float2 s = both(r.s_add * (kHalf ? tab.w_scale[c & 1] : 1.f));
+#pragma unroll
+      for (int q = 0; q < kSlice / 16; ++q) {
+        uint32_t u[16];
+        tmem_ld16(tmem + quad + kColU + 16 * q, u);
+        wait_ld();
+        if (q == kSlice / 16 - 1) {
+          before_sync();
+          warp_arrive(&tab.u_free);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          X[8 * q + j] = fma2(make_float2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1])), s,
+                              mul2(f, X[8 * q + j]));
+      }
+      if (with_out && c + 1 < nc) publish(c + 1);
+    }
+    if (writes_end && row < r.d) {
+#pragma unroll
+      for (int j = 0; j < kSlice; ++j)
+        if (j < ncol)
+          r.x_end[head + (r.x_t ? (size_t)(e0 + j) * r.d + row : (size_t)row * r.e + e0 + j)] =
+              j & 1 ? X[j / 2].y : X[j / 2].x;
+    }
+    if (g.states_only) {
+#pragma unroll
+      for (int j = 0; j < kSlice / 2; ++j) {
+        part[seg * sub_size + 2 * j * 128] = X[j].x;
+        part[seg * sub_size + (2 * j + 1) * 128] = X[j].y;
+      }
+    }
+  } else if (warp >= 12) {
+    // ---- w C: row j of the tile, its decay to the chunk's end ----
+    const int w = warp - 12, j = w * 32 + lane;
+    for (int c = 0; c < nc; ++c) {
+      const int n = tokens_of(from + c);
+      warp_wait(&tab.c_full[c & 1], c >> 1);
+      unsigned char* tile = smem + (c & 1) * K::kStage + 2 * DB * K::kBlock + j * 128;
+      const int gap = (r.rev ? j : n - 1 - j) + 1 - r.lead;
+      const float wj = j < n ? tab.pw[gap] : 0.f;
+      uint4 raw[8];
+      float2 scale = both(1.f);
+      if (j < C) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          raw[q] = *reinterpret_cast<const uint4*>(tile + ((q ^ (j & 7)) << 4));
+          if (j >= n) raw[q] = make_uint4(0, 0, 0, 0);
+        }
+      }
+      if constexpr (kHalf) {
+        float top = 0.f;
+        if (j < n)
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const uint32_t u[4] = {raw[q].x, raw[q].y, raw[q].z, raw[q].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 v = unpack<T>(u[k]);
+              top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+            }
+          }
+        const float2 f = fit_scale(group_max(top * wj, tab.red[1], w, 2));
+        scale = both(f.x);
+        if (j == 0) tab.w_scale[c & 1] = f.y;
+      }
+      if (c > 0) warp_wait(&tab.u_full, c - 1);
+      if (n < C) {
+        // Rows past the length may hold anything: the score tile's product with them ends first, then
+        // they are cleared, so that 0 * anything stays 0.
+        warp_wait(with_out ? &tab.p_full[c & 1] : &tab.ab_full[c & 1], c >> 1);
+        if (j >= n && j < C) {
+          const int db = (r.d + 63) / 64;
+          const uint4 z = make_uint4(0, 0, 0, 0);
+          for (int q = 0; q < 8; ++q) {
+            *reinterpret_cast<uint4*>(tile + (q << 4)) = z;
+            for (int k = 0; k < db; ++k)
+              *reinterpret_cast<uint4*>(smem + (c & 1) * K::kStage + (DB + k) * K::kBlock + j * 128 + (q << 4)) = z;
+          }
+        }
+      }
+      if (j < C) {
+        const float2 f = mul2(both(wj), scale);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const uint32_t u[4] = {raw[q].x, raw[q].y, raw[q].z, raw[q].w};
+          uint32_t p[3][4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float2 v = mul2(unpack<T>(u[k]), f);
+#pragma unroll
+            for (int m = 0; m < K::kParts; ++m) p[m][k] = take<T>(v);
+          }
+#pragma unroll
+          for (int m = 0; m < K::kParts; ++m)
+            *reinterpret_cast<uint4*>(smem + K::oW + m * K::kBlock + j * 128 + ((q ^ (j & 7)) << 4)) =
+                make_uint4(p[m][0], p[m][1], p[m][2], p[m][3]);
+        }
+      }
+      to_async();
+      warp_arrive(&tab.w_ready);
+    }
+  }
+  if (!ok) atomicExch(g.status, 1);
+  before_sync();
+  __syncthreads();
+  if (warp == 0) {
+    after_sync();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
+                 : "memory");
+  }
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  return fn;
+}
+
+// A sequence tensor as {d, heads, B, T}, read in boxes of 64 values of C tokens of one head.
+bool encode(CUtensorMap* map, const LaSeq& x, int d, int heads, int B, int T, int C, bool half) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)B, (cuuint64_t)T};
+  // the stride of an axis of one is never used, but has to be a legal one
+  const cuuint64_t strides[3] = {(cuuint64_t)(heads > 1 ? x.sh * 2 : 16), (cuuint64_t)(B > 1 ? x.sb * 2 : 16),
+                                 (cuuint64_t)(T > 1 ? x.st * 2 : 16)};
+  const cuuint32_t box[4] = {64, 1, 1, (cuuint32_t)C}, estr[4] = {1, 1, 1, 1};
+  return fn(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+            const_cast<void*>(x.p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool axis_ok(long long stride, int n) {
+  return n <= 1 || (stride > 0 && stride % 8 == 0 && stride < (1LL << 38));
+}
+bool seq_fits(const LaSeq& s, const LaArgs& a, int d) {
+  return (reinterpret_cast<uintptr_t>(s.p) & 15) == 0 && d % 8 == 0 && axis_ok(s.st, a.T) &&
+         axis_ok(s.sb, a.B) && axis_ok(s.sh, a.H / s.share);
+}
+
+constexpr size_t kStateBytes = kSlice * 128 * sizeof(float);  // one CTA's state in the scratch
+
+struct Plan {
+  int segs, cps, subs, cpb, slices;
+};
+
+// How many segments of time run side by side.  A role's CTAs (sequence, head, 64 columns) walk
+// their chunks one after another; with few of them the time axis is cut into segs runs whose
+// entering states a first pass over b and c computes (about half the work of a chunk, in
+// runs fine enough to fill the SMs).  The estimate counts chunk times of one CTA per SM, with about one
+// for a CTA's start and three for the second launch.  The first pass's states fit `capacity` bytes.
+Plan make_plan(const LaArgs& a, int C, int sms, size_t capacity) {
+  Plan p{1, 1, 0, 1, 1};
+  bool in_place = false;  // a segment could write the state before another has read it
+  for (int i = 0; i < a.roles; ++i) in_place = in_place || (a.role[i].x0 && a.role[i].x0 == a.role[i].x_end);
+  const int chunks = (a.T + C - 1) / C;
+  int e = 0;
+  for (int i = 0; i < a.roles; ++i) e = std::max(e, a.role[i].e);
+  p.slices = (e + kSlice - 1) / kSlice;
+  const long long ctas = (long long)a.B * a.H * p.slices * a.roles;
+  auto waves = [&](long long n) { return (double)((n + sms - 1) / sms); };
+  double best = waves(ctas) * (chunks + 1);
+  p.cps = chunks;
+  if (in_place) return p;
+  for (int segs = 2; segs <= 64 && segs <= chunks; ++segs) {
+    const int cps = (chunks + segs - 1) / segs, real = (chunks + cps - 1) / cps;
+    if (real != segs) continue;
+    for (int m = 1; m <= 4 && m <= cps; ++m) {
+      if (cps % m) continue;
+      const int cpb = cps / m, subs = (segs - 1) * m;
+      if ((size_t)ctas * subs * kStateBytes > capacity) continue;
+      const double cost = waves(ctas * segs) * (cps + 1) + waves(ctas * subs) * (0.5 * cpb + 1) + 3 +
+                          0.05 * subs;
+      if (cost < best) {
+        best = cost;
+        p = {segs, cps, subs, cpb, p.slices};
+      }
+    }
+  }
+  return p;
+}
+
+int max_d(const LaArgs& a) {
+  int d = 0;
+  for (int i = 0; i < a.roles; ++i) d = std::max(d, a.role[i].d);
+  return d;
+}
+int chunk_of(int d) { return d > 64 ? Cfg<__half, 2>::C : Cfg<__half, 1>::C; }
+
+template <typename T, int DB>
+cudaError_t launch(const Maps& maps, TcArgs g, const Plan& p, int roles, cudaStream_t s) {
+  using K = Cfg<T, DB>;
+  constexpr int smem = (int)(K::oTab + sizeof(Tables));
+  static_assert(smem <= 227 * 1024, "shared memory");
+  auto kernel = la_tc_kernel<T, DB>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const unsigned bh = (unsigned)(g.B * g.H * p.slices);
+  if (p.segs > 1) {
+    g.states_only = 1;
+    kernel<<<dim3(bh * p.subs, roles), kThreads, smem, s>>>(maps, g);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    g.states_only = 0;
+  }
+  kernel<<<dim3(bh * p.segs, roles), kThreads, smem, s>>>(maps, g);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool la_tc_serves(const LaArgs& a) {
+  if (a.dtype == PRNN_F32 || !encode_fn()) return false;
+  for (int i = 0; i < a.roles; ++i) {
+    const LaRole& r = a.role[i];
+    if (r.d > 128 || r.e > 128 || !seq_fits(r.a, a, r.d) || !seq_fits(r.b, a, r.d) ||
+        !seq_fits(r.c, a, r.e))
+      return false;
+    const int unit = r.out_f32 ? 4 : 8;
+    if (r.out && ((reinterpret_cast<uintptr_t>(r.out) & 15) || (a.T > 1 && r.ot % unit) ||
+                  (a.B > 1 && r.ob % unit) || (a.H > 1 && r.oh % unit)))
+      return false;
+  }
+  return (long long)a.B * a.H * 64 * 4 < (1LL << 31);
+}
+
+size_t la_tc_workspace(const LaArgs& a) {
+  const Plan p = make_plan(a, chunk_of(max_d(a)), seq_sm_count(), ~(size_t)0);
+  return (size_t)a.roles * a.B * a.H * p.subs * p.slices * kStateBytes;
+}
+
+cudaError_t launch_la_tc(const LaArgs& a, float* part, size_t part_bytes, cudaStream_t s) {
+  if (a.roles == 0 || a.B == 0) return cudaSuccess;
+  const int d = max_d(a), C = chunk_of(d);
+  const bool half = a.dtype == PRNN_F16;
+  const Plan p = make_plan(a, C, seq_sm_count(), part_bytes);
+  Maps maps;
+  LaSeq seen[4];
+  int width[4], n = 0;
+  auto index = [&](const LaSeq& x, int w) {
+    for (int i = 0; i < n; ++i)
+      if (seen[i].p == x.p && seen[i].st == x.st && seen[i].sb == x.sb && seen[i].sh == x.sh &&
+          seen[i].share == x.share && width[i] == w)
+        return i;
+    if (n == 4 || !encode(&maps.m[n], x, w, a.H / x.share, a.B, a.T, C, half)) return -1;
+    seen[n] = x;
+    width[n] = w;
+    return n++;
+  };
+  TcArgs g{};
+  for (int i = 0; i < a.roles; ++i) {
+    const LaRole& r = a.role[i];
+    TcRole& t = g.role[i];
+    t.ia = index(r.a, r.d);
+    t.ib = index(r.b, r.d);
+    t.ic = index(r.c, r.e);
+    if (t.ia < 0 || t.ib < 0 || t.ic < 0) return cudaErrorInvalidValue;
+    t.sa = r.a.share;
+    t.sb = r.b.share;
+    t.sc = r.c.share;
+    t.out = r.out;
+    t.ot = r.ot;
+    t.ob = r.ob;
+    t.oh = r.oh;
+    t.out_f32 = r.out_f32;
+    t.d = r.d;
+    t.e = r.e;
+    t.x0 = r.x0;
+    t.x_end = r.x_end;
+    t.x_t = r.x_t;
+    t.rev = r.rev;
+    t.lead = r.lead;
+    t.s_intra = r.s_intra;
+    t.s_inter = r.s_inter;
+    t.s_add = r.s_add;
+  }
+  for (int i = n; i < 4; ++i) maps.m[i] = maps.m[0];
+  g.T = a.T;
+  g.B = a.B;
+  g.H = a.H;
+  g.log_decay = a.log_decay;
+  g.lens = a.lens;
+  g.status = seq_status_word();
+  if (!g.status) return cudaErrorUnknown;
+  g.segs = p.segs;
+  g.cps = p.cps;
+  g.subs = p.subs;
+  g.cpb = p.cpb;
+  g.slices = p.slices;
+  g.part = part;
+  if (half)
+    return d > 64 ? launch<__half, 2>(maps, g, p, a.roles, s) : launch<__half, 1>(maps, g, p, a.roles, s);
+  return d > 64 ? launch<__nv_bfloat16, 2>(maps, g, p, a.roles, s)
+                : launch<__nv_bfloat16, 1>(maps, g, p, a.roles, s);
+}
+
+}  // namespace prnn

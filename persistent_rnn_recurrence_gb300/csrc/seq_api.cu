@@ -141,9 +141,34 @@ LaSeq in(const prnn_seq_t& x, int share) {
   return LaSeq{x.data, x.stride_t, x.stride_b, x.stride_h, share};
 }
 
-// Bytes of the fp32 partial gradients of heads that share a query and key head.
+// Bytes of the fp32 partial gradients of heads that share a query and key head (one of dq and dk).
 size_t group_bytes(const prnn_linear_attention_t* a) {
-  return a->heads == a->qk_heads ? 0 : sizeof(float) * (size_t)a->T * a->B * a->heads * a->dk;
+  if (a->heads == a->qk_heads) return 0;
+  return (sizeof(float) * (size_t)a->T * a->B * a->heads * a->dk + 15) / 16 * 16;
+}
+// Bytes of the tensor-core kernels' scratch, 0 where those cannot serve the call: any subset of the
+// backward pass's roles fits.
+size_t tc_bytes(const prnn_linear_attention_t* a, bool backward) {
+  if (a->dtype == PRNN_F32 || a->dk > 128 || a->dv > 128 || a->dk % 8 || a->dv % 8 || a->T == 0 ||
+      a->B == 0)
+    return 0;
+  LaArgs g{};
+  g.dtype = a->dtype;
+  g.T = a->T;
+  g.B = a->B;
+  g.H = a->heads;
+  size_t most = 0;
+  for (g.roles = 1; g.roles <= (backward ? 3 : 1); ++g.roles) {
+    LaRole& r = g.role[g.roles - 1];
+    r.d = backward ? std::max(a->dk, a->dv) : a->dk;
+    r.e = backward ? std::max(a->dk, a->dv) : a->dv;
+    most = std::max(most, la_tc_workspace(g));
+  }
+  return most;
+}
+cudaError_t launch_mix(const LaArgs& g, void* scratch, size_t bytes, cudaStream_t s) {
+  if (la_tc_serves(g)) return launch_la_tc(g, static_cast<float*>(scratch), bytes, s);
+  return launch_la_simt(g, s);
 }
 
 }  // namespace
@@ -277,7 +302,7 @@ prnn_status_t prnn_linear_attention_workspace(const prnn_linear_attention_t* a, 
   prnn_status_t why;
   if (!bytes) return PRNN_ERR_INVALID_ARG;
   if (!shape_ok(a, &why)) return why;
-  *bytes = backward ? 2 * group_bytes(a) : 0;
+  *bytes = (backward ? 2 * group_bytes(a) : 0) + tc_bytes(a, backward != 0);
   return PRNN_OK;
 }
 
@@ -315,6 +340,12 @@ prnn_status_t prnn_linear_attention_forward(const prnn_linear_attention_t* a, vo
       !clear_of(a->log_decay, 4ull * H, part, 4, esz, false) ||
       (a->lens && !clear_of(a->lens, 4ull * B, part, 4, esz, false)))
     return PRNN_ERR_INVALID_ARG;
+  const size_t need = tc_bytes(a, false);
+  if (need && (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < need ||
+               !clear_of(a->workspace, need, part, 4, esz, true) ||
+               (a->state && overlaps(a->state, state_bytes, a->workspace, need)) ||
+               (a->state_out && overlaps(a->state_out, state_bytes, a->workspace, need))))
+    return PRNN_ERR_INVALID_ARG;
   LaArgs g{};
   LaRole& r = g.role[0];
   r.a = in(a->q, H / Hq);
@@ -338,7 +369,7 @@ prnn_status_t prnn_linear_attention_forward(const prnn_linear_attention_t* a, vo
   g.H = H;
   g.log_decay = a->log_decay;
   g.lens = a->lens;
-  return cuda_status(launch_la_mix(g, s));
+  return cuda_status(launch_mix(g, a->workspace, need, s));
 }
 
 prnn_status_t prnn_linear_attention_backward(const prnn_linear_attention_t* a, void* stream) {
@@ -458,7 +489,8 @@ prnn_status_t prnn_linear_attention_backward(const prnn_linear_attention_t* a, v
     r.s_intra = r.s_add = a->scale;
     r.s_inter = 1.f;
   }
-  PRNN_TRY(launch_la_mix(g, s));
+  PRNN_TRY(launch_mix(g, static_cast<char*>(a->workspace) + 2 * group_bytes(a),
+                      need - 2 * group_bytes(a), s));
   if (G > 1) {
     const prnn_seq_t* out[] = {&a->d_q, &a->d_k};
     float* parts[] = {part_q, part_k};

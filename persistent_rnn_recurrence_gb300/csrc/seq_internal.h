@@ -94,7 +94,13 @@ struct LaArgs {
   const float* log_decay;
   const int32_t* lens;        // may be null
 };
-cudaError_t launch_la_mix(const LaArgs& a, cudaStream_t s);
+// On CUDA cores, for any sizes, strides and types.
+cudaError_t launch_la_simt(const LaArgs& a, cudaStream_t s);
+// On the tensor cores: whether it serves a call, the bytes of scratch it needs for these sizes
+// (the larger of what one, two or three roles need), the call.
+bool la_tc_serves(const LaArgs& a);
+size_t la_tc_workspace(const LaArgs& a);
+cudaError_t launch_la_tc(const LaArgs& a, float* part, size_t part_bytes, cudaStream_t s);
 
 // out[t][b][hq][:] = sum of the `group` heads of part [T][B][H][d] (fp32) that share hq.
 struct LaReduceArgs {
