@@ -701,8 +701,8 @@ typedef struct {
   size_t workspace_bytes;
 } prnn_linear_attention_t;
 
-/* Workspace of prnn_linear_attention_forward (backward == 0) or _backward (1) for the
- * sizes, types and layouts in `a` (its pointers are not followed). */
+/* Workspace of prnn_linear_attention_forward (backward == 0) or _backward (1) for the call that
+ * `a` describes (the alignment of its pointers counts; they are not followed). */
 prnn_status_t prnn_linear_attention_workspace(const prnn_linear_attention_t* a, int backward,
                                               size_t* bytes);
 

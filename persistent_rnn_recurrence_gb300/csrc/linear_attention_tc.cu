@@ -20,10 +20,10 @@
 // would not hold them, P is scaled by a power of two per row and X and w C per tile, taken back after the
 // product.
 //
-// Warps: 0 loads (TMA), 1 issues the matrix products, 4-7 turn scores into operands and write the
-// output, 8-11 own the state (one row of X per thread), 12-15 make w C.  The order of
-// products is QK(c+1), QS(c), KV(c), PV(c): the scores of the next chunk are being weighted while this
-// chunk's output is finished, and the state's update runs under PV.
+// Warps: 0 loads (TMA), 1 issues the matrix products, 4-7 turn scores into operands, 8-11 write the
+// output, 12-19 own the state (a row of X and half the columns per thread), 20-27 make w C.  The order of the
+// products is P(c+1), U(c), O2(c), O1(c): the next chunk's scores are weighted, the state updated and
+// this chunk's output written while the tensor cores run the others.
 #include <cuda.h>
 
 #include <algorithm>
@@ -38,9 +38,10 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 512, kSlice = 64;
+constexpr int kThreads = 896, kSlice = 64, kHalfSlice = 32;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColP = 0, kColO1 = 256, kColO2 = 320, kColU = 384;
+// columns of tensor memory: two score tiles, O1, O2 (of X's two parts side by side), U
+constexpr uint32_t kColP = 0, kColO1 = 256, kColO2 = 320, kColU = 448;
 
 template <typename T, int DB>
 struct Cfg {
@@ -57,10 +58,11 @@ struct Cfg {
 struct Tables {
   float pw[132];      // l^n
   float dec[16];      // l^(15-j), or l^j in reverse
-  float x_scale[2], w_scale[2];  // fp16: powers of two taken back from O2 and U
-  float red[2][4];
+  // fp16: powers of two taken back from O2, U and O1, each kept until its last reader is sure to be done
+  float x_scale[2], w_scale[4], row_scale[4][128];
+  float red[2][8];
   uint64_t ab_full[2], c_full[2], stage_free[2], p_full[2], p_ready[2];
-  uint64_t o_full, o_free, x_ready, w_ready, u_full, u_free, done;
+  uint64_t o_full, o_free, x_ready, x_free, w_ready, u_full, u_free, done;
   uint32_t tmem;
 };
 
@@ -69,7 +71,7 @@ struct TcRole {
   int sa, sb, sc;     // heads sharing one
   void* out;
   long long ot, ob, oh;
-  int out_f32, d, e;
+  int out_f32, out_vec, d, e;  // out_vec: rows start on 16 bytes and e is a multiple of 8
   const float* x0;
   float* x_end;
   int x_t, rev, lead;
@@ -192,14 +194,52 @@ __device__ __forceinline__ float2 fit_scale(float max) {
   k = k > 100 ? 100 : k;
   return make_float2(__uint_as_float((uint32_t)(127 + k) << 23), __uint_as_float((uint32_t)(127 - k) << 23));
 }
-// The largest of 128 threads' values (warps w = 0..3 of a group with named barrier id).
+// The largest of 256 threads' values (warps w = 0..7 of a group with named barrier id).
 __device__ __forceinline__ float group_max(float v, float* red, int w, int id) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
+  asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory");
   if ((threadIdx.x & 31) == 0) red[w] = v;
-  asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
-  return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory");
+  float m = red[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = fmaxf(m, red[i]);
+  return m;
+}
+
+// 16 columns of one row, of which the first m are the output's.
+template <typename T>
+__device__ __forceinline__ void store_out(const TcRole& r, long long at, int m, const float2 (&v)[8]) {
+  if (!r.out_vec) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (j < m) {
+        const float f = j & 1 ? v[j / 2].y : v[j / 2].x;
+        if (r.out_f32)
+          static_cast<float*>(r.out)[at + j] = f;
+        else
+          static_cast<T*>(r.out)[at + j] = from_f32<T>(f);
+      }
+    return;
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    if (8 * s >= m) break;
+    const float2* u = v + 4 * s;
+    if (r.out_f32) {
+      float4* p = reinterpret_cast<float4*>(static_cast<float*>(r.out) + at + 8 * s);
+      p[0] = make_float4(u[0].x, u[0].y, u[1].x, u[1].y);
+      p[1] = make_float4(u[2].x, u[2].y, u[3].x, u[3].y);
+    } else {
+      float2 k[4] = {u[0], u[1], u[2], u[3]};
+      uint4 p;
+      p.x = take<T>(k[0]);
+      p.y = take<T>(k[1]);
+      p.z = take<T>(k[2]);
+      p.w = take<T>(k[3]);
+      *reinterpret_cast<uint4*>(static_cast<T*>(r.out) + at + 8 * s) = p;
+    }
+  }
 }
 
 template <typename T, int DB>
@@ -241,18 +281,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ncol = min(kSlice, r.e - e0);
     for (int c = max(seg * per, chunks); c < (seg + 1) * per && c * C < g.T; ++c) {
       const int rows = min(C, g.T - c * C);
-      for (int i = tid; i < rows * (kSlice / 8); i += kThreads) {
-        const int row = i / (kSlice / 8), q = i % (kSlice / 8) * 8;
-        if (q >= ncol) continue;
-        const long long at = (long long)(c * C + row) * r.ot + b * r.ob + h * r.oh + e0 + q;
-        const uint4 z = make_uint4(0, 0, 0, 0);
-        if (r.out_f32) {
-          uint4* p = reinterpret_cast<uint4*>(static_cast<float*>(r.out) + at);
-          p[0] = z;
-          p[1] = z;
-        } else {
-          *reinterpret_cast<uint4*>(static_cast<T*>(r.out) + at) = z;
-        }
+      const float2 z[8] = {};
+      for (int i = tid; i < rows * (kSlice / 16); i += kThreads) {
+        const int row = i / (kSlice / 16), q = i % (kSlice / 16) * 16;
+        store_out<T>(r, (long long)(c * C + row) * r.ot + b * r.ob + h * r.oh + e0 + q, ncol - q, z);
       }
     }
   }
@@ -273,10 +305,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&tab.o_full, 1);
     mbar_init(&tab.o_free, 4);
-    mbar_init(&tab.x_ready, 4);
-    mbar_init(&tab.w_ready, 4);
+    mbar_init(&tab.x_ready, 8);
+    mbar_init(&tab.x_free, 1);
+    mbar_init(&tab.w_ready, 8);
     mbar_init(&tab.u_full, 1);
-    mbar_init(&tab.u_free, 4);
+    mbar_init(&tab.u_free, 8);
     mbar_init(&tab.done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -349,37 +382,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < nc; ++c) {
         const uint32_t at = base + (c & 1) * K::kStage;
         if (c + 1 < nc) qk(c + 1);
+        wait(&tab.c_full[c & 1], c >> 1);
+        wait(&tab.w_ready, c);
+        if (c > 0) wait(&tab.u_free, c - 1);
+        after_sync();
+#pragma unroll 1
+        for (int p = 0; p < K::kParts; ++p) {
+          uint64_t da = mn_desc(at + DB * K::kBlock, K::kBlock);
+          uint64_t dw = mn_desc(base + K::oW + p * K::kBlock, 1024);
+#pragma unroll
+          for (int k = 0; k < C / 16; ++k)  // 16 tokens = 2048 bytes = 128 units
+            umma_f16(tmem + kColU, da + 128 * k, dw + 128 * k, idesc<T>(128, kSlice) | kAMn | kBMn,
+                     p > 0 || k > 0);
+        }
+        umma_commit(&tab.u_full);
         if (with_out) {
           if (c > 0) wait(&tab.o_free, c - 1);
           if (c > 0 || enters) {
             wait(&tab.x_ready, enters ? c : c - 1);
             after_sync();
-            for (int p = 0; p < 2; ++p)
-              for (int k = 0; k < dsteps; ++k)
-                umma_f16(tmem + kColO2,
-                         sw128_kmajor_desc(at + (k / 4) * K::kBlock + (k % 4) * 32),
-                         mn_desc(base + K::oX + p * K::kStateTile + k * 2048, 1024),
-                         idesc<T>(128, kSlice) | kBMn, p > 0 || k > 0);
+            const uint64_t dx = mn_desc(base + K::oX, K::kStateTile);
+#pragma unroll 1
+            for (int k = 0; k < dsteps; ++k)  // both parts of X side by side: 128 columns
+              umma_f16(tmem + kColO2, sw128_kmajor_desc(at + (k / 4) * K::kBlock + (k % 4) * 32),
+                       dx + 128 * k, idesc<T>(128, 2 * kSlice) | kBMn, k > 0);
+            umma_commit(&tab.x_free);
           }
-        }
-        wait(&tab.c_full[c & 1], c >> 1);
-        wait(&tab.w_ready, c);
-        if (c > 0) wait(&tab.u_free, c - 1);
-        after_sync();
-        for (int p = 0; p < K::kParts; ++p)
-          for (int k = 0; k < C / 16; ++k)
-            umma_f16(tmem + kColU, mn_desc(at + DB * K::kBlock + k * 2048, K::kBlock),
-                     mn_desc(base + K::oW + p * K::kBlock + k * 2048, 1024),
-                     idesc<T>(128, kSlice) | kAMn | kBMn, p > 0 || k > 0);
-        umma_commit(&tab.u_full);
-        if (with_out) {
           wait(&tab.p_ready[c & 1], c >> 1);
           after_sync();
-          for (int k = 0; k < C / 16; ++k)
-            for (int p = 0; p < 2; ++p)
-              umma_ts(tmem + kColO1, tmem + kColP + (c & 1) * 128 + 16 * k + 8 * p,
-                      mn_desc(at + 2 * DB * K::kBlock + k * 2048, 1024),
-                      idesc<T>(128, kSlice) | kBMn, k > 0 || p > 0);
+          const uint64_t dc = mn_desc(at + 2 * DB * K::kBlock, 1024);
+#pragma unroll
+          for (int k = 0; k < C / 16; ++k) {
+            umma_ts(tmem + kColO1, tmem + kColP + (c & 1) * 128 + 16 * k, dc + 128 * k,
+                    idesc<T>(128, kSlice) | kBMn, k > 0);
+            umma_ts(tmem + kColO1, tmem + kColP + (c & 1) * 128 + 16 * k + 8, dc + 128 * k,
+                    idesc<T>(128, kSlice) | kBMn, 1);
+          }
           umma_commit(&tab.o_full);
         }
         umma_commit(&tab.stage_free[c & 1]);
@@ -389,35 +427,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = mbar_wait(&tab.done, 0, deadline + kSeqWaitNs) && ok;
     }
   } else if (warp >= 4 && warp < 8) {
-    // ---- scores to operands; output ----
+    // ---- scores to operands: row i of P ----
     const int w = warp - 4, i = w * 32 + lane;
     const uint32_t quad = (uint32_t)(w * 32) << 16;
-    float back[2] = {1.f, 1.f};  // fp16: the row's power of two, taken back from O1
-    auto weigh = [&](int c) {
+    for (int c = 0; c < (with_out ? nc : 0); ++c) {
       warp_wait(&tab.p_full[c & 1], c >> 1);
       after_sync();
       const uint32_t at = tmem + quad + kColP + (c & 1) * 128;
       const int n = tokens_of(from + c);
       // columns [16 jb, 16 jb + 16) against this warp's rows [32 w, 32 w + 32)
       auto nothing = [&](int jb) { return r.rev ? jb < 2 * w : jb > 2 * w + 1; };
-      auto weighted = [&](int jb, float2(&v)[8]) {
-        uint32_t raw[16];
-        tmem_ld16(at + 16 * jb, raw);
-        wait_ld();
+      auto weighted = [&](int jb, const uint32_t* raw, float2* v) {
         const bool diagonal = jb == 2 * w || jb == 2 * w + 1;
-        if (!diagonal && (n == C || 16 * jb + 16 <= n)) {
+        if (!diagonal && 16 * jb + 16 <= n) {
           const float2 f = both(tab.pw[r.rev ? 16 * jb - i : i - 16 * jb - 15]);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float2 d = *reinterpret_cast<const float2*>(tab.dec + 2 * j);
+          for (int j = 0; j < 8; j += 2) {
+            const float4 d = *reinterpret_cast<const float4*>(tab.dec + 2 * j);
             v[j] = mul2(make_float2(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1])),
-                        mul2(f, d));
+                        mul2(f, make_float2(d.x, d.y)));
+            v[j + 1] = mul2(make_float2(__uint_as_float(raw[2 * j + 2]), __uint_as_float(raw[2 * j + 3])),
+                            mul2(f, make_float2(d.z, d.w)));
           }
         } else {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const int col = 16 * jb + j, gap = r.rev ? col - i : i - col;
-            const float x = gap >= 0 && col < n ? __uint_as_float(raw[j]) * tab.pw[gap < 0 ? 0 : gap] : 0.f;
+            const float p = tab.pw[gap < 0 ? 0 : gap];
+            const float x = gap >= 0 && col < n ? __uint_as_float(raw[j]) * p : 0.f;
             if (j & 1) v[j / 2].y = x;
             else v[j / 2].x = x;
           }
@@ -429,52 +466,74 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int jb = 0; jb < C / 16; ++jb) {
           if (nothing(jb)) continue;
+          uint32_t raw[16];
+          tmem_ld16(at + 16 * jb, raw);
+          wait_ld();
           float2 v[8];
-          weighted(jb, v);
+          weighted(jb, raw, v);
 #pragma unroll
           for (int j = 0; j < 8; ++j) top = fmaxf(top, fmaxf(fabsf(v[j].x), fabsf(v[j].y)));
         }
         const float2 f = fit_scale(top);
         scale = both(f.x);
-        back[c & 1] = f.y;
+        tab.row_scale[c & 3][i] = f.y;  // read by the output warps, after p_ready and o_full
       }
+      // pairs of blocks: this warp's rows see both, or neither, but for C = 112's last single block
 #pragma unroll 1
-      for (int jb = 0; jb < C / 16; ++jb) {
+      for (int jb = 0; jb < C / 16; jb += 2) {
+        const bool two = jb + 1 < C / 16;
         uint32_t o[16];
-        if (nothing(jb)) {
+        if (nothing(jb)) {  // nothing(jb) == nothing(jb + 1)
 #pragma unroll
           for (int j = 0; j < 16; ++j) o[j] = 0u;
-        } else {
+          tmem_st16(at + 16 * jb, o);
+          if (two) tmem_st16(at + 16 * jb + 16, o);
+          continue;
+        }
+        uint32_t raw[2][16];
+        tmem_ld16(at + 16 * jb, raw[0]);
+        if (two) tmem_ld16(at + 16 * jb + 16, raw[1]);
+        wait_ld();
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          if (m == 1 && !two) break;
           float2 v[8];
-          weighted(jb, v);
+          weighted(jb + m, raw[m], v);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             if (kHalf) v[j] = mul2(v[j], scale);
             o[j] = take<T>(v[j]);
             o[8 + j] = take<T>(v[j]);
           }
+          tmem_st16(at + 16 * (jb + m), o);
         }
-        tmem_st16(at + 16 * jb, o);
       }
       wait_st();
       before_sync();
       warp_arrive(&tab.p_ready[c & 1]);
-    };
-    auto output = [&](int c) {
+    }
+  } else if (warp >= 8 && warp < 12) {
+    // ---- output: row i ----
+    const int w = warp - 8, i = w * 32 + lane;
+    const uint32_t quad = (uint32_t)(w * 32) << 16;
+    for (int c = 0; c < (with_out ? nc : 0); ++c) {
       warp_wait(&tab.o_full, c);
       after_sync();
       const int n = tokens_of(from + c), t0 = chunk_of(from + c) * C;
       const bool state = c > 0 || enters;
       const int gap = (r.rev ? n - 1 - i : i) + r.lead;
-      const float2 fi = both(r.s_intra * back[c & 1]);
+      const float2 fi = both(r.s_intra * (kHalf ? tab.row_scale[c & 3][i] : 1.f));
       const float2 fx = both(r.s_inter * tab.pw[gap < 0 ? 0 : gap] * (kHalf && state ? tab.x_scale[c & 1] : 1.f));
       const bool live = i < n, there = i < C && t0 + i < g.T && r.out;
       const long long at = (long long)(t0 + i) * r.ot + b * r.ob + h * r.oh + e0;
 #pragma unroll
       for (int q = 0; q < kSlice / 16; ++q) {
-        uint32_t a[16], x[16];
+        uint32_t a[16], x[16], y[16];
         tmem_ld16(tmem + quad + kColO1 + 16 * q, a);
-        if (state) tmem_ld16(tmem + quad + kColO2 + 16 * q, x);
+        if (state) {
+          tmem_ld16(tmem + quad + kColO2 + 16 * q, x);
+          tmem_ld16(tmem + quad + kColO2 + kSlice + 16 * q, y);
+        }
         wait_ld();
         if (q == kSlice / 16 - 1) {
           before_sync();
@@ -485,73 +544,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 8; ++j) {
           v[j] = mul2(make_float2(__uint_as_float(a[2 * j]), __uint_as_float(a[2 * j + 1])), fi);
           if (state)
-            v[j] = fma2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), fx, v[j]);
+            v[j] = fma2(add2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])),
+                             make_float2(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1]))),
+                        fx, v[j]);
           if (!live) v[j] = both(0.f);
         }
-        if (there) {
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const int col = 16 * q + 8 * s;
-            if (e0 + col < r.e) {  // e is a multiple of 8
-              const float2* u = v + 4 * s;
-              if (r.out_f32) {
-                float4* p = reinterpret_cast<float4*>(static_cast<float*>(r.out) + at + col);
-                p[0] = make_float4(u[0].x, u[0].y, u[1].x, u[1].y);
-                p[1] = make_float4(u[2].x, u[2].y, u[3].x, u[3].y);
-              } else {
-                uint4 p;
-                float2 m[4] = {u[0], u[1], u[2], u[3]};
-                p.x = take<T>(m[0]);
-                p.y = take<T>(m[1]);
-                p.z = take<T>(m[2]);
-                p.w = take<T>(m[3]);
-                *reinterpret_cast<uint4*>(static_cast<T*>(r.out) + at + col) = p;
-              }
-            }
-          }
-        }
+        if (there) store_out<T>(r, at + 16 * q, r.e - e0 - 16 * q, v);
         __syncwarp();
       }
-    };
-    if (with_out && nc > 0) {
-      weigh(0);
-      for (int c = 0; c < nc; ++c) {
-        if (c + 1 < nc) weigh(c + 1);
-        output(c);
-      }
     }
-  } else if (warp >= 8 && warp < 12) {
-    // ---- the state: row `row` of X, 64 columns ----
-    const int w = warp - 8, row = w * 32 + lane;
-    const uint32_t quad = (uint32_t)(w * 32) << 16;
-    const int ncol = min(kSlice, r.e - e0);
+  } else if (warp >= 12 && warp < 20) {
+    // ---- the state: row `row` of X, columns [32 half, 32 half + 32) of the slice ----
+    const int w = warp - 12, row = (w & 3) * 32 + lane, half = w >> 2;
+    const uint32_t from_tmem = tmem + ((uint32_t)((w & 3) * 32) << 16) + kColU + half * kHalfSlice;
+    const int col0 = e0 + half * kHalfSlice, ncol = min(kHalfSlice, r.e - col0);
     const size_t head = (size_t)bh * r.d * r.e;
-    float2 X[kSlice / 2];
+    float2 X[kHalfSlice / 2];
 #pragma unroll
-    for (int j = 0; j < kSlice / 2; ++j) X[j] = both(0.f);
+    for (int j = 0; j < kHalfSlice / 2; ++j) X[j] = both(0.f);
     const int done_before = before(from);
     if (r.x0 && !g.states_only && row < r.d) {
       const float f = decay_pow(ld, done_before);
+      const float* p = r.x0 + head + (r.x_t ? (size_t)col0 * r.d + row : (size_t)row * r.e + col0);
+      const int step = r.x_t ? r.d : 1;
 #pragma unroll
-      for (int j = 0; j < kSlice; ++j)
-        if (j < ncol) {
-          const float v = f * (r.x_t ? r.x0[head + (size_t)(e0 + j) * r.d + row]
-                                     : r.x0[head + (size_t)row * r.e + e0 + j]);
-          if (j & 1) X[j / 2].y = v;
-          else X[j / 2].x = v;
-        }
+      for (int j = 0; j < kHalfSlice / 2; ++j) {
+        if (2 * j < ncol) X[j].x = f * p[2 * j * step];
+        if (2 * j + 1 < ncol) X[j].y = f * p[(2 * j + 1) * step];
+      }
     }
-    float* part = g.part + (((size_t)blockIdx.y * g.B * g.H + bh) * g.subs * g.slices + slice) * kSlice * 128 + row;
+    float* part = g.part + ((((size_t)blockIdx.y * g.B * g.H + bh) * g.subs * g.slices + slice) * kSlice +
+                            half * kHalfSlice) * 128 + row;
     const size_t sub_size = (size_t)g.slices * kSlice * 128;
     if (!g.states_only) {
       const int subs = min(seg * (g.cps / g.cpb), (chunks + g.cpb - 1) / g.cpb);
       for (int u = 0; u < subs; ++u) {
-        const float f = decay_pow(ld, done_before - before((u + 1) * g.cpb));
+        const float2 f = both(decay_pow(ld, done_before - before((u + 1) * g.cpb)));
+        const float* p = part + u * sub_size;
 #pragma unroll
-        for (int j = 0; j < kSlice / 2; ++j) {
-          const float* p = part + u * sub_size + 2 * j * 128;
-          X[j] = fma2(make_float2(__ldcg(p), __ldcg(p + 128)), both(f), X[j]);
-        }
+        for (int j = 0; j < kHalfSlice / 2; ++j)
+          X[j] = fma2(make_float2(__ldcg(p + 2 * j * 128), __ldcg(p + (2 * j + 1) * 128)), f, X[j]);
       }
     }
     const int db = (r.d + 63) / 64;
@@ -562,14 +594,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         float top = 0.f;
         if (row < r.d)
 #pragma unroll
-          for (int j = 0; j < kSlice / 2; ++j) top = fmaxf(top, fmaxf(fabsf(X[j].x), fabsf(X[j].y)));
+          for (int j = 0; j < kHalfSlice / 2; ++j) top = fmaxf(top, fmaxf(fabsf(X[j].x), fabsf(X[j].y)));
         const float2 f = fit_scale(group_max(top, tab.red[0], w, 1));
         scale = both(f.x);
-        if (row == 0) tab.x_scale[turn & 1] = f.y;
+        if (row == 0 && half == 0) tab.x_scale[turn & 1] = f.y;
       }
       if (row < db * 64) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
+        for (int q = 0; q < 4; ++q) {
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -578,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             hi[j] = take<T>(v);
             lo[j] = take<T>(v);
           }
-          const uint32_t at = (uint32_t)((q ^ (row & 7)) << 4);
+          const uint32_t at = (uint32_t)(((half * 4 + q) ^ (row & 7)) << 4);
           *reinterpret_cast<uint4*>(tile + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           *reinterpret_cast<uint4*>(tile + K::kStateTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
@@ -590,78 +622,90 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int c = 0; c < nc; ++c) {
       warp_wait(&tab.u_full, c);
       after_sync();
-      const float2 f = both(tab.pw[min(tokens_of(from + c), 131)]);
-      const float2 s = both(r.s_add * (kHalf ? tab.w_scale[c & 1] : 1.f));
+      const float2 f = both(tab.pw[tokens_of(from + c)]);
+      const float2 s = both(r.s_add * (kHalf ? tab.w_scale[c & 3] : 1.f));
+      uint32_t u[2][16];
+      tmem_ld16(from_tmem, u[0]);
+      tmem_ld16(from_tmem + 16, u[1]);
+      wait_ld();
+      before_sync();
+      warp_arrive(&tab.u_free);
 #pragma unroll
-      for (int q = 0; q < kSlice / 16; ++q) {
-        uint32_t u[16];
-        tmem_ld16(tmem + quad + kColU + 16 * q, u);
-        wait_ld();
-        if (q == kSlice / 16 - 1) {
-          before_sync();
-          warp_arrive(&tab.u_free);
-        }
+      for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          X[8 * q + j] = fma2(make_float2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1])), s,
+          X[8 * q + j] = fma2(make_float2(__uint_as_float(u[q][2 * j]), __uint_as_float(u[q][2 * j + 1])), s,
                               mul2(f, X[8 * q + j]));
+      if (with_out && c + 1 < nc) {
+        // the product with the state before has read its tile (there was one unless none entered)
+        if (c > 0 || enters) warp_wait(&tab.x_free, enters ? c : c - 1);
+        publish(c + 1);
       }
-      if (with_out && c + 1 < nc) publish(c + 1);
     }
     if (writes_end && row < r.d) {
+      float* p = r.x_end + head + (r.x_t ? (size_t)col0 * r.d + row : (size_t)row * r.e + col0);
+      const int step = r.x_t ? r.d : 1;
 #pragma unroll
-      for (int j = 0; j < kSlice; ++j)
-        if (j < ncol)
-          r.x_end[head + (r.x_t ? (size_t)(e0 + j) * r.d + row : (size_t)row * r.e + e0 + j)] =
-              j & 1 ? X[j / 2].y : X[j / 2].x;
+      for (int j = 0; j < kHalfSlice / 2; ++j) {
+        if (2 * j < ncol) p[2 * j * step] = X[j].x;
+        if (2 * j + 1 < ncol) p[(2 * j + 1) * step] = X[j].y;
+      }
     }
     if (g.states_only) {
 #pragma unroll
-      for (int j = 0; j < kSlice / 2; ++j) {
+      for (int j = 0; j < kHalfSlice / 2; ++j) {
         part[seg * sub_size + 2 * j * 128] = X[j].x;
         part[seg * sub_size + (2 * j + 1) * 128] = X[j].y;
       }
     }
-  } else if (warp >= 12) {
-    // ---- w C: row j of the tile, its decay to the chunk's end ----
-    const int w = warp - 12, j = w * 32 + lane;
+  } else if (warp >= 20) {
+    // ---- w C: row j of the tile and half its columns, decayed to the chunk's end ----
+    const int w = warp - 20, j = (w & 3) * 32 + lane, half = w >> 2;
     for (int c = 0; c < nc; ++c) {
       const int n = tokens_of(from + c);
       warp_wait(&tab.c_full[c & 1], c >> 1);
       unsigned char* tile = smem + (c & 1) * K::kStage + 2 * DB * K::kBlock + j * 128;
       const int gap = (r.rev ? j : n - 1 - j) + 1 - r.lead;
       const float wj = j < n ? tab.pw[gap] : 0.f;
-      uint4 raw[8];
-      float2 scale = both(1.f);
-      if (j < C) {
+      uint32_t raw[4][4];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          raw[q] = *reinterpret_cast<const uint4*>(tile + ((q ^ (j & 7)) << 4));
-          if (j >= n) raw[q] = make_uint4(0, 0, 0, 0);
-        }
+      for (int q = 0; q < 4; ++q) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (j < n) v = *reinterpret_cast<const uint4*>(tile + (((half * 4 + q) ^ (j & 7)) << 4));
+        raw[q][0] = v.x;
+        raw[q][1] = v.y;
+        raw[q][2] = v.z;
+        raw[q][3] = v.w;
       }
+      float2 f = both(wj);
       if constexpr (kHalf) {
         float top = 0.f;
-        if (j < n)
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const uint32_t u[4] = {raw[q].x, raw[q].y, raw[q].z, raw[q].w};
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 v = unpack<T>(u[k]);
-              top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
-            }
+          for (int k = 0; k < 4; ++k) {
+            const float2 v = unpack<T>(raw[q][k]);
+            top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
           }
-        const float2 f = fit_scale(group_max(top * wj, tab.red[1], w, 2));
-        scale = both(f.x);
-        if (j == 0) tab.w_scale[c & 1] = f.y;
+        const float2 s = fit_scale(group_max(top * wj, tab.red[1], w, 2));
+        f = mul2(f, both(s.x));
+        if (j == 0 && half == 0) tab.w_scale[c & 3] = s.y;
       }
+      uint32_t p[K::kParts][4][4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float2 v = mul2(unpack<T>(raw[q][k]), f);
+#pragma unroll
+          for (int m = 0; m < K::kParts; ++m) p[m][q][k] = take<T>(v);
+        }
       if (c > 0) warp_wait(&tab.u_full, c - 1);
       if (n < C) {
-        // Rows past the length may hold anything: the score tile's product with them ends first, then
+        // Rows past the length may hold anything: the scores, which read them, are made first, then
         // they are cleared, so that 0 * anything stays 0.
         warp_wait(with_out ? &tab.p_full[c & 1] : &tab.ab_full[c & 1], c >> 1);
-        if (j >= n && j < C) {
+        if (j >= n && j < C && half == 0) {
           const int db = (r.d + 63) / 64;
           const uint4 z = make_uint4(0, 0, 0, 0);
           for (int q = 0; q < 8; ++q) {
@@ -671,24 +715,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (j < C) {
-        const float2 f = mul2(both(wj), scale);
+      if (j < C)
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint32_t u[4] = {raw[q].x, raw[q].y, raw[q].z, raw[q].w};
-          uint32_t p[3][4];
+        for (int m = 0; m < K::kParts; ++m)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float2 v = mul2(unpack<T>(u[k]), f);
-#pragma unroll
-            for (int m = 0; m < K::kParts; ++m) p[m][k] = take<T>(v);
-          }
-#pragma unroll
-          for (int m = 0; m < K::kParts; ++m)
-            *reinterpret_cast<uint4*>(smem + K::oW + m * K::kBlock + j * 128 + ((q ^ (j & 7)) << 4)) =
-                make_uint4(p[m][0], p[m][1], p[m][2], p[m][3]);
-        }
-      }
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint4*>(smem + K::oW + m * K::kBlock + j * 128 + (((half * 4 + q) ^ (j & 7)) << 4)) =
+                make_uint4(p[m][q][0], p[m][q][1], p[m][q][2], p[m][q][3]);
       to_async();
       warp_arrive(&tab.w_ready);
     }
@@ -718,6 +751,19 @@ EncodeTiledFn encode_fn() {
     return reinterpret_cast<EncodeTiledFn>(p);
   }();
   return fn;
+}
+
+// x [T][B][heads][d] with any strides into rows of dp >= d values, zeros behind d.
+__global__ void __launch_bounds__(256) la_copy_kernel(const uint16_t* x, long long st, long long sb,
+                                                      long long sh, int B, int heads, int d, int dp,
+                                                      long long rows, uint16_t* out) {
+  const long long n = rows * dp;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) {
+    const long long row = i / dp;
+    const int k = (int)(i - row * dp), h = (int)(row % heads);
+    const long long tb = row / heads;
+    out[i] = k < d ? x[tb / B * st + tb % B * sb + h * sh + k] : (uint16_t)0;
+  }
 }
 
 // A sequence tensor as {d, heads, B, T}, read in boxes of 64 values of C tokens of one head.
@@ -774,7 +820,7 @@ Plan make_plan(const LaArgs& a, int C, int sms, size_t capacity) {
       if (cps % m) continue;
       const int cpb = cps / m, subs = (segs - 1) * m;
       if ((size_t)ctas * subs * kStateBytes > capacity) continue;
-      const double cost = waves(ctas * segs) * (cps + 1) + waves(ctas * subs) * (0.5 * cpb + 1) + 3 +
+      const double cost = waves(ctas * segs) * (cps + 1) + waves(ctas * subs) * (0.6 * cpb + 1) + 3 +
                           0.05 * subs;
       if (cost < best) {
         best = cost;
@@ -814,18 +860,15 @@ cudaError_t launch(const Maps& maps, TcArgs g, const Plan& p, int roles, cudaStr
 }  // namespace
 
 bool la_tc_serves(const LaArgs& a) {
-  if (a.dtype == PRNN_F32 || !encode_fn()) return false;
-  for (int i = 0; i < a.roles; ++i) {
-    const LaRole& r = a.role[i];
-    if (r.d > 128 || r.e > 128 || !seq_fits(r.a, a, r.d) || !seq_fits(r.b, a, r.d) ||
-        !seq_fits(r.c, a, r.e))
-      return false;
-    const int unit = r.out_f32 ? 4 : 8;
-    if (r.out && ((reinterpret_cast<uintptr_t>(r.out) & 15) || (a.T > 1 && r.ot % unit) ||
-                  (a.B > 1 && r.ob % unit) || (a.H > 1 && r.oh % unit)))
-      return false;
-  }
-  return (long long)a.B * a.H * 64 * 4 < (1LL << 31);
+  if (a.dtype == PRNN_F32 || !encode_fn() || (long long)a.B * a.H * 64 * 4 >= (1LL << 31)) return false;
+  for (int i = 0; i < a.roles; ++i)
+    if (a.role[i].d > 128 || a.role[i].e > 128) return false;
+  return true;
+}
+
+size_t la_tc_copy_bytes(const LaSeq& x, const LaArgs& a, int d) {
+  if (seq_fits(x, a, d)) return 0;
+  return (size_t)2 * a.T * a.B * (a.H / x.share) * ((d + 7) / 8 * 8);  // a multiple of 16
 }
 
 size_t la_tc_workspace(const LaArgs& a) {
@@ -833,23 +876,38 @@ size_t la_tc_workspace(const LaArgs& a) {
   return (size_t)a.roles * a.B * a.H * p.subs * p.slices * kStateBytes;
 }
 
-cudaError_t launch_la_tc(const LaArgs& a, float* part, size_t part_bytes, cudaStream_t s) {
+cudaError_t launch_la_tc(const LaArgs& a, void* scratch, size_t bytes, cudaStream_t s) {
   if (a.roles == 0 || a.B == 0) return cudaSuccess;
   const int d = max_d(a), C = chunk_of(d);
   const bool half = a.dtype == PRNN_F16;
-  const Plan p = make_plan(a, C, seq_sm_count(), part_bytes);
   Maps maps;
   LaSeq seen[4];
   int width[4], n = 0;
-  auto index = [&](const LaSeq& x, int w) {
+  size_t used = 0;
+  cudaError_t err = cudaSuccess;
+  // The tensor map of x; a tensor that TMA cannot read (alignment, odd sizes, a stride of 0) is
+  // copied first.
+  auto index = [&](LaSeq x, int w) {
     for (int i = 0; i < n; ++i)
       if (seen[i].p == x.p && seen[i].st == x.st && seen[i].sb == x.sb && seen[i].sh == x.sh &&
           seen[i].share == x.share && width[i] == w)
         return i;
-    if (n == 4 || !encode(&maps.m[n], x, w, a.H / x.share, a.B, a.T, C, half)) return -1;
+    if (n == 4) return -1;
     seen[n] = x;
     width[n] = w;
-    return n++;
+    if (const size_t copy = la_tc_copy_bytes(x, a, w)) {
+      if (used + copy > bytes) return -1;
+      const int heads = a.H / x.share, dp = (w + 7) / 8 * 8;
+      const long long rows = (long long)a.T * a.B * heads, blocks = (rows * dp + 255) / 256;
+      uint16_t* to = reinterpret_cast<uint16_t*>(static_cast<char*>(scratch) + used);
+      la_copy_kernel<<<(unsigned)std::min<long long>(blocks, 16LL * seq_sm_count()), 256, 0, s>>>(
+          static_cast<const uint16_t*>(x.p), x.st, x.sb, x.sh, a.B, heads, w, dp, rows, to);
+      if ((err = cudaGetLastError()) != cudaSuccess) return -1;
+      used += copy;
+      x = LaSeq{to, (long long)a.B * heads * dp, (long long)heads * dp, dp, x.share};
+      w = dp;
+    }
+    return encode(&maps.m[n], x, w, a.H / x.share, a.B, a.T, C, half) ? n++ : -1;
   };
   TcArgs g{};
   for (int i = 0; i < a.roles; ++i) {
@@ -858,7 +916,7 @@ cudaError_t launch_la_tc(const LaArgs& a, float* part, size_t part_bytes, cudaSt
     t.ia = index(r.a, r.d);
     t.ib = index(r.b, r.d);
     t.ic = index(r.c, r.e);
-    if (t.ia < 0 || t.ib < 0 || t.ic < 0) return cudaErrorInvalidValue;
+    if (t.ia < 0 || t.ib < 0 || t.ic < 0) return err != cudaSuccess ? err : cudaErrorInvalidValue;
     t.sa = r.a.share;
     t.sb = r.b.share;
     t.sc = r.c.share;
@@ -867,6 +925,10 @@ cudaError_t launch_la_tc(const LaArgs& a, float* part, size_t part_bytes, cudaSt
     t.ob = r.ob;
     t.oh = r.oh;
     t.out_f32 = r.out_f32;
+    const int unit = r.out_f32 ? 4 : 8;
+    t.out_vec = r.e % 8 == 0 && (reinterpret_cast<uintptr_t>(r.out) & 15) == 0 &&
+                (a.T == 1 || r.ot % unit == 0) && (a.B == 1 || r.ob % unit == 0) &&
+                (a.H == 1 || r.oh % unit == 0);
     t.d = r.d;
     t.e = r.e;
     t.x0 = r.x0;
@@ -879,6 +941,7 @@ cudaError_t launch_la_tc(const LaArgs& a, float* part, size_t part_bytes, cudaSt
     t.s_add = r.s_add;
   }
   for (int i = n; i < 4; ++i) maps.m[i] = maps.m[0];
+  const Plan p = make_plan(a, C, seq_sm_count(), bytes - used);
   g.T = a.T;
   g.B = a.B;
   g.H = a.H;
@@ -891,7 +954,7 @@ cudaError_t launch_la_tc(const LaArgs& a, float* part, size_t part_bytes, cudaSt
   g.subs = p.subs;
   g.cpb = p.cpb;
   g.slices = p.slices;
-  g.part = part;
+  g.part = reinterpret_cast<float*>(static_cast<char*>(scratch) + used);
   if (half)
     return d > 64 ? launch<__half, 2>(maps, g, p, a.roles, s) : launch<__half, 1>(maps, g, p, a.roles, s);
   return d > 64 ? launch<__nv_bfloat16, 2>(maps, g, p, a.roles, s)

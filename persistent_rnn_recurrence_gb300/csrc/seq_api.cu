@@ -149,9 +149,7 @@ size_t group_bytes(const prnn_linear_attention_t* a) {
 // Bytes of the tensor-core kernels' scratch, 0 where those cannot serve the call: any subset of the
 // backward pass's roles fits.
 size_t tc_bytes(const prnn_linear_attention_t* a, bool backward) {
-  if (a->dtype == PRNN_F32 || a->dk > 128 || a->dv > 128 || a->dk % 8 || a->dv % 8 || a->T == 0 ||
-      a->B == 0)
-    return 0;
+  if (a->dtype == PRNN_F32 || a->dk > 128 || a->dv > 128 || a->T == 0 || a->B == 0) return 0;
   LaArgs g{};
   g.dtype = a->dtype;
   g.T = a->T;
@@ -164,10 +162,14 @@ size_t tc_bytes(const prnn_linear_attention_t* a, bool backward) {
     r.e = backward ? std::max(a->dk, a->dv) : a->dv;
     most = std::max(most, la_tc_workspace(g));
   }
+  const int share = a->heads / a->qk_heads;
+  most += la_tc_copy_bytes(in(a->q, share), g, a->dk) + la_tc_copy_bytes(in(a->k, share), g, a->dk) +
+          la_tc_copy_bytes(in(a->v, 1), g, a->dv);
+  if (backward) most += la_tc_copy_bytes(in(a->d_o, 1), g, a->dv);
   return most;
 }
 cudaError_t launch_mix(const LaArgs& g, void* scratch, size_t bytes, cudaStream_t s) {
-  if (la_tc_serves(g)) return launch_la_tc(g, static_cast<float*>(scratch), bytes, s);
+  if (la_tc_serves(g)) return launch_la_tc(g, scratch, bytes, s);
   return launch_la_simt(g, s);
 }
 

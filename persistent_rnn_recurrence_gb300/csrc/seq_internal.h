@@ -96,11 +96,12 @@ struct LaArgs {
 };
 // On CUDA cores, for any sizes, strides and types.
 cudaError_t launch_la_simt(const LaArgs& a, cudaStream_t s);
-// On the tensor cores: whether it serves a call, the bytes of scratch it needs for these sizes
-// (the larger of what one, two or three roles need), the call.
+// On the tensor cores, for fp16 and bf16 with d, e <= 128: whether it serves a call; the bytes of scratch for
+// its segments' states and for a copy of an input that it cannot read in place (0: it can); the call.
 bool la_tc_serves(const LaArgs& a);
 size_t la_tc_workspace(const LaArgs& a);
-cudaError_t launch_la_tc(const LaArgs& a, float* part, size_t part_bytes, cudaStream_t s);
+size_t la_tc_copy_bytes(const LaSeq& x, const LaArgs& a, int d);
+cudaError_t launch_la_tc(const LaArgs& a, void* scratch, size_t bytes, cudaStream_t s);
 
 // out[t][b][hq][:] = sum of the `group` heads of part [T][B][H][d] (fp32) that share hq.
 struct LaReduceArgs {
