@@ -20,10 +20,13 @@
 // would not hold them, P is scaled by a power of two per row and X and w C per tile, taken back after the
 // product.
 //
-// Warps: 0 loads (TMA), 1 issues the matrix products, 4-7 turn scores into operands, 8-11 write the
-// output, 12-19 own the state (a row of X and half the columns per thread), 20-27 make w C.  The order of the
-// products is P(c+1), U(c), O2(c), O1(c): the next chunk's scores are weighted, the state updated and
-// this chunk's output written while the tensor cores run the others.
+// Warps: 0 loads (TMA), 1 issues the matrix products, 4-11 turn scores into operands (a row per thread, every
+// other block of 16 columns), 12-19 own the state (a row of X and half the columns), 20-27 make w C
+// and write the output (a row and half the columns).  The order of the products is U(c), O2(c), P(c+1),
+// O1(c): the state is updated, the next chunk's w C made, its scores weighted and this chunk's output written while
+// the tensor cores run the others, and each tile of chunk c + 2 is requested as the last product that
+// reads chunk c's ends.  O2 is taken out of tensor memory as soon as it is there and O1 has two places, so
+// that no product waits for the output.
 #include <cuda.h>
 
 #include <algorithm>
@@ -40,8 +43,8 @@ using namespace tc;
 
 constexpr int kThreads = 896, kSlice = 64, kHalfSlice = 32;
 constexpr uint32_t kTmemCols = 512;
-// columns of tensor memory: two score tiles, O1, O2 (of X's two parts side by side), U
-constexpr uint32_t kColP = 0, kColO1 = 256, kColO2 = 320, kColU = 448;
+// columns of tensor memory: two score tiles, O1 twice, O2, U
+constexpr uint32_t kColP = 0, kColO1 = 256, kColO2 = 384, kColU = 448;
 
 template <typename T, int DB>
 struct Cfg {
@@ -61,8 +64,10 @@ struct Tables {
   // fp16: powers of two taken back from O2, U and O1, each kept until its last reader is sure to be done
   float x_scale[2], w_scale[4], row_scale[4][128];
   float red[2][8];
-  uint64_t ab_full[2], c_full[2], stage_free[2], p_full[2], p_ready[2];
-  uint64_t o_full, o_free, x_ready, x_free, w_ready, u_full, u_free, done;
+  float row_top[2][128];
+  float diag[32][36];   // l^(i-j) (in reverse l^(j-i)) of a 32 x 32 diagonal block, 0 where the mask is
+  uint64_t ab_full[2], c_full[2], a_free[2], b_free[2], c_free[2], p_full[2], p_ready[2];
+  uint64_t o_full[2], o_free[2], o2_full, o2_free, x_ready, w_ready, u_full, u_free, done;
   uint32_t tmem;
 };
 
@@ -107,6 +112,12 @@ template <typename T>
 __host__ __device__ constexpr uint32_t idesc(int M, int N) {
   return std::is_same<T, __half>::value ? f16_idesc(M, N) : bf16_idesc(M, N);
 }
+// The value, made at this place: sums with it are not hoisted out of the loop over chunks (a register
+// pair for each of some sixty products would be spilled).
+__device__ __forceinline__ uint64_t here(uint64_t v) {
+  asm volatile("" : "+l"(v));
+  return v;
+}
 // A from tensor memory
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
                                         uint32_t acc) {
@@ -135,6 +146,14 @@ __device__ __forceinline__ void after_sync() {
 }
 __device__ __forceinline__ void to_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(p));
+  return p != 0;
 }
 // One arrival for the whole warp, after every lane's work.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
@@ -172,12 +191,12 @@ __device__ __forceinline__ uint32_t take(float2& v) {
   if constexpr (std::is_same<T, __half>::value) {
     const __half2 h = __float22half2_rn(v);
     const float2 b = __half22float2(h);
-    v = add2(v, make_float2(-b.x, -b.y));
+    v = fma2(b, both(-1.f), v);
     return *reinterpret_cast<const uint32_t*>(&h);
   } else {
     const __nv_bfloat162 h = __float22bfloat162_rn(v);
     const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
-    v = add2(v, make_float2(-__uint_as_float(u << 16), -__uint_as_float(u & 0xFFFF0000u)));
+    v = fma2(make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u)), both(-1.f), v);
     return u;
   }
 }
@@ -207,12 +226,13 @@ __device__ __forceinline__ float group_max(float v, float* red, int w, int id) {
   return m;
 }
 
-// 16 columns of one row, of which the first m are the output's.
+// 32 columns of one row, of which the first m are the output's.
 template <typename T>
-__device__ __forceinline__ void store_out(const TcRole& r, long long at, int m, const float2 (&v)[8]) {
+__device__ __forceinline__ void store_out(const TcRole& r, long long at, int m,
+                                          const float2 (&v)[kHalfSlice / 2]) {
   if (!r.out_vec) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
+    for (int j = 0; j < kHalfSlice; ++j)
       if (j < m) {
         const float f = j & 1 ? v[j / 2].y : v[j / 2].x;
         if (r.out_f32)
@@ -222,24 +242,25 @@ __device__ __forceinline__ void store_out(const TcRole& r, long long at, int m, 
       }
     return;
   }
+  if (r.out_f32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(r.out) + at);
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    if (8 * s >= m) break;
-    const float2* u = v + 4 * s;
-    if (r.out_f32) {
-      float4* p = reinterpret_cast<float4*>(static_cast<float*>(r.out) + at + 8 * s);
-      p[0] = make_float4(u[0].x, u[0].y, u[1].x, u[1].y);
-      p[1] = make_float4(u[2].x, u[2].y, u[3].x, u[3].y);
-    } else {
-      float2 k[4] = {u[0], u[1], u[2], u[3]};
-      uint4 p;
-      p.x = take<T>(k[0]);
-      p.y = take<T>(k[1]);
-      p.z = take<T>(k[2]);
-      p.w = take<T>(k[3]);
-      *reinterpret_cast<uint4*>(static_cast<T*>(r.out) + at + 8 * s) = p;
-    }
+    for (int q = 0; q < kHalfSlice / 4; ++q)
+      if (4 * q < m) p[q] = make_float4(v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y);
+    return;
   }
+  uint4* p = reinterpret_cast<uint4*>(static_cast<T*>(r.out) + at);
+#pragma unroll
+  for (int q = 0; q < kHalfSlice / 8; ++q)
+    if (8 * q < m) {
+      float2 k[4] = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+      uint4 u;
+      u.x = take<T>(k[0]);
+      u.y = take<T>(k[1]);
+      u.z = take<T>(k[2]);
+      u.w = take<T>(k[3]);
+      p[q] = u;
+    }
 }
 
 template <typename T, int DB>
@@ -251,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem[];
   Tables& tab = *reinterpret_cast<Tables*>(smem + K::oTab);
   const TcRole& r = g.role[blockIdx.y];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int slice = blockIdx.x % g.slices, seg = blockIdx.x / g.slices % (g.states_only ? g.subs : g.segs);
   const int bh = blockIdx.x / g.slices / (g.states_only ? g.subs : g.segs), b = bh / g.H, h = bh % g.H;
   const int e0 = slice * kSlice;
@@ -281,9 +302,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ncol = min(kSlice, r.e - e0);
     for (int c = max(seg * per, chunks); c < (seg + 1) * per && c * C < g.T; ++c) {
       const int rows = min(C, g.T - c * C);
-      const float2 z[8] = {};
-      for (int i = tid; i < rows * (kSlice / 16); i += kThreads) {
-        const int row = i / (kSlice / 16), q = i % (kSlice / 16) * 16;
+      const float2 z[kHalfSlice / 2] = {};
+      for (int i = tid; i < rows * 2; i += kThreads) {
+        const int row = i / 2, q = i % 2 * kHalfSlice;
         store_out<T>(r, (long long)(c * C + row) * r.ot + b * r.ob + h * r.oh + e0 + q, ncol - q, z);
       }
     }
@@ -299,14 +320,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tab.ab_full[i], 1);
       mbar_init(&tab.c_full[i], 1);
-      mbar_init(&tab.stage_free[i], 1);
+      mbar_init(&tab.a_free[i], 1);
+      mbar_init(&tab.b_free[i], 1);
+      mbar_init(&tab.c_free[i], 1);
       mbar_init(&tab.p_full[i], 1);
-      mbar_init(&tab.p_ready[i], 4);
+      mbar_init(&tab.p_ready[i], 8);
+      mbar_init(&tab.o_full[i], 1);
+      mbar_init(&tab.o_free[i], 8);
     }
-    mbar_init(&tab.o_full, 1);
-    mbar_init(&tab.o_free, 4);
+    mbar_init(&tab.o2_full, 1);
+    mbar_init(&tab.o2_free, 8);
     mbar_init(&tab.x_ready, 8);
-    mbar_init(&tab.x_free, 1);
     mbar_init(&tab.w_ready, 8);
     mbar_init(&tab.u_full, 1);
     mbar_init(&tab.u_free, 8);
@@ -322,6 +346,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid < 132) tab.pw[tid] = decay_pow(ld, tid);
   else if (tid < 148) tab.dec[tid - 132] = decay_pow(ld, r.rev ? tid - 132 : 147 - tid);
+  for (int i = warp; i < 32; i += kThreads / 32) {
+    const int gap = r.rev ? lane - i : i - lane;
+    tab.diag[i][lane] = gap >= 0 ? decay_pow(ld, gap) : 0.f;
+  }
   before_sync();
   __syncthreads();
   after_sync();
@@ -340,19 +368,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ---- loads ----
+    if (elected()) {
+      // ---- loads: each tile as soon as the products that read the one before it have ended ----
       const int db = (r.d + 63) / 64;
       for (int c = 0; c < nc; ++c) {
-        const int s = c & 1, t0 = chunk_of(from + c) * C;
-        if (c >= 2) wait(&tab.stage_free[s], (c >> 1) - 1);
+        const int s = c & 1, t0 = chunk_of(from + c) * C, turn = (c >> 1) - 1;
         const uint32_t at = base + s * K::kStage;
+        if (c >= 2) wait(&tab.b_free[s], turn);
         mbar_arrive_expect_tx(&tab.ab_full[s], (with_out ? 2 : 1) * db * K::kBlock);
-        for (int k = 0; k < db; ++k) {
+        for (int k = 0; k < db; ++k)
           tma_load(at + (DB + k) * K::kBlock, &maps.m[r.ib], &tab.ab_full[s], k * 64, h / r.sb, b, t0);
-          if (with_out)
+        if (with_out) {
+          if (c >= 2) wait(&tab.a_free[s], turn);
+          for (int k = 0; k < db; ++k)
             tma_load(at + k * K::kBlock, &maps.m[r.ia], &tab.ab_full[s], k * 64, h / r.sa, b, t0);
         }
+        if (c >= 2) wait(&tab.c_free[s], turn);
         mbar_arrive_expect_tx(&tab.c_full[s], K::kBlock);
         tma_load(at + 2 * DB * K::kBlock, &maps.m[r.ic], &tab.c_full[s], e0, h / r.sc, b, t0);
       }
@@ -363,72 +394,84 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---- matrix products ----
+    if (elected()) {
+      // ---- matrix products.  One thread issues them all, so a product costs it as few instructions as
+      // can be: descriptors are made once and stepped by constants ----
       const int dsteps = (r.d + 15) / 16;
+      const uint64_t da0 = sw128_kmajor_desc(base), db0 = sw128_kmajor_desc(base + DB * K::kBlock);
+      const uint64_t dbt0 = mn_desc(base + DB * K::kBlock, K::kBlock);
+      const uint64_t dc0 = mn_desc(base + 2 * DB * K::kBlock, 1024);
+      const uint64_t dw = mn_desc(base + K::oW, 1024), dx = mn_desc(base + K::oX, 1024);
+      constexpr uint64_t stage = K::kStage >> 4;
+      constexpr auto kstep = [](int k) { return (uint64_t)(((k / 4) * K::kBlock + (k % 4) * 32) >> 4); };
       auto qk = [&](int c) {
         wait(&tab.ab_full[c & 1], c >> 1);
         if (!with_out) return;
         after_sync();
-        const uint32_t at = base + (c & 1) * K::kStage;
-        for (int k = 0; k < dsteps; ++k) {
-          const uint32_t off = (k / 4) * K::kBlock + (k % 4) * 32;
-          umma_f16(tmem + kColP + (c & 1) * 128, sw128_kmajor_desc(at + off),
-                   sw128_kmajor_desc(at + DB * K::kBlock + off), idesc<T>(128, C), k > 0);
-        }
+        const uint64_t da = here(da0 + (c & 1) * stage), db = here(db0 + (c & 1) * stage);
+        const uint32_t d = tmem + kColP + (c & 1) * 128;
+#pragma unroll
+        for (int k = 0; k < 4 * DB; ++k)
+          if (k < dsteps) umma_f16(d, da + kstep(k), db + kstep(k), idesc<T>(128, C), k > 0);
         umma_commit(&tab.p_full[c & 1]);
       };
       if (nc > 0) qk(0);
       for (int c = 0; c < nc; ++c) {
-        const uint32_t at = base + (c & 1) * K::kStage;
-        if (c + 1 < nc) qk(c + 1);
+        const uint64_t off = (c & 1) * stage;
         wait(&tab.c_full[c & 1], c >> 1);
         wait(&tab.w_ready, c);
         if (c > 0) wait(&tab.u_free, c - 1);
         after_sync();
-#pragma unroll 1
-        for (int p = 0; p < K::kParts; ++p) {
-          uint64_t da = mn_desc(at + DB * K::kBlock, K::kBlock);
-          uint64_t dw = mn_desc(base + K::oW + p * K::kBlock, 1024);
+        const uint64_t dbt = here(dbt0 + off), dwc = here(dw);
+#pragma unroll
+        for (int p = 0; p < K::kParts; ++p)
 #pragma unroll
           for (int k = 0; k < C / 16; ++k)  // 16 tokens = 2048 bytes = 128 units
-            umma_f16(tmem + kColU, da + 128 * k, dw + 128 * k, idesc<T>(128, kSlice) | kAMn | kBMn,
-                     p > 0 || k > 0);
-        }
+            umma_f16(tmem + kColU, dbt + 128 * k, dwc + p * (K::kBlock >> 4) + 128 * k,
+                     idesc<T>(128, kSlice) | kAMn | kBMn, p > 0 || k > 0);
         umma_commit(&tab.u_full);
+        umma_commit(&tab.b_free[c & 1]);
         if (with_out) {
-          if (c > 0) wait(&tab.o_free, c - 1);
           if (c > 0 || enters) {
-            wait(&tab.x_ready, enters ? c : c - 1);
+            const int turn = enters ? c : c - 1;
+            wait(&tab.x_ready, turn);
+            if (turn > 0) wait(&tab.o2_free, turn - 1);
             after_sync();
-            const uint64_t dx = mn_desc(base + K::oX, K::kStateTile);
-#pragma unroll 1
-            for (int k = 0; k < dsteps; ++k)  // both parts of X side by side: 128 columns
-              umma_f16(tmem + kColO2, sw128_kmajor_desc(at + (k / 4) * K::kBlock + (k % 4) * 32),
-                       dx + 128 * k, idesc<T>(128, 2 * kSlice) | kBMn, k > 0);
-            umma_commit(&tab.x_free);
+            const uint64_t da = here(da0 + off), dxc = here(dx);
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+              for (int k = 0; k < 4 * DB; ++k)
+                if (k < dsteps)
+                  umma_f16(tmem + kColO2, da + kstep(k), dxc + p * (K::kStateTile >> 4) + 128 * k,
+                           idesc<T>(128, kSlice) | kBMn, p > 0 || k > 0);
+            umma_commit(&tab.o2_full);
           }
+          umma_commit(&tab.a_free[c & 1]);
+        }
+        if (c + 1 < nc) qk(c + 1);
+        if (with_out) {
           wait(&tab.p_ready[c & 1], c >> 1);
+          if (c >= 2) wait(&tab.o_free[c & 1], (c >> 1) - 1);
           after_sync();
-          const uint64_t dc = mn_desc(at + 2 * DB * K::kBlock, 1024);
+          const uint32_t pa = tmem + kColP + (c & 1) * 128, d = tmem + kColO1 + (c & 1) * kSlice;
+          const uint64_t dc = here(dc0 + off);
 #pragma unroll
           for (int k = 0; k < C / 16; ++k) {
-            umma_ts(tmem + kColO1, tmem + kColP + (c & 1) * 128 + 16 * k, dc + 128 * k,
-                    idesc<T>(128, kSlice) | kBMn, k > 0);
-            umma_ts(tmem + kColO1, tmem + kColP + (c & 1) * 128 + 16 * k + 8, dc + 128 * k,
-                    idesc<T>(128, kSlice) | kBMn, 1);
+            umma_ts(d, pa + 16 * k, dc + 128 * k, idesc<T>(128, kSlice) | kBMn, k > 0);
+            umma_ts(d, pa + 16 * k + 8, dc + 128 * k, idesc<T>(128, kSlice) | kBMn, 1);
           }
-          umma_commit(&tab.o_full);
+          umma_commit(&tab.o_full[c & 1]);
         }
-        umma_commit(&tab.stage_free[c & 1]);
+        umma_commit(&tab.c_free[c & 1]);
       }
       // every product has read its operands before the CTA leaves
       umma_commit(&tab.done);
       ok = mbar_wait(&tab.done, 0, deadline + kSeqWaitNs) && ok;
     }
-  } else if (warp >= 4 && warp < 8) {
-    // ---- scores to operands: row i of P ----
-    const int w = warp - 4, i = w * 32 + lane;
+  } else if (warp >= 4 && warp < 12) {
+    // ---- scores to operands: row i of P, blocks of 16 columns half, half + 2, ... ----
+    const int w = (warp - 4) & 3, half = (warp - 4) >> 2, i = w * 32 + lane;
     const uint32_t quad = (uint32_t)(w * 32) << 16;
     for (int c = 0; c < (with_out ? nc : 0); ++c) {
       warp_wait(&tab.p_full[c & 1], c >> 1);
@@ -437,121 +480,74 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = tokens_of(from + c);
       // columns [16 jb, 16 jb + 16) against this warp's rows [32 w, 32 w + 32)
       auto nothing = [&](int jb) { return r.rev ? jb < 2 * w : jb > 2 * w + 1; };
-      auto weighted = [&](int jb, const uint32_t* raw, float2* v) {
-        const bool diagonal = jb == 2 * w || jb == 2 * w + 1;
-        if (!diagonal && 16 * jb + 16 <= n) {
-          const float2 f = both(tab.pw[r.rev ? 16 * jb - i : i - 16 * jb - 15]);
-#pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            const float4 d = *reinterpret_cast<const float4*>(tab.dec + 2 * j);
-            v[j] = mul2(make_float2(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1])),
-                        mul2(f, make_float2(d.x, d.y)));
-            v[j + 1] = mul2(make_float2(__uint_as_float(raw[2 * j + 2]), __uint_as_float(raw[2 * j + 3])),
-                            mul2(f, make_float2(d.z, d.w)));
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int col = 16 * jb + j, gap = r.rev ? col - i : i - col;
-            const float p = tab.pw[gap < 0 ? 0 : gap];
-            const float x = gap >= 0 && col < n ? __uint_as_float(raw[j]) * p : 0.f;
-            if (j & 1) v[j / 2].y = x;
-            else v[j / 2].x = x;
-          }
-        }
-      };
       float2 scale = both(1.f);
       if constexpr (kHalf) {
+        // the largest score of the blocks that count: the weights are at most 1
         float top = 0.f;
 #pragma unroll 1
-        for (int jb = 0; jb < C / 16; ++jb) {
+        for (int jb = half; jb < C / 16; jb += 2) {
           if (nothing(jb)) continue;
           uint32_t raw[16];
           tmem_ld16(at + 16 * jb, raw);
           wait_ld();
-          float2 v[8];
-          weighted(jb, raw, v);
+          if (16 * jb + 16 <= n) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) top = fmaxf(top, fmaxf(fabsf(v[j].x), fabsf(v[j].y)));
+            for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(__uint_as_float(raw[j])));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (16 * jb + j < n) top = fmaxf(top, fabsf(__uint_as_float(raw[j])));
+          }
         }
-        const float2 f = fit_scale(top);
+        tab.row_top[half][i] = top;
+        asm volatile("bar.sync 3, 256;" ::: "memory");
+        const float2 f = fit_scale(fmaxf(tab.row_top[0][i], tab.row_top[1][i]));
+        asm volatile("bar.sync 3, 256;" ::: "memory");
         scale = both(f.x);
-        tab.row_scale[c & 3][i] = f.y;  // read by the output warps, after p_ready and o_full
+        if (half == 0) tab.row_scale[c & 3][i] = f.y;  // read by the output warps, after p_ready and o_full
       }
-      // pairs of blocks: this warp's rows see both, or neither, but for C = 112's last single block
 #pragma unroll 1
-      for (int jb = 0; jb < C / 16; jb += 2) {
-        const bool two = jb + 1 < C / 16;
+      for (int jb = half; jb < C / 16; jb += 2) {
         uint32_t o[16];
-        if (nothing(jb)) {  // nothing(jb) == nothing(jb + 1)
+        if (nothing(jb)) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) o[j] = 0u;
           tmem_st16(at + 16 * jb, o);
-          if (two) tmem_st16(at + 16 * jb + 16, o);
           continue;
         }
-        uint32_t raw[2][16];
-        tmem_ld16(at + 16 * jb, raw[0]);
-        if (two) tmem_ld16(at + 16 * jb + 16, raw[1]);
+        uint32_t raw[16];
+        tmem_ld16(at + 16 * jb, raw);
+        const bool diagonal = (jb >> 1) == w;
+        const float* dec = diagonal ? tab.diag[lane] + (jb & 1) * 16 : tab.dec;
+        const float2 f = both((diagonal ? 1.f : tab.pw[r.rev ? 16 * jb - i : i - 16 * jb - 15]) * scale.x);
         wait_ld();
+        if (16 * jb + 16 > n)  // columns past the length, which may hold anything
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          if (m == 1 && !two) break;
-          float2 v[8];
-          weighted(jb + m, raw[m], v);
+          for (int j = 0; j < 16; ++j)
+            if (16 * jb + j >= n) raw[j] = 0u;
+        if (diagonal) {  // so may the masked ones
+          const int gap = r.rev ? i - 16 * jb : 16 * jb + 15 - i;  // in reverse the first `gap` columns, else the last
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (kHalf) v[j] = mul2(v[j], scale);
-            o[j] = take<T>(v[j]);
-            o[8 + j] = take<T>(v[j]);
-          }
-          tmem_st16(at + 16 * (jb + m), o);
+          for (int j = 0; j < 16; ++j)
+            if ((r.rev ? j : 15 - j) < gap) raw[j] = 0u;
         }
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const float4 d = *reinterpret_cast<const float4*>(dec + 2 * j);
+          float2 v = mul2(make_float2(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1])),
+                          mul2(f, make_float2(d.x, d.y)));
+          o[j] = take<T>(v);
+          o[8 + j] = take<T>(v);
+          v = mul2(make_float2(__uint_as_float(raw[2 * j + 2]), __uint_as_float(raw[2 * j + 3])),
+                   mul2(f, make_float2(d.z, d.w)));
+          o[j + 1] = take<T>(v);
+          o[8 + j + 1] = take<T>(v);
+        }
+        tmem_st16(at + 16 * jb, o);
       }
       wait_st();
       before_sync();
       warp_arrive(&tab.p_ready[c & 1]);
-    }
-  } else if (warp >= 8 && warp < 12) {
-    // ---- output: row i ----
-    const int w = warp - 8, i = w * 32 + lane;
-    const uint32_t quad = (uint32_t)(w * 32) << 16;
-    for (int c = 0; c < (with_out ? nc : 0); ++c) {
-      warp_wait(&tab.o_full, c);
-      after_sync();
-      const int n = tokens_of(from + c), t0 = chunk_of(from + c) * C;
-      const bool state = c > 0 || enters;
-      const int gap = (r.rev ? n - 1 - i : i) + r.lead;
-      const float2 fi = both(r.s_intra * (kHalf ? tab.row_scale[c & 3][i] : 1.f));
-      const float2 fx = both(r.s_inter * tab.pw[gap < 0 ? 0 : gap] * (kHalf && state ? tab.x_scale[c & 1] : 1.f));
-      const bool live = i < n, there = i < C && t0 + i < g.T && r.out;
-      const long long at = (long long)(t0 + i) * r.ot + b * r.ob + h * r.oh + e0;
-#pragma unroll
-      for (int q = 0; q < kSlice / 16; ++q) {
-        uint32_t a[16], x[16], y[16];
-        tmem_ld16(tmem + quad + kColO1 + 16 * q, a);
-        if (state) {
-          tmem_ld16(tmem + quad + kColO2 + 16 * q, x);
-          tmem_ld16(tmem + quad + kColO2 + kSlice + 16 * q, y);
-        }
-        wait_ld();
-        if (q == kSlice / 16 - 1) {
-          before_sync();
-          warp_arrive(&tab.o_free);
-        }
-        float2 v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          v[j] = mul2(make_float2(__uint_as_float(a[2 * j]), __uint_as_float(a[2 * j + 1])), fi);
-          if (state)
-            v[j] = fma2(add2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])),
-                             make_float2(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1]))),
-                        fx, v[j]);
-          if (!live) v[j] = both(0.f);
-        }
-        if (there) store_out<T>(r, at + 16 * q, r.e - e0 - 16 * q, v);
-        __syncwarp();
-      }
     }
   } else if (warp >= 12 && warp < 20) {
     // ---- the state: row `row` of X, columns [32 half, 32 half + 32) of the slice ----
@@ -624,21 +620,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       after_sync();
       const float2 f = both(tab.pw[tokens_of(from + c)]);
       const float2 s = both(r.s_add * (kHalf ? tab.w_scale[c & 3] : 1.f));
-      uint32_t u[2][16];
-      tmem_ld16(from_tmem, u[0]);
-      tmem_ld16(from_tmem + 16, u[1]);
-      wait_ld();
-      before_sync();
-      warp_arrive(&tab.u_free);
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+      for (int q = 0; q < 2; ++q) {
+        uint32_t u[16];
+        tmem_ld16(from_tmem + 16 * q, u);
+        wait_ld();
+        if (q == 1) {
+          before_sync();
+          warp_arrive(&tab.u_free);
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          X[8 * q + j] = fma2(make_float2(__uint_as_float(u[q][2 * j]), __uint_as_float(u[q][2 * j + 1])), s,
+          X[8 * q + j] = fma2(make_float2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1])), s,
                               mul2(f, X[8 * q + j]));
+      }
       if (with_out && c + 1 < nc) {
         // the product with the state before has read its tile (there was one unless none entered)
-        if (c > 0 || enters) warp_wait(&tab.x_free, enters ? c : c - 1);
+        if (c > 0 || enters) warp_wait(&tab.o2_full, enters ? c : c - 1);
         publish(c + 1);
       }
     }
@@ -659,19 +657,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp >= 20) {
-    // ---- w C: row j of the tile and half its columns, decayed to the chunk's end ----
-    const int w = warp - 20, j = (w & 3) * 32 + lane, half = w >> 2;
-    for (int c = 0; c < nc; ++c) {
+    // ---- w C: row i of the tile, decayed to the chunk's end; output: row i.  Columns [32 half, 32 half + 32)
+    // of the slice ----
+    const int w = warp - 20, half = w >> 2, i = (w & 3) * 32 + lane;
+    const uint32_t from_tmem = tmem + ((uint32_t)((w & 3) * 32) << 16) + half * kHalfSlice;
+    const int col0 = e0 + half * kHalfSlice;
+    auto decayed = [&](int c) {
       const int n = tokens_of(from + c);
       warp_wait(&tab.c_full[c & 1], c >> 1);
-      unsigned char* tile = smem + (c & 1) * K::kStage + 2 * DB * K::kBlock + j * 128;
-      const int gap = (r.rev ? j : n - 1 - j) + 1 - r.lead;
-      const float wj = j < n ? tab.pw[gap] : 0.f;
+      unsigned char* tile = smem + (c & 1) * K::kStage + 2 * DB * K::kBlock + i * 128;
+      const int gap = (r.rev ? i : n - 1 - i) + 1 - r.lead;
+      const float wj = i < n ? tab.pw[gap] : 0.f;
       uint32_t raw[4][4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (j < n) v = *reinterpret_cast<const uint4*>(tile + (((half * 4 + q) ^ (j & 7)) << 4));
+        if (i < n) v = *reinterpret_cast<const uint4*>(tile + (((half * 4 + q) ^ (i & 7)) << 4));
         raw[q][0] = v.x;
         raw[q][1] = v.y;
         raw[q][2] = v.z;
@@ -689,41 +690,91 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         const float2 s = fit_scale(group_max(top * wj, tab.red[1], w, 2));
         f = mul2(f, both(s.x));
-        if (j == 0 && half == 0) tab.w_scale[c & 3] = s.y;
+        if (i == 0 && half == 0) tab.w_scale[c & 3] = s.y;
       }
-      uint32_t p[K::kParts][4][4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float2 v = mul2(unpack<T>(raw[q][k]), f);
-#pragma unroll
-          for (int m = 0; m < K::kParts; ++m) p[m][q][k] = take<T>(v);
-        }
       if (c > 0) warp_wait(&tab.u_full, c - 1);
       if (n < C) {
         // Rows past the length may hold anything: the scores, which read them, are made first, then
         // they are cleared, so that 0 * anything stays 0.
         warp_wait(with_out ? &tab.p_full[c & 1] : &tab.ab_full[c & 1], c >> 1);
-        if (j >= n && j < C && half == 0) {
+        if (i >= n && i < C && half == 0) {
           const int db = (r.d + 63) / 64;
           const uint4 z = make_uint4(0, 0, 0, 0);
           for (int q = 0; q < 8; ++q) {
             *reinterpret_cast<uint4*>(tile + (q << 4)) = z;
             for (int k = 0; k < db; ++k)
-              *reinterpret_cast<uint4*>(smem + (c & 1) * K::kStage + (DB + k) * K::kBlock + j * 128 + (q << 4)) = z;
+              *reinterpret_cast<uint4*>(smem + (c & 1) * K::kStage + (DB + k) * K::kBlock + i * 128 + (q << 4)) = z;
           }
         }
       }
-      if (j < C)
+      if (i < C)
 #pragma unroll
-        for (int m = 0; m < K::kParts; ++m)
+        for (int q = 0; q < 4; ++q) {
+          uint32_t p[K::kParts][4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<uint4*>(smem + K::oW + m * K::kBlock + j * 128 + (((half * 4 + q) ^ (j & 7)) << 4)) =
-                make_uint4(p[m][q][0], p[m][q][1], p[m][q][2], p[m][q][3]);
+          for (int k = 0; k < 4; ++k) {
+            float2 v = mul2(unpack<T>(raw[q][k]), f);
+#pragma unroll
+            for (int m = 0; m < K::kParts; ++m) p[m][k] = take<T>(v);
+          }
+#pragma unroll
+          for (int m = 0; m < K::kParts; ++m)
+            *reinterpret_cast<uint4*>(smem + K::oW + m * K::kBlock + i * 128 + (((half * 4 + q) ^ (i & 7)) << 4)) =
+                make_uint4(p[m][0], p[m][1], p[m][2], p[m][3]);
+        }
       to_async();
       warp_arrive(&tab.w_ready);
+    };
+    auto output = [&](int c) {
+      const int n = tokens_of(from + c), t0 = chunk_of(from + c) * C;
+      float2 v[kHalfSlice / 2];
+#pragma unroll
+      for (int j = 0; j < kHalfSlice / 2; ++j) v[j] = both(0.f);
+      if (c > 0 || enters) {
+        warp_wait(&tab.o2_full, enters ? c : c - 1);
+        after_sync();
+        const int gap = (r.rev ? n - 1 - i : i) + r.lead;
+        const float2 fx = both(r.s_inter * tab.pw[gap < 0 ? 0 : gap] * (kHalf ? tab.x_scale[c & 1] : 1.f));
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t x[16];
+          tmem_ld16(from_tmem + kColO2 + 16 * q, x);
+          wait_ld();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            v[8 * q + j] = mul2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), fx);
+        }
+        before_sync();
+        warp_arrive(&tab.o2_free);
+      }
+      warp_wait(&tab.o_full[c & 1], c >> 1);
+      after_sync();
+      const float2 fi = both(r.s_intra * (kHalf ? tab.row_scale[c & 3][i] : 1.f));
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t a[16];
+        tmem_ld16(from_tmem + kColO1 + (c & 1) * kSlice + 16 * q, a);
+        wait_ld();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[8 * q + j] = fma2(make_float2(__uint_as_float(a[2 * j]), __uint_as_float(a[2 * j + 1])), fi,
+                              v[8 * q + j]);
+      }
+      before_sync();
+      warp_arrive(&tab.o_free[c & 1]);
+      if (i >= n)
+#pragma unroll
+        for (int j = 0; j < kHalfSlice / 2; ++j) v[j] = both(0.f);
+      if (i < C && t0 + i < g.T && r.out) {
+        const long long at = (long long)(t0 + i) * r.ot + b * r.ob + h * r.oh + col0;
+        store_out<T>(r, at, r.e - col0, v);
+      }
+      __syncwarp();
+    };
+    if (nc > 0) decayed(0);
+    for (int c = 0; c < nc; ++c) {
+      if (c + 1 < nc) decayed(c + 1);
+      if (with_out) output(c);
     }
   }
   if (!ok) atomicExch(g.status, 1);
@@ -842,7 +893,7 @@ template <typename T, int DB>
 cudaError_t launch(const Maps& maps, TcArgs g, const Plan& p, int roles, cudaStream_t s) {
   using K = Cfg<T, DB>;
   constexpr int smem = (int)(K::oTab + sizeof(Tables));
-  static_assert(smem <= 227 * 1024, "shared memory");
+  static_assert(smem <= 227 * 1024 && K::oTab % 16 == 0, "shared memory");
   auto kernel = la_tc_kernel<T, DB>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
