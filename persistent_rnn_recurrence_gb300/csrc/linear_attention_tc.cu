@@ -15,18 +15,18 @@
 //
 // Rounding.  The products take 16-bit operands.  The data enters as it is; what is computed in
 // between enters as a sum of parts of the data's type: P and X in two (bf16: 16 bits; their error
-// stays far below the output's one rounding), w C in three for bf16 (24 bits) and two for fp16
-// (22), because U sums into the fp32 state.  All products accumulate in fp32.  For fp16, whose range
+// stays far below the output's one rounding), w C in two for fp16 (22 bits), and for bf16 in three
+// (24 bits) where the fp32 state is an output and two where it only feeds 16-bit ones.  All products accumulate in fp32.  For fp16, whose range
 // would not hold them, P is scaled by a power of two per row and X and w C per tile, taken back after the
 // product.
 //
 // Warps: 0 loads (TMA), 1 issues the matrix products, 4-11 turn scores into operands (a row per thread, every
 // other block of 16 columns), 12-19 own the state (a row of X and half the columns), 20-27 make w C
 // and write the output (a row and half the columns).  The order of the products is U(c), O2(c), P(c+1),
-// O1(c): the state is updated, the next chunk's w C made, its scores weighted and this chunk's output written while
-// the tensor cores run the others, and each tile of chunk c + 2 is requested as the last product that
-// reads chunk c's ends.  O2 is taken out of tensor memory as soon as it is there and O1 has two places, so
-// that no product waits for the output.
+// O1(c): the state is updated, the next chunk's w C made and its scores weighted while the tensor cores run
+// the others, and each tile of chunk c + 2 is requested as the last product that reads chunk c's ends.
+// What bounds a chunk is shared memory, from which the products read their operands: the two parts of X
+// stand side by side in one product (N = 128), which reads Q once.
 #include <cuda.h>
 
 #include <algorithm>
@@ -43,13 +43,13 @@ using namespace tc;
 
 constexpr int kThreads = 896, kSlice = 64, kHalfSlice = 32;
 constexpr uint32_t kTmemCols = 512;
-// columns of tensor memory: two score tiles, O1 twice, O2, U
-constexpr uint32_t kColP = 0, kColO1 = 256, kColO2 = 384, kColU = 448;
+// columns of tensor memory: two score tiles, O1, O2 (a part of X each), U
+constexpr uint32_t kColP = 0, kColO1 = 256, kColO2 = 320, kColU = 448;
 
-template <typename T, int DB>
+template <typename T, int DB, int PARTS>
 struct Cfg {
   static constexpr int C = DB == 2 ? 112 : 128;  // tokens per chunk: what the rings leave room for
-  static constexpr int kParts = std::is_same<T, __half>::value ? 2 : 3;
+  static constexpr int kParts = PARTS;           // of w C
   static constexpr uint32_t kBlock = C * 128;    // one [C][64] tile, 128-byte swizzled
   static constexpr uint32_t kStage = (2 * DB + 1) * kBlock;
   static constexpr uint32_t kStateTile = DB * 64 * 128;
@@ -67,7 +67,7 @@ struct Tables {
   float row_top[2][128];
   float diag[32][36];   // l^(i-j) (in reverse l^(j-i)) of a 32 x 32 diagonal block, 0 where the mask is
   uint64_t ab_full[2], c_full[2], a_free[2], b_free[2], c_free[2], p_full[2], p_ready[2];
-  uint64_t o_full[2], o_free[2], o2_full, o2_free, x_ready, w_ready, u_full, u_free, done;
+  uint64_t o_full, o_free, o2_full, o2_free, x_ready, w_ready, u_full, u_free, done;
   uint32_t tmem;
 };
 
@@ -263,10 +263,10 @@ __device__ __forceinline__ void store_out(const TcRole& r, long long at, int m,
     }
 }
 
-template <typename T, int DB>
+template <typename T, int DB, int PARTS>
 __global__ void __launch_bounds__(kThreads, 1)
     la_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g) {
-  using K = Cfg<T, DB>;
+  using K = Cfg<T, DB, PARTS>;
   constexpr int C = K::C;
   constexpr bool kHalf = std::is_same<T, __half>::value;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -325,9 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&tab.c_free[i], 1);
       mbar_init(&tab.p_full[i], 1);
       mbar_init(&tab.p_ready[i], 8);
-      mbar_init(&tab.o_full[i], 1);
-      mbar_init(&tab.o_free[i], 8);
     }
+    mbar_init(&tab.o_full, 1);
+    mbar_init(&tab.o_free, 8);
     mbar_init(&tab.o2_full, 1);
     mbar_init(&tab.o2_free, 8);
     mbar_init(&tab.x_ready, 8);
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t da0 = sw128_kmajor_desc(base), db0 = sw128_kmajor_desc(base + DB * K::kBlock);
       const uint64_t dbt0 = mn_desc(base + DB * K::kBlock, K::kBlock);
       const uint64_t dc0 = mn_desc(base + 2 * DB * K::kBlock, 1024);
-      const uint64_t dw = mn_desc(base + K::oW, 1024), dx = mn_desc(base + K::oX, 1024);
+      const uint64_t dw = mn_desc(base + K::oW, 1024), dx = mn_desc(base + K::oX, K::kStateTile);
       constexpr uint64_t stage = K::kStage >> 4;
       constexpr auto kstep = [](int k) { return (uint64_t)(((k / 4) * K::kBlock + (k % 4) * 32) >> 4); };
       auto qk = [&](int c) {
@@ -424,10 +424,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         after_sync();
         const uint64_t dbt = here(dbt0 + off), dwc = here(dw);
 #pragma unroll
-        for (int p = 0; p < K::kParts; ++p)
+        for (int p = 0; p < PARTS; ++p)
 #pragma unroll
           for (int k = 0; k < C / 16; ++k)  // 16 tokens = 2048 bytes = 128 units
-            umma_f16(tmem + kColU, dbt + 128 * k, dwc + p * (K::kBlock >> 4) + 128 * k,
+            umma_f16(tmem + kColU, dbt + 128 * k, dwc + (PARTS - 1 - p) * (K::kBlock >> 4) + 128 * k,
                      idesc<T>(128, kSlice) | kAMn | kBMn, p > 0 || k > 0);
         umma_commit(&tab.u_full);
         umma_commit(&tab.b_free[c & 1]);
@@ -439,12 +439,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             after_sync();
             const uint64_t da = here(da0 + off), dxc = here(dx);
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
-#pragma unroll
-              for (int k = 0; k < 4 * DB; ++k)
-                if (k < dsteps)
-                  umma_f16(tmem + kColO2, da + kstep(k), dxc + p * (K::kStateTile >> 4) + 128 * k,
-                           idesc<T>(128, kSlice) | kBMn, p > 0 || k > 0);
+            for (int k = 0; k < 4 * DB; ++k)
+              if (k < dsteps)
+                umma_f16(tmem + kColO2, da + kstep(k), dxc + 128 * k, idesc<T>(128, 2 * kSlice) | kBMn, k > 0);
             umma_commit(&tab.o2_full);
           }
           umma_commit(&tab.a_free[c & 1]);
@@ -452,16 +449,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c + 1 < nc) qk(c + 1);
         if (with_out) {
           wait(&tab.p_ready[c & 1], c >> 1);
-          if (c >= 2) wait(&tab.o_free[c & 1], (c >> 1) - 1);
+          if (c > 0) wait(&tab.o_free, c - 1);
           after_sync();
-          const uint32_t pa = tmem + kColP + (c & 1) * 128, d = tmem + kColO1 + (c & 1) * kSlice;
+          const uint32_t pa = tmem + kColP + (c & 1) * 128, d = tmem + kColO1;
           const uint64_t dc = here(dc0 + off);
 #pragma unroll
           for (int k = 0; k < C / 16; ++k) {
             umma_ts(d, pa + 16 * k, dc + 128 * k, idesc<T>(128, kSlice) | kBMn, k > 0);
             umma_ts(d, pa + 16 * k + 8, dc + 128 * k, idesc<T>(128, kSlice) | kBMn, 1);
           }
-          umma_commit(&tab.o_full[c & 1]);
+          umma_commit(&tab.o_full);
         }
         umma_commit(&tab.c_free[c & 1]);
       }
@@ -696,7 +693,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n < C) {
         // Rows past the length may hold anything: the scores, which read them, are made first, then
         // they are cleared, so that 0 * anything stays 0.
-        warp_wait(with_out ? &tab.p_full[c & 1] : &tab.ab_full[c & 1], c >> 1);
+        if (with_out) warp_wait(&tab.p_full[c & 1], c >> 1);
+        else warp_wait(&tab.ab_full[c & 1], c >> 1);
         if (i >= n && i < C && half == 0) {
           const int db = (r.d + 63) / 64;
           const uint4 z = make_uint4(0, 0, 0, 0);
@@ -737,23 +735,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 fx = both(r.s_inter * tab.pw[gap < 0 ? 0 : gap] * (kHalf ? tab.x_scale[c & 1] : 1.f));
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          uint32_t x[16];
+          uint32_t x[16], y[16];
           tmem_ld16(from_tmem + kColO2 + 16 * q, x);
+          tmem_ld16(from_tmem + kColO2 + kSlice + 16 * q, y);
           wait_ld();
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            v[8 * q + j] = mul2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), fx);
+            v[8 * q + j] = mul2(add2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])),
+                                     make_float2(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1]))), fx);
         }
         before_sync();
         warp_arrive(&tab.o2_free);
       }
-      warp_wait(&tab.o_full[c & 1], c >> 1);
+      warp_wait(&tab.o_full, c);
       after_sync();
       const float2 fi = both(r.s_intra * (kHalf ? tab.row_scale[c & 3][i] : 1.f));
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         uint32_t a[16];
-        tmem_ld16(from_tmem + kColO1 + (c & 1) * kSlice + 16 * q, a);
+        tmem_ld16(from_tmem + kColO1 + 16 * q, a);
         wait_ld();
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                               v[8 * q + j]);
       }
       before_sync();
-      warp_arrive(&tab.o_free[c & 1]);
+      warp_arrive(&tab.o_free);
       if (i >= n)
 #pragma unroll
         for (int j = 0; j < kHalfSlice / 2; ++j) v[j] = both(0.f);
@@ -864,21 +864,18 @@ Plan make_plan(const LaArgs& a, int C, int sms, size_t capacity) {
   double best = waves(ctas) * (chunks + 1);
   p.cps = chunks;
   if (in_place) return p;
-  for (int segs = 2; segs <= 64 && segs <= chunks; ++segs) {
-    const int cps = (chunks + segs - 1) / segs, real = (chunks + cps - 1) / cps;
-    if (real != segs) continue;
-    for (int m = 1; m <= 4 && m <= cps; ++m) {
-      if (cps % m) continue;
-      const int cpb = cps / m, subs = (segs - 1) * m;
-      if ((size_t)ctas * subs * kStateBytes > capacity) continue;
-      const double cost = waves(ctas * segs) * (cps + 1) + waves(ctas * subs) * (0.6 * cpb + 1) + 3 +
+  for (int want = 2; want <= 64 && want <= chunks; ++want)
+    for (int m = 1; m <= 4; ++m) {
+      const int cpb = (chunks + want * m - 1) / (want * m), cps = cpb * m;
+      const int segs = (chunks + cps - 1) / cps, subs = (segs - 1) * m;
+      if (segs < 2 || (size_t)ctas * subs * kStateBytes > capacity) continue;
+      const double cost = waves(ctas * segs) * (cps + 1) + waves(ctas * subs) * (0.5 * cpb + 1) + 3 +
                           0.05 * subs;
       if (cost < best) {
         best = cost;
         p = {segs, cps, subs, cpb, p.slices};
       }
     }
-  }
   return p;
 }
 
@@ -887,14 +884,14 @@ int max_d(const LaArgs& a) {
   for (int i = 0; i < a.roles; ++i) d = std::max(d, a.role[i].d);
   return d;
 }
-int chunk_of(int d) { return d > 64 ? Cfg<__half, 2>::C : Cfg<__half, 1>::C; }
+int chunk_of(int d) { return d > 64 ? Cfg<__half, 2, 2>::C : Cfg<__half, 1, 2>::C; }
 
-template <typename T, int DB>
+template <typename T, int DB, int PARTS>
 cudaError_t launch(const Maps& maps, TcArgs g, const Plan& p, int roles, cudaStream_t s) {
-  using K = Cfg<T, DB>;
+  using K = Cfg<T, DB, PARTS>;
   constexpr int smem = (int)(K::oTab + sizeof(Tables));
   static_assert(smem <= 227 * 1024 && K::oTab % 16 == 0, "shared memory");
-  auto kernel = la_tc_kernel<T, DB>;
+  auto kernel = la_tc_kernel<T, DB, PARTS>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const unsigned bh = (unsigned)(g.B * g.H * p.slices);
@@ -1006,10 +1003,15 @@ cudaError_t launch_la_tc(const LaArgs& a, void* scratch, size_t bytes, cudaStrea
   g.cpb = p.cpb;
   g.slices = p.slices;
   g.part = reinterpret_cast<float*>(static_cast<char*>(scratch) + used);
+  bool ends = false;
+  for (int i = 0; i < a.roles; ++i) ends = ends || a.role[i].x_end;
   if (half)
-    return d > 64 ? launch<__half, 2>(maps, g, p, a.roles, s) : launch<__half, 1>(maps, g, p, a.roles, s);
-  return d > 64 ? launch<__nv_bfloat16, 2>(maps, g, p, a.roles, s)
-                : launch<__nv_bfloat16, 1>(maps, g, p, a.roles, s);
+    return d > 64 ? launch<__half, 2, 2>(maps, g, p, a.roles, s) : launch<__half, 1, 2>(maps, g, p, a.roles, s);
+  if (ends)
+    return d > 64 ? launch<__nv_bfloat16, 2, 3>(maps, g, p, a.roles, s)
+                  : launch<__nv_bfloat16, 1, 3>(maps, g, p, a.roles, s);
+  return d > 64 ? launch<__nv_bfloat16, 2, 2>(maps, g, p, a.roles, s)
+                : launch<__nv_bfloat16, 1, 2>(maps, g, p, a.roles, s);
 }
 
 }  // namespace prnn
