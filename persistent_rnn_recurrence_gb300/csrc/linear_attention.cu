@@ -9,13 +9,20 @@
 // so a chunk is four small matrix products and only the chunks are serial.
 // Every exponent is >= 0: no power of the decay can overflow, whatever the
 // decay, which factoring l^(i-j) into l^i l^-j would not give.
+#include "linear_attention_plan.h"
 #include "seq_common.cuh"
 #include "seq_internal.h"
 
 namespace prnn {
 namespace {
 
-constexpr int kChunk = 32, kCols = 32, kThreads = 256;
+constexpr int kChunk = 32, kCols = 64, kThreads = 128, kStride = kChunk + 4, kWide = kCols + 4;
+
+struct SimtArgs {
+  LaArgs g;
+  int segs, cps, subs, cpb, slices, states_only;
+  float* part;  // [role][B*H][subs][slices][D * kCols]
+};
 
 __device__ __forceinline__ int seq_len(const LaArgs& a, int b) {
   if (!a.lens) return a.T;
@@ -27,95 +34,256 @@ template <typename T>
 __device__ __forceinline__ const T* seq_row(const LaSeq& s, long long t, int b, int h) {
   return static_cast<const T*>(s.p) + t * s.st + b * s.sb + (h / s.share) * s.sh;
 }
-
-// One block: one role, one (sequence, head) and kCols of the e columns.
+// Four consecutive values of a row of n, zeros past it; `vec`: rows start on 16 bytes.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) la_mix_kernel(const __grid_constant__ LaArgs g) {
-  const LaRole& r = g.role[blockIdx.z];
-  const int col0 = blockIdx.y * kCols;
-  if (col0 >= r.e) return;
-  const int bh = blockIdx.x, b = bh / g.H, h = bh % g.H, d = r.d, tid = threadIdx.x;
-  const int len = seq_len(g, b), ncol = min(kCols, r.e - col0);
-  extern __shared__ float sm[];
-  float* A = sm;                       // [kChunk][d + 1]
-  float* Bm = A + kChunk * (d + 1);    // [kChunk][d + 1]
-  float* Cm = Bm + kChunk * (d + 1);   // [kChunk][kCols]
-  float* P = Cm + kChunk * kCols;      // [kChunk][kChunk + 1]
-  float* X = P + kChunk * (kChunk + 1);  // [d][kCols]
-  float* pw = X + d * kCols;           // [kChunk + 1]
+__device__ __forceinline__ float4 load4(const T* p, int at, int n, bool vec) {
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  if (vec && at + 4 <= n) {
+    const Pack<T, 4> q = load_pack<T, 4>(p + at);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = to_f32(q.v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (at + j < n) v[j] = to_f32(p[at + j]);
+  }
+  return make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+
+// One block: one role, one (sequence, head), kCols of the e columns and one segment of time.  The state
+// stays in registers (thread (rg, cg): rows rg + 16 m, columns 4 cg .. and 32 + 4 cg ..) and is copied to
+// shared memory once a chunk as an operand.  a and b are kept with the tokens innermost (a lane per token
+// as they are loaded, so no bank conflicts), which serves the scores, the product with the state
+// and the state's update: each product is a tile of 4 x 4 (scores 4 x 2, state 8 x 8) values
+// per thread fed by 16-byte reads, 16 to 64 multiply-adds for two to four of them.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, D <= 64 ? 3 : (D <= 128 ? 2 : 1))
+    la_simt_kernel(const __grid_constant__ SimtArgs args) {
+  constexpr int M = D / 16;
+  const LaArgs& g = args.g;
+  const LaRole& r = g.role[blockIdx.y];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int runs = args.states_only ? args.subs : args.segs;
+  const int slice = blockIdx.x % args.slices, seg = blockIdx.x / args.slices % runs;
+  const int bh = blockIdx.x / args.slices / runs, b = bh / g.H, h = bh % g.H;
+  const int e0 = slice * kCols;
+  if (e0 >= r.e) return;
+  const int d = r.d, ncol = min(kCols, r.e - e0), len = seq_len(g, b);
+  const int chunks = (len + kChunk - 1) / kChunk, last = len - (chunks - 1) * kChunk;
+  const int per = args.states_only ? args.cpb : args.cps;
+  const int from = min(seg * per, chunks), to = min((seg + 1) * per, chunks);
+  auto before = [&](int c) {  // tokens processed before chunk c of the order
+    if (c <= 0) return 0;
+    if (c >= chunks) return len;
+    return r.rev ? last + (c - 1) * kChunk : c * kChunk;
+  };
+  const bool with_out = !args.states_only && r.out;
+  const bool writes_end = !args.states_only && r.x_end && (to > from ? to == chunks : chunks == 0 && seg == 0);
+  if (with_out) {  // zeros past the length
+    const int t0 = max(seg * per, chunks) * kChunk, t1 = min((seg + 1) * per * kChunk, g.T);
+    for (long long p = tid; p < (long long)max(0, t1 - t0) * ncol; p += kThreads) {
+      const long long at = (t0 + p / ncol) * r.ot + b * r.ob + h * r.oh + e0 + p % ncol;
+      if (r.out_f32) static_cast<float*>(r.out)[at] = 0.f;
+      else static_cast<T*>(r.out)[at] = from_f32<T>(0.f);
+    }
+  }
+  if (to == from && !writes_end) return;
+
+  extern __shared__ __align__(16) float sm[];
+  float* At = sm;                    // [D][kStride]
+  float* Bt = At + D * kStride;      // [D][kStride]
+  float* Cs = Bt + D * kStride;      // [kChunk][kWide]
+  float* Pt = Cs + kChunk * kWide;   // [kChunk (j)][kStride (i)]
+  float* Xs = Pt + kChunk * kStride; // [D][kWide]
+  __shared__ float pw[kChunk + 1];
   const float ld = g.log_decay[h];
   if (tid <= kChunk) pw[tid] = decay_pow(ld, tid);
-  for (int i = tid; i < d * kCols; i += kThreads) {
-    const int k = i / kCols, c = i % kCols;
-    float v = 0.f;
-    if (r.x0 && c < ncol)
-      v = r.x0[(size_t)bh * d * r.e + (r.x_t ? (size_t)(col0 + c) * d + k
-                                             : (size_t)k * r.e + col0 + c)];
-    X[i] = v;
+
+  const int rg = warp * 4 + (lane >> 3), cg = lane & 7;  // the state's tile
+  float X[M][8];
+  const size_t head = (size_t)bh * d * r.e;
+  const int done = before(from);
+  const float f0 = decay_pow(ld, done);
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const int k = rg + 16 * m, col = (c & 4) * 8 + 4 * cg + (c & 3);
+      X[m][c] = 0.f;
+      if (r.x0 && !args.states_only && k < d && col < ncol)
+        X[m][c] = f0 * r.x0[head + (r.x_t ? (size_t)(e0 + col) * d + k : (size_t)k * r.e + e0 + col)];
+    }
+  float* part = args.part + ((((size_t)blockIdx.y * g.B * g.H + bh) * args.subs) * args.slices + slice) * D * kCols;
+  const size_t sub_size = (size_t)args.slices * D * kCols;
+  if (!args.states_only) {
+    const int subs = min(seg * (args.cps / args.cpb), (chunks + args.cpb - 1) / args.cpb);
+    for (int u = 0; u < subs; ++u) {
+      const float f = decay_pow(ld, done - before((u + 1) * args.cpb));
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(part + u * sub_size + (rg + 16 * m) * kCols + 32 * q + 4 * cg));
+          X[m][4 * q] = fmaf(f, v.x, X[m][4 * q]);
+          X[m][4 * q + 1] = fmaf(f, v.y, X[m][4 * q + 1]);
+          X[m][4 * q + 2] = fmaf(f, v.z, X[m][4 * q + 2]);
+          X[m][4 * q + 3] = fmaf(f, v.w, X[m][4 * q + 3]);
+        }
+    }
   }
-  const int chunks = (len + kChunk - 1) / kChunk;
-  for (int ci = 0; ci < chunks; ++ci) {
+  auto vec_of = [&](const LaSeq& s) {
+    return (((reinterpret_cast<uintptr_t>(s.p) / sizeof(T)) | (uintptr_t)s.st | (uintptr_t)s.sb | (uintptr_t)s.sh) & 3) == 0;
+  };
+  const bool va = vec_of(r.a), vb = vec_of(r.b), vc = vec_of(r.c);
+  const int r0 = 4 * (lane >> 2);                         // rows of the scores' and the output's tile
+  const int pc = 8 * warp + 2 * (lane & 3), oc = 16 * warp + 4 * (lane & 3);  // their columns
+
+  for (int ci = from; ci < to; ++ci) {
     const int t0 = (r.rev ? chunks - 1 - ci : ci) * kChunk, n = min(kChunk, len - t0);
     __syncthreads();
-    for (int i = tid; i < kChunk * d; i += kThreads) {
-      const int j = i / d, k = i % d;
-      A[j * (d + 1) + k] = j < n ? to_f32(seq_row<T>(r.a, t0 + j, b, h)[k]) : 0.f;
-      Bm[j * (d + 1) + k] = j < n ? to_f32(seq_row<T>(r.b, t0 + j, b, h)[k]) : 0.f;
-    }
-    for (int i = tid; i < kChunk * kCols; i += kThreads) {
-      const int j = i / kCols, c = i % kCols;
-      Cm[i] = j < n && c < ncol ? to_f32(seq_row<T>(r.c, t0 + j, b, h)[col0 + c]) : 0.f;
-    }
-    __syncthreads();
-    for (int p = tid; p < kChunk * kChunk; p += kThreads) {
-      const int i = p / kChunk, j = p % kChunk;
-      float s = 0.f;
-      if (r.rev ? j >= i : j <= i) {
-        for (int k = 0; k < d; ++k) s = fmaf(A[i * (d + 1) + k], Bm[j * (d + 1) + k], s);
-        s *= pw[r.rev ? j - i : i - j];
+    if (with_out)
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          *reinterpret_cast<float4*>(Xs + (rg + 16 * m) * kWide + 32 * q + 4 * cg) =
+              make_float4(X[m][4 * q], X[m][4 * q + 1], X[m][4 * q + 2], X[m][4 * q + 3]);
+    {
+      const T* pa = seq_row<T>(r.a, t0 + lane, b, h);
+      const T* pb = seq_row<T>(r.b, t0 + lane, b, h);
+#pragma unroll 4
+      for (int k = 4 * warp; k < D; k += 16) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        if (lane < n && k < d) {
+          if (with_out) x = load4(pa, k, d, va);
+          y = load4(pb, k, d, vb);
+        }
+        if (with_out) {
+          At[k * kStride + lane] = x.x;
+          At[(k + 1) * kStride + lane] = x.y;
+          At[(k + 2) * kStride + lane] = x.z;
+          At[(k + 3) * kStride + lane] = x.w;
+        }
+        Bt[k * kStride + lane] = y.x;
+        Bt[(k + 1) * kStride + lane] = y.y;
+        Bt[(k + 2) * kStride + lane] = y.z;
+        Bt[(k + 3) * kStride + lane] = y.w;
       }
-      P[i * (kChunk + 1) + j] = s;
-    }
-    __syncthreads();
-    for (int p = tid; p < n * kCols; p += kThreads) {
-      const int i = p / kCols, c = p % kCols;
-      float intra = 0.f, inter = 0.f;
-      for (int j = 0; j < n; ++j) intra = fmaf(P[i * (kChunk + 1) + j], Cm[j * kCols + c], intra);
-      for (int k = 0; k < d; ++k) inter = fmaf(A[i * (d + 1) + k], X[k * kCols + c], inter);
-      const float v = r.s_intra * intra + r.s_inter * pw[(r.rev ? n - 1 - i : i) + r.lead] * inter;
-      if (r.out && c < ncol) {
-        const long long at = (long long)(t0 + i) * r.ot + b * r.ob + h * r.oh + col0 + c;
-        if (r.out_f32)
-          static_cast<float*>(r.out)[at] = v;
-        else
-          static_cast<T*>(r.out)[at] = from_f32<T>(v);
+#pragma unroll
+      for (int i = tid; i < kChunk * kCols / 4; i += kThreads) {
+        const int j = i / (kCols / 4), c = i % (kCols / 4) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j < n) v = load4(seq_row<T>(r.c, t0 + j, b, h) + e0, c, ncol, vc);
+        *reinterpret_cast<float4*>(Cs + j * kWide + c) = v;
       }
     }
     __syncthreads();
-    for (int p = tid; p < d * kCols; p += kThreads) {
-      const int k = p / kCols, c = p % kCols;
-      float s = 0.f;
-      for (int j = 0; j < n; ++j)
-        s = fmaf(Bm[j * (d + 1) + k] * pw[(r.rev ? j : n - 1 - j) + 1 - r.lead], Cm[j * kCols + c], s);
-      X[p] = pw[n] * X[p] + r.s_add * s;
+    if (with_out) {
+      // scores, weighted and masked
+      float p[4][2] = {};
+#pragma unroll 8
+      for (int k = 0; k < d; ++k) {
+        const float4 x = ld4(At + k * kStride + r0);
+        const float2 y = *reinterpret_cast<const float2*>(Bt + k * kStride + pc);
+        const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p[i][0] = fmaf(xs[i], y.x, p[i][0]);
+          p[i][1] = fmaf(xs[i], y.y, p[i][1]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int gap = r.rev ? pc + j - (r0 + i) : r0 + i - (pc + j);
+          w[i] = gap >= 0 ? r.s_intra * p[i][j] * pw[gap] : 0.f;
+        }
+        *reinterpret_cast<float4*>(Pt + (pc + j) * kStride + r0) = make_float4(w[0], w[1], w[2], w[3]);
+      }
+      __syncthreads();
+      float o[4][4] = {};
+      auto product = [&](const float* x, int xstride, const float* y, int count) {
+#pragma unroll 4
+        for (int k = 0; k < count; ++k) {
+          const float4 u = ld4(x + k * xstride + r0), v = ld4(y + k * kWide + oc);
+          const float us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][j] = fmaf(us[i], vs[j], o[i][j]);
+        }
+      };
+      product(At, kStride, Xs, d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = r0 + i, gap = (r.rev ? n - 1 - row : row) + r.lead;
+        const float f = r.s_inter * pw[gap < 0 ? 0 : (gap > kChunk ? kChunk : gap)];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][j] *= f;
+      }
+      product(Pt, kStride, Cs, kChunk);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (t0 + r0 + i >= g.T) break;
+        const long long at = (long long)(t0 + r0 + i) * r.ot + b * r.ob + h * r.oh + e0 + oc;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (oc + j < ncol) {  // rows past the length: 0
+            const float v = r0 + i < n ? o[i][j] : 0.f;
+            if (r.out_f32) static_cast<float*>(r.out)[at + j] = v;
+            else static_cast<T*>(r.out)[at + j] = from_f32<T>(v);
+          }
+      }
+    }
+    // X <- l^n X + s_add sum_j w_j b_j c_j
+    const float fn = pw[n];
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) X[m][c] *= fn;
+#pragma unroll 1
+    for (int j = 0; j < kChunk; j += 4) {
+      float bt[M][4];
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        const float4 v = ld4(Bt + (rg + 16 * m) * kStride + j);
+        bt[m][0] = v.x;
+        bt[m][1] = v.y;
+        bt[m][2] = v.z;
+        bt[m][3] = v.w;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int gap = (r.rev ? j + q : n - 1 - j - q) + 1 - r.lead;
+        const float w = j + q < n ? r.s_add * pw[gap] : 0.f;
+        const float4 u = ld4(Cs + (j + q) * kWide + 4 * cg), v = ld4(Cs + (j + q) * kWide + 32 + 4 * cg);
+        const float cw[8] = {w * u.x, w * u.y, w * u.z, w * u.w, w * v.x, w * v.y, w * v.z, w * v.w};
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) X[m][c] = fmaf(bt[m][q], cw[c], X[m][c]);
+      }
     }
   }
-  __syncthreads();
-  if (r.x_end)
-    for (int i = tid; i < d * kCols; i += kThreads) {
-      const int k = i / kCols, c = i % kCols;
-      if (c < ncol)
-        r.x_end[(size_t)bh * d * r.e + (r.x_t ? (size_t)(col0 + c) * d + k
-                                              : (size_t)k * r.e + col0 + c)] = X[i];
-    }
-  if (r.out)
-    for (long long p = tid; p < (long long)(g.T - len) * ncol; p += kThreads) {
-      const long long at = (len + p / ncol) * r.ot + b * r.ob + h * r.oh + col0 + p % ncol;
-      if (r.out_f32)
-        static_cast<float*>(r.out)[at] = 0.f;
-      else
-        static_cast<T*>(r.out)[at] = from_f32<T>(0.f);
-    }
+  if (writes_end)
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int k = rg + 16 * m, col = (c & 4) * 8 + 4 * cg + (c & 3);
+        if (k < d && col < ncol)
+          r.x_end[head + (r.x_t ? (size_t)(e0 + col) * d + k : (size_t)k * r.e + e0 + col)] = X[m][c];
+      }
+  if (args.states_only)
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        *reinterpret_cast<float4*>(part + seg * sub_size + (rg + 16 * m) * kCols + 32 * q + 4 * cg) =
+            make_float4(X[m][4 * q], X[m][4 * q + 1], X[m][4 * q + 2], X[m][4 * q + 3]);
 }
 
 template <typename T>
@@ -132,28 +300,54 @@ __global__ void __launch_bounds__(256) la_reduce_kernel(LaReduceArgs a) {
   }
 }
 
-size_t mix_smem(int d) {
-  return sizeof(float) * (2 * kChunk * (d + 1) + kChunk * kCols + kChunk * (kChunk + 1) +
-                          d * kCols + kChunk + 1);
+int max_d(const LaArgs& a) {
+  int d = 0;
+  for (int i = 0; i < a.roles; ++i) d = std::max(d, a.role[i].d);
+  return d <= 64 ? 64 : (d <= 128 ? 128 : 256);
+}
+size_t smem_of(int D) {
+  return sizeof(float) * (2 * D * kStride + kChunk * kWide + kChunk * kStride + D * kWide);
+}
+LaPlan make_plan(const LaArgs& a, size_t capacity) {
+  const int D = max_d(a), at_once = std::min<int>(3, (int)(227 * 1024 / (smem_of(D) + 1024)));
+  return la_plan(a, kChunk, kCols, at_once * seq_sm_count(), 0.45, sizeof(float) * D * kCols, capacity);
+}
+
+template <typename T, int D>
+cudaError_t launch(SimtArgs& s, const LaPlan& p, cudaStream_t stream) {
+  auto kernel = la_simt_kernel<T, D>;
+  const size_t smem = smem_of(D);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const unsigned bh = (unsigned)(s.g.B * s.g.H * p.slices);
+  if (p.segs > 1) {
+    s.states_only = 1;
+    kernel<<<dim3(bh * p.subs, s.g.roles), kThreads, smem, stream>>>(s);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    s.states_only = 0;
+  }
+  kernel<<<dim3(bh * p.segs, s.g.roles), kThreads, smem, stream>>>(s);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_la_simt(const LaArgs& a, cudaStream_t s) {
-  int d = 0, e = 0;
-  for (int i = 0; i < a.roles; ++i) {
-    d = a.role[i].d > d ? a.role[i].d : d;
-    e = a.role[i].e > e ? a.role[i].e : e;
-  }
+size_t la_simt_workspace(const LaArgs& a) {
+  const LaPlan p = make_plan(a, ~(size_t)0);
+  return sizeof(float) * a.roles * a.B * a.H * p.subs * p.slices * max_d(a) * kCols;
+}
+
+cudaError_t launch_la_simt(const LaArgs& a, void* scratch, size_t bytes, cudaStream_t stream) {
   if (a.roles == 0 || a.B == 0) return cudaSuccess;
-  const size_t smem = mix_smem(d);
-  const dim3 grid(a.B * a.H, (e + kCols - 1) / kCols, a.roles);
-  cudaError_t err = cudaSuccess;
-  PRNN_BY_DTYPE(a.dtype, T,
-                err = cudaFuncSetAttribute(la_mix_kernel<T>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-                if (err == cudaSuccess) la_mix_kernel<T><<<grid, kThreads, smem, s>>>(a));
-  return err != cudaSuccess ? err : cudaGetLastError();
+  const LaPlan p = make_plan(a, bytes);
+  SimtArgs s{a, p.segs, p.cps, p.subs, p.cpb, p.slices, 0, static_cast<float*>(scratch)};
+  cudaError_t e = cudaSuccess;
+  switch (max_d(a)) {
+    case 64: PRNN_BY_DTYPE(a.dtype, T, (e = launch<T, 64>(s, p, stream))); break;
+    case 128: PRNN_BY_DTYPE(a.dtype, T, (e = launch<T, 128>(s, p, stream))); break;
+    default: PRNN_BY_DTYPE(a.dtype, T, (e = launch<T, 256>(s, p, stream))); break;
+  }
+  return e;
 }
 
 cudaError_t launch_la_reduce(const LaReduceArgs& a, cudaStream_t s) {

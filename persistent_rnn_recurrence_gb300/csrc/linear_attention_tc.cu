@@ -20,11 +20,11 @@
 // would not hold them, P is scaled by a power of two per row and X and w C per tile, taken back after the
 // product.
 //
-// Warps: 0 loads (TMA), 1 issues the matrix products, 4-11 turn scores into operands (a row per thread, every
-// other block of 16 columns), 12-19 own the state (a row of X and half the columns), 20-27 make w C
-// and write the output (a row and half the columns).  The order of the products is U(c), O2(c), P(c+1),
-// O1(c): the state is updated, the next chunk's w C made and its scores weighted while the tensor cores run
-// the others, and each tile of chunk c + 2 is requested as the last product that reads chunk c's ends.
+// Warps: 0 loads (TMA), 1 and 2 issue the matrix products, 4-11 turn scores into operands (a row per thread,
+// every other block of 16 columns), 12-19 own the state (a row of X and half the columns), 20-27 make
+// w C and write the output (a row and half the columns).  The tensor cores run U(c), O2(c), P(c+1) and
+// O1(c) while the state is updated, the next chunk's w C made, its scores weighted and the last output
+// written; each tile of chunk c + 2 is requested as the last product that reads chunk c's ends.
 // What bounds a chunk is shared memory, from which the products read their operands: the two parts of X
 // stand side by side in one product (N = 128), which reads Q once.
 #include <cuda.h>
@@ -32,6 +32,7 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "linear_attention_plan.h"
 #include "seq_common.cuh"
 #include "seq_internal.h"
 #include "tc_common.cuh"
@@ -67,7 +68,7 @@ struct Tables {
   float row_top[2][128];
   float diag[32][36];   // l^(i-j) (in reverse l^(j-i)) of a 32 x 32 diagonal block, 0 where the mask is
   uint64_t ab_full[2], c_full[2], a_free[2], b_free[2], c_free[2], p_full[2], p_ready[2];
-  uint64_t o_full, o_free, o2_full, o2_free, x_ready, w_ready, u_full, u_free, done;
+  uint64_t w_ready[2], o_full, o_free, o2_full, o2_free, x_ready, u_full, u_free, done;
   uint32_t tmem;
 };
 
@@ -311,6 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (nc == 0 && !writes_end) return;
 
+  const bool with_out = !g.states_only;
   const uint32_t base = smem_u32(smem);
   if (base & 1023u) {  // the swizzled tiles need it; no static shared memory precedes them
     if (tid == 0) atomicExch(g.status, 1);
@@ -320,21 +322,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tab.ab_full[i], 1);
       mbar_init(&tab.c_full[i], 1);
-      mbar_init(&tab.a_free[i], 1);
-      mbar_init(&tab.b_free[i], 1);
+      mbar_init(&tab.a_free[i], 2);
+      mbar_init(&tab.b_free[i], with_out ? 2 : 1);
       mbar_init(&tab.c_free[i], 1);
       mbar_init(&tab.p_full[i], 1);
       mbar_init(&tab.p_ready[i], 8);
+      mbar_init(&tab.w_ready[i], 8);
     }
     mbar_init(&tab.o_full, 1);
     mbar_init(&tab.o_free, 8);
     mbar_init(&tab.o2_full, 1);
     mbar_init(&tab.o2_free, 8);
     mbar_init(&tab.x_ready, 8);
-    mbar_init(&tab.w_ready, 8);
     mbar_init(&tab.u_full, 1);
     mbar_init(&tab.u_free, 8);
-    mbar_init(&tab.done, 1);
+    mbar_init(&tab.done, 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
@@ -357,7 +359,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint64_t deadline = global_ns() + kSeqWaitNs;
   // a state enters the first chunk unless it is known to be zero
   const bool enters = r.x0 != nullptr || (seg > 0 && !g.states_only);
-  const bool with_out = !g.states_only;
   // A wait that runs out is remembered and the work goes on (every later wait then ends at once):
   // no thread leaves the others waiting, and nothing is left in flight.
   bool ok = true;
@@ -393,45 +394,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = mbar_wait(&tab.c_full[c & 1], (c >> 1) & 1, limit) && ok;
       }
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 2) {
+    // ---- matrix products: warp 1 those of the state (U, O2), warp 2 those of the scores (P, O1), so that
+    // one's waits run under the other's products.  A product costs its thread as few instructions as can be:
+    // descriptors are made once and stepped by constants ----
     if (elected()) {
-      // ---- matrix products.  One thread issues them all, so a product costs it as few instructions as
-      // can be: descriptors are made once and stepped by constants ----
       const int dsteps = (r.d + 15) / 16;
       const uint64_t da0 = sw128_kmajor_desc(base), db0 = sw128_kmajor_desc(base + DB * K::kBlock);
-      const uint64_t dbt0 = mn_desc(base + DB * K::kBlock, K::kBlock);
-      const uint64_t dc0 = mn_desc(base + 2 * DB * K::kBlock, 1024);
-      const uint64_t dw = mn_desc(base + K::oW, 1024), dx = mn_desc(base + K::oX, K::kStateTile);
       constexpr uint64_t stage = K::kStage >> 4;
       constexpr auto kstep = [](int k) { return (uint64_t)(((k / 4) * K::kBlock + (k % 4) * 32) >> 4); };
-      auto qk = [&](int c) {
-        wait(&tab.ab_full[c & 1], c >> 1);
-        if (!with_out) return;
-        after_sync();
-        const uint64_t da = here(da0 + (c & 1) * stage), db = here(db0 + (c & 1) * stage);
-        const uint32_t d = tmem + kColP + (c & 1) * 128;
+      if (warp == 1) {
+        const uint64_t dbt0 = mn_desc(base + DB * K::kBlock, K::kBlock);
+        const uint64_t dw = mn_desc(base + K::oW, 1024), dx = mn_desc(base + K::oX, K::kStateTile);
+        for (int c = 0; c < nc; ++c) {
+          const uint64_t off = (c & 1) * stage;
+          wait(&tab.ab_full[c & 1], c >> 1);
+          wait(&tab.w_ready[c & 1], c >> 1);
+          if (c > 0) wait(&tab.u_free, c - 1);
+          after_sync();
+          const uint64_t dbt = here(dbt0 + off), dwc = here(dw);
 #pragma unroll
-        for (int k = 0; k < 4 * DB; ++k)
-          if (k < dsteps) umma_f16(d, da + kstep(k), db + kstep(k), idesc<T>(128, C), k > 0);
-        umma_commit(&tab.p_full[c & 1]);
-      };
-      if (nc > 0) qk(0);
-      for (int c = 0; c < nc; ++c) {
-        const uint64_t off = (c & 1) * stage;
-        wait(&tab.c_full[c & 1], c >> 1);
-        wait(&tab.w_ready, c);
-        if (c > 0) wait(&tab.u_free, c - 1);
-        after_sync();
-        const uint64_t dbt = here(dbt0 + off), dwc = here(dw);
+          for (int p = 0; p < PARTS; ++p)
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p)
-#pragma unroll
-          for (int k = 0; k < C / 16; ++k)  // 16 tokens = 2048 bytes = 128 units
-            umma_f16(tmem + kColU, dbt + 128 * k, dwc + (PARTS - 1 - p) * (K::kBlock >> 4) + 128 * k,
-                     idesc<T>(128, kSlice) | kAMn | kBMn, p > 0 || k > 0);
-        umma_commit(&tab.u_full);
-        umma_commit(&tab.b_free[c & 1]);
-        if (with_out) {
+            for (int k = 0; k < C / 16; ++k)  // 16 tokens = 2048 bytes = 128 units
+              umma_f16(tmem + kColU, dbt + 128 * k, dwc + (PARTS - 1 - p) * (K::kBlock >> 4) + 128 * k,
+                       idesc<T>(128, kSlice) | kAMn | kBMn, p > 0 || k > 0);
+          umma_commit(&tab.u_full);
+          umma_commit(&tab.b_free[c & 1]);
+          if (!with_out) {
+            umma_commit(&tab.c_free[c & 1]);
+            continue;
+          }
           if (c > 0 || enters) {
             const int turn = enters ? c : c - 1;
             wait(&tab.x_ready, turn);
@@ -446,21 +439,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           umma_commit(&tab.a_free[c & 1]);
         }
-        if (c + 1 < nc) qk(c + 1);
-        if (with_out) {
+      } else if (with_out) {
+        const uint64_t dc0 = mn_desc(base + 2 * DB * K::kBlock, 1024);
+        auto qk = [&](int c) {
+          wait(&tab.ab_full[c & 1], c >> 1);
+          after_sync();
+          const uint64_t da = here(da0 + (c & 1) * stage), db = here(db0 + (c & 1) * stage);
+          const uint32_t d = tmem + kColP + (c & 1) * 128;
+#pragma unroll
+          for (int k = 0; k < 4 * DB; ++k)
+            if (k < dsteps) umma_f16(d, da + kstep(k), db + kstep(k), idesc<T>(128, C), k > 0);
+          umma_commit(&tab.p_full[c & 1]);
+          umma_commit(&tab.a_free[c & 1]);
+          umma_commit(&tab.b_free[c & 1]);
+        };
+        if (nc > 0) qk(0);
+        for (int c = 0; c < nc; ++c) {
+          if (c + 1 < nc) qk(c + 1);
+          wait(&tab.c_full[c & 1], c >> 1);
+          wait(&tab.w_ready[c & 1], c >> 1);  // rows of C past the length have been cleared
           wait(&tab.p_ready[c & 1], c >> 1);
           if (c > 0) wait(&tab.o_free, c - 1);
           after_sync();
           const uint32_t pa = tmem + kColP + (c & 1) * 128, d = tmem + kColO1;
-          const uint64_t dc = here(dc0 + off);
+          const uint64_t dc = here(dc0 + (c & 1) * stage);
 #pragma unroll
           for (int k = 0; k < C / 16; ++k) {
             umma_ts(d, pa + 16 * k, dc + 128 * k, idesc<T>(128, kSlice) | kBMn, k > 0);
             umma_ts(d, pa + 16 * k + 8, dc + 128 * k, idesc<T>(128, kSlice) | kBMn, 1);
           }
           umma_commit(&tab.o_full);
+          umma_commit(&tab.c_free[c & 1]);
         }
-        umma_commit(&tab.c_free[c & 1]);
       }
       // every product has read its operands before the CTA leaves
       umma_commit(&tab.done);
@@ -721,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_uint4(p[m][0], p[m][1], p[m][2], p[m][3]);
         }
       to_async();
-      warp_arrive(&tab.w_ready);
+      warp_arrive(&tab.w_ready[c & 1]);
     };
     auto output = [&](int c) {
       const int n = tokens_of(from + c), t0 = chunk_of(from + c) * C;
@@ -842,41 +852,8 @@ bool seq_fits(const LaSeq& s, const LaArgs& a, int d) {
 
 constexpr size_t kStateBytes = kSlice * 128 * sizeof(float);  // one CTA's state in the scratch
 
-struct Plan {
-  int segs, cps, subs, cpb, slices;
-};
-
-// How many segments of time run side by side.  A role's CTAs (sequence, head, 64 columns) walk
-// their chunks one after another; with few of them the time axis is cut into segs runs whose
-// entering states a first pass over b and c computes (about half the work of a chunk, in
-// runs fine enough to fill the SMs).  The estimate counts chunk times of one CTA per SM, with about one
-// for a CTA's start and three for the second launch.  The first pass's states fit `capacity` bytes.
-Plan make_plan(const LaArgs& a, int C, int sms, size_t capacity) {
-  Plan p{1, 1, 0, 1, 1};
-  bool in_place = false;  // a segment could write the state before another has read it
-  for (int i = 0; i < a.roles; ++i) in_place = in_place || (a.role[i].x0 && a.role[i].x0 == a.role[i].x_end);
-  const int chunks = (a.T + C - 1) / C;
-  int e = 0;
-  for (int i = 0; i < a.roles; ++i) e = std::max(e, a.role[i].e);
-  p.slices = (e + kSlice - 1) / kSlice;
-  const long long ctas = (long long)a.B * a.H * p.slices * a.roles;
-  auto waves = [&](long long n) { return (double)((n + sms - 1) / sms); };
-  double best = waves(ctas) * (chunks + 1);
-  p.cps = chunks;
-  if (in_place) return p;
-  for (int want = 2; want <= 64 && want <= chunks; ++want)
-    for (int m = 1; m <= 4; ++m) {
-      const int cpb = (chunks + want * m - 1) / (want * m), cps = cpb * m;
-      const int segs = (chunks + cps - 1) / cps, subs = (segs - 1) * m;
-      if (segs < 2 || (size_t)ctas * subs * kStateBytes > capacity) continue;
-      const double cost = waves(ctas * segs) * (cps + 1) + waves(ctas * subs) * (0.5 * cpb + 1) + 3 +
-                          0.05 * subs;
-      if (cost < best) {
-        best = cost;
-        p = {segs, cps, subs, cpb, p.slices};
-      }
-    }
-  return p;
+LaPlan make_plan(const LaArgs& a, int C, size_t capacity) {
+  return la_plan(a, C, kSlice, seq_sm_count(), 0.5, kStateBytes, capacity);
 }
 
 int max_d(const LaArgs& a) {
@@ -887,7 +864,7 @@ int max_d(const LaArgs& a) {
 int chunk_of(int d) { return d > 64 ? Cfg<__half, 2, 2>::C : Cfg<__half, 1, 2>::C; }
 
 template <typename T, int DB, int PARTS>
-cudaError_t launch(const Maps& maps, TcArgs g, const Plan& p, int roles, cudaStream_t s) {
+cudaError_t launch(const Maps& maps, TcArgs g, const LaPlan& p, int roles, cudaStream_t s) {
   using K = Cfg<T, DB, PARTS>;
   constexpr int smem = (int)(K::oTab + sizeof(Tables));
   static_assert(smem <= 227 * 1024 && K::oTab % 16 == 0, "shared memory");
@@ -920,7 +897,7 @@ size_t la_tc_copy_bytes(const LaSeq& x, const LaArgs& a, int d) {
 }
 
 size_t la_tc_workspace(const LaArgs& a) {
-  const Plan p = make_plan(a, chunk_of(max_d(a)), seq_sm_count(), ~(size_t)0);
+  const LaPlan p = make_plan(a, chunk_of(max_d(a)), ~(size_t)0);
   return (size_t)a.roles * a.B * a.H * p.subs * p.slices * kStateBytes;
 }
 
@@ -989,7 +966,7 @@ cudaError_t launch_la_tc(const LaArgs& a, void* scratch, size_t bytes, cudaStrea
     t.s_add = r.s_add;
   }
   for (int i = n; i < 4; ++i) maps.m[i] = maps.m[0];
-  const Plan p = make_plan(a, C, seq_sm_count(), bytes - used);
+  const LaPlan p = make_plan(a, C, bytes - used);
   g.T = a.T;
   g.B = a.B;
   g.H = a.H;

@@ -146,22 +146,24 @@ size_t group_bytes(const prnn_linear_attention_t* a) {
   if (a->heads == a->qk_heads) return 0;
   return (sizeof(float) * (size_t)a->T * a->B * a->heads * a->dk + 15) / 16 * 16;
 }
-// Bytes of the tensor-core kernels' scratch, 0 where those cannot serve the call: any subset of the
-// backward pass's roles fits.
-size_t tc_bytes(const prnn_linear_attention_t* a, bool backward) {
-  if (a->dtype == PRNN_F32 || a->dk > 128 || a->dv > 128 || a->T == 0 || a->B == 0) return 0;
+// Bytes of the kernels' scratch for these sizes: any subset of the backward pass's roles fits.
+size_t mix_bytes(const prnn_linear_attention_t* a, bool backward) {
+  if (a->T == 0 || a->B == 0) return 0;
   LaArgs g{};
   g.dtype = a->dtype;
   g.T = a->T;
   g.B = a->B;
   g.H = a->heads;
-  size_t most = 0;
-  for (g.roles = 1; g.roles <= (backward ? 3 : 1); ++g.roles) {
-    LaRole& r = g.role[g.roles - 1];
+  for (LaRole& r : g.role) {
     r.d = backward ? std::max(a->dk, a->dv) : a->dk;
     r.e = backward ? std::max(a->dk, a->dv) : a->dv;
-    most = std::max(most, la_tc_workspace(g));
   }
+  g.roles = backward ? 3 : 1;
+  const bool tc = la_tc_serves(g);
+  size_t most = 0;
+  for (g.roles = 1; g.roles <= (backward ? 3 : 1); ++g.roles)
+    most = std::max(most, tc ? la_tc_workspace(g) : la_simt_workspace(g));
+  if (!tc) return most;
   const int share = a->heads / a->qk_heads;
   most += la_tc_copy_bytes(in(a->q, share), g, a->dk) + la_tc_copy_bytes(in(a->k, share), g, a->dk) +
           la_tc_copy_bytes(in(a->v, 1), g, a->dv);
@@ -170,7 +172,7 @@ size_t tc_bytes(const prnn_linear_attention_t* a, bool backward) {
 }
 cudaError_t launch_mix(const LaArgs& g, void* scratch, size_t bytes, cudaStream_t s) {
   if (la_tc_serves(g)) return launch_la_tc(g, scratch, bytes, s);
-  return launch_la_simt(g, s);
+  return launch_la_simt(g, scratch, bytes, s);
 }
 
 }  // namespace
@@ -304,7 +306,7 @@ prnn_status_t prnn_linear_attention_workspace(const prnn_linear_attention_t* a, 
   prnn_status_t why;
   if (!bytes) return PRNN_ERR_INVALID_ARG;
   if (!shape_ok(a, &why)) return why;
-  *bytes = (backward ? 2 * group_bytes(a) : 0) + tc_bytes(a, backward != 0);
+  *bytes = (backward ? 2 * group_bytes(a) : 0) + mix_bytes(a, backward != 0);
   return PRNN_OK;
 }
 
@@ -342,7 +344,7 @@ prnn_status_t prnn_linear_attention_forward(const prnn_linear_attention_t* a, vo
       !clear_of(a->log_decay, 4ull * H, part, 4, esz, false) ||
       (a->lens && !clear_of(a->lens, 4ull * B, part, 4, esz, false)))
     return PRNN_ERR_INVALID_ARG;
-  const size_t need = tc_bytes(a, false);
+  const size_t need = mix_bytes(a, false);
   if (need && (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < need ||
                !clear_of(a->workspace, need, part, 4, esz, true) ||
                (a->state && overlaps(a->state, state_bytes, a->workspace, need)) ||

@@ -95,7 +95,8 @@ struct LaArgs {
   const int32_t* lens;        // may be null
 };
 // On CUDA cores, for any sizes, strides and types.
-cudaError_t launch_la_simt(const LaArgs& a, cudaStream_t s);
+size_t la_simt_workspace(const LaArgs& a);
+cudaError_t launch_la_simt(const LaArgs& a, void* scratch, size_t bytes, cudaStream_t s);
 // On the tensor cores, for fp16 and bf16 with d, e <= 128: whether it serves a call; the bytes of scratch for
 // its segments' states and for a copy of an input that it cannot read in place (0: it can); the call.
 bool la_tc_serves(const LaArgs& a);
