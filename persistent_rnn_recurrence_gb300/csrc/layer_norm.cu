@@ -843,10 +843,9 @@ cudaError_t launch_layer_norm(const LayerNormArgs& a, cudaStream_t s) {
   // Through shared memory where that measured faster: rows that 16-byte accesses do not fit (8192 x 2001
   // bf16: 28 against 43 us; 20000 x 301 fp16: 16 against 21) and rows of more than 16 KB (8192 x 5760 fp32:
   // 71 against 78 us; at 8 KB, 8192 x 4096 bf16: 42 against 30), with two rows or more an SM.
-  const int sms = seq_sm_count();
-  if ((!vec || packs > 1024) && a.rows >= 2LL * sms && packs <= ring_max_packs(esz)) {
+  if ((!vec || packs > 1024) && packs <= ring_max_packs(esz) && a.rows >= 2LL * seq_sm_count()) {
     cudaError_t e = cudaSuccess;
-    PRNN_BY_DTYPE(a.dtype, T, (e = pick_ring<T>(a, vec, sms, s)));
+    PRNN_BY_DTYPE(a.dtype, T, (e = pick_ring<T>(a, vec, seq_sm_count(), s)));
     return e;
   }
   if (vec) {

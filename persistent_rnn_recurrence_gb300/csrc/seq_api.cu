@@ -2,6 +2,7 @@
 // division of workspaces, and the roles of linear attention's forward and
 // backward passes.  Contracts are in include/prnn.h.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -22,10 +23,13 @@ int* seq_status_word() {
 }
 
 int seq_sm_count() {
+  // a device's count never changes; kept because a short call would spend as long asking as launching
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
-    n = 1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

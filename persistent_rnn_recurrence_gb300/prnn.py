@@ -461,54 +461,61 @@ def prnn_linear_attention_step(a: bytes, state_pool, n_slots, slots=None, stream
 # ---- sequence operators on tensors -------------------------------------------------
 # Tensors in, tensors out, on the current stream.  `stream` (a torch stream) runs the call, and
 # allocates its outputs, on that stream instead; the caller orders it after the inputs' producers.
-_dtypes = {}
+# The kernels of a decoding step take a few microseconds, so these wrappers touch each tensor's
+# properties as little as the checks allow.
+_torch = None
+_codes = {}          # torch dtype -> prnn_dtype_t
+_raw_stream = None   # device index -> the current stream's handle
+
+
+def _load_torch():
+    global _torch, _raw_stream
+    import torch
+    _codes.update({torch.float32: PRNN_F32, torch.float16: PRNN_F16, torch.bfloat16: PRNN_BF16})
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda i: torch.cuda.current_stream(i).cuda_stream)
+    _torch = torch
 
 
 def _dtype(t) -> int:
-    if not _dtypes:
-        import torch
-        _dtypes.update({torch.float32: PRNN_F32, torch.float16: PRNN_F16,
-                        torch.bfloat16: PRNN_BF16})
-    try:
-        return _dtypes[t.dtype]
-    except KeyError:
-        raise ValueError(f"dtype {t.dtype}: float32, float16 or bfloat16 is needed") from None
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise ValueError(f"dtype {t.dtype}: float32, float16 or bfloat16 is needed")
+    return code
 
 
-def _like(t, ref, shape, what, dtype=None) -> None:
-    """t is on ref's device, has `dtype` (default ref's) and `shape`, last axis contiguous."""
-    if t.shape != shape or t.dtype != (dtype or ref.dtype) or t.device != ref.device:
-        raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype} on {t.device}, expected "
-                         f"{tuple(shape)} {dtype or ref.dtype} on {ref.device}")
-    if t.ndim and t.stride(-1) != 1 and t.shape[-1] > 1:
+def _start(t, what):
+    """t is a CUDA tensor of the current device; (its type's code, its device's index, the current
+    stream's handle)."""
+    if _torch is None:
+        _load_torch()
+    i = t.get_device()
+    if i < 0:
+        raise ValueError(f"{what}: a CUDA tensor is needed")
+    if i != _torch.cuda.current_device():
+        raise ValueError(f"{what}: on cuda:{i}, but the current device is "
+                         f"{_torch.cuda.current_device()}")
+    return _dtype(t), i, _raw_stream(i)
+
+
+def _like(t, shape, dtype, device, what) -> None:
+    """t has this shape, dtype and device index, and its last axis is contiguous."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype} on device {t.get_device()}, expected "
+                         f"{tuple(shape)} {dtype} on device {device}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{what}: the last axis must be contiguous")
 
 
-def _vector(t, ref, n, what, dtype=None):
-    """Address of a contiguous vector of n values (None: NULL)."""
+def _vector(t, n, dtype, device, what):
+    """Address of a contiguous vector of n values (None: 0)."""
     if t is None:
-        return None
-    import torch
-    _like(t, ref, (n,), what, dtype or torch.float32)
+        return 0
+    if t.shape != (n,) or t.dtype is not dtype or t.get_device() != device or \
+            (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype} on device {t.get_device()}, expected "
+                         f"{n} contiguous {dtype} on device {device}")
     return t.data_ptr()
-
-
-def _decays(t, ref, n, what):
-    """Address of log_decay [n] fp32, contiguous."""
-    if t is None:
-        raise ValueError(f"{what}: log_decay is needed")
-    return _vector(t, ref, n, what)
-
-
-def _device(t, what):
-    """t is a CUDA tensor of the current device; returns the current stream's handle."""
-    import torch
-    if not t.is_cuda:
-        raise ValueError(f"{what}: a CUDA tensor is needed")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what}: on {t.device}, but the current device is "
-                         f"{torch.cuda.current_device()}")
-    return torch.cuda.current_stream().cuda_stream
 
 
 def _rows(t, what):
@@ -537,76 +544,78 @@ def _rows(t, what):
 def layer_norm(x, gamma=None, beta=None, eps=1e-5, y=None, stream=None):
     """Layer norm over x's last axis (prnn_layer_norm_forward): (y, mean, rstd), the
     statistics fp32 with x's leading shape.  gamma, beta: fp32 [cols] or None.  y may be x."""
-    import torch
     if stream is not None:
+        import torch
         with torch.cuda.stream(stream):
             return layer_norm(x, gamma, beta, eps, y)
-    st = _device(x, "layer_norm: x")
-    dt = _dtype(x)
+    code, dev, st = _start(x, "layer_norm: x")
     rows, cols, xs = _rows(x, "layer_norm: x")
     if y is None:
-        y, ys = torch.empty(x.shape, dtype=x.dtype, device=x.device), cols
+        y, ys = _torch.empty_like(x, memory_format=_torch.contiguous_format), cols
     else:
-        _like(y, x, x.shape, "layer_norm: y")
+        _like(y, x.shape, x.dtype, dev, "layer_norm: y")
         ys = _rows(y, "layer_norm: y")[2]
-    stats = torch.empty((2,) + x.shape[:-1], dtype=torch.float32, device=x.device)
-    mean, rstd = stats.unbind(0)
-    p = stats.data_ptr()
-    _check(_lib.prnn_layer_norm_forward(dt, rows, cols, x.data_ptr(), xs,
-                                        _vector(gamma, x, cols, "layer_norm: gamma"),
-                                        _vector(beta, x, cols, "layer_norm: beta"), eps,
-                                        y.data_ptr(), ys, p, p + 4 * rows, st),
+    f32 = _torch.float32
+    lead, on = x.shape[:-1], x.device
+    mean, rstd = _torch.empty(lead, dtype=f32, device=on), _torch.empty(lead, dtype=f32, device=on)
+    _check(_lib.prnn_layer_norm_forward(code, rows, cols, x.data_ptr(), xs,
+                                        _vector(gamma, cols, f32, dev, "layer_norm: gamma"),
+                                        _vector(beta, cols, f32, dev, "layer_norm: beta"), eps,
+                                        y.data_ptr(), ys, mean.data_ptr(), rstd.data_ptr(), st),
            "prnn_layer_norm_forward")
     return y, mean, rstd
 
 
 def layer_norm_backward(dy, x, gamma, mean, rstd, stream=None):
     """Gradients of layer_norm: (dx, dgamma, dbeta), the last two fp32 [cols]."""
-    import torch
     if stream is not None:
+        import torch
         with torch.cuda.stream(stream):
             return layer_norm_backward(dy, x, gamma, mean, rstd)
-    st = _device(x, "layer_norm_backward: x")
-    dt = _dtype(x)
+    code, dev, st = _start(x, "layer_norm_backward: x")
     rows, cols, xs = _rows(x, "layer_norm_backward: x")
-    _like(dy, x, x.shape, "layer_norm_backward: dy")
+    _like(dy, x.shape, x.dtype, dev, "layer_norm_backward: dy")
     dys = _rows(dy, "layer_norm_backward: dy")[2]
+    f32 = _torch.float32
     for t, what in ((mean, "mean"), (rstd, "rstd")):
-        _like(t, x, x.shape[:-1], "layer_norm_backward: " + what, torch.float32)
-        if not t.is_contiguous():
-            raise ValueError(f"layer_norm_backward: {what} must be contiguous")
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if t.shape != x.shape[:-1] or t.dtype is not f32 or t.get_device() != dev or \
+                not t.is_contiguous():
+            raise ValueError(f"layer_norm_backward: {what} {tuple(t.shape)} {t.dtype}: expected "
+                             f"{tuple(x.shape[:-1])} contiguous {f32} on device {dev}")
+    dx = _torch.empty_like(x, memory_format=_torch.contiguous_format)
     need = prnn_layer_norm_workspace(rows, cols)
-    sums = torch.empty(2 * cols, dtype=torch.float32, device=x.device)
-    ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-    p = sums.data_ptr()
-    _check(_lib.prnn_layer_norm_backward(dt, rows, cols, dy.data_ptr(), dys, x.data_ptr(), xs,
-                                         _vector(gamma, x, cols, "layer_norm_backward: gamma"),
+    # dgamma, dbeta and, past them on the next 16 bytes, the workspace
+    dgamma, dbeta, ws = _torch.empty(2 * cols + 3 + (need + 3) // 4, dtype=f32,
+                                     device=x.device).split((cols, cols, 3 + (need + 3) // 4))
+    p = ws.data_ptr() + 15 & ~15
+    _check(_lib.prnn_layer_norm_backward(code, rows, cols, dy.data_ptr(), dys, x.data_ptr(), xs,
+                                         _vector(gamma, cols, f32, dev, "layer_norm_backward: gamma"),
                                          mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), cols,
-                                         p, p + 4 * cols, ws.data_ptr(), need, st),
+                                         dgamma.data_ptr(), dbeta.data_ptr(), p, need, st),
            "prnn_layer_norm_backward")
-    return dx, sums[:cols], sums[cols:]
+    return dx, dgamma, dbeta
 
 
 def dropout(x, p, seed, offset=0, residual=None, y=None, stream=None):
     """Dropout of x plus the residual (prnn_dropout_forward); contiguous tensors of one
     shape.  Give every use in a training step its own offset."""
-    import torch
     if stream is not None:
+        import torch
         with torch.cuda.stream(stream):
             return dropout(x, p, seed, offset, residual, y)
-    st = _device(x, "dropout: x")
-    dt = _dtype(x)
+    code, dev, st = _start(x, "dropout: x")
+    if not x.is_contiguous():
+        raise ValueError("dropout: x must be contiguous")
+    for t, what in ((residual, "residual"), (y, "y")):
+        if t is not None and t is not x:
+            if t.shape != x.shape or t.dtype is not x.dtype or t.get_device() != dev or \
+                    not t.is_contiguous():
+                raise ValueError(f"dropout: {what} {tuple(t.shape)} {t.dtype}: expected contiguous "
+                                 f"{tuple(x.shape)} {x.dtype} on device {dev}")
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    for t, what in ((x, "x"), (residual, "residual"), (y, "y")):
-        if t is None or t is x and what != "x":
-            continue
-        _like(t, x, x.shape, "dropout: " + what)
-        if not t.is_contiguous():
-            raise ValueError(f"dropout: {what} must be contiguous")
-    _check(_lib.prnn_dropout_forward(dt, x.numel(), x.data_ptr(),
-                                     None if residual is None else residual.data_ptr(),
+        y = _torch.empty_like(x)
+    _check(_lib.prnn_dropout_forward(code, x.numel(), x.data_ptr(),
+                                     0 if residual is None else residual.data_ptr(),
                                      y.data_ptr(), p, seed, offset, st), "prnn_dropout_forward")
     return y
 
@@ -620,10 +629,14 @@ def dropout_backward(dy, p, seed, offset=0, dx=None, stream=None):
 _NO_SEQ = (0, 0, 0, 0)
 
 
-def _seq4(t, ref, shape, what):
+def _seq4(t, shape, dtype, device, what):
     """(address, strides) of a [T, B, heads, d] tensor, for prnn_seq_t."""
-    _like(t, ref, shape, what)
-    st, sb, sh, _ = t.stride()
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype} on device {t.get_device()}, expected "
+                         f"{tuple(shape)} {dtype} on device {device}")
+    st, sb, sh, s1 = t.stride()
+    if s1 != 1 and shape[3] > 1:
+        raise ValueError(f"{what}: the last axis must be contiguous")
     return t.data_ptr(), st, sb, sh
 
 
@@ -631,18 +644,23 @@ def _attention_shape(q, v):
     if q.ndim != 4 or v.ndim != 4 or q.shape[:2] != v.shape[:2]:
         raise ValueError(f"q {tuple(q.shape)} and v {tuple(v.shape)}: expected [T, B, qk_heads, dk] "
                          "and [T, B, heads, dv]")
-    T, B, H, dv = v.shape
-    return T, B, H, q.shape[2], q.shape[3], dv
 
 
-def _state(t, ref, shape, what):
+def _state(t, shape, device, what):
+    """Address of a contiguous fp32 state (None: 0)."""
     if t is None:
         return 0
-    import torch
-    _like(t, ref, shape, what, torch.float32)
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
+    if t.shape != shape or t.dtype is not _torch.float32 or t.get_device() != device or \
+            not t.is_contiguous():
+        raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype}, expected contiguous {tuple(shape)} "
+                         f"float32 on device {device}")
     return t.data_ptr()
+
+
+def _decays(t, n, device, what):
+    if t is None:
+        raise ValueError(f"{what}: log_decay is needed")
+    return _vector(t, n, _torch.float32, device, what)
 
 
 def linear_attention(q, k, v, log_decay, scale=1.0, state=None, lens=None, o=None, stream=None):
@@ -651,39 +669,40 @@ def linear_attention(q, k, v, log_decay, scale=1.0, state=None, lens=None, o=Non
     with the last axis contiguous; log_decay fp32 [heads]; state fp32 [B, heads, dk, dv] or
     None (zeros); lens int32 [B] on the device or None.  Returns (o [T, B, heads, dv], the state
     after the last token)."""
-    import torch
     if stream is not None:
+        import torch
         with torch.cuda.stream(stream):
             return linear_attention(q, k, v, log_decay, scale, state, lens, o)
-    st = _device(q, "linear_attention: q")
-    T, B, H, Hq, dk, dv = _attention_shape(q, v)
+    what = "linear_attention: "
+    code, dev, st = _start(q, what + "q")
+    _attention_shape(q, v)
+    qs, vs, dt = q.shape, v.shape, q.dtype
+    T, B, H, dv = vs
+    Hq, dk = qs[2:]
     if o is None:
-        o = torch.empty((T, B, H, dv), dtype=v.dtype, device=q.device)
-    end = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
-    head = (_dtype(q), T, B, H, Hq, dk, dv, scale,
-            _decays(log_decay, q, H, "linear_attention: log_decay"),
-            _vector(lens, q, B, "linear_attention: lens", torch.int32) or 0,
-            *_seq4(q, q, q.shape, "linear_attention: q"),
-            *_seq4(k, q, q.shape, "linear_attention: k"),
-            *_seq4(v, q, v.shape, "linear_attention: v"),
-            _state(state, q, end.shape, "linear_attention: state"),
-            *_seq4(o, q, v.shape, "linear_attention: o"), end.data_ptr(),
+        o = _torch.empty(vs, dtype=dt, device=q.device)
+    end = _torch.empty((B, H, dk, dv), dtype=_torch.float32, device=q.device)
+    head = (code, T, B, H, Hq, dk, dv, scale, _decays(log_decay, H, dev, what + "log_decay"),
+            _vector(lens, B, _torch.int32, dev, what + "lens"),
+            *_seq4(q, qs, dt, dev, what + "q"), *_seq4(k, qs, dt, dev, what + "k"),
+            *_seq4(v, vs, dt, dev, what + "v"), _state(state, end.shape, dev, what + "state"),
+            *_seq4(o, vs, dt, dev, what + "o"), end.data_ptr(),
             *_NO_SEQ, 0, *_NO_SEQ, *_NO_SEQ, *_NO_SEQ, 0)
-    ws, need = _attention_workspace(head, 0, q.device)
-    _check(_lib.prnn_linear_attention_forward(
-        _LA_PACK(*head, 0 if ws is None else ws.data_ptr(), need), st),
-        "prnn_linear_attention_forward")
+    ws, p, need = _attention_workspace(head, 0, q)
+    _check(_lib.prnn_linear_attention_forward(_LA_PACK(*head, p, need), st),
+           "prnn_linear_attention_forward")
     return o, end
 
 
-def _attention_workspace(head, backward, device):
+def _attention_workspace(head, backward, q):
+    """(tensor, its address, its bytes); it must outlive the call."""
     n = ctypes.c_size_t()
     _check(_lib.prnn_linear_attention_workspace(_LA_PACK(*head, 0, 0), backward, ctypes.byref(n)),
            "prnn_linear_attention_workspace")
     if n.value == 0:
-        return None, 0
-    import torch
-    return torch.empty(n.value, dtype=torch.uint8, device=device), n.value
+        return None, 0, 0
+    ws = _torch.empty(n.value, dtype=_torch.uint8, device=q.device)
+    return ws, ws.data_ptr(), n.value
 
 
 def linear_attention_backward(do, q, k, v, log_decay, scale=1.0, state=None, lens=None,
@@ -691,31 +710,33 @@ def linear_attention_backward(do, q, k, v, log_decay, scale=1.0, state=None, len
     """Gradients of linear_attention for the loss whose gradient is `do` with respect to o and
     `dstate` (or None) with respect to the returned state: dict of dq, dk, dv and, when a state was
     given, dstate."""
-    import torch
     if stream is not None:
+        import torch
         with torch.cuda.stream(stream):
             return linear_attention_backward(do, q, k, v, log_decay, scale, state, lens, dstate)
-    st = _device(q, "linear_attention_backward: q")
-    T, B, H, Hq, dk, dv = _attention_shape(q, v)
-    shape = (B, H, dk, dv)
-    g = {"dq": torch.empty(q.shape, dtype=q.dtype, device=q.device),
-         "dk": torch.empty(q.shape, dtype=q.dtype, device=q.device),
-         "dv": torch.empty(v.shape, dtype=q.dtype, device=q.device)}
-    if state is not None:
-        g["dstate"] = torch.empty(shape, dtype=torch.float32, device=q.device)
     what = "linear_attention_backward: "
-    head = (_dtype(q), T, B, H, Hq, dk, dv, scale, _decays(log_decay, q, H, what + "log_decay"),
-            _vector(lens, q, B, what + "lens", torch.int32) or 0,
-            *_seq4(q, q, q.shape, what + "q"), *_seq4(k, q, q.shape, what + "k"),
-            *_seq4(v, q, v.shape, what + "v"), _state(state, q, shape, what + "state"),
-            *_NO_SEQ, 0, *_seq4(do, q, v.shape, what + "do"),
-            _state(dstate, q, shape, what + "dstate"), *_seq4(g["dq"], q, q.shape, "dq"),
-            *_seq4(g["dk"], q, q.shape, "dk"), *_seq4(g["dv"], q, v.shape, "dv"),
+    code, dev, st = _start(q, what + "q")
+    _attention_shape(q, v)
+    qs, vs, dt = q.shape, v.shape, q.dtype
+    T, B, H, dv = vs
+    Hq, dk = qs[2:]
+    shape = (B, H, dk, dv)
+    g = {"dq": _torch.empty(qs, dtype=dt, device=q.device),
+         "dk": _torch.empty(qs, dtype=dt, device=q.device),
+         "dv": _torch.empty(vs, dtype=dt, device=q.device)}
+    if state is not None:
+        g["dstate"] = _torch.empty(shape, dtype=_torch.float32, device=q.device)
+    head = (code, T, B, H, Hq, dk, dv, scale, _decays(log_decay, H, dev, what + "log_decay"),
+            _vector(lens, B, _torch.int32, dev, what + "lens"),
+            *_seq4(q, qs, dt, dev, what + "q"), *_seq4(k, qs, dt, dev, what + "k"),
+            *_seq4(v, vs, dt, dev, what + "v"), _state(state, shape, dev, what + "state"),
+            *_NO_SEQ, 0, *_seq4(do, vs, dt, dev, what + "do"),
+            _state(dstate, shape, dev, what + "dstate"), *_seq4(g["dq"], qs, dt, dev, "dq"),
+            *_seq4(g["dk"], qs, dt, dev, "dk"), *_seq4(g["dv"], vs, dt, dev, "dv"),
             g["dstate"].data_ptr() if state is not None else 0)
-    ws, need = _attention_workspace(head, 1, q.device)
-    _check(_lib.prnn_linear_attention_backward(
-        _LA_PACK(*head, 0 if ws is None else ws.data_ptr(), need), st),
-        "prnn_linear_attention_backward")
+    ws, p, need = _attention_workspace(head, 1, q)
+    _check(_lib.prnn_linear_attention_backward(_LA_PACK(*head, p, need), st),
+           "prnn_linear_attention_backward")
     return g
 
 
@@ -724,29 +745,33 @@ def linear_attention_step(q, k, v, log_decay, state, scale=1.0, slots=None, o=No
     v [B, heads, dv]; state fp32 [n, heads, dk, dv], updated in place: sequence b's is
     state[slots[b]] (int32 on the device; outside 0 .. n-1 marks a padding row), or state[b].
     Returns o [B, heads, dv]."""
-    import torch
     if stream is not None:
+        import torch
         with torch.cuda.stream(stream):
             return linear_attention_step(q, k, v, log_decay, state, scale, slots, o)
-    st = _device(q, "linear_attention_step: q")
+    what = "linear_attention_step: "
+    code, dev, st = _start(q, what + "q")
     if q.ndim != 3 or v.ndim != 3 or q.shape[0] != v.shape[0]:
         raise ValueError(f"q {tuple(q.shape)} and v {tuple(v.shape)}: expected [B, qk_heads, dk] and "
                          "[B, heads, dv]")
-    B, H, dv = v.shape
-    Hq, dk = q.shape[1:]
+    qs, vs, dt = q.shape, v.shape, q.dtype
+    B, H, dv = vs
+    Hq, dk = qs[1:]
     if o is None:
-        o = torch.empty((B, H, dv), dtype=q.dtype, device=q.device)
-    for t, shape, n in ((q, q.shape, "q"), (k, q.shape, "k"), (v, v.shape, "v"), (o, v.shape, "o")):
-        _like(t, q, shape, "linear_attention_step: " + n)
+        o = _torch.empty(vs, dtype=dt, device=q.device)
+    for t, shape, n in ((q, qs, "q"), (k, qs, "k"), (v, vs, "v"), (o, vs, "o")):
+        _like(t, shape, dt, dev, what + n)
     n_slots = state.shape[0]
-    pool = _state(state, q, (n_slots, H, dk, dv), "linear_attention_step: state")
-    a = _LA_PACK(_dtype(q), 1, B, H, Hq, dk, dv, scale,
-                 _decays(log_decay, q, H, "linear_attention_step: log_decay"), 0,
-                 q.data_ptr(), 0, *q.stride()[:2], k.data_ptr(), 0, *k.stride()[:2],
-                 v.data_ptr(), 0, *v.stride()[:2], 0, o.data_ptr(), 0, *o.stride()[:2], 0,
-                 *_NO_SEQ, 0, *_NO_SEQ, *_NO_SEQ, *_NO_SEQ, 0, 0, 0)
+    pool = _state(state, (n_slots, H, dk, dv), dev, what + "state")
+    qb, qh, _ = q.stride()
+    kb, kh, _ = k.stride()
+    vb, vh, _ = v.stride()
+    ob, oh, _ = o.stride()
+    a = _LA_PACK(code, 1, B, H, Hq, dk, dv, scale, _decays(log_decay, H, dev, what + "log_decay"), 0,
+                 q.data_ptr(), 0, qb, qh, k.data_ptr(), 0, kb, kh, v.data_ptr(), 0, vb, vh, 0,
+                 o.data_ptr(), 0, ob, oh, 0, *_NO_SEQ, 0, *_NO_SEQ, *_NO_SEQ, *_NO_SEQ, 0, 0, 0)
     _check(_lib.prnn_linear_attention_step(
-        a, pool, n_slots, _vector(slots, q, B, "linear_attention_step: slots", torch.int32), st),
+        a, pool, n_slots, _vector(slots, B, _torch.int32, dev, what + "slots"), st),
         "prnn_linear_attention_step")
     return o
 
