@@ -77,7 +77,7 @@ struct TcRole {
   int sa, sb, sc;     // heads sharing one
   void* out;
   long long ot, ob, oh;
-  int out_f32, out_vec, d, e;  // out_vec: rows start on 16 bytes and e is a multiple of 8
+  int form, d, e;     // how the output is stored (OutForm)
   const float* x0;
   float* x_end;
   int x_t, rev, lead;
@@ -227,41 +227,39 @@ __device__ __forceinline__ float group_max(float v, float* red, int w, int id) {
   return m;
 }
 
-// 32 columns of one row, of which the first m are the output's.
+// 32 columns of one row at p, of which the first m are the output's.
+enum OutForm { kOutPacked = 0, kOutF32 = 1, kOutSingle = 2 };  // kOutSingle: value by value (| kOutF32)
 template <typename T>
-__device__ __forceinline__ void store_out(const TcRole& r, long long at, int m,
-                                          const float2 (&v)[kHalfSlice / 2]) {
-  if (!r.out_vec) {
+__device__ __forceinline__ void store_out(char* p, int form, int m, const float2 (&v)[kHalfSlice / 2]) {
+  if (form == kOutPacked) {
+    uint4* to = reinterpret_cast<uint4*>(p);
+#pragma unroll
+    for (int q = 0; q < kHalfSlice / 8; ++q)
+      if (8 * q < m) {
+        float2 k[4] = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+        uint4 u;
+        u.x = take<T>(k[0]);
+        u.y = take<T>(k[1]);
+        u.z = take<T>(k[2]);
+        u.w = take<T>(k[3]);
+        to[q] = u;
+      }
+  } else if (form == kOutF32) {
+    float4* to = reinterpret_cast<float4*>(p);
+#pragma unroll
+    for (int q = 0; q < kHalfSlice / 4; ++q)
+      if (4 * q < m) to[q] = make_float4(v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y);
+  } else {
 #pragma unroll
     for (int j = 0; j < kHalfSlice; ++j)
       if (j < m) {
         const float f = j & 1 ? v[j / 2].y : v[j / 2].x;
-        if (r.out_f32)
-          static_cast<float*>(r.out)[at + j] = f;
+        if (form & kOutF32)
+          reinterpret_cast<float*>(p)[j] = f;
         else
-          static_cast<T*>(r.out)[at + j] = from_f32<T>(f);
+          reinterpret_cast<T*>(p)[j] = from_f32<T>(f);
       }
-    return;
   }
-  if (r.out_f32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(r.out) + at);
-#pragma unroll
-    for (int q = 0; q < kHalfSlice / 4; ++q)
-      if (4 * q < m) p[q] = make_float4(v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y);
-    return;
-  }
-  uint4* p = reinterpret_cast<uint4*>(static_cast<T*>(r.out) + at);
-#pragma unroll
-  for (int q = 0; q < kHalfSlice / 8; ++q)
-    if (8 * q < m) {
-      float2 k[4] = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-      uint4 u;
-      u.x = take<T>(k[0]);
-      u.y = take<T>(k[1]);
-      u.z = take<T>(k[2]);
-      u.w = take<T>(k[3]);
-      p[q] = u;
-    }
 }
 
 template <typename T, int DB, int PARTS>
@@ -299,6 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   const bool writes_end = !g.states_only && r.x_end && (nc > 0 ? to == chunks : (chunks == 0 && seg == 0));
 
+  const int osize = r.form & kOutF32 ? 4 : (int)sizeof(T);
   if (!g.states_only && r.out) {  // zeros past the length
     const int ncol = min(kSlice, r.e - e0);
     for (int c = max(seg * per, chunks); c < (seg + 1) * per && c * C < g.T; ++c) {
@@ -306,7 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float2 z[kHalfSlice / 2] = {};
       for (int i = tid; i < rows * 2; i += kThreads) {
         const int row = i / 2, q = i % 2 * kHalfSlice;
-        store_out<T>(r, (long long)(c * C + row) * r.ot + b * r.ob + h * r.oh + e0 + q, ncol - q, z);
+        store_out<T>(static_cast<char*>(r.out) + ((c * C + row) * r.ot + b * r.ob + h * r.oh + e0 + q) * osize,
+                     r.form, ncol - q, z);
       }
     }
   }
@@ -480,13 +480,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- scores to operands: row i of P, blocks of 16 columns half, half + 2, ... ----
     const int w = (warp - 4) & 3, half = (warp - 4) >> 2, i = w * 32 + lane;
     const uint32_t quad = (uint32_t)(w * 32) << 16;
+    const bool rev = r.rev;
     for (int c = 0; c < (with_out ? nc : 0); ++c) {
       warp_wait(&tab.p_full[c & 1], c >> 1);
       after_sync();
       const uint32_t at = tmem + quad + kColP + (c & 1) * 128;
       const int n = tokens_of(from + c);
       // columns [16 jb, 16 jb + 16) against this warp's rows [32 w, 32 w + 32)
-      auto nothing = [&](int jb) { return r.rev ? jb < 2 * w : jb > 2 * w + 1; };
+      auto nothing = [&](int jb) { return rev ? jb < 2 * w : jb > 2 * w + 1; };
       float2 scale = both(1.f);
       if constexpr (kHalf) {
         // the largest score of the blocks that count: the weights are at most 1
@@ -526,17 +527,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld16(at + 16 * jb, raw);
         const bool diagonal = (jb >> 1) == w;
         const float* dec = diagonal ? tab.diag[lane] + (jb & 1) * 16 : tab.dec;
-        const float2 f = both((diagonal ? 1.f : tab.pw[r.rev ? 16 * jb - i : i - 16 * jb - 15]) * scale.x);
+        const float2 f = both((diagonal ? 1.f : tab.pw[rev ? 16 * jb - i : i - 16 * jb - 15]) * scale.x);
         wait_ld();
         if (16 * jb + 16 > n)  // columns past the length, which may hold anything
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             if (16 * jb + j >= n) raw[j] = 0u;
         if (diagonal) {  // so may the masked ones
-          const int gap = r.rev ? i - 16 * jb : 16 * jb + 15 - i;  // in reverse the first `gap` columns, else the last
+          const int gap = rev ? i - 16 * jb : 16 * jb + 15 - i;  // in reverse the first `gap` columns, else the last
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            if ((r.rev ? j : 15 - j) < gap) raw[j] = 0u;
+            if ((rev ? j : 15 - j) < gap) raw[j] = 0u;
         }
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
@@ -622,11 +623,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       warp_arrive(&tab.x_ready);
     };
     if (enters && with_out && nc > 0) publish(0);
+    const float s_add = r.s_add;
     for (int c = 0; c < nc; ++c) {
+      const float2 f = both(tab.pw[tokens_of(from + c)]);
       warp_wait(&tab.u_full, c);
       after_sync();
-      const float2 f = both(tab.pw[tokens_of(from + c)]);
-      const float2 s = both(r.s_add * (kHalf ? tab.w_scale[c & 3] : 1.f));
+      const float2 s = both(s_add * (kHalf ? tab.w_scale[c & 3] : 1.f));
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         uint32_t u[16];
@@ -668,12 +670,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // of the slice ----
     const int w = warp - 20, half = w >> 2, i = (w & 3) * 32 + lane;
     const uint32_t from_tmem = tmem + ((uint32_t)((w & 3) * 32) << 16) + half * kHalfSlice;
-    const int col0 = e0 + half * kHalfSlice;
+    const int col0 = e0 + half * kHalfSlice, ncol = r.e - col0;
+    // what every chunk needs of the role, taken from the parameters once
+    const bool rev = r.rev;
+    const int form = r.form, lead = r.lead;
+    const float s_intra = r.s_intra, s_inter = r.s_inter;
+    const long long row_bytes = r.ot * osize;
+    char* const out = r.out ? static_cast<char*>(r.out) + (b * r.ob + h * r.oh + col0) * osize + i * row_bytes : nullptr;
     auto decayed = [&](int c) {
       const int n = tokens_of(from + c);
       warp_wait(&tab.c_full[c & 1], c >> 1);
       unsigned char* tile = smem + (c & 1) * K::kStage + 2 * DB * K::kBlock + i * 128;
-      const int gap = (r.rev ? i : n - 1 - i) + 1 - r.lead;
+      const int gap = (rev ? i : n - 1 - i) + 1 - lead;
       const float wj = i < n ? tab.pw[gap] : 0.f;
       uint32_t raw[4][4];
 #pragma unroll
@@ -741,8 +749,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (c > 0 || enters) {
         warp_wait(&tab.o2_full, enters ? c : c - 1);
         after_sync();
-        const int gap = (r.rev ? n - 1 - i : i) + r.lead;
-        const float2 fx = both(r.s_inter * tab.pw[gap < 0 ? 0 : gap] * (kHalf ? tab.x_scale[c & 1] : 1.f));
+        const int gap = (rev ? n - 1 - i : i) + lead;
+        const float2 fx = both(s_inter * tab.pw[gap < 0 ? 0 : gap] * (kHalf ? tab.x_scale[c & 1] : 1.f));
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t x[16], y[16];
@@ -759,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       warp_wait(&tab.o_full, c);
       after_sync();
-      const float2 fi = both(r.s_intra * (kHalf ? tab.row_scale[c & 3][i] : 1.f));
+      const float2 fi = both(s_intra * (kHalf ? tab.row_scale[c & 3][i] : 1.f));
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         uint32_t a[16];
@@ -775,10 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i >= n)
 #pragma unroll
         for (int j = 0; j < kHalfSlice / 2; ++j) v[j] = both(0.f);
-      if (i < C && t0 + i < g.T && r.out) {
-        const long long at = (long long)(t0 + i) * r.ot + b * r.ob + h * r.oh + col0;
-        store_out<T>(r, at, r.e - col0, v);
-      }
+      if (i < C && t0 + i < g.T && out) store_out<T>(out + t0 * row_bytes, form, ncol, v);
       __syncwarp();
     };
     if (nc > 0) decayed(0);
@@ -949,11 +954,11 @@ cudaError_t launch_la_tc(const LaArgs& a, void* scratch, size_t bytes, cudaStrea
     t.ot = r.ot;
     t.ob = r.ob;
     t.oh = r.oh;
-    t.out_f32 = r.out_f32;
     const int unit = r.out_f32 ? 4 : 8;
-    t.out_vec = r.e % 8 == 0 && (reinterpret_cast<uintptr_t>(r.out) & 15) == 0 &&
+    const bool packs = r.e % 8 == 0 && (reinterpret_cast<uintptr_t>(r.out) & 15) == 0 &&
                 (a.T == 1 || r.ot % unit == 0) && (a.B == 1 || r.ob % unit == 0) &&
                 (a.H == 1 || r.oh % unit == 0);
+    t.form = (packs ? 0 : kOutSingle) | (r.out_f32 ? kOutF32 : 0);
     t.d = r.d;
     t.e = r.e;
     t.x0 = r.x0;
