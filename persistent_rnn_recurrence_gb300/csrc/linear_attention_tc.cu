@@ -318,6 +318,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) atomicExch(g.status, 1);
     return;
   }
+  if (tid == 32) {
+    for (int i : {r.ia, r.ib, r.ic})
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.m[i])) : "memory");
+  }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tab.ab_full[i], 1);
