@@ -49,6 +49,9 @@ __device__ __forceinline__ float4 load4(const T* p, int at, int n, bool vec) {
   }
   return make_float4(v[0], v[1], v[2], v[3]);
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
 // One block: one role, one (sequence, head), kCols of the e columns and one segment of time.  The state
@@ -178,6 +181,15 @@ __global__ void __launch_bounds__(kThreads, D <= 64 ? 3 : (D <= 128 ? 2 : 1))
         *reinterpret_cast<float4*>(Cs + j * kWide + c) = v;
       }
     }
+    if (ci + 1 < to) {  // the next chunk on its way to L2 while this one is computed
+      const int u0 = (r.rev ? chunks - 2 - ci : ci + 1) * kChunk, row = min(u0 + tid % kChunk, g.T - 1);
+      const int at = tid / kChunk * (128 / (int)sizeof(T));  // a 128-byte line of the row per warp
+      for (int k = at; k < d; k += 4 * (128 / (int)sizeof(T))) {
+        if (with_out) prefetch_l2(seq_row<T>(r.a, row, b, h) + k);
+        prefetch_l2(seq_row<T>(r.b, row, b, h) + k);
+      }
+      if (at < ncol) prefetch_l2(seq_row<T>(r.c, row, b, h) + e0 + at);
+    }
     __syncthreads();
     if (with_out) {
       // scores, weighted and masked
@@ -206,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, D <= 64 ? 3 : (D <= 128 ? 2 : 1))
       __syncthreads();
       float o[4][4] = {};
       auto product = [&](const float* x, int xstride, const float* y, int count) {
-#pragma unroll 4
+#pragma unroll 8
         for (int k = 0; k < count; ++k) {
           const float4 u = ld4(x + k * xstride + r0), v = ld4(y + k * kWide + oc);
           const float us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
