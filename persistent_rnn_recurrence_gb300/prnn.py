@@ -96,6 +96,7 @@ class prnn_linear_attention_t(ctypes.Structure):
 # The same layout for struct.pack, which fills it in one call (a decoding step
 # is short enough for the difference to show).
 _LA_PACK = struct.Struct("=7if40q").pack
+_STEP_PACK = struct.Struct("=7if19q168x").pack   # up to o; the step uses no field behind it
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -541,6 +542,18 @@ def _rows(t, what):
     return rows, cols, cols if stride is None else stride
 
 
+_sizes = {}          # workspace bytes by what they depend on: sizes, layouts, device
+
+
+def _norm_workspace(rows, cols):
+    need = _sizes.get((rows, cols))
+    if need is None:
+        if len(_sizes) > 4096:
+            _sizes.clear()
+        need = _sizes[rows, cols] = prnn_layer_norm_workspace(rows, cols)
+    return need
+
+
 def layer_norm(x, gamma=None, beta=None, eps=1e-5, y=None, stream=None):
     """Layer norm over x's last axis (prnn_layer_norm_forward): (y, mean, rstd), the
     statistics fp32 with x's leading shape.  gamma, beta: fp32 [cols] or None.  y may be x."""
@@ -576,22 +589,21 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, stream=None):
     rows, cols, xs = _rows(x, "layer_norm_backward: x")
     _like(dy, x.shape, x.dtype, dev, "layer_norm_backward: dy")
     dys = _rows(dy, "layer_norm_backward: dy")[2]
-    f32 = _torch.float32
+    f32, lead = _torch.float32, x.shape[:-1]
     for t, what in ((mean, "mean"), (rstd, "rstd")):
-        if t.shape != x.shape[:-1] or t.dtype is not f32 or t.get_device() != dev or \
+        if t.shape != lead or t.dtype is not f32 or t.get_device() != dev or \
                 not t.is_contiguous():
             raise ValueError(f"layer_norm_backward: {what} {tuple(t.shape)} {t.dtype}: expected "
-                             f"{tuple(x.shape[:-1])} contiguous {f32} on device {dev}")
+                             f"{tuple(lead)} contiguous {f32} on device {dev}")
     dx = _torch.empty_like(x, memory_format=_torch.contiguous_format)
-    need = prnn_layer_norm_workspace(rows, cols)
-    # dgamma, dbeta and, past them on the next 16 bytes, the workspace
-    dgamma, dbeta, ws = _torch.empty(2 * cols + 3 + (need + 3) // 4, dtype=f32,
-                                     device=x.device).split((cols, cols, 3 + (need + 3) // 4))
-    p = ws.data_ptr() + 15 & ~15
+    need = _norm_workspace(rows, cols)
+    on = x.device
+    dgamma, dbeta = _torch.empty(cols, dtype=f32, device=on), _torch.empty(cols, dtype=f32, device=on)
+    ws = _torch.empty(need, dtype=_torch.uint8, device=on)
     _check(_lib.prnn_layer_norm_backward(code, rows, cols, dy.data_ptr(), dys, x.data_ptr(), xs,
                                          _vector(gamma, cols, f32, dev, "layer_norm_backward: gamma"),
                                          mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), cols,
-                                         dgamma.data_ptr(), dbeta.data_ptr(), p, need, st),
+                                         dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), need, st),
            "prnn_layer_norm_backward")
     return dx, dgamma, dbeta
 
@@ -679,30 +691,46 @@ def linear_attention(q, k, v, log_decay, scale=1.0, state=None, lens=None, o=Non
     qs, vs, dt = q.shape, v.shape, q.dtype
     T, B, H, dv = vs
     Hq, dk = qs[2:]
+    on, shape = q.device, (B, H, dk, dv)
     if o is None:
-        o = _torch.empty(vs, dtype=dt, device=q.device)
-    end = _torch.empty((B, H, dk, dv), dtype=_torch.float32, device=q.device)
+        o = _torch.empty(vs, dtype=dt, device=on)
+        o4 = (o.data_ptr(), B * H * dv, H * dv, dv)
+    else:
+        o4 = _seq4(o, vs, dt, dev, what + "o")
+    end = _torch.empty(shape, dtype=_torch.float32, device=on)
     head = (code, T, B, H, Hq, dk, dv, scale, _decays(log_decay, H, dev, what + "log_decay"),
             _vector(lens, B, _torch.int32, dev, what + "lens"),
             *_seq4(q, qs, dt, dev, what + "q"), *_seq4(k, qs, dt, dev, what + "k"),
-            *_seq4(v, vs, dt, dev, what + "v"), _state(state, end.shape, dev, what + "state"),
-            *_seq4(o, vs, dt, dev, what + "o"), end.data_ptr(),
+            *_seq4(v, vs, dt, dev, what + "v"), _state(state, shape, dev, what + "state"),
+            *o4, end.data_ptr(),
             *_NO_SEQ, 0, *_NO_SEQ, *_NO_SEQ, *_NO_SEQ, 0)
-    ws, p, need = _attention_workspace(head, 0, q)
+    ws, p, need = _attention_workspace(head, 0, dev, on)
     _check(_lib.prnn_linear_attention_forward(_LA_PACK(*head, p, need), st),
            "prnn_linear_attention_forward")
     return o, end
 
 
-def _attention_workspace(head, backward, q):
-    """(tensor, its address, its bytes); it must outlive the call."""
-    n = ctypes.c_size_t()
-    _check(_lib.prnn_linear_attention_workspace(_LA_PACK(*head, 0, 0), backward, ctypes.byref(n)),
-           "prnn_linear_attention_workspace")
-    if n.value == 0:
+def _attention_workspace(head, backward, dev, on):
+    """(tensor, its address, its bytes); it must outlive the call.  The size depends on the sizes,
+    the strides and the alignment of the inputs, not on where they are."""
+    key = (dev, backward, *head[:7], *head[11:14], *head[15:18], *head[19:22], *head[29:32],
+           (head[10] | head[14] | head[18] | head[28]) & 15)
+    need = _sizes.get(key)
+    if need is None:
+        if len(_sizes) > 4096:
+            _sizes.clear()
+        n = ctypes.c_size_t()
+        _check(_lib.prnn_linear_attention_workspace(_LA_PACK(*head, 0, 0), backward,
+                                                    ctypes.byref(n)),
+               "prnn_linear_attention_workspace")
+        need = n.value
+        # with an input off 16 bytes the size says nothing of the others' alignment
+        if key[-1] == 0:
+            _sizes[key] = need
+    if need == 0:
         return None, 0, 0
-    ws = _torch.empty(n.value, dtype=_torch.uint8, device=q.device)
-    return ws, ws.data_ptr(), n.value
+    ws = _torch.empty(need, dtype=_torch.uint8, device=on)
+    return ws, ws.data_ptr(), need
 
 
 def linear_attention_backward(do, q, k, v, log_decay, scale=1.0, state=None, lens=None,
@@ -720,24 +748,35 @@ def linear_attention_backward(do, q, k, v, log_decay, scale=1.0, state=None, len
     qs, vs, dt = q.shape, v.shape, q.dtype
     T, B, H, dv = vs
     Hq, dk = qs[2:]
-    shape = (B, H, dk, dv)
-    g = {"dq": _torch.empty(qs, dtype=dt, device=q.device),
-         "dk": _torch.empty(qs, dtype=dt, device=q.device),
-         "dv": _torch.empty(vs, dtype=dt, device=q.device)}
+    on, shape = q.device, (B, H, dk, dv)
+    dq, dkk = (_torch.empty(qs, dtype=dt, device=on) for _ in range(2))
+    dvv = _torch.empty(vs, dtype=dt, device=on)
+    g = {"dq": dq, "dk": dkk, "dv": dvv}
     if state is not None:
-        g["dstate"] = _torch.empty(shape, dtype=_torch.float32, device=q.device)
+        g["dstate"] = _torch.empty(shape, dtype=_torch.float32, device=on)
+    qd = (B * Hq * dk, Hq * dk, dk)
     head = (code, T, B, H, Hq, dk, dv, scale, _decays(log_decay, H, dev, what + "log_decay"),
             _vector(lens, B, _torch.int32, dev, what + "lens"),
             *_seq4(q, qs, dt, dev, what + "q"), *_seq4(k, qs, dt, dev, what + "k"),
             *_seq4(v, vs, dt, dev, what + "v"), _state(state, shape, dev, what + "state"),
             *_NO_SEQ, 0, *_seq4(do, vs, dt, dev, what + "do"),
-            _state(dstate, shape, dev, what + "dstate"), *_seq4(g["dq"], qs, dt, dev, "dq"),
-            *_seq4(g["dk"], qs, dt, dev, "dk"), *_seq4(g["dv"], vs, dt, dev, "dv"),
+            _state(dstate, shape, dev, what + "dstate"), dq.data_ptr(), *qd, dkk.data_ptr(), *qd,
+            dvv.data_ptr(), B * H * dv, H * dv, dv,
             g["dstate"].data_ptr() if state is not None else 0)
-    ws, p, need = _attention_workspace(head, 1, q)
+    ws, p, need = _attention_workspace(head, 1, dev, on)
     _check(_lib.prnn_linear_attention_backward(_LA_PACK(*head, p, need), st),
            "prnn_linear_attention_backward")
     return g
+
+
+def _step_strides(t, shape, dtype, device, what):
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype} on device {t.get_device()}, expected "
+                         f"{tuple(shape)} {dtype} on device {device}")
+    b, h, last = t.stride()
+    if last != 1 and shape[2] > 1:
+        raise ValueError(f"{what}: the last axis must be contiguous")
+    return b, h
 
 
 def linear_attention_step(q, k, v, log_decay, state, scale=1.0, slots=None, o=None, stream=None):
@@ -757,19 +796,20 @@ def linear_attention_step(q, k, v, log_decay, state, scale=1.0, slots=None, o=No
     qs, vs, dt = q.shape, v.shape, q.dtype
     B, H, dv = vs
     Hq, dk = qs[1:]
+    qb, qh, q1 = q.stride()
+    if q1 != 1 and dk > 1:
+        raise ValueError(what + "q: the last axis must be contiguous")
+    kb, kh = _step_strides(k, qs, dt, dev, what + "k")
+    vb, vh = _step_strides(v, vs, dt, dev, what + "v")
     if o is None:
-        o = _torch.empty(vs, dtype=dt, device=q.device)
-    for t, shape, n in ((q, qs, "q"), (k, qs, "k"), (v, vs, "v"), (o, vs, "o")):
-        _like(t, shape, dt, dev, what + n)
+        o, ob, oh = _torch.empty(vs, dtype=dt, device=q.device), H * dv, dv
+    else:
+        ob, oh = _step_strides(o, vs, dt, dev, what + "o")
     n_slots = state.shape[0]
     pool = _state(state, (n_slots, H, dk, dv), dev, what + "state")
-    qb, qh, _ = q.stride()
-    kb, kh, _ = k.stride()
-    vb, vh, _ = v.stride()
-    ob, oh, _ = o.stride()
-    a = _LA_PACK(code, 1, B, H, Hq, dk, dv, scale, _decays(log_decay, H, dev, what + "log_decay"), 0,
-                 q.data_ptr(), 0, qb, qh, k.data_ptr(), 0, kb, kh, v.data_ptr(), 0, vb, vh, 0,
-                 o.data_ptr(), 0, ob, oh, 0, *_NO_SEQ, 0, *_NO_SEQ, *_NO_SEQ, *_NO_SEQ, 0, 0, 0)
+    a = _STEP_PACK(code, 1, B, H, Hq, dk, dv, scale,
+                   _decays(log_decay, H, dev, what + "log_decay"), 0, q.data_ptr(), 0, qb, qh,
+                   k.data_ptr(), 0, kb, kh, v.data_ptr(), 0, vb, vh, 0, o.data_ptr(), 0, ob, oh)
     _check(_lib.prnn_linear_attention_step(
         a, pool, n_slots, _vector(slots, B, _torch.int32, dev, what + "slots"), st),
         "prnn_linear_attention_step")
