@@ -681,7 +681,7 @@ typedef struct {
   prnn_dtype_t dtype;         /* of q, k, v, o and their gradients                               */
   int T, B;                   /* steps, sequences                                                */
   int heads, qk_heads;        /* heads % qk_heads == 0                                           */
-  int dk, dv;                 /* 1 .. 256 each                                                   */
+  int dk, dv;                 /* 1 .. 256 each; T <= 2^29, B * heads <= 2^24                     */
   float scale;
   const float* log_decay;     /* [heads] fp32, device; <= 0; a constant of the layer (no gradient) */
   const int32_t* lens;        /* [B] device: length of each sequence, clamped to 0 .. T;

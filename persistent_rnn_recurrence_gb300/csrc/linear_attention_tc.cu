@@ -262,6 +262,11 @@ __device__ __forceinline__ void store_out(char* p, int form, int m, const float2
   }
 }
 
+// The state's rows start on 16 bytes and are not transposed.
+__device__ __forceinline__ bool rows_of_4(const TcRole& r, const float* p) {
+  return !r.x_t && r.e % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+}
+
 template <typename T, int DB, int PARTS>
 __global__ void __launch_bounds__(kThreads, 1)
     la_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g) {
@@ -318,14 +323,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) atomicExch(g.status, 1);
     return;
   }
-  if (tid == 32) {
-    for (int i : {r.ia, r.ib, r.ic})
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.m[i])) : "memory");
-  }
-  if (tid == 0) {
+  // The loads of one chunk: b and a (scores, state), then c.
+  const int db = (r.d + 63) / 64;
+  auto load_b = [&](int c) {
+    const int s = c & 1, t0 = chunk_of(from + c) * C;
+    const uint32_t at = base + s * K::kStage + DB * K::kBlock;
+    mbar_arrive_expect_tx(&tab.ab_full[s], (with_out ? 2 : 1) * db * K::kBlock);
+    for (int k = 0; k < db; ++k)
+      tma_load(at + k * K::kBlock, &maps.m[r.ib], &tab.ab_full[s], k * 64, h / r.sb, b, t0);
+  };
+  auto load_a = [&](int c) {
+    const int s = c & 1, t0 = chunk_of(from + c) * C;
+    for (int k = 0; k < db; ++k)
+      tma_load(base + s * K::kStage + k * K::kBlock, &maps.m[r.ia], &tab.ab_full[s], k * 64, h / r.sa, b, t0);
+  };
+  auto load_c = [&](int c) {
+    const int s = c & 1, t0 = chunk_of(from + c) * C;
+    mbar_arrive_expect_tx(&tab.c_full[s], K::kBlock);
+    tma_load(base + s * K::kStage + 2 * DB * K::kBlock, &maps.m[r.ic], &tab.c_full[s], e0, h / r.sc, b, t0);
+  };
+  // The first two chunks are requested before anything else is set up.
+  if (warp == 0 && elected()) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tab.ab_full[i], 1);
       mbar_init(&tab.c_full[i], 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    for (int c = 0; c < min(nc, 2); ++c) {
+      load_b(c);
+      if (with_out) load_a(c);
+      load_c(c);
+    }
+  }
+  if (tid == 32) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&tab.a_free[i], 2);
       mbar_init(&tab.b_free[i], with_out ? 2 : 1);
       mbar_init(&tab.c_free[i], 1);
@@ -343,13 +374,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&tab.done, 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 0) {
+  if (warp == 3) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&tab.tmem)),
                  "r"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  __syncwarp();
   if (tid < 132) tab.pw[tid] = decay_pow(ld, tid);
   else if (tid < 148) tab.dec[tid - 132] = decay_pow(ld, r.rev ? tid - 132 : 147 - tid);
   for (int i = warp; i < 32; i += kThreads / 32) {
@@ -375,22 +407,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (elected()) {
       // ---- loads: each tile as soon as the products that read the one before it have ended ----
-      const int db = (r.d + 63) / 64;
-      for (int c = 0; c < nc; ++c) {
-        const int s = c & 1, t0 = chunk_of(from + c) * C, turn = (c >> 1) - 1;
-        const uint32_t at = base + s * K::kStage;
-        if (c >= 2) wait(&tab.b_free[s], turn);
-        mbar_arrive_expect_tx(&tab.ab_full[s], (with_out ? 2 : 1) * db * K::kBlock);
-        for (int k = 0; k < db; ++k)
-          tma_load(at + (DB + k) * K::kBlock, &maps.m[r.ib], &tab.ab_full[s], k * 64, h / r.sb, b, t0);
+      for (int c = 2; c < nc; ++c) {
+        const int s = c & 1, turn = (c >> 1) - 1;
+        wait(&tab.b_free[s], turn);
+        load_b(c);
         if (with_out) {
-          if (c >= 2) wait(&tab.a_free[s], turn);
-          for (int k = 0; k < db; ++k)
-            tma_load(at + k * K::kBlock, &maps.m[r.ia], &tab.ab_full[s], k * 64, h / r.sa, b, t0);
+          wait(&tab.a_free[s], turn);
+          load_a(c);
         }
-        if (c >= 2) wait(&tab.c_free[s], turn);
-        mbar_arrive_expect_tx(&tab.c_full[s], K::kBlock);
-        tma_load(at + 2 * DB * K::kBlock, &maps.m[r.ic], &tab.c_full[s], e0, h / r.sc, b, t0);
+        wait(&tab.c_free[s], turn);
+        load_c(c);
       }
       for (int c = max(0, nc - 2); c < nc; ++c) {  // every load lands before the CTA leaves
         const uint64_t limit = deadline + kSeqWaitNs;
@@ -575,10 +601,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float f = decay_pow(ld, done_before);
       const float* p = r.x0 + head + (r.x_t ? (size_t)col0 * r.d + row : (size_t)row * r.e + col0);
       const int step = r.x_t ? r.d : 1;
+      if (rows_of_4(r, r.x0) && ncol == kHalfSlice) {
 #pragma unroll
-      for (int j = 0; j < kHalfSlice / 2; ++j) {
-        if (2 * j < ncol) X[j].x = f * p[2 * j * step];
-        if (2 * j + 1 < ncol) X[j].y = f * p[(2 * j + 1) * step];
+        for (int j = 0; j < kHalfSlice / 4; ++j) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(p) + j);
+          X[2 * j] = make_float2(f * v.x, f * v.y);
+          X[2 * j + 1] = make_float2(f * v.z, f * v.w);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kHalfSlice / 2; ++j) {
+          if (2 * j < ncol) X[j].x = f * p[2 * j * step];
+          if (2 * j + 1 < ncol) X[j].y = f * p[(2 * j + 1) * step];
+        }
       }
     }
     float* part = g.part + ((((size_t)blockIdx.y * g.B * g.H + bh) * g.subs * g.slices + slice) * kSlice +
@@ -594,7 +629,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           X[j] = fma2(make_float2(__ldcg(p + 2 * j * 128), __ldcg(p + (2 * j + 1) * 128)), f, X[j]);
       }
     }
-    const int db = (r.d + 63) / 64;
     unsigned char* tile = smem + K::oX + row * 128;
     auto publish = [&](int turn) {  // X as parts in shared memory, for the chunk of this turn
       float2 scale = both(1.f);
@@ -656,10 +690,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (writes_end && row < r.d) {
       float* p = r.x_end + head + (r.x_t ? (size_t)col0 * r.d + row : (size_t)row * r.e + col0);
       const int step = r.x_t ? r.d : 1;
+      if (rows_of_4(r, r.x_end) && ncol == kHalfSlice) {
 #pragma unroll
-      for (int j = 0; j < kHalfSlice / 2; ++j) {
-        if (2 * j < ncol) p[2 * j * step] = X[j].x;
-        if (2 * j + 1 < ncol) p[(2 * j + 1) * step] = X[j].y;
+        for (int j = 0; j < kHalfSlice / 4; ++j)
+          reinterpret_cast<float4*>(p)[j] = make_float4(X[2 * j].x, X[2 * j].y, X[2 * j + 1].x, X[2 * j + 1].y);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kHalfSlice / 2; ++j) {
+          if (2 * j < ncol) p[2 * j * step] = X[j].x;
+          if (2 * j + 1 < ncol) p[(2 * j + 1) * step] = X[j].y;
+        }
       }
     }
     if (g.states_only) {
@@ -718,7 +758,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (with_out) warp_wait(&tab.p_full[c & 1], c >> 1);
         else warp_wait(&tab.ab_full[c & 1], c >> 1);
         if (i >= n && i < C && half == 0) {
-          const int db = (r.d + 63) / 64;
           const uint4 z = make_uint4(0, 0, 0, 0);
           for (int q = 0; q < 8; ++q) {
             *reinterpret_cast<uint4*>(tile + (q << 4)) = z;
@@ -799,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!ok) atomicExch(g.status, 1);
   before_sync();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 3) {
     after_sync();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
                  : "memory");

@@ -107,7 +107,7 @@ bool shape_ok(const prnn_linear_attention_t* a, prnn_status_t* why) {
   if (!a || !known(a->dtype) || a->T < 0 || a->B < 0 || a->heads < 1 || a->qk_heads < 1 ||
       a->heads % a->qk_heads != 0 || a->dk < 1 || a->dv < 1 || !std::isfinite(a->scale))
     return false;
-  if (a->dk > 256 || a->dv > 256 || (long long)a->B * a->heads > (1 << 24)) {
+  if (a->dk > 256 || a->dv > 256 || a->T > (1 << 29) || (long long)a->B * a->heads > (1 << 24)) {
     *why = PRNN_ERR_UNSUPPORTED;
     return false;
   }
