@@ -778,6 +778,8 @@ cudaError_t pick_grad(const LayerNormGradArgs& a, bool vec, int sms, int* blocks
   if (packs <= 64) return run_grad<T, 2, 32, 2>(a, vec, sms, blocks, s);
   if (packs <= 128) return run_grad<T, 1, 128, 2>(a, vec, sms, blocks, s);
   if (packs <= 256) return run_grad<T, 2, 128, 2>(a, vec, sms, blocks, s);
+  // four groups a block where their ring of fp32 rows still fits twice: 32768 x 1152 82 us against 96
+  if (packs <= 512 && sizeof(T) == 4) return run_grad<T, 4, 128, 1>(a, vec, sms, blocks, s);
   if (packs <= 512) return run_grad<T, 2, 256, 2>(a, vec, sms, blocks, s);
   if (packs <= 1024) return run_grad<T, 2, 512, 2>(a, vec, sms, blocks, s);
   if constexpr (sizeof(T) == 4)

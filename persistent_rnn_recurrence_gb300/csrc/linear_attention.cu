@@ -16,7 +16,7 @@
 namespace prnn {
 namespace {
 
-constexpr int kChunk = 32, kCols = 64, kThreads = 128, kStride = kChunk + 4, kWide = kCols + 4;
+constexpr int kChunk = 32, kCols = 64, kGroup = 128, kThreads = 2 * kGroup, kStride = kChunk + 4, kWide = kCols + 4;
 
 struct SimtArgs {
   LaArgs g;
@@ -54,8 +54,9 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
 }
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
-// One block: one role, one (sequence, head), kCols of the e columns and one segment of time.  The state
-// stays in registers (thread (rg, cg): rows rg + 16 m, columns 4 cg .. and 32 + 4 cg ..) and is copied to
+// One block: one role, one (sequence, head), kCols of the e columns and one segment of time.  Both need
+// only the chunk's tiles and the state before it, so half of the warps make the output while the other half
+// update the state.  The state stays in registers (thread (rg, cg): rows rg + 16 m, columns 4 cg .. and 32 + 4 cg ..) and is copied to
 // shared memory once a chunk as an operand.  a and b are kept with the tokens innermost (a lane per token
 // as they are loaded, so no bank conflicts), which serves the scores, the product with the state
 // and the state's update: each product is a tile of 4 x 4 (scores 4 x 2, state 8 x 8) values
@@ -66,7 +67,9 @@ __global__ void __launch_bounds__(kThreads, D <= 64 ? 3 : (D <= 128 ? 2 : 1))
   constexpr int M = D / 16;
   const LaArgs& g = args.g;
   const LaRole& r = g.role[blockIdx.y];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const bool keeps_state = tid >= kGroup;       // the second group of warps; the first makes the output
+  const int warp = (tid % kGroup) >> 5;         // within its group
   const int runs = args.states_only ? args.subs : args.segs;
   const int slice = blockIdx.x % args.slices, seg = blockIdx.x / args.slices % runs;
   const int bh = blockIdx.x / args.slices / runs, b = bh / g.H, h = bh % g.H;
@@ -104,22 +107,22 @@ __global__ void __launch_bounds__(kThreads, D <= 64 ? 3 : (D <= 128 ? 2 : 1))
   if (tid <= kChunk) pw[tid] = decay_pow(ld, tid);
 
   const int rg = warp * 4 + (lane >> 3), cg = lane & 7;  // the state's tile
-  float X[M][8];
+  float X[M][8] = {};
   const size_t head = (size_t)bh * d * r.e;
   const int done = before(from);
   const float f0 = decay_pow(ld, done);
+  if (keeps_state && r.x0 && !args.states_only)
 #pragma unroll
   for (int m = 0; m < M; ++m)
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       const int k = rg + 16 * m, col = (c & 4) * 8 + 4 * cg + (c & 3);
-      X[m][c] = 0.f;
-      if (r.x0 && !args.states_only && k < d && col < ncol)
+      if (k < d && col < ncol)
         X[m][c] = f0 * r.x0[head + (r.x_t ? (size_t)(e0 + col) * d + k : (size_t)k * r.e + e0 + col)];
     }
   float* part = args.part + ((((size_t)blockIdx.y * g.B * g.H + bh) * args.subs) * args.slices + slice) * D * kCols;
   const size_t sub_size = (size_t)args.slices * D * kCols;
-  if (!args.states_only) {
+  if (keeps_state && !args.states_only) {
     const int subs = min(seg * (args.cps / args.cpb), (chunks + args.cpb - 1) / args.cpb);
     for (int u = 0; u < subs; ++u) {
       const float f = decay_pow(ld, done - before((u + 1) * args.cpb));
@@ -145,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, D <= 64 ? 3 : (D <= 128 ? 2 : 1))
   for (int ci = from; ci < to; ++ci) {
     const int t0 = (r.rev ? chunks - 1 - ci : ci) * kChunk, n = min(kChunk, len - t0);
     __syncthreads();
-    if (with_out)
+    if (with_out && keeps_state)
 #pragma unroll
       for (int m = 0; m < M; ++m)
 #pragma unroll
@@ -155,8 +158,8 @@ __global__ void __launch_bounds__(kThreads, D <= 64 ? 3 : (D <= 128 ? 2 : 1))
     {
       const T* pa = seq_row<T>(r.a, t0 + lane, b, h);
       const T* pb = seq_row<T>(r.b, t0 + lane, b, h);
-#pragma unroll 4
-      for (int k = 4 * warp; k < D; k += 16) {
+#pragma unroll 2
+      for (int k = 4 * (tid >> 5); k < D; k += kThreads / 8) {
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
         if (lane < n && k < d) {
           if (with_out) x = load4(pa, k, d, va);
@@ -184,14 +187,14 @@ __global__ void __launch_bounds__(kThreads, D <= 64 ? 3 : (D <= 128 ? 2 : 1))
     if (ci + 1 < to) {  // the next chunk on its way to L2 while this one is computed
       const int u0 = (r.rev ? chunks - 2 - ci : ci + 1) * kChunk, row = min(u0 + tid % kChunk, g.T - 1);
       const int at = tid / kChunk * (128 / (int)sizeof(T));  // a 128-byte line of the row per warp
-      for (int k = at; k < d; k += 4 * (128 / (int)sizeof(T))) {
+      for (int k = at; k < d; k += kThreads / kChunk * (128 / (int)sizeof(T))) {
         if (with_out) prefetch_l2(seq_row<T>(r.a, row, b, h) + k);
         prefetch_l2(seq_row<T>(r.b, row, b, h) + k);
       }
       if (at < ncol) prefetch_l2(seq_row<T>(r.c, row, b, h) + e0 + at);
     }
     __syncthreads();
-    if (with_out) {
+    if (with_out && !keeps_state) {
       // scores, weighted and masked
       float p[4][2] = {};
 #pragma unroll 8
@@ -215,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, D <= 64 ? 3 : (D <= 128 ? 2 : 1))
         }
         *reinterpret_cast<float4*>(Pt + (pc + j) * kStride + r0) = make_float4(w[0], w[1], w[2], w[3]);
       }
-      __syncthreads();
+      asm volatile("bar.sync 1, %0;" ::"n"(kGroup) : "memory");
       float o[4][4] = {};
       auto product = [&](const float* x, int xstride, const float* y, int count) {
 #pragma unroll 8
@@ -250,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, D <= 64 ? 3 : (D <= 128 ? 2 : 1))
           }
       }
     }
+    if (!keeps_state) continue;
     // X <- l^n X + s_add sum_j w_j b_j c_j
     const float fn = pw[n];
 #pragma unroll
@@ -280,6 +284,7 @@ __global__ void __launch_bounds__(kThreads, D <= 64 ? 3 : (D <= 128 ? 2 : 1))
       }
     }
   }
+  if (!keeps_state) return;
   if (writes_end)
 #pragma unroll
     for (int m = 0; m < M; ++m)
