@@ -56,7 +56,7 @@ __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast
 
 // One block: one role, one (sequence, head), kCols of the e columns and one segment of time.  Both need
 // only the chunk's tiles and the state before it, so half of the warps make the output while the other half
-// update the state.  The state stays in registers (thread (rg, cg): rows rg + 16 m, columns 4 cg .. and 32 + 4 cg ..) and is copied to
+// make the scores, which the output needs last, and update the state.  The state stays in registers (thread (rg, cg): rows rg + 16 m, columns 4 cg .. and 32 + 4 cg ..) and is copied to
 // shared memory once a chunk as an operand.  a and b are kept with the tokens innermost (a lane per token
 // as they are loaded, so no bank conflicts), which serves the scores, the product with the state
 // and the state's update: each product is a tile of 4 x 4 (scores 4 x 2, state 8 x 8) values
@@ -195,6 +195,43 @@ __global__ void __launch_bounds__(kThreads, D <= 64 ? 3 : (D <= 128 ? 2 : 1))
     }
     __syncthreads();
     if (with_out && !keeps_state) {
+      float o[4][4] = {};
+      auto product = [&](const float* x, int xstride, const float* y, int count) {
+#pragma unroll 8
+        for (int k = 0; k < count; ++k) {
+          const float4 u = ld4(x + k * xstride + r0), v = ld4(y + k * kWide + oc);
+          const float us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][j] = fmaf(us[i], vs[j], o[i][j]);
+        }
+      };
+      product(At, kStride, Xs, d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = r0 + i, gap = (r.rev ? n - 1 - row : row) + r.lead;
+        const float f = r.s_inter * pw[gap < 0 ? 0 : (gap > kChunk ? kChunk : gap)];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][j] *= f;
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");  // the scores are there
+      product(Pt, kStride, Cs, kChunk);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (t0 + r0 + i >= g.T) break;
+        const long long at = (long long)(t0 + r0 + i) * r.ot + b * r.ob + h * r.oh + e0 + oc;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (oc + j < ncol) {  // rows past the length: 0
+            const float v = r0 + i < n ? o[i][j] : 0.f;
+            if (r.out_f32) static_cast<float*>(r.out)[at + j] = v;
+            else static_cast<T*>(r.out)[at + j] = from_f32<T>(v);
+          }
+      }
+    }
+    if (!keeps_state) continue;
+    if (with_out) {
       // scores, weighted and masked
       float p[4][2] = {};
 #pragma unroll 8
@@ -218,42 +255,8 @@ __global__ void __launch_bounds__(kThreads, D <= 64 ? 3 : (D <= 128 ? 2 : 1))
         }
         *reinterpret_cast<float4*>(Pt + (pc + j) * kStride + r0) = make_float4(w[0], w[1], w[2], w[3]);
       }
-      asm volatile("bar.sync 1, %0;" ::"n"(kGroup) : "memory");
-      float o[4][4] = {};
-      auto product = [&](const float* x, int xstride, const float* y, int count) {
-#pragma unroll 8
-        for (int k = 0; k < count; ++k) {
-          const float4 u = ld4(x + k * xstride + r0), v = ld4(y + k * kWide + oc);
-          const float us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[i][j] = fmaf(us[i], vs[j], o[i][j]);
-        }
-      };
-      product(At, kStride, Xs, d);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = r0 + i, gap = (r.rev ? n - 1 - row : row) + r.lead;
-        const float f = r.s_inter * pw[gap < 0 ? 0 : (gap > kChunk ? kChunk : gap)];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][j] *= f;
-      }
-      product(Pt, kStride, Cs, kChunk);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (t0 + r0 + i >= g.T) break;
-        const long long at = (long long)(t0 + r0 + i) * r.ot + b * r.ob + h * r.oh + e0 + oc;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (oc + j < ncol) {  // rows past the length: 0
-            const float v = r0 + i < n ? o[i][j] : 0.f;
-            if (r.out_f32) static_cast<float*>(r.out)[at + j] = v;
-            else static_cast<T*>(r.out)[at + j] = from_f32<T>(v);
-          }
-      }
+      asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
     }
-    if (!keeps_state) continue;
     // X <- l^n X + s_add sum_j w_j b_j c_j
     const float fn = pw[n];
 #pragma unroll
