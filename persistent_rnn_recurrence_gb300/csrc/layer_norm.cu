@@ -481,7 +481,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
   }
 }
 
-// The forward pass of many rows: a row's values stay in registers between the two sums and the output.
+// The forward pass of many rows of any alignment: a row's values stay in registers between the two sums and
+// the output.
 template <typename T, int NV, int TPR, int R, bool VEC>
 __global__ void __launch_bounds__(kRingThreads, 1)
     layer_norm_ring_kernel(const __grid_constant__ LayerNormArgs a,
@@ -708,27 +709,44 @@ bool vec_ok(const void* p, long long stride, size_t esz) {
 }
 
 template <typename T, int V, int NV, int TPR>
-void run(const LayerNormArgs& a, cudaStream_t s) {
+bool run(const LayerNormArgs& a, cudaStream_t s) {
   const long long blocks = (a.rows + kRows<TPR> - 1) / kRows<TPR>;
   layer_norm_kernel<T, V, NV, TPR><<<(unsigned)blocks, TPR * kRows<TPR>, 0, s>>>(a);
+  return true;
 }
 
-// Threads per row: the fewest that hold the row in NV packs each.  A warp per row needs no
-// barrier; rows of more than 4 packs a lane get 128, 256, 512 or 1024 threads.
+// Packs per thread and threads per row.  The fewest threads that hold the row at up to 40 values each: a
+// warp per row needs no barrier (32768 x 1152 fp32: 47 us against 54 with 128 threads, 70 with 256),
+// and more values cost the occupancy that hides the loads (8192 x 4096 bf16: 30 us at 32 values, 39 at
+// 64, 47 at 128).
 template <typename T, int V>
 bool pick(const LayerNormArgs& a, cudaStream_t s) {
   const int packs = (a.cols + V - 1) / V;
-  if (packs <= 32) run<T, V, 1, 32>(a, s);
-  else if (packs <= 64) run<T, V, 2, 32>(a, s);
-  else if (packs <= 128) run<T, V, 4, 32>(a, s);
-  else if (packs <= 256) run<T, V, 2, 128>(a, s);
-  else if (packs <= 512) run<T, V, 4, 128>(a, s);
-  else if (packs <= 1024) run<T, V, 4, 256>(a, s);
-  else if (packs <= 2048) run<T, V, 4, 512>(a, s);
-  else if (packs <= 4096) run<T, V, 4, 1024>(a, s);
-  else if (V == 1 && packs <= 8192) run<T, V, V == 1 ? 8 : 4, 1024>(a, s);
-  else return false;
-  return true;
+  if (packs <= 32) return run<T, V, 1, 32>(a, s);
+  if (packs <= 64) return run<T, V, 2, 32>(a, s);
+  if (packs <= 128) return run<T, V, 4, 32>(a, s);
+  if constexpr (V == 8) {
+    if (packs <= 160) return run<T, V, 5, 32>(a, s);
+    if (packs <= 256) return run<T, V, 4, 64>(a, s);
+    if (packs <= 512) return run<T, V, 4, 128>(a, s);
+    if (packs <= 1024) return run<T, V, 4, 256>(a, s);
+    if (packs <= 2048) return run<T, V, 4, 512>(a, s);
+    if (packs <= 4096) return run<T, V, 4, 1024>(a, s);
+  } else if constexpr (V == 4) {
+    if (packs <= 192) return run<T, V, 6, 32>(a, s);
+    if (packs <= 320) return run<T, V, 10, 32>(a, s);
+    if (packs <= 512) return run<T, V, 8, 64>(a, s);
+    if (packs <= 1024) return run<T, V, 8, 128>(a, s);
+    if (packs <= 2048) return run<T, V, 8, 256>(a, s);
+    if (packs <= 4096) return run<T, V, 4, 1024>(a, s);
+  } else {
+    if (packs <= 256) return run<T, V, 8, 32>(a, s);
+    if (packs <= 512) return run<T, V, 16, 32>(a, s);
+    if (packs <= 1024) return run<T, V, 16, 64>(a, s);
+    if (packs <= 2048) return run<T, V, 16, 128>(a, s);
+    if (packs <= 8192) return run<T, V, 16, 512>(a, s);
+  }
+  return false;
 }
 
 // ---- plans of the ring kernels ------------------------------------------------------------
@@ -842,10 +860,10 @@ cudaError_t launch_layer_norm(const LayerNormArgs& a, cudaStream_t s) {
                    vec_ok(a.beta, 0, 4);
   bool done = false;
   const long long packs = ((long long)a.cols * (long long)esz + 15) / 16;
-  // Through shared memory where that measured faster: rows that 16-byte accesses do not fit (8192 x 2001
-  // bf16: 28 against 43 us; 20000 x 301 fp16: 16 against 21) and rows of more than 16 KB (8192 x 5760 fp32:
-  // 71 against 78 us; at 8 KB, 8192 x 4096 bf16: 42 against 30), with two rows or more an SM.
-  if ((!vec || packs > 1024) && packs <= ring_max_packs(esz) && a.rows >= 2LL * seq_sm_count()) {
+  // Through shared memory where 16-byte accesses do not fit the rows and there are two rows or more an SM:
+  // 8192 x 2001 bf16 28 us against 64, 20000 x 301 fp16 16 against 24; 300 x 2001 bf16 5.8 either way.  Rows
+  // that they fit are faster from registers: 8192 x 5760 fp32 57 against 71.
+  if (!vec && packs <= ring_max_packs(esz) && a.rows >= 2LL * seq_sm_count()) {
     cudaError_t e = cudaSuccess;
     PRNN_BY_DTYPE(a.dtype, T, (e = pick_ring<T>(a, vec, seq_sm_count(), s)));
     return e;
