@@ -670,7 +670,9 @@ prnn_status_t prnn_dropout_backward(prnn_dtype_t dtype, long long n, const void*
  * A tensor of a sequence holds element (t, b, h, d) at t*stride_t + b*stride_b + h*stride_h + d
  * (elements), so that time-major and packed layouts, and slices of a joint projection, are read in
  * place.  q and k have qk_heads heads, v and o `heads` (a multiple of qk_heads): head h uses query
- * and key head h / (heads / qk_heads).
+ * and key head h / (heads / qk_heads).  Tokens are worked on in chunks of up to 128: an infinity or
+ * NaN in a token within the length may also reach, as NaN, the outputs and gradients of its own
+ * sequence up to 127 tokens away; tokens past the length reach nothing, whatever they hold.
  */
 typedef struct {
   void* data;                                /* dtype; outputs are written, inputs only read */

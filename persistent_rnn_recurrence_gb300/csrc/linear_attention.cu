@@ -1,6 +1,6 @@
 // linear_attention.cu -- linear attention with a decay per head over whole
-// sequences: the `mix` operation of seq_internal.h in all its roles, for any
-// sizes, strides and types.
+// sequences: the `mix` operation of seq_internal.h in all its roles, on CUDA cores,
+// for any sizes, strides and types (fp32, and heads wider than 128).
 //
 // Unrolling S_t = l S_{t-1} + b_t c_t^T over a chunk of n tokens entered with
 // state X gives
@@ -9,6 +9,13 @@
 // so a chunk is four small matrix products and only the chunks are serial.
 // Every exponent is >= 0: no power of the decay can overflow, whatever the
 // decay, which factoring l^(i-j) into l^i l^-j would not give.
+//
+// Bound by the fp32 units in the limit (32-token chunks: 22 K multiply-adds per token and head at 128 x
+// 128); what holds it at 0.24 of them is the latency of shared memory and loads at 16 warps an SM,
+// which is what its tiles leave room for.  fp32 is kept to fp32 products: the tensor cores would need
+// every operand in three 16-bit parts and six products.  Measured on GB300: T = 2048, 4 sequences of 16
+// heads of 128 x 128 fp32 620 us (a plain one-column-slice kernel: 2984), T = 700, 5 sequences, 72 x
+// 100 106 us (505).
 #include "linear_attention_plan.h"
 #include "seq_common.cuh"
 #include "seq_internal.h"
@@ -55,12 +62,13 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
 // One block: one role, one (sequence, head), kCols of the e columns and one segment of time.  Both need
-// only the chunk's tiles and the state before it, so half of the warps make the output while the other half
-// make the scores, which the output needs last, and update the state.  The state stays in registers (thread (rg, cg): rows rg + 16 m, columns 4 cg .. and 32 + 4 cg ..) and is copied to
-// shared memory once a chunk as an operand.  a and b are kept with the tokens innermost (a lane per token
-// as they are loaded, so no bank conflicts), which serves the scores, the product with the state
-// and the state's update: each product is a tile of 4 x 4 (scores 4 x 2, state 8 x 8) values
-// per thread fed by 16-byte reads, 16 to 64 multiply-adds for two to four of them.
+// only the chunk's tiles and the state before it, so half of the warps make the output while the other
+// half make the scores, which the output needs last, and update the state.  The state stays in
+// registers (thread (rg, cg): rows rg + 16 m, columns 4 cg .. and 32 + 4 cg ..) and is copied to shared
+// memory once a chunk as an operand.  a and b are kept with the tokens innermost (a lane per token as
+// they are loaded, so no bank conflicts), which serves the scores, the product with the state and the
+// state's update: each product is a tile of 4 x 4 (scores 4 x 2, state 8 x 8) values per thread fed by
+// 16-byte reads, 16 to 64 multiply-adds for two to four of them.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, D <= 64 ? 3 : (D <= 128 ? 2 : 1))
     la_simt_kernel(const __grid_constant__ SimtArgs args) {

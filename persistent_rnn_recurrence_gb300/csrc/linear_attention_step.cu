@@ -1,8 +1,9 @@
 // linear_attention_step.cu -- one token of linear attention with a decay per
 // head: S <- l S + k v^T, o = scale S^T q, the fp32 state in place.
 //
-// Bound by memory: the state is read and written once, 8 dk dv bytes per head
-// against 5 dk dv flops.
+// Bound by memory: the state is read and written once, 8 dk dv bytes per head against 5 dk dv flops.
+// Measured on GB300: 96 sequences of 16 heads of 128 x 128 36.6 us (0.82 of the copy rate of 6.69
+// TB/s), 16 of them 10.5, one of 8 heads of 64 x 64 2.5 (a launch).
 #include "seq_common.cuh"
 #include "seq_internal.h"
 

@@ -13,20 +13,27 @@
 // exponent >= 0 (D in blocks of 16 columns: l^(i-j) = l^(i-j0-15) l^(15-(j-j0))), so no decay
 // overflows.
 //
-// Rounding.  The products take 16-bit operands.  The data enters as it is; what is computed in
-// between enters as a sum of parts of the data's type: P and X in two (bf16: 16 bits; their error
-// stays far below the output's one rounding), w C in two for fp16 (22 bits), and for bf16 in three
-// (24 bits) where the fp32 state is an output and two where it only feeds 16-bit ones.  All products accumulate in fp32.  For fp16, whose range
-// would not hold them, P is scaled by a power of two per row and X and w C per tile, taken back after the
-// product.
+// Rounding.  The products take 16-bit operands.  The data enters as it is; what is computed in between
+// enters as a sum of parts of the data's type: P and X in two (bf16: 16 bits; their error stays far
+// below the output's one rounding), w C in two for fp16 (22 bits), and for bf16 in three (24 bits)
+// where the fp32 state is an output and two where it only feeds 16-bit ones.  All products accumulate
+// in fp32.  For fp16, whose range would not hold them, P is scaled by a power of two per row and X and
+// w C per tile, taken back after the product.
 //
-// Warps: 0 loads (TMA), 1 and 2 issue the matrix products, 4-11 turn scores into operands (a row per thread,
-// every other block of 16 columns), 12-19 own the state (a row of X and half the columns), 20-27 make
-// w C and write the output (a row and half the columns).  The tensor cores run U(c), O2(c), P(c+1) and
-// O1(c) while the state is updated, the next chunk's w C made, its scores weighted and the last output
-// written; each tile of chunk c + 2 is requested as the last product that reads chunk c's ends.
-// What bounds a chunk is shared memory, from which the products read their operands: the two parts of X
-// stand side by side in one product (N = 128), which reads Q once.
+// Warps: 0 loads (TMA), 1 and 2 issue the matrix products, 4-11 turn scores into operands (a row per
+// thread, every other block of 16 columns), 12-19 own the state (a row of X and half the columns),
+// 20-27 make w C and write the output (a row and half the columns).  The tensor cores run U(c), O2(c),
+// P(c+1) and O1(c) while the state is updated, the next chunk's w C made, its scores weighted and the
+// last output written; each tile of chunk c + 2 is requested as the last product that reads chunk c's
+// ends. The two parts of X stand side by side in one product (N = 128), which reads Q once.
+//
+// What bounds it: memory would take 40 us for T = 8192, 2 sequences of 16 heads of 128 x 128 bf16, and the
+// kernel takes 130.  A chunk of 112 tokens costs a CTA about 4600 cycles: the products read 280 KB of
+// operands from shared memory, TMA and the warps move 190 KB more (3600 cycles at 128 bytes each), and the
+// chain w C -> U -> X -> O2 with its barriers is about as long.  C = 112 is what two chunks in flight
+// leave room for at 128 x 128; 96 took 136 us, 80 with three chunks in flight 152.  Other figures, us:
+// T = 2048, 4 sequences 54; at 64 x 64 39; T = 256, 32 sequences 97; gradients of T = 2048, 4 sequences 134.
+// The CUDA-core kernel of the first version took 10353 for the first of these.
 #include <cuda.h>
 
 #include <algorithm>
