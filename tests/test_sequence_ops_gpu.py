@@ -619,3 +619,47 @@ def test_captured_in_a_graph(env):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_linear_attention_state_in_place(env, dtype):
+    """state_out may be `state` itself: with few sequences and a long prompt, where time would
+    otherwise be cut over blocks, the result is that of separate arrays."""
+    torch, prnn = env
+    dt = types(torch)[dtype][0]
+    x = make(torch, 2000, 1, 2, 2, 64, 64, dt, 1700, state=True)
+    o, end = prnn.linear_attention(x["q"], x["k"], x["v"], x["ld"], x["scale"], x["state"])
+    place, o2 = x["state"].clone(), torch.empty_like(o)
+    a = prnn.prnn_linear_attention_t(dtype={"f32": 0, "bf16": 2}[dtype], T=2000, B=1, heads=2, qk_heads=2,
+                                     dk=64, dv=64, scale=x["scale"], log_decay=x["ld"].data_ptr(),
+                                     state=place.data_ptr(), state_out=place.data_ptr())
+    for n, t in (("q", x["q"]), ("k", x["k"]), ("v", x["v"]), ("o", o2)):
+        setattr(a, n, prnn.prnn_seq_t(t.data_ptr(), *t.stride()[:3]))
+    ws = torch.empty(prnn.prnn_linear_attention_workspace(bytes(a), False), dtype=torch.uint8, device="cuda")
+    a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
+    prnn.prnn_linear_attention_forward(bytes(a))
+    M, Mend = attention_reference(torch, **absolute(x))
+    tol, tol32 = attention_tolerance(dtype, 2000, 64)
+    u = types(torch)[dtype][1]
+    within(o2, o.double(), 2 * u * o.double().abs() + 2 * tol * M, "o")
+    within(place, end.double(), 2 * tol32 * Mend, "state")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_linear_attention_all_sequences_empty(env, dtype):
+    torch, prnn = env
+    dt = types(torch)[dtype][0]
+    x = make(torch, 300, 3, 2, 1, 64, 40, dt, 1800, state=True, lens=[0, 0, -3])
+    for n in ("q", "k", "v"):
+        x[n].fill_(float("nan"))
+    o, end = prnn.linear_attention(x["q"], x["k"], x["v"], x["ld"], x["scale"], x["state"], x["lens"])
+    assert bool((o == 0).all()) and torch.equal(end, x["state"])
+    g = prnn.linear_attention_backward(x["v"], x["q"], x["k"], x["v"], x["ld"], x["scale"], x["state"],
+                                       x["lens"], x["state"])
+    assert all(bool((g[n] == 0).all()) for n in ("dq", "dk", "dv")) and torch.equal(g["dstate"], x["state"])
+
+
+def test_no_wait_has_run_out(env):
+    """Every call of this file is behind it: none of the kernels' bounded waits gave up."""
+    torch, prnn = env
+    assert prnn.prnn_sequence_status() == prnn.PRNN_OK

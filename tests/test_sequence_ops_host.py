@@ -70,6 +70,7 @@ def test_layer_norm_refusals(prnn):
                dict(gamma=BASE + 4096 + 16), dict(mean=BASE + 8192, rstd=BASE + 8192 + 8),
                dict(rows=2 ** 62, xs=2 ** 40)):
         assert fwd(**kw) == E, kw
+    assert fwd(rows=2 ** 33 + 1, y=BASE + 2 ** 40) == prnn.PRNN_ERR_UNSUPPORTED
 
     n = ctypes.c_size_t()
     assert prnn._lib.prnn_layer_norm_workspace(4, 8, ctypes.byref(n)) == prnn.PRNN_OK
@@ -137,7 +138,7 @@ def test_linear_attention_refusals(prnn):
                             {"state": BASE + (32 << 20), "state_out": BASE + (32 << 20) + 64},
                             {"lens": BASE + (4 << 20)}]:
         assert f(_attention(prnn, **kw), None) == E, kw
-    for kw in ({"dk": 257}, {"dv": 257}, {"B": 1 << 24}):
+    for kw in ({"dk": 257}, {"dv": 257}, {"B": 1 << 24}, {"T": (1 << 29) + 1}):
         assert f(_attention(prnn, **kw), None) == U, kw
     assert f(_attention(prnn, B=0), None) == prnn.PRNN_OK
     assert f(_attention(prnn, T=0), None) == prnn.PRNN_OK     # no state wanted: nothing to do
