@@ -619,7 +619,7 @@ prnn_status_t prnn_sequence_status(void* stream);
  * x and y hold row r at r*x_stride and r*y_stride (elements, >= cols); y may be
  * x itself (same stride).  gamma and beta [cols] fp32, each NULL for none (1 and 0).
  * mean and rstd [rows] fp32 receive the statistics for the backward pass; both may be
- * NULL.  1 <= cols; rows <= 2^33, 0 is a no-op; eps >= 0.
+ * NULL.  1 <= cols; rows == 0 is a no-op; eps >= 0.
  */
 prnn_status_t prnn_layer_norm_forward(prnn_dtype_t dtype, long long rows, int cols, const void* x,
                                       long long x_stride, const float* gamma, const float* beta,

@@ -208,7 +208,6 @@ prnn_status_t prnn_layer_norm_forward(prnn_dtype_t dtype, long long rows, int co
   const long long nx = row_extent(rows, cols, rows > 1 ? x_stride : cols);
   const long long ny = row_extent(rows, cols, rows > 1 ? y_stride : cols);
   if (nx < 0 || ny < 0) return PRNN_ERR_INVALID_ARG;
-  if (rows > 1LL << 33) return PRNN_ERR_UNSUPPORTED;  // 8 narrow rows a block in at most 2^30 blocks
   const bool in_place = x == y && (rows == 1 || x_stride == y_stride);
   if (!in_place && overlaps(x, nx * esz, y, ny * esz)) return PRNN_ERR_INVALID_ARG;
   struct { const void* p; size_t n; } par[2] = {{gamma, 4ull * cols}, {beta, 4ull * cols}},
