@@ -720,16 +720,27 @@ bool run(const LayerNormArgs& a, cudaStream_t s) {
   return true;
 }
 
-// Packs per thread and threads per row.  The fewest threads that hold the row at up to 40 values each: a
-// warp per row needs no barrier (32768 x 1152 fp32: 47 us against 54 with 128 threads, 70 with 256),
-// and more values cost the occupancy that hides the loads (8192 x 4096 bf16: 30 us at 32 values, 39 at
-// 64, 47 at 128).
+// Packs per thread and threads per row.  With fewer than two rows an SM there is room for all rows at
+// once, and many threads a row are fastest (4 x 1792 fp32 2.4 us against 3.7 with the plans below, 300 x
+// 1152 2.6 against 4.4; 600 rows of 512 bf16 values take 2.5 either way, 1200 of them 3.9 against
+// 2.5).  Else the fewest threads that hold the row at up to 40 values each: a warp per row needs no
+// barrier (32768 x 1152 fp32: 47 us against 54 with 128 threads, 70 with 256), and more values cost the
+// occupancy that hides the loads (8192 x 4096 bf16: 30 us at 32 values, 39 at 64, 47 at 128).
 template <typename T, int V>
 bool pick(const LayerNormArgs& a, cudaStream_t s) {
   const int packs = (a.cols + V - 1) / V;
   if (packs <= 32) return run<T, V, 1, 32>(a, s);
-  if (packs <= 64) return run<T, V, 2, 32>(a, s);
-  if (packs <= 128) return run<T, V, 4, 32>(a, s);
+  if (a.rows < 2LL * seq_sm_count()) {
+    if (packs <= 256) return run<T, V, 1, 256>(a, s);
+    if (packs <= 512) return run<T, V, 2, 256>(a, s);
+    if (packs <= 1024) return run<T, V, 4, 256>(a, s);
+    if (packs <= 2048) return run<T, V, 4, 512>(a, s);
+    if (packs <= 4096) return run<T, V, 4, 1024>(a, s);
+  }
+  if constexpr (V > 1) {
+    if (packs <= 64) return run<T, V, 2, 32>(a, s);
+    if (packs <= 128) return run<T, V, 4, 32>(a, s);
+  }
   if constexpr (V == 8) {
     if (packs <= 160) return run<T, V, 5, 32>(a, s);
     if (packs <= 256) return run<T, V, 4, 64>(a, s);
@@ -744,11 +755,7 @@ bool pick(const LayerNormArgs& a, cudaStream_t s) {
     if (packs <= 1024) return run<T, V, 8, 128>(a, s);
     if (packs <= 2048) return run<T, V, 8, 256>(a, s);
     if (packs <= 4096) return run<T, V, 4, 1024>(a, s);
-  } else {
-    if (packs <= 256) return run<T, V, 8, 32>(a, s);
-    if (packs <= 512) return run<T, V, 16, 32>(a, s);
-    if (packs <= 1024) return run<T, V, 16, 64>(a, s);
-    if (packs <= 2048) return run<T, V, 16, 128>(a, s);
+  } else {  // the rest goes through shared memory
     if (packs <= 8192) return run<T, V, 16, 512>(a, s);
   }
   return false;
@@ -866,8 +873,8 @@ cudaError_t launch_layer_norm(const LayerNormArgs& a, cudaStream_t s) {
   bool done = false;
   const long long packs = ((long long)a.cols * (long long)esz + 15) / 16;
   // Through shared memory where 16-byte accesses do not fit the rows and there are two rows or more an SM:
-  // 8192 x 2001 bf16 28 us against 64, 20000 x 301 fp16 16 against 24; 300 x 2001 bf16 5.8 either way.  Rows
-  // that they fit are faster from registers: 8192 x 5760 fp32 57 against 71.
+  // 8192 x 2001 bf16 28 us against 64, 20000 x 301 fp16 16 against 24, but 300 x 2001 bf16 5.8 against
+  // 3.2.  Rows that they fit are faster from registers: 8192 x 5760 fp32 57 against 71.
   if (!vec && packs <= ring_max_packs(esz) && a.rows >= 2LL * seq_sm_count()) {
     cudaError_t e = cudaSuccess;
     PRNN_BY_DTYPE(a.dtype, T, (e = pick_ring<T>(a, vec, seq_sm_count(), s)));
