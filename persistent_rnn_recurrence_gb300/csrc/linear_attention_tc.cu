@@ -40,6 +40,7 @@
 #include <cstdint>
 
 #include "linear_attention_plan.h"
+#include "linear_attention_tables.h"
 #include "seq_common.cuh"
 #include "seq_internal.h"
 #include "tc_common.cuh"
@@ -64,19 +65,6 @@ struct Cfg {
   static constexpr uint32_t oW = 2 * kStage;     // w C, kParts tiles
   static constexpr uint32_t oX = oW + kParts * kBlock;  // X, two tiles
   static constexpr uint32_t oTab = oX + 2 * kStateTile;
-};
-
-struct Tables {
-  float pw[132];      // l^n
-  float dec[16];      // l^(15-j), or l^j in reverse
-  // fp16: powers of two taken back from O2, U and O1, each kept until its last reader is sure to be done
-  float x_scale[2], w_scale[4], row_scale[4][128];
-  float red[2][8];
-  float row_top[2][128];
-  float diag[32][36];   // l^(i-j) (in reverse l^(j-i)) of a 32 x 32 diagonal block, 0 where the mask is
-  uint64_t ab_full[2], c_full[2], a_free[2], b_free[2], c_free[2], p_full[2], p_ready[2];
-  uint64_t w_ready[2], o_full, o_free, o2_full, o2_free, x_ready, u_full, u_free, done;
-  uint32_t tmem;
 };
 
 struct TcRole {
