@@ -123,7 +123,8 @@ __global__ void __launch_bounds__(TPR* kRows<TPR>) layer_norm_kernel(LayerNormAr
   }
 }
 
-// Rows too long for registers: one block per row, read three times (the second and third from L2).
+// Rows too long for registers: one block per row, read three times (the second and third from L2).  Columns
+// are counted in 64 bits: a step past the last of nearly 2^31 does not fit 32.
 template <typename T>
 __global__ void __launch_bounds__(1024) layer_norm_long_kernel(LayerNormArgs a) {
   __shared__ float part[2][32];
@@ -131,15 +132,15 @@ __global__ void __launch_bounds__(1024) layer_norm_long_kernel(LayerNormArgs a) 
     const T* x = static_cast<const T*>(a.x) + r * a.x_stride;
     T* y = static_cast<T*>(a.y) + r * a.y_stride;
     float s = 0.f;
-    for (int c = threadIdx.x; c < a.cols; c += blockDim.x) s += to_f32(x[c]);
+    for (long long c = threadIdx.x; c < a.cols; c += blockDim.x) s += to_f32(x[c]);
     const float mean = block_sum(s, part[0]) / a.cols;
     float q = 0.f;
-    for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+    for (long long c = threadIdx.x; c < a.cols; c += blockDim.x) {
       const float d = to_f32(x[c]) - mean;
       q += d * d;
     }
     const float rstd = 1.f / sqrtf(block_sum(q, part[1]) / a.cols + a.eps);
-    for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+    for (long long c = threadIdx.x; c < a.cols; c += blockDim.x) {
       const float g = a.gamma ? a.gamma[c] : 1.f, b = a.beta ? a.beta[c] : 0.f;
       y[c] = from_f32<T>((to_f32(x[c]) - mean) * rstd * g + b);
     }
@@ -641,14 +642,14 @@ __global__ void __launch_bounds__(1024) layer_norm_dx_long_kernel(LayerNormGradA
     T* dx = static_cast<T*>(a.dx) + r * a.dx_stride;
     const float mean = a.mean[r], rstd = a.rstd[r];
     float s = 0.f, q = 0.f;
-    for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+    for (long long c = threadIdx.x; c < a.cols; c += blockDim.x) {
       const float g = to_f32(dy[c]) * (a.gamma ? a.gamma[c] : 1.f);
       s += g;
       q += g * ((to_f32(x[c]) - mean) * rstd);
     }
     s = block_sum(s, part[0]) / a.cols;
     q = block_sum(q, part[1]) / a.cols;
-    for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+    for (long long c = threadIdx.x; c < a.cols; c += blockDim.x) {
       const float g = to_f32(dy[c]) * (a.gamma ? a.gamma[c] : 1.f);
       dx[c] = from_f32<T>(rstd * (g - s - (to_f32(x[c]) - mean) * rstd * q));
     }
@@ -659,7 +660,8 @@ __global__ void __launch_bounds__(1024) layer_norm_dx_long_kernel(LayerNormGradA
 template <typename T>
 __global__ void layer_norm_dw_long_kernel(LayerNormGradArgs a, int splits) {
   __shared__ float pg[32][33], pb[32][33];
-  const int tx = threadIdx.x, ty = threadIdx.y, c = blockIdx.x * 32 + tx;
+  const int tx = threadIdx.x, ty = threadIdx.y;
+  const long long c = blockIdx.x * 32LL + tx;
   const long long share = (a.rows + splits - 1) / splits;
   const long long lo = blockIdx.y * share, hi = lo + share < a.rows ? lo + share : a.rows;
   float g = 0.f, b = 0.f;
@@ -690,7 +692,8 @@ __global__ void __launch_bounds__(256) layer_norm_dw_join_kernel(const float* pa
                                                                  float* dbeta) {
   __shared__ float sum[8][33];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const long long c = blockIdx.x * 32LL + tx;
   float* out = blockIdx.y ? dbeta : dgamma;
   if (!out) return;
   const float* p = partial + (size_t)blockIdx.y * splits * cols;
@@ -917,7 +920,7 @@ cudaError_t launch_layer_norm_grad(const LayerNormGradArgs& args, cudaStream_t s
     if (sums) {
       const long long want = (a.rows + 63) / 64;
       if (want < splits) splits = (int)want;
-      const dim3 grid((a.cols + 31) / 32, splits);
+      const dim3 grid((unsigned)((a.cols + 31LL) / 32), splits);
       PRNN_BY_DTYPE(a.dtype, T,
                     (layer_norm_dw_long_kernel<T><<<grid, dim3(32, 32), 0, s>>>(a, splits)));
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -926,7 +929,7 @@ cudaError_t launch_layer_norm_grad(const LayerNormGradArgs& args, cudaStream_t s
   if (!sums) return cudaSuccess;
   // launched as the gradient kernel's programmatic dependent: its launch overlaps that kernel's end
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.cols + 31) / 32, 2);
+  cfg.gridDim = dim3((unsigned)((a.cols + 31LL) / 32), 2);
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
