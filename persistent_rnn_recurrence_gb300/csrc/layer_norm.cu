@@ -11,7 +11,6 @@
 
 #include "seq_common.cuh"
 #include "seq_internal.h"
-#include "tc_common.cuh"
 
 namespace prnn {
 namespace {
@@ -231,8 +230,9 @@ __device__ __forceinline__ void ring_fill(const RingArgs<NT>& ring, unsigned cha
 // After a wait that ran out: report it and leave no copy in flight.  `fills`: how many this thread issued.
 __device__ __noinline__ void ring_late(uint64_t* bars, int stages, int fills, int* status) {
   atomicExch(status, 1);
+  bool ok = true;
   for (int i = 0; i < stages && i < fills; ++i)
-    tc::mbar_wait(&bars[i], (uint32_t)((fills - 1 - i) / stages) & 1u, global_ns() + kSeqWaitNs);
+    seq_wait(&bars[i], (uint32_t)((fills - 1 - i) / stages) & 1u, ok);
 }
 
 // Parameters (gamma, beta) in shared memory beside packs of V values: pack p of thread t reads its V
@@ -337,8 +337,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
   stats(first);
   __syncthreads();
   const float inv = 1.f / a.cols;
-  const uint64_t deadline = global_ns() + kSeqWaitNs;
-  bool late = false;
+  bool ok = true;
   int s = 0, turn = 0;
   uint32_t parity = 0;
   for (long long r = first; r < a.rows; r += R * step) {
@@ -353,7 +352,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
       rs[k] = rstd[k];
       px[k] = py[k] = nullptr;
       if (r + k * step < a.rows) {
-        if (!tc::mbar_wait(&bars[g][next], next_parity, deadline)) late = true;
+        seq_wait(&bars[g][next], next_parity, ok);
         const unsigned char* at = mine + (size_t)next * 2 * ring.pitch;
         uintptr_t ox = 0, oy = 0;
         if constexpr (!VEC) {
@@ -462,7 +461,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     s = next;
     parity = next_parity;
   }
-  if (late) ring_late(bars[g], ring.stages, t == 0 ? fills : 0, ring.status);
+  if (!ok) ring_late(bars[g], ring.stages, t == 0 ? fills : 0, ring.status);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!a.partial) return;
   // partial: [2][grid][cols], the groups' sums added in order
@@ -522,8 +521,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
   }
   __syncthreads();
   const float inv = 1.f / a.cols;
-  const uint64_t deadline = global_ns() + kSeqWaitNs;
-  bool late = false;
+  bool ok = true;
   int s = 0;
   uint32_t parity = 0;
   for (long long r = first; r < a.rows; r += R * step) {
@@ -537,7 +535,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
       in[k] = r + k * step < a.rows;
       float2 acc = both(0.f);
       if (in[k]) {
-        if (!tc::mbar_wait(&bars[g][next], next_parity, deadline)) late = true;
+        seq_wait(&bars[g][next], next_parity, ok);
         const unsigned char* at = mine + (size_t)next * ring.pitch;
         if constexpr (!VEC)
           at += (reinterpret_cast<uintptr_t>(a.x) + (r + k * step) * a.x_stride * sizeof(T)) & 15;
@@ -629,7 +627,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     s = next;
     parity = next_parity;
   }
-  if (late) ring_late(bars[g], ring.stages, t == 0 ? fills : 0, ring.status);
+  if (!ok) ring_late(bars[g], ring.stages, t == 0 ? fills : 0, ring.status);
 }
 
 // dx of rows too long for registers, and their sums (partial: [2][splits][cols]).

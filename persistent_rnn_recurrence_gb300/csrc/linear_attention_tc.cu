@@ -43,7 +43,6 @@
 #include "linear_attention_tables.h"
 #include "seq_common.cuh"
 #include "seq_internal.h"
-#include "tc_common.cuh"
 
 namespace prnn {
 namespace {
@@ -387,13 +386,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   after_sync();
   const uint32_t tmem = tab.tmem;
-  const uint64_t deadline = global_ns() + kSeqWaitNs;
   // a state enters the first chunk unless it is known to be zero
   const bool enters = r.x0 != nullptr || (seg > 0 && !g.states_only);
   // A wait that runs out is remembered and the work goes on (every later wait then ends at once):
   // no thread leaves the others waiting, and nothing is left in flight.
   bool ok = true;
-  auto wait = [&](uint64_t* bar, int turn) { ok = mbar_wait(bar, turn & 1, deadline) && ok; };
+  auto wait = [&](uint64_t* bar, int turn) { seq_wait(bar, turn & 1, ok); };
   auto warp_wait = [&](uint64_t* bar, int turn) {
     wait(bar, turn);
     __syncwarp();
@@ -414,9 +412,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_c(c);
       }
       for (int c = max(0, nc - 2); c < nc; ++c) {  // every load lands before the CTA leaves
-        const uint64_t limit = deadline + kSeqWaitNs;
-        ok = mbar_wait(&tab.ab_full[c & 1], (c >> 1) & 1, limit) && ok;
-        ok = mbar_wait(&tab.c_full[c & 1], (c >> 1) & 1, limit) && ok;
+        bool landed = true;  // with a limit of its own, whatever has run out before
+        seq_wait(&tab.ab_full[c & 1], (c >> 1) & 1, landed);
+        seq_wait(&tab.c_full[c & 1], (c >> 1) & 1, landed);
+        ok = ok && landed;
       }
     }
   } else if (warp == 1 || warp == 2) {
@@ -499,7 +498,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // every product has read its operands before the CTA leaves
       umma_commit(&tab.done);
-      ok = mbar_wait(&tab.done, 0, deadline + kSeqWaitNs) && ok;
+      bool read = true;
+      seq_wait(&tab.done, 0, read);
+      ok = ok && read;
     }
   } else if (warp >= 4 && warp < 12) {
     // ---- scores to operands: row i of P, blocks of 16 columns half, half + 2, ... ----

@@ -1,5 +1,5 @@
 // seq_common.cuh -- device helpers of the sequence operators: conversion
-// between the storage types and fp32, and sums over warps and blocks.
+// between the storage types and fp32, sums over warps and blocks, and bounded waits.
 #pragma once
 
 #include <cstdint>
@@ -7,6 +7,8 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include "tc_common.cuh"
 
 namespace prnn {
 
@@ -129,9 +131,27 @@ __device__ __forceinline__ float decay_pow(float ld, int n) {
   return n == 0 ? 1.f : expf(ld * (float)n);
 }
 
-// Waits of the sequence operators' kernels for their own copies and matrix products end after
-// this long and set the word that prnn_sequence_status reports.
+// Waits of the sequence operators' kernels for their own copies and matrix products.  Each one ends
+// once it has lasted this long by itself, however long its block has been at work; the word that
+// prnn_sequence_status reports is then set.
 constexpr uint64_t kSeqWaitNs = 2000ull * 1000 * 1000;
+
+// Waits for the phase of `bar` with the given parity.  A wait that runs out clears `ok`; the thread goes on,
+// and with `ok` cleared its later waits end after the first polls, so that the block comes to its end.
+// The clock is read only where 256 polls have not been enough.
+__device__ __forceinline__ void seq_wait(uint64_t* bar, uint32_t parity, bool& ok) {
+  uint32_t polls = 0;
+  uint64_t since = 0;
+  while (!tc::mbar_try_wait(bar, parity)) {
+    if ((++polls & 255u) != 0u) continue;
+    const uint64_t now = global_ns();
+    if (since == 0) since = now;
+    if (!ok || now - since > kSeqWaitNs) {
+      ok = false;
+      return;
+    }
+  }
+}
 
 // Run `f.template operator()<T>()` with the element type of dtype.
 #define PRNN_BY_DTYPE(dtype, T, ...)                 \
