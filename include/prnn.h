@@ -672,7 +672,8 @@ prnn_status_t prnn_dropout_backward(prnn_dtype_t dtype, long long n, const void*
  * place.  q and k have qk_heads heads, v and o `heads` (a multiple of qk_heads): head h uses query
  * and key head h / (heads / qk_heads).  Tokens are worked on in chunks of up to 128: an infinity or
  * NaN in a token within the length may also reach, as NaN, the outputs and gradients of its own
- * sequence up to 127 tokens away; tokens past the length reach nothing, whatever they hold.
+ * sequence up to 127 tokens away, and a result that is infinite may come out as NaN; no infinity
+ * becomes a number.  Tokens past the length reach nothing, whatever they hold.
  */
 typedef struct {
   void* data;                                /* dtype; outputs are written, inputs only read */
