@@ -141,6 +141,14 @@ bool clear_of(const void* p, size_t bytes, const Part* part, int n, size_t esz, 
   return true;
 }
 
+// What a call writes beside its sequence outputs must not overlap the small arrays it reads (the decays, and the
+// lengths or slots): blocks read them while others write.
+bool tables_clear(const void* p, size_t bytes, const prnn_linear_attention_t* a, const int32_t* per_sequence) {
+  if (!p || !bytes) return true;
+  return !overlaps(p, bytes, a->log_decay, sizeof(float) * (size_t)a->heads) &&
+         (!per_sequence || !overlaps(p, bytes, per_sequence, sizeof(int32_t) * (size_t)a->B));
+}
+
 LaSeq in(const prnn_seq_t& x, int share) {
   return LaSeq{x.data, x.stride_t, x.stride_b, x.stride_h, share};
 }
@@ -354,6 +362,8 @@ prnn_status_t prnn_linear_attention_forward(const prnn_linear_attention_t* a, vo
                (a->state && overlaps(a->state, state_bytes, a->workspace, need)) ||
                (a->state_out && overlaps(a->state_out, state_bytes, a->workspace, need))))
     return PRNN_ERR_INVALID_ARG;
+  if (!tables_clear(a->state_out, state_bytes, a, a->lens) || !tables_clear(a->workspace, need, a, a->lens))
+    return PRNN_ERR_INVALID_ARG;
   LaArgs g{};
   LaRole& r = g.role[0];
   r.a = in(a->q, H / Hq);
@@ -430,6 +440,8 @@ prnn_status_t prnn_linear_attention_backward(const prnn_linear_attention_t* a, v
   if (need)
     for (const float* p : {a->state, a->d_state_out, static_cast<const float*>(a->d_state)})
       if (p && overlaps(p, state_bytes, a->workspace, need)) return PRNN_ERR_INVALID_ARG;
+  if (!tables_clear(a->d_state, state_bytes, a, a->lens) || !tables_clear(a->workspace, need, a, a->lens))
+    return PRNN_ERR_INVALID_ARG;
 
   LaArgs g{};
   g.dtype = a->dtype;
@@ -534,7 +546,7 @@ prnn_status_t prnn_linear_attention_step(const prnn_linear_attention_t* a, float
   }
   if (!outputs_apart(part, 4, esz) || !clear_of(state_pool, pool_bytes, part, 4, esz, true) ||
       !clear_of(a->log_decay, 4ull * H, part, 4, esz, false) ||
-      (slots && !clear_of(slots, 4ull * B, part, 4, esz, false)))
+      (slots && !clear_of(slots, 4ull * B, part, 4, esz, false)) || !tables_clear(state_pool, pool_bytes, a, slots))
     return PRNN_ERR_INVALID_ARG;
   LaStepArgs r{};
   r.dtype = a->dtype;
