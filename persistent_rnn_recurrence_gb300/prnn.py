@@ -461,7 +461,9 @@ def prnn_linear_attention_step(a: bytes, state_pool, n_slots, slots=None, stream
 
 # ---- sequence operators on tensors -------------------------------------------------
 # Tensors in, tensors out, on the current stream.  `stream` (a torch stream) runs the call, and
-# allocates its outputs, on that stream instead; the caller orders it after the inputs' producers.
+# allocates its outputs, on that stream instead; the caller orders it after the inputs' producers.  The
+# tensors given to such a call may be dropped at once: their memory is not used again before the
+# call has run.  (Its outputs belong to `stream`, as anything allocated there does.)
 # The kernels of a decoding step take a few microseconds, so these wrappers touch each tensor's
 # properties as little as the checks allow.
 _torch = None
@@ -476,6 +478,13 @@ def _load_torch():
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda i: torch.cuda.current_stream(i).cuda_stream)
     _torch = torch
+
+
+def _used_on(stream, *tensors) -> None:
+    """Keeps the memory of tensors that other streams allocated until `stream` has done what it has to do so far."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def _dtype(t) -> int:
@@ -560,7 +569,9 @@ def layer_norm(x, gamma=None, beta=None, eps=1e-5, y=None, stream=None):
     if stream is not None:
         import torch
         with torch.cuda.stream(stream):
-            return layer_norm(x, gamma, beta, eps, y)
+            out = layer_norm(x, gamma, beta, eps, y)
+        _used_on(stream, x, gamma, beta, y)
+        return out
     code, dev, st = _start(x, "layer_norm: x")
     rows, cols, xs = _rows(x, "layer_norm: x")
     if y is None:
@@ -584,7 +595,9 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, stream=None):
     if stream is not None:
         import torch
         with torch.cuda.stream(stream):
-            return layer_norm_backward(dy, x, gamma, mean, rstd)
+            out = layer_norm_backward(dy, x, gamma, mean, rstd)
+        _used_on(stream, dy, x, gamma, mean, rstd)
+        return out
     code, dev, st = _start(x, "layer_norm_backward: x")
     rows, cols, xs = _rows(x, "layer_norm_backward: x")
     _like(dy, x.shape, x.dtype, dev, "layer_norm_backward: dy")
@@ -614,7 +627,9 @@ def dropout(x, p, seed, offset=0, residual=None, y=None, stream=None):
     if stream is not None:
         import torch
         with torch.cuda.stream(stream):
-            return dropout(x, p, seed, offset, residual, y)
+            out = dropout(x, p, seed, offset, residual, y)
+        _used_on(stream, x, residual, y)
+        return out
     code, dev, st = _start(x, "dropout: x")
     if not x.is_contiguous():
         raise ValueError("dropout: x must be contiguous")
@@ -684,7 +699,9 @@ def linear_attention(q, k, v, log_decay, scale=1.0, state=None, lens=None, o=Non
     if stream is not None:
         import torch
         with torch.cuda.stream(stream):
-            return linear_attention(q, k, v, log_decay, scale, state, lens, o)
+            out = linear_attention(q, k, v, log_decay, scale, state, lens, o)
+        _used_on(stream, q, k, v, log_decay, state, lens, o)
+        return out
     what = "linear_attention: "
     code, dev, st = _start(q, what + "q")
     _attention_shape(q, v)
@@ -741,7 +758,9 @@ def linear_attention_backward(do, q, k, v, log_decay, scale=1.0, state=None, len
     if stream is not None:
         import torch
         with torch.cuda.stream(stream):
-            return linear_attention_backward(do, q, k, v, log_decay, scale, state, lens, dstate)
+            out = linear_attention_backward(do, q, k, v, log_decay, scale, state, lens, dstate)
+        _used_on(stream, do, q, k, v, log_decay, state, lens, dstate)
+        return out
     what = "linear_attention_backward: "
     code, dev, st = _start(q, what + "q")
     _attention_shape(q, v)
@@ -787,7 +806,9 @@ def linear_attention_step(q, k, v, log_decay, state, scale=1.0, slots=None, o=No
     if stream is not None:
         import torch
         with torch.cuda.stream(stream):
-            return linear_attention_step(q, k, v, log_decay, state, scale, slots, o)
+            out = linear_attention_step(q, k, v, log_decay, state, scale, slots, o)
+        _used_on(stream, q, k, v, log_decay, state, slots, o)
+        return out
     what = "linear_attention_step: "
     code, dev, st = _start(q, what + "q")
     if q.ndim != 3 or v.ndim != 3 or q.shape[0] != v.shape[0]:
