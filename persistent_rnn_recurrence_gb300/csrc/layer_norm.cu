@@ -168,7 +168,6 @@ struct RingArgs {
   const void* base[NT];
   long long stride[NT];   // elements
   long long bytes[NT];    // extent of the tensor
-  long long rows;
   int cols, stages;
   uint32_t pitch;         // bytes of one row's place in the ring (a multiple of 16)
   int* status;
@@ -486,14 +485,14 @@ __global__ void __launch_bounds__(kRingThreads, 1)
   }
 }
 
-// The forward pass of many rows of any alignment: a row's values stay in registers between the two sums and
+// The forward pass of many rows that 16-byte accesses do not fit: a row's values stay in registers between the two sums and
 // the output.
-template <typename T, int NV, int TPR, int R, bool VEC>
+template <typename T, int NV, int TPR, int R>
 __global__ void __launch_bounds__(kRingThreads, 1)
     layer_norm_ring_kernel(const __grid_constant__ LayerNormArgs a,
                            const __grid_constant__ RingArgs<1> ring) {
-  using S = Share<T, NV, TPR, VEC>;
-  constexpr int V = S::V, H = S::H, N = S::N, G = S::G;
+  using S = Share<T, NV, TPR, false>;
+  constexpr int V = S::V, N = S::N, G = S::G;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ __align__(8) uint64_t bars[G][kRingMost];
   __shared__ float part[G][2][R][TPR / 32];
@@ -509,15 +508,14 @@ __global__ void __launch_bounds__(kRingThreads, 1)
   const long long first = (long long)blockIdx.x * G + g, step = (long long)gridDim.x * G;
   int fills = 0;
   auto fill = [&](long long r, int s) {
-    ring_fill<T, 1, VEC>(ring, mine + (size_t)s * ring.pitch, &bars[g][s], r);
+    ring_fill<T, 1, false>(ring, mine + (size_t)s * ring.pitch, &bars[g][s], r);
     ++fills;
   };
   if (t == 0)
     for (int s = 0; s < ring.stages && first + s * step < a.rows; ++s) fill(first + s * step, s);
   for (int c = threadIdx.x; c < a.cols; c += kRingThreads) {
-    const int at = VEC ? param_place<V, TPR>(c) : c;
-    gam[at] = a.gamma ? a.gamma[c] : 1.f;
-    bet[at] = a.beta ? a.beta[c] : 0.f;
+    gam[c] = a.gamma ? a.gamma[c] : 1.f;
+    bet[c] = a.beta ? a.beta[c] : 0.f;
   }
   __syncthreads();
   const float inv = 1.f / a.cols;
@@ -536,33 +534,19 @@ __global__ void __launch_bounds__(kRingThreads, 1)
       float2 acc = both(0.f);
       if (in[k]) {
         seq_wait(&bars[g][next], next_parity, ok);
-        const unsigned char* at = mine + (size_t)next * ring.pitch;
-        if constexpr (!VEC)
-          at += (reinterpret_cast<uintptr_t>(a.x) + (r + k * step) * a.x_stride * sizeof(T)) & 15;
-        const T* px = reinterpret_cast<const T*>(at);
+        const T* px = reinterpret_cast<const T*>(
+            mine + (size_t)next * ring.pitch +
+            ((reinterpret_cast<uintptr_t>(a.x) + (r + k * step) * a.x_stride * sizeof(T)) & 15));
         if (++next == ring.stages) {
           next = 0;
           next_parity ^= 1;
         }
-        if constexpr (VEC) {
 #pragma unroll
-          for (int p = 0; p < NV; ++p)
-            if ((p * TPR + t) * V < a.cols) {
-              const Pack<T, V> q = load_pack<T, V>(px + (p * TPR + t) * V);
-#pragma unroll
-              for (int i = 0; i < H; ++i) {
-                f[k][p * H + i] = pair_of<T, V>(q, i);
-                acc = add2(acc, f[k][p * H + i]);
-              }
-            }
-        } else {
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (sh.col(i) < a.cols) {
-              f[k][i] = sh.single(px, i, 0.f);
-              acc = add2(acc, f[k][i]);
-            }
-        }
+        for (int i = 0; i < N; ++i)
+          if (sh.col(i) < a.cols) {
+            f[k][i] = sh.single(px, i, 0.f);
+            acc = add2(acc, f[k][i]);
+          }
       }
       sum[k] = acc.x + acc.y;
     }
@@ -586,7 +570,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
       for (int i = 0; i < N; ++i)
         if (sh.col(i) < a.cols) {
           f[k][i] = add2(f[k][i], both(-mean[k]));
-          if (!VEC && sh.col2(i) >= a.cols) f[k][i].y = 0.f;
+          if (sh.col2(i) >= a.cols) f[k][i].y = 0.f;
           acc = fma2(f[k][i], f[k][i], acc);
         }
       sum[k] = acc.x + acc.y;
@@ -597,28 +581,14 @@ __global__ void __launch_bounds__(kRingThreads, 1)
       if (!in[k]) continue;
       const float rstd = 1.f / sqrtf(sum[k] * inv + a.eps);
       T* y = static_cast<T*>(a.y) + (r + k * step) * a.y_stride;
-      if constexpr (VEC) {
 #pragma unroll
-        for (int p = 0; p < NV; ++p)
-          if ((p * TPR + t) * V < a.cols) {
-            const Pack<float, V> gm = param_pack<V, TPR>(gam, p, t), bt = param_pack<V, TPR>(bet, p, t);
-            Pack<T, V> o;
-#pragma unroll
-            for (int i = 0; i < H; ++i)
-              set_pair<T, V>(o, i, fma2(mul2(f[k][p * H + i], both(rstd)), pair_of<float, V>(gm, i),
-                                        pair_of<float, V>(bt, i)));
-            store_pack<T, V>(y + (p * TPR + t) * V, o);
-          }
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (sh.col(i) < a.cols) {
-            const float2 v = fma2(mul2(f[k][i], both(rstd)), sh.single(gam, i, 0.f),
-                                  sh.single(bet, i, 0.f));
-            y[sh.col(i)] = from_f32<T>(v.x);
-            if (sh.col2(i) < a.cols) y[sh.col2(i)] = from_f32<T>(v.y);
-          }
-      }
+      for (int i = 0; i < N; ++i)
+        if (sh.col(i) < a.cols) {
+          const float2 v = fma2(mul2(f[k][i], both(rstd)), sh.single(gam, i, 0.f),
+                                sh.single(bet, i, 0.f));
+          y[sh.col(i)] = from_f32<T>(v.x);
+          if (sh.col2(i) < a.cols) y[sh.col2(i)] = from_f32<T>(v.y);
+        }
       if (t == 0) {
         if (a.mean) a.mean[r + k * step] = mean[k];
         if (a.rstd) a.rstd[r + k * step] = rstd;
@@ -789,7 +759,6 @@ cudaError_t run_grad(const LayerNormGradArgs& a, bool vec, int sms, int* blocks,
   ring.stride[1] = a.dy_stride;
   ring.bytes[0] = ((a.rows - 1) * a.x_stride + a.cols) * n;
   ring.bytes[1] = ((a.rows - 1) * a.dy_stride + a.cols) * n;
-  ring.rows = a.rows;
   ring.cols = a.cols;
   size_t smem = 0;
   if (!make_ring<T, NV, TPR, 2>(ring, vec, 1, R, &smem)) return cudaErrorInvalidConfiguration;
@@ -821,19 +790,17 @@ cudaError_t pick_grad(const LayerNormGradArgs& a, bool vec, int sms, int* blocks
 }
 
 template <typename T, int NV, int TPR, int R>
-cudaError_t run_ring(const LayerNormArgs& a, bool vec, int sms, cudaStream_t s) {
+cudaError_t run_ring(const LayerNormArgs& a, int sms, cudaStream_t s) {
   constexpr int G = kRingThreads / TPR;
   RingArgs<1> ring{};
   ring.base[0] = a.x;
   ring.stride[0] = a.x_stride;
   ring.bytes[0] = ((a.rows - 1) * a.x_stride + a.cols) * (long long)sizeof(T);
-  ring.rows = a.rows;
   ring.cols = a.cols;
   size_t smem = 0;
-  if (!make_ring<T, NV, TPR, 1>(ring, vec, 2, R, &smem)) return cudaErrorInvalidConfiguration;
+  if (!make_ring<T, NV, TPR, 1>(ring, false, 2, R, &smem)) return cudaErrorInvalidConfiguration;
   const int blocks = (int)std::min<long long>((a.rows + G - 1) / G, sms);
-  auto kernel = vec ? layer_norm_ring_kernel<T, NV, TPR, R, true>
-                    : layer_norm_ring_kernel<T, NV, TPR, R, false>;
+  auto kernel = layer_norm_ring_kernel<T, NV, TPR, R>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   kernel<<<blocks, kRingThreads, smem, s>>>(a, ring);
@@ -841,18 +808,18 @@ cudaError_t run_ring(const LayerNormArgs& a, bool vec, int sms, cudaStream_t s) 
 }
 
 template <typename T>
-cudaError_t pick_ring(const LayerNormArgs& a, bool vec, int sms, cudaStream_t s) {
+cudaError_t pick_ring(const LayerNormArgs& a, int sms, cudaStream_t s) {
   const int packs = (int)((a.cols * sizeof(T) + 15) / 16);
-  if (packs <= 32) return run_ring<T, 1, 32, 2>(a, vec, sms, s);
-  if (packs <= 64) return run_ring<T, 2, 32, 2>(a, vec, sms, s);
-  if (packs <= 128) return run_ring<T, 1, 128, 2>(a, vec, sms, s);
-  if (packs <= 256) return run_ring<T, 2, 128, 2>(a, vec, sms, s);
-  if (packs <= 512) return run_ring<T, 2, 256, 2>(a, vec, sms, s);
-  if (packs <= 1024) return run_ring<T, 2, 512, 2>(a, vec, sms, s);
+  if (packs <= 32) return run_ring<T, 1, 32, 2>(a, sms, s);
+  if (packs <= 64) return run_ring<T, 2, 32, 2>(a, sms, s);
+  if (packs <= 128) return run_ring<T, 1, 128, 2>(a, sms, s);
+  if (packs <= 256) return run_ring<T, 2, 128, 2>(a, sms, s);
+  if (packs <= 512) return run_ring<T, 2, 256, 2>(a, sms, s);
+  if (packs <= 1024) return run_ring<T, 2, 512, 2>(a, sms, s);
   if constexpr (sizeof(T) == 4)
-    return run_ring<T, 4, 512, 2>(a, vec, sms, s);
+    return run_ring<T, 4, 512, 2>(a, sms, s);
   else
-    return run_ring<T, 3, 512, 1>(a, vec, sms, s);
+    return run_ring<T, 3, 512, 1>(a, sms, s);
 }
 // The longest rows they take, in 16-byte packs.
 constexpr int ring_max_packs(size_t esz) { return esz == 4 ? 2048 : 1536; }
@@ -878,7 +845,7 @@ cudaError_t launch_layer_norm(const LayerNormArgs& a, cudaStream_t s) {
   // 3.2.  Rows that they fit are faster from registers: 8192 x 5760 fp32 57 against 71.
   if (!vec && packs <= ring_max_packs(esz) && a.rows >= 2LL * seq_sm_count()) {
     cudaError_t e = cudaSuccess;
-    PRNN_BY_DTYPE(a.dtype, T, (e = pick_ring<T>(a, vec, seq_sm_count(), s)));
+    PRNN_BY_DTYPE(a.dtype, T, (e = pick_ring<T>(a, seq_sm_count(), s)));
     return e;
   }
   if (vec) {
