@@ -382,7 +382,7 @@ cudaError_t launch_la_reduce(const LaReduceArgs& a, cudaStream_t s) {
   const long long n = (long long)a.T * a.B * (a.H / a.group) * a.d;
   if (n == 0) return cudaSuccess;
   const long long want = (n + 255) / 256;
-  const int blocks = (int)(want < 152 * 16 ? want : 152 * 16);
+  const int blocks = (int)std::min<long long>(want, 16LL * seq_sm_count());
   PRNN_BY_DTYPE(a.dtype, T, (la_reduce_kernel<T><<<blocks, 256, 0, s>>>(a)));
   return cudaGetLastError();
 }

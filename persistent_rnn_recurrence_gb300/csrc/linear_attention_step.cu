@@ -101,7 +101,7 @@ cudaError_t launch_la_step(const LaStepArgs& a, cudaStream_t s) {
   int slice = vec ? 128 : 32;
   while (slice > a.dv && slice > 16) slice /= 2;
   if (slice < a.dv && slice * 2 >= a.dv && slice < (vec ? 128 : 32)) slice *= 2;
-  while (slice > 16 && (long long)a.B * a.H * ((a.dv + slice - 1) / slice) < 152) slice /= 2;
+  while (slice > 16 && (long long)a.B * a.H * ((a.dv + slice - 1) / slice) < seq_sm_count()) slice /= 2;
   if (vec) {
     PRNN_BY_DTYPE(a.dtype, T, (launch<T, 4>(a, slice, s)));
   } else {
