@@ -595,7 +595,8 @@ prnn_status_t prnn_stack_destroy(prnn_stack_t s);
  * normalisation, dropout with the residual, and linear attention with a decay
  * per head, each with its gradient.  They need no handle.  Device pointers
  * throughout; data in fp32, fp16 or bf16 (`dtype`), arithmetic, statistics and
- * states in fp32, one rounding at each 16-bit output.  Asynchronous on `stream`;
+ * states in fp32, one rounding at each 16-bit output (what linear attention rounds between its
+ * products of 16-bit data is stated there).  Asynchronous on `stream`;
  * a call allocates nothing: what scratch it needs is the caller's `workspace`,
  * 16-byte aligned, of the size its *_workspace query gives, used by the call
  * on its stream only (give overlapping calls their own).  Results do not depend on the
@@ -670,10 +671,18 @@ prnn_status_t prnn_dropout_backward(prnn_dtype_t dtype, long long n, const void*
  * A tensor of a sequence holds element (t, b, h, d) at t*stride_t + b*stride_b + h*stride_h + d
  * (elements), so that time-major and packed layouts, and slices of a joint projection, are read in
  * place.  q and k have qk_heads heads, v and o `heads` (a multiple of qk_heads): head h uses query
- * and key head h / (heads / qk_heads).  Tokens are worked on in chunks of up to 128: an infinity or
- * NaN in a token within the length may also reach, as NaN, the outputs and gradients of its own
- * sequence up to 127 tokens away, and a result that is infinite may come out as NaN; no infinity
- * becomes a number.  Tokens past the length reach nothing, whatever they hold.
+ * and key head h / (heads / qk_heads).
+ * fp32 data, and heads wider than 128, are multiplied in fp32.  16-bit data with dk, dv <= 128 goes through the
+ * tensor cores: the data enters as it is, and what is computed in between (scores, the state as an
+ * operand, decayed values) as a sum of two or three parts of the data's type, all products
+ * summed in fp32.  A score or state entry is so rounded by 2^-16 of itself at most in bf16 and by 2^-22
+ * in fp16, where the entries of a row of scores, or of 64 columns of a state, share a power of two: one more
+ * than 2^16 below the largest of them keeps fewer bits.  The outputs' own rounding is 2^-8 and
+ * 2^-11.  States that are returned are fp32 sums of terms rounded by 2^-24 (bf16) or 2^-22 (fp16).
+ * Tokens are worked on in chunks of up to 128: an infinity or NaN in a token within the length may
+ * also reach, as NaN, the outputs and gradients of its own sequence up to 127 tokens away, and a
+ * result that is infinite may come out as NaN; no infinity becomes a number.  Tokens past the
+ * length reach nothing, whatever they hold.
  */
 typedef struct {
   void* data;                                /* dtype; outputs are written, inputs only read */

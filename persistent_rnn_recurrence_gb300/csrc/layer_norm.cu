@@ -3,8 +3,8 @@
 // Both are bound by memory: 8 to 14 flops per element against 4 to 12 bytes.  A row is read once: the
 // forward pass keeps it in registers between the sums and the output, the gradient in a ring in shared
 // memory.  Measured on GB300 against the copy rate of 6.69 TB/s: forward 8192 x 5760 fp32 57 us (0.99),
-// 32768 x 1152 fp32 47 (0.96), 8192 x 4096 bf16 30 (0.68: with half the bytes per value the rows in
-// flight, bounded by registers, hold too few bytes); gradient 8192 x 5760 fp32 101 (0.84), 32768 x
+// 32768 x 1152 fp32 47 (0.96), 8192 x 4096 bf16 30 (0.68: the rows, held as
+// fp32 values, keep half as many bytes in flight and the loads wait); gradient 8192 x 5760 fp32 101 (0.84), 32768 x
 // 1152 fp32 82 (0.83), 8192 x 4096 bf16 48 (0.62: the chain of one row's barrier and sums).  Ragged
 // rows are slower for their 2- or 4-byte accesses: 8192 x 2001 bf16 28 and 40 us (0.36, 0.37).
 #include <algorithm>

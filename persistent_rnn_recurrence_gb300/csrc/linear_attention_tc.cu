@@ -18,7 +18,9 @@
 // below the output's one rounding), w C in two for fp16 (22 bits), and for bf16 in three (24 bits)
 // where the fp32 state is an output and two where it only feeds 16-bit ones.  All products accumulate
 // in fp32.  For fp16, whose range would not hold them, P is scaled by a power of two per row (its largest
-// weighted score) and X and w C per tile, taken back after the product.
+// weighted score) and X and w C per tile, taken back after the product.  A value 2^27 and more below the largest
+// finite one of its tile keeps fewer bits than a 16-bit output has; a scale per column would need
+// the columns' maxima over all tokens before the first could be stored.
 //
 // Warps: 0 loads (TMA), 1 and 2 issue the matrix products, 4-11 turn scores into operands (a row per
 // thread, every other block of 16 columns), 12-19 own the state (a row of X and half the columns),
@@ -28,11 +30,12 @@
 // ends. The two parts of X stand side by side in one product (N = 128), which reads Q once.
 //
 // What bounds it: memory would take 40 us for T = 8192, 2 sequences of 16 heads of 128 x 128 bf16, and the
-// kernel takes 130.  A chunk of 112 tokens costs a CTA about 4600 cycles: the products read 280 KB of
+// kernel takes 127.  A chunk of 112 tokens costs a CTA about 4600 cycles: the products read 280 KB of
 // operands from shared memory, TMA and the warps move 190 KB more (3600 cycles at 128 bytes each), and the
 // chain w C -> U -> X -> O2 with its barriers is about as long.  C = 112 is what two chunks in flight
-// leave room for at 128 x 128; 96 took 136 us, 80 with three chunks in flight 152.  Other figures, us:
-// T = 2048, 4 sequences 54; at 64 x 64 39; T = 256, 32 sequences 97; gradients of T = 2048, 4 sequences 134.
+// leave room for at 128 x 128; 96 took 136 us, 80 with three chunks in flight 152 (112 took 130 then).  Other figures,
+// us: T = 2048, 4 sequences 52; at 64 x 64 37; T = 256, 32 sequences 96; gradients of T = 2048, 4 sequences 136.
+// fp16 takes 145, 61, 41, 99 and 176 for its maxima.
 // The CUDA-core kernel of the first version took 10353 for the first of these.
 #include <cuda.h>
 
