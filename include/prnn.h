@@ -646,6 +646,49 @@ prnn_status_t prnn_layer_norm_backward(prnn_dtype_t dtype, long long rows, int c
                                        size_t workspace_bytes, void* stream);
 
 /*
+ * Root-mean-square norm over the last axis of `rows` rows of `cols` values, after the residual's addition:
+ *     h_c = x_c + residual_c, rounded to dtype (h is x where residual is NULL, and nothing is written there),
+ *     rstd = 1 / sqrt(sum_c h_c^2 / cols + eps),   y_c = h_c * rstd * weight_c.
+ * The stream is normalised as it is stored, so that the backward pass reads what the forward pass used.  Rows lie
+ * at multiples of their strides (elements, >= cols).  h may be x or residual itself, y may be x or residual
+ * itself (same stride); y and h must not overlap.  weight [cols] fp32, NULL: 1.  rstd [rows] fp32 is for the
+ * backward pass and may be NULL.  rows == 0 is a no-op; eps >= 0.  Over the last axis of queries and keys
+ * [T][B][heads][d] with weight d^-1/2 it makes them of length one (but for eps).
+ */
+prnn_status_t prnn_rms_norm_forward(prnn_dtype_t dtype, long long rows, int cols, const void* x, long long x_stride,
+                                    const void* residual, long long residual_stride, const float* weight, float eps,
+                                    void* y, long long y_stride, void* h, long long h_stride, float* rstd,
+                                    void* stream);
+
+/*
+ * The same with an output in 8 bits, as a product in 8 bits takes it: for every group of columns of a row,
+ *     scale = max |y| / 448 (1 where that maximum is 0 or NaN),   q_c = y_c / scale rounded to e4m3.
+ * group: 128 columns (the last of a row may be fewer) or 0, the row.  q [rows] bytes of e4m3 (no infinities; 0x7f
+ * and 0xff are NaN), rows q_stride >= cols apart; scale [rows][ceil(cols / group)] fp32 ([rows] for 0).  q overlaps
+ * nothing else.
+ */
+prnn_status_t prnn_rms_norm_quantized(prnn_dtype_t dtype, long long rows, int cols, const void* x,
+                                         long long x_stride, const void* residual, long long residual_stride,
+                                         const float* weight, float eps, int group, void* q, long long q_stride,
+                                         float* scale, void* h, long long h_stride, float* rstd, void* stream);
+
+/* Workspace of prnn_rms_norm_backward for this many rows and columns. */
+prnn_status_t prnn_rms_norm_workspace(long long rows, int cols, size_t* bytes);
+
+/*
+ * Its gradient, with xhat = h * rstd and g = dy * weight:
+ *     dx = rstd * (g - xhat * sum(g * xhat) / cols) + dh   (sums over the row),   dweight_c = sum_r dy_rc * xhat_rc.
+ * dh is the gradient of the stream h from elsewhere, NULL: none; dx is the gradient of x and of residual alike.  dx
+ * may be dy or dh itself.  dx and dweight [cols] (fp32) are overwritten; each may be NULL (not computed; the
+ * workspace is needed for dweight only).  rows == 0 writes a zero dweight.
+ */
+prnn_status_t prnn_rms_norm_backward(prnn_dtype_t dtype, long long rows, int cols, const void* dy,
+                                     long long dy_stride, const void* h, long long h_stride, const float* weight,
+                                     const float* rstd, const void* dh, long long dh_stride, void* dx,
+                                     long long dx_stride, float* dweight, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/*
  * Dropout of n contiguous values, with an optional residual:
  *     y_i = (w_i >= p * 2^32 ? x_i / (1 - p) : 0) + residual_i,
  * w_i = word i mod 4 of the block Philox4x32-10 (Salmon et al., "Parallel random

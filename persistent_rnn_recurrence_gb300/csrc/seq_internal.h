@@ -47,6 +47,42 @@ struct LayerNormGradArgs {
 int layer_norm_splits(long long rows, int cols);
 cudaError_t launch_layer_norm_grad(const LayerNormGradArgs& a, cudaStream_t s);
 
+// ---- root-mean-square norm (rms_norm.cu) ------------------------------------
+struct RmsNormArgs {
+  prnn_dtype_t dtype;
+  long long rows;
+  int cols;
+  const void* x;
+  long long x_stride;
+  const void* residual;       // may be null, and then h is
+  long long residual_stride;
+  const float* weight;        // may be null
+  float eps;
+  void* y;                    // dtype, or bytes of e4m3 where scale is set
+  long long y_stride;
+  void* h;
+  long long h_stride;
+  float* rstd;                // may be null
+  int group;                  // columns of one scale: 128, or 0 for the row
+  float* scale;
+};
+cudaError_t launch_rms_norm(const RmsNormArgs& a, cudaStream_t s);
+
+struct RmsNormGradArgs {
+  prnn_dtype_t dtype;
+  long long rows;
+  int cols;
+  const void *dy, *h, *dh;    // dh may be null
+  long long dy_stride, h_stride, dh_stride;
+  const float *weight, *rstd;
+  void* dx;                   // may be null
+  long long dx_stride;
+  float* dweight;             // may be null
+  float* partial;             // [rms_norm_splits][cols]
+};
+int rms_norm_splits(long long rows, int cols);
+cudaError_t launch_rms_norm_grad(const RmsNormGradArgs& a, cudaStream_t s);
+
 // ---- dropout (dropout.cu) ---------------------------------------------------
 struct DropoutArgs {
   prnn_dtype_t dtype;

@@ -47,6 +47,7 @@ EXPORTS = ["prnn_create", "prnn_set_weights_dense", "prnn_set_weights_sparse",
            "prnn_stack_get_status", "prnn_stack_set_option", "prnn_stack_get_timing",
            "prnn_stack_get_info", "prnn_stack_destroy", "prnn_backward",
            "prnn_sequence_status", "prnn_layer_norm_forward", "prnn_layer_norm_workspace", "prnn_layer_norm_backward",
+           "prnn_rms_norm_forward", "prnn_rms_norm_quantized", "prnn_rms_norm_workspace", "prnn_rms_norm_backward",
            "prnn_dropout_forward", "prnn_dropout_backward",
            "prnn_linear_attention_workspace", "prnn_linear_attention_forward",
            "prnn_linear_attention_backward", "prnn_linear_attention_step"]
@@ -142,6 +143,12 @@ _sig = {
     "prnn_layer_norm_workspace": ([_L, _I, ctypes.POINTER(ctypes.c_size_t)], _I),
     "prnn_layer_norm_backward": ([_I, _L, _I, _P, _L, _P, _L, _P, _P, _P, _P, _L, _P, _P, _P,
                                   ctypes.c_size_t, _P], _I),
+    "prnn_rms_norm_forward": ([_I, _L, _I, _P, _L, _P, _L, _P, ctypes.c_float, _P, _L, _P, _L, _P, _P], _I),
+    "prnn_rms_norm_quantized": ([_I, _L, _I, _P, _L, _P, _L, _P, ctypes.c_float, _I, _P, _L, _P, _P, _L, _P,
+                                    _P], _I),
+    "prnn_rms_norm_workspace": ([_L, _I, ctypes.POINTER(ctypes.c_size_t)], _I),
+    "prnn_rms_norm_backward": ([_I, _L, _I, _P, _L, _P, _L, _P, _P, _P, _L, _P, _L, _P, _P, ctypes.c_size_t, _P],
+                               _I),
     "prnn_dropout_forward": ([_I, _L, _P, _P, _P, ctypes.c_double, ctypes.c_uint64,
                               ctypes.c_uint64, _P], _I),
     "prnn_dropout_backward": ([_I, _L, _P, _P, ctypes.c_double, ctypes.c_uint64, ctypes.c_uint64,
@@ -427,6 +434,34 @@ def prnn_layer_norm_backward(dtype, rows, cols, dy, dy_stride, x, x_stride, gamm
            "prnn_layer_norm_backward")
 
 
+def prnn_rms_norm_forward(dtype, rows, cols, x, x_stride, residual, residual_stride, weight, eps, y, y_stride, h,
+                          h_stride, rstd, stream=None) -> None:
+    _check(_lib.prnn_rms_norm_forward(dtype, rows, cols, _ptr(x), x_stride, _ptr(residual), residual_stride,
+                                      _ptr(weight), eps, _ptr(y), y_stride, _ptr(h), h_stride, _ptr(rstd),
+                                      _stream(stream)), "prnn_rms_norm_forward")
+
+
+def prnn_rms_norm_quantized(dtype, rows, cols, x, x_stride, residual, residual_stride, weight, eps, group, q,
+                               q_stride, scale, h, h_stride, rstd, stream=None) -> None:
+    _check(_lib.prnn_rms_norm_quantized(dtype, rows, cols, _ptr(x), x_stride, _ptr(residual), residual_stride,
+                                           _ptr(weight), eps, group, _ptr(q), q_stride, _ptr(scale), _ptr(h),
+                                           h_stride, _ptr(rstd), _stream(stream)), "prnn_rms_norm_quantized")
+
+
+def prnn_rms_norm_workspace(rows, cols) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.prnn_rms_norm_workspace(rows, cols, ctypes.byref(n)), "prnn_rms_norm_workspace")
+    return n.value
+
+
+def prnn_rms_norm_backward(dtype, rows, cols, dy, dy_stride, h, h_stride, weight, rstd, dh, dh_stride, dx, dx_stride,
+                           dweight, workspace, workspace_bytes, stream=None) -> None:
+    _check(_lib.prnn_rms_norm_backward(dtype, rows, cols, _ptr(dy), dy_stride, _ptr(h), h_stride, _ptr(weight),
+                                       _ptr(rstd), _ptr(dh), dh_stride, _ptr(dx), dx_stride, _ptr(dweight),
+                                       _ptr(workspace), workspace_bytes, _stream(stream)),
+           "prnn_rms_norm_backward")
+
+
 def prnn_dropout_forward(dtype, n, x, residual, y, p, seed, offset, stream=None) -> None:
     _check(_lib.prnn_dropout_forward(dtype, n, _ptr(x), _ptr(residual), _ptr(y), p, seed, offset,
                                      _stream(stream)), "prnn_dropout_forward")
@@ -619,6 +654,110 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, stream=None):
                                          dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), need, st),
            "prnn_layer_norm_backward")
     return dx, dgamma, dbeta
+
+
+def _same_rows(t, x, device, what):
+    """Address and row stride of rows shaped and typed like x."""
+    _like(t, x.shape, x.dtype, device, what)
+    return t.data_ptr(), _rows(t, what)[2]
+
+
+def _rms_inputs(x, residual, h, device, cols, what):
+    """(residual's address and stride, h, its address and stride); h is the stream that the norm reads."""
+    if residual is None:
+        if h is not None:
+            raise ValueError(f"{what}: h is written only where a residual is added")
+        return 0, 0, x, 0, 0
+    r, rs = _same_rows(residual, x, device, what + ": residual")
+    if h is None:
+        h = _torch.empty_like(x, memory_format=_torch.contiguous_format)
+        return r, rs, h, h.data_ptr(), cols
+    return r, rs, h, *_same_rows(h, x, device, what + ": h")
+
+
+def rms_norm(x, weight=None, eps=1e-6, residual=None, y=None, h=None, stream=None):
+    """Root-mean-square norm over the last axis of the stream h = x + residual (prnn_rms_norm_forward):
+    (y, h, rstd), rstd fp32 with x's leading shape.  Without a residual h is x itself.  weight: fp32 [cols] or
+    None.  h may be x or residual, y may be x or residual (not both the same)."""
+    if stream is not None:
+        import torch
+        with torch.cuda.stream(stream):
+            out = rms_norm(x, weight, eps, residual, y, h)
+        _used_on(stream, x, weight, residual, y, h)
+        return out
+    code, dev, st = _start(x, "rms_norm: x")
+    rows, cols, xs = _rows(x, "rms_norm: x")
+    r, rs, h, hp, hs = _rms_inputs(x, residual, h, dev, cols, "rms_norm")
+    if y is None:
+        y = _torch.empty_like(x, memory_format=_torch.contiguous_format)
+        yp, ys = y.data_ptr(), cols
+    else:
+        yp, ys = _same_rows(y, x, dev, "rms_norm: y")
+    rstd = _torch.empty(x.shape[:-1], dtype=_torch.float32, device=x.device)
+    _check(_lib.prnn_rms_norm_forward(code, rows, cols, x.data_ptr(), xs, r, rs,
+                                      _vector(weight, cols, _torch.float32, dev, "rms_norm: weight"), eps, yp, ys,
+                                      hp, hs, rstd.data_ptr(), st), "prnn_rms_norm_forward")
+    return y, h, rstd
+
+
+def rms_norm_e4m3(x, weight=None, eps=1e-6, residual=None, group=128, h=None, stream=None):
+    """rms_norm with its output in 8 bits (prnn_rms_norm_quantized): (q, scale, h, rstd).  q float8_e4m3fn,
+    x's shape, contiguous; q * scale is the norm's output, a scale (fp32) for every `group` columns of a
+    row: scale [..., ceil(cols / 128)] for 128, [..., 1] for 0 (the row)."""
+    if stream is not None:
+        import torch
+        with torch.cuda.stream(stream):
+            out = rms_norm_e4m3(x, weight, eps, residual, group, h)
+        _used_on(stream, x, weight, residual, h)
+        return out
+    code, dev, st = _start(x, "rms_norm_e4m3: x")
+    rows, cols, xs = _rows(x, "rms_norm_e4m3: x")
+    if group not in (0, 128):
+        raise ValueError(f"rms_norm_e4m3: group {group}: 128 columns or 0 (the row)")
+    r, rs, h, hp, hs = _rms_inputs(x, residual, h, dev, cols, "rms_norm_e4m3")
+    lead, on = x.shape[:-1], x.device
+    q = _torch.empty(x.shape, dtype=_torch.float8_e4m3fn, device=on)
+    scale = _torch.empty((*lead, -(-cols // group) if group else 1), dtype=_torch.float32, device=on)
+    rstd = _torch.empty(lead, dtype=_torch.float32, device=on)
+    _check(_lib.prnn_rms_norm_quantized(code, rows, cols, x.data_ptr(), xs, r, rs,
+                                           _vector(weight, cols, _torch.float32, dev, "rms_norm_e4m3: weight"), eps,
+                                           group, q.data_ptr(), cols, scale.data_ptr(), hp, hs, rstd.data_ptr(), st),
+           "prnn_rms_norm_quantized")
+    return q, scale, h, rstd
+
+
+def rms_norm_backward(dy, h, weight, rstd, dh=None, dx=None, stream=None):
+    """Gradients of rms_norm and rms_norm_e4m3 from the stream h that they returned: (dx, dweight), dx that of x
+    and of the residual alike, with dh (the gradient of the stream from elsewhere, or None) added; dweight fp32
+    [cols].  dx may be dy or dh."""
+    if stream is not None:
+        import torch
+        with torch.cuda.stream(stream):
+            out = rms_norm_backward(dy, h, weight, rstd, dh, dx)
+        _used_on(stream, dy, h, weight, rstd, dh, dx)
+        return out
+    what = "rms_norm_backward"
+    code, dev, st = _start(h, what + ": h")
+    rows, cols, hs = _rows(h, what + ": h")
+    dyp, dys = _same_rows(dy, h, dev, what + ": dy")
+    dhp, dhs = (0, 0) if dh is None else _same_rows(dh, h, dev, what + ": dh")
+    f32, lead, on = _torch.float32, h.shape[:-1], h.device
+    if rstd.shape != lead or rstd.dtype is not f32 or rstd.get_device() != dev or not rstd.is_contiguous():
+        raise ValueError(f"{what}: rstd {tuple(rstd.shape)} {rstd.dtype}: expected {tuple(lead)} contiguous {f32} "
+                         f"on device {dev}")
+    if dx is None:
+        dx = _torch.empty_like(h, memory_format=_torch.contiguous_format)
+        dxp, dxs = dx.data_ptr(), cols
+    else:
+        dxp, dxs = _same_rows(dx, h, dev, what + ": dx")
+    need = prnn_rms_norm_workspace(rows, cols)
+    dweight = _torch.empty(cols, dtype=f32, device=on)
+    ws = _torch.empty(need, dtype=_torch.uint8, device=on)
+    _check(_lib.prnn_rms_norm_backward(code, rows, cols, dyp, dys, h.data_ptr(), hs,
+                                       _vector(weight, cols, f32, dev, what + ": weight"), rstd.data_ptr(), dhp, dhs,
+                                       dxp, dxs, dweight.data_ptr(), ws.data_ptr(), need, st),
+           "prnn_rms_norm_backward")
+    return dx, dweight
 
 
 def dropout(x, p, seed, offset=0, residual=None, y=None, stream=None):
