@@ -785,6 +785,64 @@ prnn_status_t prnn_linear_attention_backward(const prnn_linear_attention_t* a, v
 prnn_status_t prnn_linear_attention_step(const prnn_linear_attention_t* a, float* state_pool,
                                          int n_slots, const int32_t* slots, void* stream);
 
+/*
+ * The gated delta rule: the matrix recurrence that takes out what its state already holds for a key before it
+ * adds the value, with a decay and a writing strength per token and head.  With a = exp(log_decay_t):
+ *     S' = a S_{t-1},   e_t = v_t - S'^T k_t,   S_t = S' + k_t (beta_t e_t)^T  [dk][dv],   o_t = scale * S_t^T q_t.
+ * Tensors, shared heads, lengths and states are as in linear attention.  Keys are meant to be of length one (a
+ * prnn_rms_norm over the last axis with weight dk^-1/2 makes them so) and beta in 0 .. 2: with longer keys the state
+ * grows without bound, and so do its results.  fp32 sums, states and gates throughout; one rounding at each
+ * 16-bit output.  An infinity or NaN in a token within the length may reach, as NaN, the
+ * outputs and gradients of its own sequence and head up to 127 tokens before it and everywhere behind it.  Tokens
+ * past the length reach nothing, whatever they hold.
+ */
+typedef struct {
+  prnn_dtype_t dtype;         /* of q, k, v, o and their gradients                               */
+  int T, B;                   /* steps, sequences                                                */
+  int heads, qk_heads;        /* heads % qk_heads == 0                                           */
+  int dk, dv;                 /* 1 .. 256 each; T <= 2^29, B * heads <= 2^24                     */
+  float scale;
+  const int32_t* lens;        /* [B] device: length of each sequence, clamped to 0 .. T; NULL: T */
+  prnn_seq_t q, k, v;         /* inputs                                                          */
+  prnn_seq_t log_decay, beta; /* fp32 inputs, one value per token and head: element (t, b, h) at
+                                 t*stride_t + b*stride_b + h*stride_h; log_decay <= 0            */
+  const float* state;         /* [B][heads][dk][dv] S before the first token, NULL: zeros        */
+  prnn_seq_t o;               /* forward: output                                                 */
+  float* state_out;           /* forward: S after the last token; may be NULL or `state` itself  */
+  /* backward only */
+  prnn_seq_t d_o;             /* gradient of o (input)                                           */
+  const float* d_state_out;   /* gradient of state_out (input), NULL: zeros                      */
+  prnn_seq_t d_q, d_k, d_v;   /* gradients; data NULL: not computed                              */
+  prnn_seq_t d_log_decay, d_beta;   /* fp32 gradients; data NULL: not computed                   */
+  float* d_state;             /* gradient of `state`, NULL: not computed                         */
+  void* workspace;
+  size_t workspace_bytes;
+} prnn_gated_delta_t;
+
+/* Workspace of prnn_gated_delta_forward (backward == 0) or _backward (1) for the call that `a` describes (its
+ * pointers are not followed). */
+prnn_status_t prnn_gated_delta_workspace(const prnn_gated_delta_t* a, int backward, size_t* bytes);
+
+/* All T tokens.  T == 0 copies the state; B == 0 is a no-op. */
+prnn_status_t prnn_gated_delta_forward(const prnn_gated_delta_t* a, void* stream);
+
+/*
+ * Gradients of the forward call with the same inputs, for the loss whose gradient is d_o with respect to o and
+ * d_state_out with respect to state_out.  From the last token, with R = d_state_out:
+ *     R += scale q_t do_t^T;  du = R^T k_t;  dv_t = beta_t du;  dbeta_t = e_t . du;  dq_t = scale S_t do_t;
+ *     dk_t = R (beta_t e_t) - S' dv_t;  R <- R - k_t dv_t^T;  dlog_decay_t = sum of S' * R;  R <- a R,
+ * d_state = R at the end; dq and dk are summed over the heads that share them.
+ */
+prnn_status_t prnn_gated_delta_backward(const prnn_gated_delta_t* a, void* stream);
+
+/*
+ * One token for each of B sequences (decoding), states in `state_pool` [n_slots][heads][dk][dv] fp32 updated in
+ * place through `slots`, as prnn_linear_attention_step: a->T, lens and the strides over t are not used.  No
+ * workspace.
+ */
+prnn_status_t prnn_gated_delta_step(const prnn_gated_delta_t* a, float* state_pool, int n_slots,
+                                    const int32_t* slots, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

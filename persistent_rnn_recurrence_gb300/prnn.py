@@ -50,7 +50,9 @@ EXPORTS = ["prnn_create", "prnn_set_weights_dense", "prnn_set_weights_sparse",
            "prnn_rms_norm_forward", "prnn_rms_norm_quantized", "prnn_rms_norm_workspace", "prnn_rms_norm_backward",
            "prnn_dropout_forward", "prnn_dropout_backward",
            "prnn_linear_attention_workspace", "prnn_linear_attention_forward",
-           "prnn_linear_attention_backward", "prnn_linear_attention_step"]
+           "prnn_linear_attention_backward", "prnn_linear_attention_step",
+           "prnn_gated_delta_workspace", "prnn_gated_delta_forward", "prnn_gated_delta_backward",
+           "prnn_gated_delta_step"]
 
 
 class prnn_info_t(ctypes.Structure):
@@ -94,10 +96,24 @@ class prnn_linear_attention_t(ctypes.Structure):
         ("workspace_bytes", ctypes.c_size_t)]
 
 
+class prnn_gated_delta_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "dtype", "T", "B", "heads", "qk_heads", "dk", "dv")] + [
+        ("scale", ctypes.c_float), ("lens", ctypes.c_void_p), ("q", prnn_seq_t), ("k", prnn_seq_t),
+        ("v", prnn_seq_t), ("log_decay", prnn_seq_t), ("beta", prnn_seq_t), ("state", ctypes.c_void_p),
+        ("o", prnn_seq_t), ("state_out", ctypes.c_void_p), ("d_o", prnn_seq_t),
+        ("d_state_out", ctypes.c_void_p), ("d_q", prnn_seq_t), ("d_k", prnn_seq_t), ("d_v", prnn_seq_t),
+        ("d_log_decay", prnn_seq_t), ("d_beta", prnn_seq_t), ("d_state", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
 # The same layout for struct.pack, which fills it in one call (a decoding step
 # is short enough for the difference to show).
 _LA_PACK = struct.Struct("=7if40q").pack
 _STEP_PACK = struct.Struct("=7if19q168x").pack   # up to o; the step uses no field behind it
+
+_GD_PACK = struct.Struct("=7if55q").pack
+_GD_STEP_PACK = struct.Struct("=7if26q232x").pack   # up to o
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -157,6 +173,10 @@ _sig = {
     "prnn_linear_attention_forward": ([_A, _P], _I),
     "prnn_linear_attention_backward": ([_A, _P], _I),
     "prnn_linear_attention_step": ([_A, _P, _I, _P, _P], _I),
+    "prnn_gated_delta_workspace": ([_A, _I, ctypes.POINTER(ctypes.c_size_t)], _I),
+    "prnn_gated_delta_forward": ([_A, _P], _I),
+    "prnn_gated_delta_backward": ([_A, _P], _I),
+    "prnn_gated_delta_step": ([_A, _P, _I, _P, _P], _I),
 }
 for _name, (_args, _res) in _sig.items():
     _fn = getattr(_lib, _name)
@@ -492,6 +512,26 @@ def prnn_linear_attention_backward(a: bytes, stream=None) -> None:
 def prnn_linear_attention_step(a: bytes, state_pool, n_slots, slots=None, stream=None) -> None:
     _check(_lib.prnn_linear_attention_step(a, _ptr(state_pool), n_slots, _ptr(slots),
                                            _stream(stream)), "prnn_linear_attention_step")
+
+
+def prnn_gated_delta_workspace(a: bytes, backward) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.prnn_gated_delta_workspace(a, backward, ctypes.byref(n)), "prnn_gated_delta_workspace")
+    return n.value
+
+
+def prnn_gated_delta_forward(a: bytes, stream=None) -> None:
+    """`a`: a prnn_gated_delta_t as bytes."""
+    _check(_lib.prnn_gated_delta_forward(a, _stream(stream)), "prnn_gated_delta_forward")
+
+
+def prnn_gated_delta_backward(a: bytes, stream=None) -> None:
+    _check(_lib.prnn_gated_delta_backward(a, _stream(stream)), "prnn_gated_delta_backward")
+
+
+def prnn_gated_delta_step(a: bytes, state_pool, n_slots, slots=None, stream=None) -> None:
+    _check(_lib.prnn_gated_delta_step(a, _ptr(state_pool), n_slots, _ptr(slots), _stream(stream)),
+           "prnn_gated_delta_step")
 
 
 # ---- sequence operators on tensors -------------------------------------------------
@@ -973,6 +1013,136 @@ def linear_attention_step(q, k, v, log_decay, state, scale=1.0, slots=None, o=No
     _check(_lib.prnn_linear_attention_step(
         a, pool, n_slots, _vector(slots, B, _torch.int32, dev, what + "slots"), st),
         "prnn_linear_attention_step")
+    return o
+
+
+def _gate(t, shape, device, what):
+    """(address, strides) of fp32 gates [T, B, heads] of any strides, for prnn_seq_t."""
+    if t.shape != shape or t.dtype is not _torch.float32 or t.get_device() != device:
+        raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype} on device {t.get_device()}, expected "
+                         f"{tuple(shape)} float32 on device {device}")
+    return t.data_ptr(), *t.stride()
+
+
+def gated_delta_rule(q, k, v, log_decay, beta, scale=1.0, state=None, lens=None, o=None, stream=None):
+    """The gated delta rule over whole sequences (prnn_gated_delta_forward).  q, k [T, B, qk_heads, dk],
+    v [T, B, heads, dv], any strides with the last axis contiguous; log_decay (<= 0) and beta fp32
+    [T, B, heads], any strides; state fp32 [B, heads, dk, dv] or None (zeros); lens int32 [B] on the device
+    or None.  Returns (o [T, B, heads, dv], the state after the last token)."""
+    if stream is not None:
+        import torch
+        with torch.cuda.stream(stream):
+            out = gated_delta_rule(q, k, v, log_decay, beta, scale, state, lens, o)
+        _used_on(stream, q, k, v, log_decay, beta, state, lens, o)
+        return out
+    what = "gated_delta_rule: "
+    code, dev, st = _start(q, what + "q")
+    _attention_shape(q, v)
+    qs, vs, dt = q.shape, v.shape, q.dtype
+    T, B, H, dv = vs
+    Hq, dk = qs[2:]
+    on, shape = q.device, (B, H, dk, dv)
+    if o is None:
+        o = _torch.empty(vs, dtype=dt, device=on)
+        o4 = (o.data_ptr(), B * H * dv, H * dv, dv)
+    else:
+        o4 = _seq4(o, vs, dt, dev, what + "o")
+    end = _torch.empty(shape, dtype=_torch.float32, device=on)
+    head = (code, T, B, H, Hq, dk, dv, scale, _vector(lens, B, _torch.int32, dev, what + "lens"),
+            *_seq4(q, qs, dt, dev, what + "q"), *_seq4(k, qs, dt, dev, what + "k"),
+            *_seq4(v, vs, dt, dev, what + "v"), *_gate(log_decay, vs[:3], dev, what + "log_decay"),
+            *_gate(beta, vs[:3], dev, what + "beta"), _state(state, shape, dev, what + "state"), *o4,
+            end.data_ptr(), *_NO_SEQ, 0, *_NO_SEQ, *_NO_SEQ, *_NO_SEQ, *_NO_SEQ, *_NO_SEQ, 0)
+    ws, p, need = _delta_workspace(head, 0, dev, on)
+    _check(_lib.prnn_gated_delta_forward(_GD_PACK(*head, p, need), st), "prnn_gated_delta_forward")
+    return o, end
+
+
+def _delta_workspace(head, backward, dev, on):
+    """(tensor, its address, its bytes); it must outlive the call.  The size depends on the sizes alone."""
+    key = ("delta", dev, backward, *head[:7])
+    need = _sizes.get(key)
+    if need is None:
+        if len(_sizes) > 4096:
+            _sizes.clear()
+        need = _sizes[key] = prnn_gated_delta_workspace(_GD_PACK(*head, 0, 0), backward)
+    if need == 0:
+        return None, 0, 0
+    ws = _torch.empty(need, dtype=_torch.uint8, device=on)
+    return ws, ws.data_ptr(), need
+
+
+def gated_delta_rule_backward(do, q, k, v, log_decay, beta, scale=1.0, state=None, lens=None, dstate=None,
+                              stream=None) -> dict:
+    """Gradients of gated_delta_rule for the loss whose gradient is `do` with respect to o and `dstate` (or
+    None) with respect to the returned state: dict of dq, dk, dv, dlog_decay and dbeta (fp32 [T, B, heads]) and,
+    when a state was given, dstate."""
+    if stream is not None:
+        import torch
+        with torch.cuda.stream(stream):
+            out = gated_delta_rule_backward(do, q, k, v, log_decay, beta, scale, state, lens, dstate)
+        _used_on(stream, do, q, k, v, log_decay, beta, state, lens, dstate)
+        return out
+    what = "gated_delta_rule_backward: "
+    code, dev, st = _start(q, what + "q")
+    _attention_shape(q, v)
+    qs, vs, dt = q.shape, v.shape, q.dtype
+    T, B, H, dv = vs
+    Hq, dk = qs[2:]
+    on, shape, f32 = q.device, (B, H, dk, dv), _torch.float32
+    dq, dkk = (_torch.empty(qs, dtype=dt, device=on) for _ in range(2))
+    dvv = _torch.empty(vs, dtype=dt, device=on)
+    dg, db = (_torch.empty(vs[:3], dtype=f32, device=on) for _ in range(2))
+    g = {"dq": dq, "dk": dkk, "dv": dvv, "dlog_decay": dg, "dbeta": db}
+    if state is not None:
+        g["dstate"] = _torch.empty(shape, dtype=f32, device=on)
+    qd, gd = (B * Hq * dk, Hq * dk, dk), (B * H, H, 1)
+    head = (code, T, B, H, Hq, dk, dv, scale, _vector(lens, B, _torch.int32, dev, what + "lens"),
+            *_seq4(q, qs, dt, dev, what + "q"), *_seq4(k, qs, dt, dev, what + "k"),
+            *_seq4(v, vs, dt, dev, what + "v"), *_gate(log_decay, vs[:3], dev, what + "log_decay"),
+            *_gate(beta, vs[:3], dev, what + "beta"), _state(state, shape, dev, what + "state"), *_NO_SEQ, 0,
+            *_seq4(do, vs, dt, dev, what + "do"), _state(dstate, shape, dev, what + "dstate"),
+            dq.data_ptr(), *qd, dkk.data_ptr(), *qd, dvv.data_ptr(), B * H * dv, H * dv, dv,
+            dg.data_ptr(), *gd, db.data_ptr(), *gd, g["dstate"].data_ptr() if state is not None else 0)
+    ws, p, need = _delta_workspace(head, 1, dev, on)
+    _check(_lib.prnn_gated_delta_backward(_GD_PACK(*head, p, need), st), "prnn_gated_delta_backward")
+    return g
+
+
+def gated_delta_rule_step(q, k, v, log_decay, beta, state, scale=1.0, slots=None, o=None, stream=None):
+    """One token of the gated delta rule for each sequence (prnn_gated_delta_step): q, k [B, qk_heads, dk],
+    v [B, heads, dv], log_decay and beta fp32 [B, heads]; state fp32 [n, heads, dk, dv], updated in place:
+    sequence b's is state[slots[b]] (int32 on the device; outside 0 .. n-1 marks a padding row), or state[b].
+    Returns o [B, heads, dv]."""
+    if stream is not None:
+        import torch
+        with torch.cuda.stream(stream):
+            out = gated_delta_rule_step(q, k, v, log_decay, beta, state, scale, slots, o)
+        _used_on(stream, q, k, v, log_decay, beta, state, slots, o)
+        return out
+    what = "gated_delta_rule_step: "
+    code, dev, st = _start(q, what + "q")
+    if q.ndim != 3 or v.ndim != 3 or q.shape[0] != v.shape[0]:
+        raise ValueError(f"q {tuple(q.shape)} and v {tuple(v.shape)}: expected [B, qk_heads, dk] and "
+                         "[B, heads, dv]")
+    qs, vs, dt = q.shape, v.shape, q.dtype
+    B, H, dv = vs
+    Hq, dk = qs[1:]
+    qb, qh = _step_strides(q, qs, dt, dev, what + "q")
+    kb, kh = _step_strides(k, qs, dt, dev, what + "k")
+    vb, vh = _step_strides(v, vs, dt, dev, what + "v")
+    gp, gb, gh = _gate(log_decay, vs[:2], dev, what + "log_decay")
+    bp, bb, bh = _gate(beta, vs[:2], dev, what + "beta")
+    if o is None:
+        o, ob, oh = _torch.empty(vs, dtype=dt, device=q.device), H * dv, dv
+    else:
+        ob, oh = _step_strides(o, vs, dt, dev, what + "o")
+    n_slots = state.shape[0]
+    pool = _state(state, (n_slots, H, dk, dv), dev, what + "state")
+    a = _GD_STEP_PACK(code, 1, B, H, Hq, dk, dv, scale, 0, q.data_ptr(), 0, qb, qh, k.data_ptr(), 0, kb, kh,
+                      v.data_ptr(), 0, vb, vh, gp, 0, gb, gh, bp, 0, bb, bh, 0, o.data_ptr(), 0, ob, oh)
+    _check(_lib.prnn_gated_delta_step(a, pool, n_slots, _vector(slots, B, _torch.int32, dev, what + "slots"), st),
+           "prnn_gated_delta_step")
     return o
 
 
