@@ -20,18 +20,24 @@ struct GdArgs {
   long long ot, ob, oh;
   float* state_out;             // may be null
   const float* d_state_out;     // may be null
-  void* dv_out;                 // may be null
-  long long dvt, dvb, dvh;
+  void *dq_out, *dk_out, *dv_out;  // may be null
+  long long dqt, dqb, dqh, dkt, dkb, dkh, dvt, dvb, dvh;
   float *dg, *dbeta;            // may be null
   long long dgt, dgb, dgh, dbt, dbb, dbh;
   float* d_state;               // may be null
   // scratch, fp32: [T][B][H][dv] e (null: not kept) and du, [T][B][H][dk] gradients before shared heads are summed,
-  // the states at the ends of blocks [blocks][B*H][dk][dv] and their products with the gradients [blocks][B*H][dk]
+  // (tensor cores: null where no heads share theirs), the states at the ends of blocks [blocks][B*H][dk][dv] and their products with the gradients [blocks][B*H][dk]
   float *e, *du, *dq_part, *dk_part, *marks, *leaves;
 };
 
 cudaError_t launch_gd_walk_forward(const GdArgs& a, cudaStream_t s);
 cudaError_t launch_gd_walk_backward(const GdArgs& a, cudaStream_t s);
+
+// On the tensor cores, in chunks, for dk and dv up to 128: whether it serves a call, its scratch, the call.
+constexpr int kGdTcLeast = 32;  // tokens
+bool gd_tc_serves(prnn_dtype_t dtype, int T, int dk, int dv);
+size_t gd_tc_workspace(prnn_dtype_t dtype, int T, int B, int H, int dk, int dv, bool backward);
+cudaError_t launch_gd_tc(const GdArgs& a, void* scratch, bool backward, cudaStream_t s);
 
 struct GdStepArgs {
   prnn_dtype_t dtype;

@@ -89,6 +89,8 @@ Parts walk_parts(const Call* a) {
   return p;
 }
 
+bool on_tensor_cores(const Call* a) { return gd_tc_serves(a->dtype, a->T, a->dk, a->dv); }
+
 GdArgs common(const Call* a) {
   GdArgs g{};
   g.dtype = a->dtype;
@@ -125,7 +127,12 @@ prnn_status_t prnn_gated_delta_workspace(const prnn_gated_delta_t* a, int backwa
   if (!shape_ok(a, &why)) return why;
   *bytes = 0;
   if (a->T == 0 || a->B == 0) return PRNN_OK;
-  if (backward) *bytes = walk_parts(a).total;
+  if (on_tensor_cores(a)) {
+    *bytes = gd_tc_workspace(a->dtype, a->T, a->B, a->heads, a->dk, a->dv, backward != 0);
+    if (backward && a->heads > a->qk_heads) *bytes += 2 * walk_parts(a).dq;
+  } else if (backward) {
+    *bytes = walk_parts(a).total;
+  }
   return PRNN_OK;
 }
 
@@ -159,7 +166,7 @@ prnn_status_t prnn_gated_delta_forward(const prnn_gated_delta_t* a, void* stream
   g.ob = a->o.stride_b;
   g.oh = a->o.stride_h;
   g.state_out = a->state_out;
-  return cuda_status(launch_gd_walk_forward(g, s));
+  return cuda_status(on_tensor_cores(a) ? launch_gd_tc(g, a->workspace, false, s) : launch_gd_walk_forward(g, s));
 }
 
 prnn_status_t prnn_gated_delta_backward(const prnn_gated_delta_t* a, void* stream) {
@@ -197,6 +204,14 @@ prnn_status_t prnn_gated_delta_backward(const prnn_gated_delta_t* a, void* strea
   g.d_o = in(a->d_o, 1);
   g.d_state_out = a->d_state_out;
   g.d_state = a->d_state;
+  g.dq_out = a->d_q.data;
+  g.dqt = a->d_q.stride_t;
+  g.dqb = a->d_q.stride_b;
+  g.dqh = a->d_q.stride_h;
+  g.dk_out = a->d_k.data;
+  g.dkt = a->d_k.stride_t;
+  g.dkb = a->d_k.stride_b;
+  g.dkh = a->d_k.stride_h;
   g.dv_out = a->d_v.data;
   g.dvt = a->d_v.stride_t;
   g.dvb = a->d_v.stride_b;
@@ -216,13 +231,21 @@ prnn_status_t prnn_gated_delta_backward(const prnn_gated_delta_t* a, void* strea
     w += n;
     return at;
   };
-  g.e = take(p.e);
-  g.du = take(p.e);
-  g.dq_part = take(p.dq);
-  g.dk_part = take(p.dq);
-  g.marks = take(p.marks);
-  g.leaves = take(p.leaves);
-  PRNN_TRY(launch_gd_walk_backward(g, s));
+  const bool tc = on_tensor_cores(a);
+  if (!tc || H > Hq) {
+    g.dq_part = take(p.dq);
+    g.dk_part = take(p.dq);
+  }
+  if (tc) {
+    PRNN_TRY(launch_gd_tc(g, w, true, s));
+    if (H == Hq) return PRNN_OK;
+  } else {
+    g.e = take(p.e);
+    g.du = take(p.e);
+    g.marks = take(p.marks);
+    g.leaves = take(p.leaves);
+    PRNN_TRY(launch_gd_walk_backward(g, s));
+  }
   const prnn_seq_t* out[] = {&a->d_q, &a->d_k};
   const float* part[] = {g.dq_part, g.dk_part};
   for (int i = 0; i < 2; ++i)

@@ -1,0 +1,314 @@
+// gated_delta_tc.cuh -- what the gated delta rule's tensor-core kernels share.
+//
+// A chunk of C tokens entered with the state S0, G the running sum of its log-decays, D_ij = exp(G_i - G_j) for
+// j <= i:
+//   M = strict_lower((K K^T) o D),   Tt = (I + M diag(beta))^-1,   W = Tt diag(e^G) K,
+//   E = Tt V - W S0,   U = beta E,   o = scale (e^G Q S0 + ((Q K^T) o D) U),   S <- e^G_C S0 + (e^(G_C - G) K)^T U;
+// and backwards, R the loss's gradient by the state that leaves it, dO times scale:
+//   X = ((Q K^T) o D)^T dO + e^(G_C - G) K R,   R <- e^G_C R + (e^G Q)^T dO - W^T (beta X),   dV = Tt^T (beta X),
+//   dbeta_i = e_i . du_i,  du_i = dv_i / beta_i = x_i - sum_{j > i} M_ji dv_j,
+//   Y = strict_lower((dV U^T) o D), Z = (dO U^T) o D:
+//   dQ = e^G dO S0^T + Z K,   dK = e^(G_C - G) U R^T + Z^T Q - (Y + Y^T) K - e^G dV S0^T,
+//   dlog_decay_t = sum_{i >= t} (q_i . dq_i - v_i . dv_i) + <S_C, R>.
+// All but the two lines with S0 and R on both sides go chunk by chunk side by side; those are walked by one kernel in
+// two roles.
+//
+// Every operand is a sum of bf16 parts: the data exactly (bf16 one part, fp16 two, fp32 three of 8 bits each), what is
+// computed in between three (24 bits), two where it feeds 16-bit outputs only; products of parts below 2^-24 of the
+// whole are left out, all sums are fp32.  bf16 has fp32's range, so nothing is scaled to fit.  Log-decays are
+// summed in 64 bits and kept as two fp32 values, so that differences of distant sums keep their bits; one below
+// -1000 counts as -1000 (exp is 0 from -104), which keeps those differences finite.
+#pragma once
+
+#include "gated_delta.h"
+#include "seq_tc.cuh"
+
+namespace prnn {
+namespace gd {
+
+using namespace tc;
+using bf16 = __nv_bfloat16;
+
+constexpr int C = 128, kThreads = 256, kP = 3;        // tokens per chunk; threads; parts of computed values
+constexpr uint32_t kTile = 16384;                     // [128][64] bf16, 128-byte swizzled
+template <typename T>
+constexpr int kData = std::is_same<T, float>::value ? 3 : (std::is_same<T, __half>::value ? 2 : 1);
+
+// Per chunk and head, fp32 [128] each: sums of log-decays in two parts, their exponentials, those to the
+// chunk's end, betas.
+struct Gates {
+  float hi[C], lo[C], up[C], down[C], beta[C];
+};
+
+struct Args {
+  GdArgs a;
+  int chunks, bh0, nbh;        // chunks of T; the heads of this launch: bh0 ... bh0 + nbh
+  int dkt, dvt;                // tiles of 64 columns
+  bool vec;                    // data tensors allow 16-byte loads
+  int* status;
+  // scratch per (head, chunk): W and K as operand tiles [dkt][parts][128][64]; fp32 matrices in quads of
+  // columns, [cols / 4][rows][4]: E and X [128][64 dvt], states (a slot more per head) and their gradients
+  // [64 dkt][64 dvt], Tt [128][128], Z0 = (e^G Q)^T dO
+  unsigned char *wimg, *kimg;
+  Gates* gates;
+  float *E, *S, *inv, *X, *Z0, *R;
+};
+
+__device__ __forceinline__ int length_of(const GdArgs& a, int b) {
+  int len = a.T;
+  if (a.lens) {
+    len = a.lens[b];
+    len = len < 0 ? 0 : (len > a.T ? a.T : len);
+  }
+  return len;
+}
+struct Place {  // of one block: a head's chunk
+  int bh, b, h, hq, c, n, len;
+  size_t at, slot;  // index of the chunk's scratch, of its state
+  long long t0;
+};
+__device__ __forceinline__ Place place_of(const Args& g) {
+  Place p;
+  const int local = blockIdx.x / g.chunks;
+  p.c = blockIdx.x % g.chunks;
+  p.bh = g.bh0 + local;
+  p.b = p.bh / g.a.H;
+  p.h = p.bh % g.a.H;
+  p.hq = p.h / g.a.q.share;
+  p.len = length_of(g.a, p.b);
+  p.t0 = (long long)p.c * C;
+  const long long left = p.len - p.t0;
+  p.n = left < 0 ? 0 : (left > C ? C : (int)left);
+  p.at = (size_t)local * g.chunks + p.c;
+  p.slot = (size_t)local * (g.chunks + 1) + p.c;
+  return p;
+}
+template <typename T>
+__device__ __forceinline__ const T* rows_of(const LaSeq& x, long long t0, int b, int head) {
+  return static_cast<const T*>(x.p) + t0 * x.st + b * x.sb + head * x.sh;
+}
+
+// exp(G_i - G_j).
+__device__ __forceinline__ float decay_between(float hi_i, float lo_i, float hi_j, float lo_j) {
+  return expf((hi_i - hi_j) + (lo_i - lo_j));
+}
+
+// 8 values of row r, columns 8 chunk ..., as P parts into tiles `stride` bytes apart.
+template <int P>
+__device__ __forceinline__ void put8(unsigned char* tile, uint32_t stride, int r, int chunk, float2 (&v)[4]) {
+  const uint32_t at = (uint32_t)(r * 128 + ((chunk ^ (r & 7)) << 4));
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    uint4 u;
+    u.x = take<bf16>(v[0]);
+    u.y = take<bf16>(v[1]);
+    u.z = take<bf16>(v[2]);
+    u.w = take<bf16>(v[3]);
+    *reinterpret_cast<uint4*>(tile + p * stride + at) = u;
+  }
+}
+
+// 8 values from p, of which the first m count.
+template <typename T>
+__device__ __forceinline__ void get8(const T* p, int m, bool vec, float2 (&v)[4]) {
+  if (vec && m >= 8) {
+    if constexpr (sizeof(T) == 2) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+      v[0] = unpack<T>(u.x);
+      v[1] = unpack<T>(u.y);
+      v[2] = unpack<T>(u.z);
+      v[3] = unpack<T>(u.w);
+    } else {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+      v[0] = make_float2(a.x, a.y);
+      v[1] = make_float2(a.z, a.w);
+      v[2] = make_float2(b.x, b.y);
+      v[3] = make_float2(b.z, b.w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = make_float2(2 * i < m ? to_f32(p[2 * i]) : 0.f, 2 * i + 1 < m ? to_f32(p[2 * i + 1]) : 0.f);
+  }
+}
+
+// Rows [r0, r0 + rows) of a data tensor (from its row of token 0 of the chunk), columns [c0, c0 + 64) of d, as P parts
+// into a tile of `rows` rows; zeros past n rows and d columns.  Each row times scale[row] where that is given.  Eight
+// neighbouring threads take a row.  img: a copy of the tile in device memory, parts kTile apart.
+template <typename T, int P>
+__device__ __forceinline__ void load_data(unsigned char* tile, uint32_t stride, const T* x, long long st, int r0,
+                                          int rows, int n, int c0, int d, bool vec, const float* scale,
+                                          unsigned char* img = nullptr) {
+  for (int u = threadIdx.x; u < rows * 8; u += kThreads) {
+    const int r = r0 + (u >> 3), chunk = u & 7, c = c0 + chunk * 8;
+    float2 v[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
+    if (r < n && c < d) get8<T>(x + r * st + c, d - c, vec, v);
+    if (scale) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = r < n ? mul2(v[i], both(scale[r])) : both(0.f);
+    }
+    float2 w[4] = {v[0], v[1], v[2], v[3]};
+    put8<P>(tile, stride, u >> 3, chunk, v);
+    if (img) put8<P>(img, kTile, r, chunk, w);
+  }
+}
+// The same from an fp32 matrix of R rows in quads; a row per lane.
+template <int P>
+__device__ __forceinline__ void load_quads(unsigned char* tile, uint32_t stride, const float* m, int R, int rows, int c0,
+                                           const float* scale) {
+  for (int u = threadIdx.x; u < rows * 8; u += kThreads) {
+    const int r = u % rows, chunk = u / rows;
+    const float4* q = reinterpret_cast<const float4*>(m) + ((size_t)(c0 / 4 + 2 * chunk) * R + r);
+    const float4 a = q[0], b = q[R];
+    float2 v[4] = {make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)};
+    if (scale) {
+      const float2 f = both(scale[r]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], f);
+    }
+    put8<P>(tile, stride, r, chunk, v);
+  }
+}
+
+// An operand: descriptor of its first part, bytes from one part to the next, and of its steps of 16 along K.
+struct Operand {
+  uint64_t desc;
+  uint32_t part, tile;  // units of 16 bytes; tile 0: MN-major, K along the rows
+  __device__ __forceinline__ uint64_t at(int p, int k) const {
+    return desc + p * part + (tile ? (k >> 2) * tile + (k & 3) * 2 : k * 128);
+  }
+};
+__device__ __forceinline__ Operand k_major(uint32_t addr, uint32_t part, uint32_t tile) {
+  return {sw128_kmajor_desc(addr), part >> 4, tile >> 4};
+}
+__device__ __forceinline__ Operand mn_major(uint32_t addr, uint32_t part, uint32_t tile) {
+  return {mn_desc(addr, tile), part >> 4, 0};
+}
+// D (+)= A B over `steps` steps of 16: every pair of parts whose places add up to less than three, small ones first.
+template <int PA, int PB>
+__device__ __forceinline__ void product(uint32_t d, const Operand& a, const Operand& b, int steps, uint32_t id,
+                                        bool add) {
+  uint32_t acc = add;
+#pragma unroll
+  for (int s = PA + PB - 2 < 2 ? PA + PB - 2 : 2; s >= 0; --s)
+#pragma unroll
+    for (int p = 0; p < PA; ++p) {
+      if (s - p < 0 || s - p >= PB) continue;
+      for (int k = 0; k < steps; ++k) {
+        umma_f16(d, a.at(p, k), b.at(s - p, k), id, acc);
+        acc = 1;
+      }
+    }
+}
+__device__ __forceinline__ uint32_t id_of(int n, bool a_mn, bool b_mn) {
+  return bf16_idesc(128, n) | (a_mn ? kAMn : 0u) | (b_mn ? kBMn : 0u);
+}
+
+// Blocks that work in step: operands are placed by all threads, one thread issues the products, all wait for them.
+struct Steps {
+  uint64_t* bar;
+  uint32_t turn = 0;
+  bool ok = true;
+  template <typename F>
+  __device__ __forceinline__ void run(F&& issue) {
+    to_async();
+    before_sync();
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      if (elected()) {
+        after_sync();
+        issue();
+        umma_commit(bar);
+      }
+      __syncwarp();
+    }
+  }
+  __device__ __forceinline__ void wait() {
+    seq_wait(bar, turn & 1, ok);
+    ++turn;
+    __syncwarp();
+    after_sync();
+  }
+};
+
+// Set-up and end of a block that works in step: a barrier and `cols` columns of tensor memory.
+__device__ __forceinline__ bool begin(uint64_t* bar, uint32_t* tmem, uint32_t cols, const unsigned char* smem,
+                                      int* status) {
+  if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it; no static shared memory precedes them
+    if (threadIdx.x == 0) atomicExch(status, 1);
+    return false;
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(bar, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (threadIdx.x < 32) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  before_sync();
+  __syncthreads();
+  after_sync();
+  return true;
+}
+__device__ __forceinline__ void finish(uint32_t tmem, uint32_t cols, bool ok, int* status) {
+  if (!ok) atomicExch(status, 1);
+  before_sync();
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    after_sync();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
+  }
+}
+
+// 16 columns of this thread's row of an accumulator.
+__device__ __forceinline__ void read16(uint32_t at, float2 (&v)[8]) {
+  uint32_t r[16];
+  tmem_ld16(at, r);
+  wait_ld();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = pair_at(r, i);
+}
+// 16 columns c0 ... of row r to an fp32 matrix of R rows in quads.
+__device__ __forceinline__ void store_quads(float* m, int R, int r, int c0, const float2 (&v)[8]) {
+  float4* q = reinterpret_cast<float4*>(m) + ((size_t)(c0 / 4) * R + r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) q[(size_t)i * R] = make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
+}
+// 16 values as P parts: row r, columns c0 ... of tiles of 64 columns, parts `stride` bytes apart.
+template <int P>
+__device__ __forceinline__ void put16(unsigned char* tiles, uint32_t stride, int r, int c0, const float2 (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float2 w[4] = {v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
+    put8<P>(tiles + (c0 >> 6) * kTile, stride, r, ((c0 & 63) >> 3) + j, w);
+  }
+}
+// 16 values of one row at p, of which the first m are the output's.
+template <typename T>
+__device__ __forceinline__ void store16(T* p, int m, bool vec, const float2 (&v)[8]) {
+  constexpr int V = 16 / sizeof(T);
+  if (vec && m >= 16) {
+#pragma unroll
+    for (int i = 0; i < 16 / V; ++i) {
+      Pack<T, V> o;
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) set_pair<T, V>(o, j, v[i * V / 2 + j]);
+      store_pack<T, V>(p + i * V, o);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < m) p[i] = from_f32<T>(i & 1 ? v[i / 2].y : v[i / 2].x);
+  }
+}
+
+cudaError_t launch_prepare(const Args& g, bool keep_inverse, cudaStream_t s);
+cudaError_t launch_chain(const Args& g, bool reverse, cudaStream_t s);
+cudaError_t launch_outputs(const Args& g, cudaStream_t s);
+cudaError_t launch_before_reverse(const Args& g, cudaStream_t s);
+cudaError_t launch_gradients(const Args& g, cudaStream_t s);
+
+}  // namespace gd
+}  // namespace prnn

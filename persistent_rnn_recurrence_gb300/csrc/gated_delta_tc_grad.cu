@@ -1,0 +1,433 @@
+// gated_delta_tc_grad.cu -- the chunks' gradients of the gated delta rule on the 5th-generation tensor cores: what the
+// walk over the states' gradients needs beforehand, and what follows from it.  The algebra and the rounding are in
+// gated_delta_tc.cuh.
+#include "gated_delta_tc.cuh"
+
+namespace prnn {
+namespace gd {
+namespace {
+
+// Two operands of [128][128] in three parts, and a third by pieces of 64 columns and as many tokens as fit.
+constexpr uint32_t kMatrix = kP * 2 * kTile, kOne = 0, kTwo = kMatrix, kThree = 2 * kMatrix, kPiece = 24 * 1024,
+                   kTab = kThree + kPiece;
+struct Tab {
+  Gates gates;
+  float rows[2][3][C];   // per half of the columns: q . dq, v . dv, and dbeta's sum
+  float leaves[8];
+  uint64_t bar;
+  uint32_t tmem;
+};
+static_assert(kTab + sizeof(Tab) <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ void copy_gates(Gates& to, const Gates* from) {
+  for (int i = threadIdx.x; i < (int)(sizeof(Gates) / 4); i += kThreads)
+    reinterpret_cast<float*>(&to)[i] = reinterpret_cast<const float*>(from)[i];
+}
+
+// A product over the chunk's tokens with a data tensor x (its rows tokens, MN-major) as the right operand,
+// d += left x, or twice with two left operands, piece by piece.  The left one has PA parts.
+template <typename T, typename F>
+__device__ __forceinline__ void over_tokens(Steps& steps, unsigned char* smem, const T* x, long long st, int n, int d,
+                                            int tiles, bool vec, F&& issue) {
+  constexpr int DP = kData<T>, ROWS = DP * kTile <= kPiece ? C : C / 2;
+  for (int ct = 0; ct < tiles; ++ct)
+    for (int r0 = 0; r0 < C && r0 < n; r0 += ROWS) {
+      load_data<T, DP>(smem + kThree, ROWS * 128, x, st, r0, ROWS, n, ct * 64, d, vec, nullptr);
+      steps.run([&] {
+        issue(ct, r0 / 16, mn_major(smem_u32(smem) + kThree, ROWS * 128, ROWS * 128), ROWS / 16, r0 > 0);
+      });
+      steps.wait();
+    }
+}
+// The left operand of such a product from its step of 16 tokens on.
+__device__ __forceinline__ Operand from_step(Operand o, int k) {
+  o.desc += o.tile ? (k >> 2) * o.tile + (k & 3) * 2 : k * 128;
+  return o;
+}
+
+// ---- before the walk backwards: X0 = ((Q K^T) o D)^T dO, Z0 = (e^G Q)^T dO, dO times scale -------------------
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1) gd_before_reverse_kernel(const __grid_constant__ Args g) {
+  constexpr int DP = kData<T>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  Tab& tab = *reinterpret_cast<Tab*>(smem + kTab);
+  const GdArgs& a = g.a;
+  const Place p = place_of(g);
+  if (p.n == 0) return;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = (warp & 3) * 32 + lane, half = warp >> 2;
+  if (!begin(&tab.bar, &tab.tmem, 512, smem, g.status)) return;
+  Steps steps{&tab.bar};
+  const uint32_t tmem = tab.tmem, mine = tmem + ((uint32_t)((warp & 3) * 32) << 16), base = smem_u32(smem);
+  copy_gates(tab.gates, g.gates + p.at);
+  const int rows = 64 * g.dkt, cols = 64 * g.dvt;
+  const uint32_t part = g.dkt * kTile;
+  const T *q = rows_of<T>(a.q, p.t0, p.b, p.hq), *k = rows_of<T>(a.k, p.t0, p.b, p.hq),
+          *d_o = rows_of<T>(a.d_o, p.t0, p.b, p.h);
+  for (int ct = 0; ct < g.dkt; ++ct) {
+    load_data<T, DP>(smem + kOne + ct * kTile, part, q, a.q.st, 0, C, p.n, ct * 64, a.dk, g.vec, nullptr);
+    load_data<T, DP>(smem + kTwo + ct * kTile, part, k, a.k.st, 0, C, p.n, ct * 64, a.dk, g.vec, nullptr);
+  }
+  steps.run([&] {
+    product<DP, DP>(tmem, k_major(base + kOne, part, kTile), k_major(base + kTwo, part, kTile), (a.dk + 15) / 16,
+                    id_of(128, false, false), false);
+  });
+  steps.wait();
+  if (tid < C) tab.rows[0][0][tid] = a.scale * tab.gates.up[tid];
+  const float hi = tab.gates.hi[row], lo = tab.gates.lo[row];
+#pragma unroll 1
+  for (int x = 0; x < 4; ++x) {
+    const int c0 = half * 64 + x * 16;
+    float2 v[8];
+    read16(mine + c0, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int j = c0 + 2 * i;
+      v[i].x = j <= row ? a.scale * v[i].x * decay_between(hi, lo, tab.gates.hi[j], tab.gates.lo[j]) : 0.f;
+      v[i].y = j < row ? a.scale * v[i].y * decay_between(hi, lo, tab.gates.hi[j + 1], tab.gates.lo[j + 1]) : 0.f;
+    }
+    put16<kP>(smem + kTwo, 2 * kTile, row, c0, v);
+  }
+  __syncthreads();
+  for (int ct = 0; ct < g.dkt; ++ct)
+    load_data<T, kP>(smem + kOne + ct * kTile, part, q, a.q.st, 0, C, p.n, ct * 64, a.dk, g.vec, tab.rows[0][0]);
+  const Operand P = mn_major(base + kTwo, 2 * kTile, kTile), Q = mn_major(base + kOne, part, kTile);
+  over_tokens<T>(steps, smem, d_o, a.d_o.st, p.n, a.dv, g.dvt, g.vec,
+                 [&](int ct, int k0, const Operand& right, int n, bool add) {
+    product<kP, DP>(tmem + 128 + 64 * ct, from_step(P, k0), right, n, id_of(64, true, true), add);
+    product<kP, DP>(tmem + 256 + 64 * ct, from_step(Q, k0), right, n, id_of(64, true, true), add);
+  });
+  float *X = g.X + p.at * C * cols, *Z0 = g.Z0 + p.at * rows * cols;
+#pragma unroll 1
+  for (int x = 0; x < 2 * g.dvt; ++x) {
+    const int c0 = (half * 2 * g.dvt + x) * 16;
+    float2 v[8];
+    read16(mine + 128 + c0, v);
+    store_quads(X, C, row, c0, v);
+    read16(mine + 256 + c0, v);
+    if (row < rows) store_quads(Z0, rows, row, c0, v);
+  }
+  finish(tmem, 512, steps.ok, g.status);
+}
+
+// ---- the gradients of a chunk ----------------------------------------------------------------------------
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_constant__ Args g, bool dq_vec,
+                                                                   bool dk_vec, bool dv_vec) {
+  constexpr int DP = kData<T>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  Tab& tab = *reinterpret_cast<Tab*>(smem + kTab);
+  const GdArgs& a = g.a;
+  const Place p = place_of(g);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = (warp & 3) * 32 + lane, half = warp >> 2;
+  // where this head's rows of gradients go: the tensors themselves, or fp32 parts that are summed over heads later
+  const bool parts = a.dq_part != nullptr;
+  auto zero_rows = [&](auto* x, long long st, int d, int live) {
+    using E = std::remove_reference_t<decltype(*x)>;
+    for (int i = tid; i < (live - p.n) * d; i += kThreads) x[(p.t0 + p.n + i / d) * st + i % d] = from_f32<E>(0.f);
+  };
+  const int live = (int)(a.T - p.t0 < C ? a.T - p.t0 : C);
+  const long long part_t = (long long)a.B * a.H * a.dk, part_at = ((long long)p.b * a.H + p.h) * a.dk;
+  T *dq = static_cast<T*>(a.dq_out) + p.b * a.dqb + p.h * a.dqh, *dk = static_cast<T*>(a.dk_out) + p.b * a.dkb + p.h * a.dkh,
+    *dv = static_cast<T*>(a.dv_out) + p.b * a.dvb + p.h * a.dvh;
+  if (p.n < live) {
+    if (parts) {
+      zero_rows(a.dq_part + part_at, part_t, a.dk, live);
+      zero_rows(a.dk_part + part_at, part_t, a.dk, live);
+    } else {
+      if (a.dq_out) zero_rows(dq, a.dqt, a.dk, live);
+      if (a.dk_out) zero_rows(dk, a.dkt, a.dk, live);
+    }
+    if (a.dv_out) zero_rows(dv, a.dvt, a.dv, live);
+    for (int i = p.n + tid; i < live; i += kThreads) {
+      if (a.dg) a.dg[(p.t0 + i) * a.dgt + p.b * a.dgb + p.h * a.dgh] = 0.f;
+      if (a.dbeta) a.dbeta[(p.t0 + i) * a.dbt + p.b * a.dbb + p.h * a.dbh] = 0.f;
+    }
+  }
+  if (p.n == 0) return;
+  if (!begin(&tab.bar, &tab.tmem, 512, smem, g.status)) return;
+  Steps steps{&tab.bar};
+  const uint32_t tmem = tab.tmem, mine = tmem + ((uint32_t)((warp & 3) * 32) << 16), base = smem_u32(smem);
+  const uint32_t D0 = 0, D1 = 128, D2 = 256, D3 = 384;
+  copy_gates(tab.gates, g.gates + p.at);
+  __syncthreads();
+  const int rows = 64 * g.dkt, cols = 64 * g.dvt;
+  const uint32_t kpart = g.dkt * kTile, vpart = g.dvt * kTile;
+  const float *E = g.E + p.at * C * cols, *X = g.X + p.at * C * cols, *S = g.S + p.slot * rows * cols,
+              *R = g.R + p.at * rows * cols, *inv = g.inv + p.at * C * C;
+  const T *q = rows_of<T>(a.q, p.t0, p.b, p.hq), *k = rows_of<T>(a.k, p.t0, p.b, p.hq),
+          *v = rows_of<T>(a.v, p.t0, p.b, p.h), *d_o = rows_of<T>(a.d_o, p.t0, p.b, p.h);
+  const float hi = tab.gates.hi[row], lo = tab.gates.lo[row], up = tab.gates.up[row], down = tab.gates.down[row],
+              beta = tab.gates.beta[row];
+  const bool mine_live = row < p.n;
+  auto quads = [&](uint32_t where, const float* m, int R_, int rows_, int tiles, const float* scale) {
+    for (int t = 0; t < tiles; ++t) load_quads<kP>(smem + where + t * kTile, tiles * kTile, m, R_, rows_, t * 64, scale);
+  };
+  // this row's 16 values at columns c0 of a data tensor's row times v, summed
+  auto dot_row = [&](const T* x, int c0, int d, const float2 (&f)[8]) {
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float2 y[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
+      if (c0 + 8 * j < d) get8<T>(x + c0 + 8 * j, d - c0 - 8 * j, g.vec, y);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s = fmaf(y[i].x, f[4 * j + i].x, fmaf(y[i].y, f[4 * j + i].y, s));
+    }
+    return s;
+  };
+
+  // dV = Tt^T (beta X)
+  quads(kOne, inv, C, C, 2, nullptr);
+  quads(kTwo, X, C, C, g.dvt, tab.gates.beta);
+  steps.run([&] {
+    product<kP, kP>(tmem + D0, mn_major(base + kOne, 2 * kTile, kTile), mn_major(base + kTwo, vpart, kTile), 8,
+                    id_of(cols, true, true), false);
+  });
+  // dbeta_i = e_i . du_i, du_i = dv_i / beta_i = x_i - sum_{j > i} M_ji dv_j.  The quotient keeps its bits however small
+  // beta is (dv_i is beta_i times sums without it); the difference cancels where keys repeat, and stands for beta = 0.
+  const bool tiny = !(fabsf(beta) > 1e-20f);
+  const bool any_tiny = __syncthreads_or(tiny && mine_live);
+  float es = 0.f;  // e . x or e . dv
+  if (any_tiny)
+    for (int c = half * 32 * g.dvt; c < (half + 1) * 32 * g.dvt; c += 4) {
+      const size_t i = (size_t)(c / 4) * C + row;
+      const float4 e = reinterpret_cast<const float4*>(E)[i], x = reinterpret_cast<const float4*>(X)[i];
+      es = fmaf(e.x, x.x, fmaf(e.y, x.y, fmaf(e.z, x.z, fmaf(e.w, x.w, es))));
+    }
+  steps.wait();
+  {
+    float s = 0.f, ev = 0.f;
+#pragma unroll 1
+    for (int x = 0; x < 2 * g.dvt; ++x) {
+      const int c0 = (half * 2 * g.dvt + x) * 16;
+      float2 f[8];
+      read16(mine + D0 + c0, f);
+      if (mine_live) {
+        s += dot_row(v + row * a.v.st, c0, a.dv, f);
+        if (a.dv_out) store16<T>(dv + (p.t0 + row) * a.dvt + c0, a.dv - c0, dv_vec, f);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 e = reinterpret_cast<const float4*>(E)[(size_t)(c0 / 4 + i) * C + row];
+        ev = fmaf(e.x, f[2 * i].x, fmaf(e.y, f[2 * i].y, fmaf(e.z, f[2 * i + 1].x, fmaf(e.w, f[2 * i + 1].y, ev))));
+      }
+      put16<kP>(smem + kTwo, vpart, row, c0, f);
+    }
+    tab.rows[half][1][row] = s;
+    if (!tiny) es = ev / beta;
+  }
+  // dV E^T, E dV^T, and K K^T where a beta is 0
+  quads(kOne, E, C, C, g.dvt, nullptr);
+  const Operand one_v = k_major(base + kOne, vpart, kTile), two_v = k_major(base + kTwo, vpart, kTile);
+  const int vsteps = (a.dv + 15) / 16, ksteps = (a.dk + 15) / 16;
+  steps.run([&] {
+    product<kP, kP>(tmem + D0, two_v, one_v, vsteps, id_of(128, false, false), false);
+    product<kP, kP>(tmem + D1, one_v, two_v, vsteps, id_of(128, false, false), false);
+  });
+  steps.wait();
+  if (any_tiny) {
+    for (int ct = 0; ct < g.dkt; ++ct)
+      load_data<T, DP>(smem + kOne + ct * kTile, kpart, k, a.k.st, 0, C, p.n, ct * 64, a.dk, g.vec, nullptr);
+    steps.run([&] {
+      const Operand K = k_major(base + kOne, kpart, kTile);
+      product<DP, DP>(tmem + D2, K, K, ksteps, id_of(128, false, false), false);
+    });
+    steps.wait();
+  }
+  {  // -(Y + Y^T) as the next left operand, dbeta
+    float s = es;
+#pragma unroll 1
+    for (int x = 0; x < 4; ++x) {
+      const int c0 = half * 64 + x * 16;
+      float2 y1[8], y2[8], kk[8] = {};
+      read16(mine + D0 + c0, y1);
+      read16(mine + D1 + c0, y2);
+      if (any_tiny) read16(mine + D2 + c0, kk);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int j = c0 + i;
+        const float hj = tab.gates.hi[j], lj = tab.gates.lo[j];
+        const float f1 = i & 1 ? y1[i / 2].y : y1[i / 2].x, f2 = i & 1 ? y2[i / 2].y : y2[i / 2].x,
+                    fk = i & 1 ? kk[i / 2].y : kk[i / 2].x;
+        float y = 0.f;
+        if (j < row) {
+          y = -f1 * tab.gates.beta[j] * decay_between(hi, lo, hj, lj);
+        } else if (j > row) {
+          const float w = f2 * decay_between(hj, lj, hi, lo);
+          y = -w * beta;
+          if (tiny) s = fmaf(-fk, w, s);
+        }
+        if (i & 1) y1[i / 2].y = y;
+        else y1[i / 2].x = y;
+      }
+      put16<kP>(smem + kOne, 2 * kTile, row, c0, y1);
+    }
+    tab.rows[half][2][row] = s;
+  }
+  before_sync();
+  __syncthreads();
+  after_sync();
+  // D3 = -(Y + Y^T) K
+  const Operand one_t = k_major(base + kOne, 2 * kTile, kTile);
+  over_tokens<T>(steps, smem, k, a.k.st, p.n, a.dk, g.dkt, g.vec,
+                 [&](int ct, int k0, const Operand& right, int n, bool add) {
+    product<kP, DP>(tmem + D3 + 64 * ct, from_step(one_t, k0), right, n, id_of(64, false, true), add);
+  });
+  // D0 = dV S0^T
+  quads(kOne, S, rows, rows, g.dvt, nullptr);
+  steps.run([&] { product<kP, kP>(tmem + D0, two_v, one_v, vsteps, id_of(rows, false, false), false); });
+  steps.wait();
+  // D1 = dO S0^T
+  for (int vt = 0; vt < g.dvt; ++vt)
+    load_data<T, DP>(smem + kTwo + vt * kTile, vpart, d_o, a.d_o.st, 0, C, p.n, vt * 64, a.dv, g.vec, nullptr);
+  steps.run([&] { product<DP, kP>(tmem + D1, two_v, one_v, vsteps, id_of(rows, false, false), false); });
+  steps.wait();
+  // D2 = dO U^T
+  quads(kOne, E, C, C, g.dvt, tab.gates.beta);
+  steps.run([&] { product<DP, kP>(tmem + D2, two_v, one_v, vsteps, id_of(128, false, false), false); });
+  steps.wait();
+#pragma unroll 1
+  for (int x = 0; x < 4; ++x) {
+    const int c0 = half * 64 + x * 16;
+    float2 f[8];
+    read16(mine + D2 + c0, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int j = c0 + 2 * i;
+      f[i].x = j <= row ? a.scale * f[i].x * decay_between(hi, lo, tab.gates.hi[j], tab.gates.lo[j]) : 0.f;
+      f[i].y = j < row ? a.scale * f[i].y * decay_between(hi, lo, tab.gates.hi[j + 1], tab.gates.lo[j + 1]) : 0.f;
+    }
+    put16<kP>(smem + kTwo, 2 * kTile, row, c0, f);
+  }
+  before_sync();
+  __syncthreads();
+  after_sync();
+  // D2 = Z K
+  const Operand two_t = k_major(base + kTwo, 2 * kTile, kTile), two_tt = mn_major(base + kTwo, 2 * kTile, kTile);
+  over_tokens<T>(steps, smem, k, a.k.st, p.n, a.dk, g.dkt, g.vec,
+                 [&](int ct, int k0, const Operand& right, int n, bool add) {
+    product<kP, DP>(tmem + D2 + 64 * ct, from_step(two_t, k0), right, n, id_of(64, false, true), add);
+  });
+  {
+    float s = 0.f;
+    const float f0 = a.scale * up;
+#pragma unroll 1
+    for (int x = 0; x < 2 * g.dkt; ++x) {
+      const int c0 = (half * 2 * g.dkt + x) * 16;
+      float2 f[8], h[8];
+      read16(mine + D1 + c0, f);
+      read16(mine + D2 + c0, h);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = fma2(both(f0), f[i], h[i]);
+      if (mine_live) {
+        s += dot_row(q + row * a.q.st, c0, a.dk, f);
+        if (parts) store16<float>(a.dq_part + (p.t0 + row) * part_t + part_at + c0, a.dk - c0, dq_vec, f);
+        else if (a.dq_out) store16<T>(dq + (p.t0 + row) * a.dqt + c0, a.dk - c0, dq_vec, f);
+      }
+    }
+    tab.rows[half][0][row] = s;
+  }
+  before_sync();
+  __syncthreads();
+  after_sync();
+  // D3 += Z^T Q
+  over_tokens<T>(steps, smem, q, a.q.st, p.n, a.dk, g.dkt, g.vec,
+                 [&](int ct, int k0, const Operand& right, int n, bool) {
+    product<kP, DP>(tmem + D3 + 64 * ct, from_step(two_tt, k0), right, n, id_of(64, true, true), true);
+  });
+  // D1 = U R^T
+  quads(kTwo, R, rows, rows, g.dvt, nullptr);
+  steps.run([&] { product<kP, kP>(tmem + D1, one_v, two_v, vsteps, id_of(rows, false, false), false); });
+  // <S, R> where the chunk ends
+  float leave = 0.f;
+  for (int i = tid; i < rows * ((a.dv + 3) / 4); i += kThreads) {  // columns behind dv may never have been written
+    const float4 s = reinterpret_cast<const float4*>(S + rows * cols)[i], r = reinterpret_cast<const float4*>(R)[i];
+    leave = fmaf(s.x, r.x, fmaf(s.y, r.y, fmaf(s.z, r.z, fmaf(s.w, r.w, leave))));
+  }
+  leave = warp_sum(leave);
+  if (lane == 0) tab.leaves[warp] = leave;
+  steps.wait();
+#pragma unroll 1
+  for (int x = 0; x < 2 * g.dkt; ++x) {
+    const int c0 = (half * 2 * g.dkt + x) * 16;
+    float2 f[8], h[8];
+    read16(mine + D3 + c0, f);
+    read16(mine + D0 + c0, h);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = fma2(both(-up), h[i], f[i]);
+    read16(mine + D1 + c0, h);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = fma2(both(down), h[i], f[i]);
+    if (mine_live) {
+      if (parts) store16<float>(a.dk_part + (p.t0 + row) * part_t + part_at + c0, a.dk - c0, dk_vec, f);
+      else if (a.dk_out) store16<T>(dk + (p.t0 + row) * a.dkt + c0, a.dk - c0, dk_vec, f);
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {  // the gates: a lane has 4 tokens, summed from the chunk's end
+    float base_ = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) base_ += tab.leaves[i];
+    float s[4], run = 0.f;
+#pragma unroll
+    for (int i = 3; i >= 0; --i) {
+      const int r = lane * 4 + i;
+      const float dqq = tab.rows[0][0][r] + tab.rows[1][0][r], dvv = tab.rows[0][1][r] + tab.rows[1][1][r];
+      s[i] = run += r < p.n ? dqq - dvv : 0.f;
+    }
+    float after = run;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float x = __shfl_down_sync(0xffffffffu, after, o);
+      if (lane + o < 32) after += x;
+    }
+    after = __shfl_down_sync(0xffffffffu, after, 1);
+    if (lane == 31) after = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = lane * 4 + i;
+      if (r >= p.n) continue;
+      if (a.dg) a.dg[(p.t0 + r) * a.dgt + p.b * a.dgb + p.h * a.dgh] = s[i] + after + base_;
+      if (a.dbeta)
+        a.dbeta[(p.t0 + r) * a.dbt + p.b * a.dbb + p.h * a.dbh] = tab.rows[0][2][r] + tab.rows[1][2][r];
+    }
+  }
+  finish(tmem, 512, steps.ok, g.status);
+}
+
+bool packs(const GdArgs& a, const void* p, int e, long long t, long long b, long long h) {
+  const int v = 16 / e;
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (a.T == 1 || t % v == 0) && (a.B == 1 || b % v == 0) &&
+         (a.H == 1 || h % v == 0);
+}
+
+}  // namespace
+
+cudaError_t launch_before_reverse(const Args& g, cudaStream_t s) {
+  PRNN_BY_DTYPE(g.a.dtype, T, {
+    constexpr uint32_t smem = kTab + sizeof(Tab);
+    const cudaError_t e = cudaFuncSetAttribute(gd_before_reverse_kernel<T>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    gd_before_reverse_kernel<T><<<(unsigned)(g.nbh * g.chunks), kThreads, smem, s>>>(g);
+  });
+  return cudaGetLastError();
+}
+
+cudaError_t launch_gradients(const Args& g, cudaStream_t s) {
+  const GdArgs& a = g.a;
+  PRNN_BY_DTYPE(a.dtype, T, {
+    constexpr uint32_t smem = kTab + sizeof(Tab);
+    const cudaError_t e = cudaFuncSetAttribute(gd_gradients_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)smem);
+    if (e != cudaSuccess) return e;
+    const bool part = packs(a, a.dq_part, 4, a.dk, a.dk, a.dk);
+    const bool dq = a.dq_part ? part : packs(a, a.dq_out, sizeof(T), a.dqt, a.dqb, a.dqh);
+    const bool dk = a.dq_part ? part : packs(a, a.dk_out, sizeof(T), a.dkt, a.dkb, a.dkh);
+    const bool dv = packs(a, a.dv_out, sizeof(T), a.dvt, a.dvb, a.dvh);
+    gd_gradients_kernel<T><<<(unsigned)(g.nbh * g.chunks), kThreads, smem, s>>>(g, dq, dk, dv);
+  });
+  return cudaGetLastError();
+}
+
+}  // namespace gd
+}  // namespace prnn
