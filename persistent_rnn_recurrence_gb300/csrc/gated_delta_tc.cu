@@ -22,19 +22,19 @@ struct PrepTab {
 constexpr uint32_t kPrepRight = 96 * 1024, kPrepTab = 192 * 1024;
 static_assert(2 * C * kLd * sizeof(float) <= kPrepTab && kPrepTab + sizeof(PrepTab) <= 227 * 1024, "shared memory");
 
-// A's and T's blocks of 32, T in place beside A: block (i, j) of T <- -T_ii (sum_{m=j}^{i-1} A_im T_mj), the sum kept in
-// T's unused block (j, i).  Q threads share a block.
+// A's and T's blocks of 32: block (i, j) of T <- -T_ii (sum_{m=j}^{i-1} A_im T_mj), the sum kept in T's unused block
+// (j, i).  Q threads share a block, X x W values each.
 template <int GAP>
 __device__ __forceinline__ void lower_blocks(const float* A, float* T) {
-  constexpr int BLOCKS = 4 - GAP, Q = GAP == 1 ? 64 : (GAP == 2 ? 128 : 256), W = 1024 / Q / 4;  // 4 x W values a thread
+  constexpr int BLOCKS = 4 - GAP, Q = GAP == 1 ? 128 : (GAP == 2 ? 256 : 512), W = GAP == 3 ? 1 : 2, X = 1024 / Q / W;
   const int j = threadIdx.x / Q, q = threadIdx.x % Q, i = j + GAP;
-  const int r = q / (32 / W) * 4, c = q % (32 / W) * W;
+  const int r = q / (32 / W) * X, c = q % (32 / W) * W;
 #pragma unroll
   for (int pass = 0; pass < 2; ++pass) {
     if (j < BLOCKS) {
-      float s[4][W];
+      float s[X][W];
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
+      for (int x = 0; x < X; ++x)
 #pragma unroll
         for (int y = 0; y < W; ++y) s[x][y] = 0.f;
       // pass 0: A[i][j .. i-1] T[j .. i-1][j]; pass 1: T[i][i] times that
@@ -43,22 +43,22 @@ __device__ __forceinline__ void lower_blocks(const float* A, float* T) {
       const int depth = pass == 0 ? 32 * GAP : 32;
 #pragma unroll 2
       for (int m = 0; m < depth; m += 4) {
-        float4 l[4];
+        float4 l[X];
+        Pack<float, W> f[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) l[x] = *reinterpret_cast<const float4*>(left + x * kLd + m);
+        for (int x = 0; x < X; ++x) l[x] = *reinterpret_cast<const float4*>(left + x * kLd + m);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 4; ++k) f[k] = load_pack<float, W>(right + (m + k) * kLd);
 #pragma unroll
-          for (int y = 0; y < W; ++y) {
-            const float f = right[(m + k) * kLd + y];
+        for (int x = 0; x < X; ++x)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) s[x][y] = fmaf(k == 0 ? l[x].x : (k == 1 ? l[x].y : (k == 2 ? l[x].z : l[x].w)),
-                                                       f, s[x][y]);
-          }
+          for (int y = 0; y < W; ++y)
+            s[x][y] = fmaf(l[x].w, f[3].v[y], fmaf(l[x].z, f[2].v[y], fmaf(l[x].y, f[1].v[y],
+                                                                        fmaf(l[x].x, f[0].v[y], s[x][y]))));
       }
       float* to = pass == 0 ? T + (32 * j + r) * kLd + 32 * i + c : T + (32 * i + r) * kLd + 32 * j + c;
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
+      for (int x = 0; x < X; ++x)
 #pragma unroll
         for (int y = 0; y < W; ++y) to[x * kLd + y] = pass == 0 ? s[x][y] : -s[x][y];
     }
@@ -66,42 +66,47 @@ __device__ __forceinline__ void lower_blocks(const float* A, float* T) {
   }
 }
 
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+
+constexpr int kPrepThreads = 512;
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 1) gd_prepare_kernel(const __grid_constant__ Args g, int keep_inverse) {
-  constexpr int DP = kData<T>;
+__global__ void __launch_bounds__(kPrepThreads, 1) gd_prepare_kernel(const __grid_constant__ Args g, int keep_inverse) {
+  constexpr int DP = kData<T>, NT = kPrepThreads;
   extern __shared__ __align__(1024) unsigned char smem[];
   PrepTab& tab = *reinterpret_cast<PrepTab*>(smem + kPrepTab);
   const GdArgs& a = g.a;
   const Place p = place_of(g);
   if (p.n == 0) return;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = (warp & 3) * 32 + lane, half = warp >> 2;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = (warp & 3) * 32 + lane, quarter = warp >> 2;
+  const T *k = rows_of<T>(a.k, p.t0, p.b, p.hq), *v = rows_of<T>(a.v, p.t0, p.b, p.h);
+  DataRows<T, C, 2, NT> rows;
+  rows.fetch(k, a.k.st, 0, p.n, 0, a.dk, g.dkt, g.vec);
   if (!begin(&tab.bar, &tab.tmem, 256, smem, g.status)) return;
   Steps steps{&tab.bar};
   const uint32_t tmem = tab.tmem, mine = tmem + ((uint32_t)((warp & 3) * 32) << 16), base = smem_u32(smem);
-  const T* k = rows_of<T>(a.k, p.t0, p.b, p.hq);
-  // K, both halves, parts side by side
-  const uint32_t part = g.dkt * kTile;
-  for (int ct = 0; ct < g.dkt; ++ct)
-    load_data<T, DP>(smem + ct * kTile, part, k, a.k.st, 0, C, p.n, ct * 64, a.dk, g.vec, nullptr,
-                     g.kimg + ((p.at * g.dkt + ct) * DP) * kTile);
+  const uint32_t part = g.dkt * kTile, vpart = g.dvt * kTile;
   double G = 0;
   if (tid < C) {
     if (tid < p.n) {
       const long long t = p.t0 + tid;
-      float v = a.g[t * a.gt + p.b * a.gb + p.h * a.gh];
-      if (v < -1000.f) v = -1000.f;
-      G = v;
+      float x = a.g[t * a.gt + p.b * a.gb + p.h * a.gh];
+      if (x < -1000.f) x = -1000.f;
+      G = x * 1.4426950408889634;
       tab.gates.beta[tid] = a.beta[t * a.bt + p.b * a.bb + p.h * a.bh];
     } else {
       tab.gates.beta[tid] = 0.f;
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const double v = __shfl_up_sync(0xffffffffu, G, o);
-      if (lane >= o) G += v;
+      const double x = __shfl_up_sync(0xffffffffu, G, o);
+      if (lane >= o) G += x;
     }
     if (lane == 31) tab.part[warp] = G;
   }
+  rows.template place<DP>(smem, part, kTile);
   __syncthreads();
   if (tid < C) {
     double all = 0;
@@ -113,39 +118,46 @@ __global__ void __launch_bounds__(kThreads, 1) gd_prepare_kernel(const __grid_co
     const float hi = (float)G;
     tab.gates.hi[tid] = hi;
     tab.gates.lo[tid] = hi == hi ? (float)(G - hi) : hi;
-    tab.gates.up[tid] = expf(hi);
-    tab.gates.down[tid] = expf((float)(all - G));
+    tab.gates.up[tid] = exp2f(hi);
+    tab.gates.down[tid] = exp2f((float)(all - G));
   }
   const Operand K = k_major(base, part, kTile);
   steps.run([&] { product<DP, DP>(tmem, K, K, (a.dk + 15) / 16, id_of(128, false, false), false); });
+  if (tid == 0) {  // the walk's copy of K
+    for (int ct = 0; ct < g.dkt; ++ct)
+      for (int q = 0; q < DP; ++q)
+        bulk_store(g.kimg + ((p.at * g.dkt + ct) * DP + q) * kTile, base + q * part + ct * kTile, kTile);
+    bulk_commit();
+  }
   {
     const float* from = reinterpret_cast<const float*>(&tab.gates);
     float* to = reinterpret_cast<float*>(g.gates + p.at);
-    for (int i = tid; i < (int)(sizeof(Gates) / 4); i += kThreads) to[i] = from[i];
+    for (int i = tid; i < (int)(sizeof(Gates) / 4); i += NT) to[i] = from[i];
   }
+  if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   steps.wait();
+  __syncthreads();  // K's place may be written again
   float* A = reinterpret_cast<float*>(smem);
   float* inv = A + C * kLd;
   {  // A_ij = (k_i . k_j) D_ij beta_j below the diagonal
     const float hi = tab.gates.hi[row], lo = tab.gates.lo[row];
 #pragma unroll 1
-    for (int q = 0; q < 4; ++q) {
-      const int c0 = half * 64 + q * 16;
-      float2 v[8];
-      read16(mine + c0, v);
+    for (int q = 0; q < 2; ++q) {
+      const int c0 = quarter * 32 + q * 16;
+      float2 x[8];
+      read16(mine + c0, x);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int j = c0 + i;
-        float f = 0.f;
-        if (j < row)
-          f = (i & 1 ? v[i / 2].y : v[i / 2].x) * decay_between(hi, lo, tab.gates.hi[j], tab.gates.lo[j]) * tab.gates.beta[j];
-        if (i & 1) v[i / 2].y = f;
-        else v[i / 2].x = f;
+      for (int i = 0; i < 8; ++i) {
+        const int j = c0 + 2 * i;
+        x[i].x = j < row ? x[i].x * decay_between(hi, lo, tab.gates.hi[j], tab.gates.lo[j]) * tab.gates.beta[j] : 0.f;
+        x[i].y = j + 1 < row
+                     ? x[i].y * decay_between(hi, lo, tab.gates.hi[j + 1], tab.gates.lo[j + 1]) * tab.gates.beta[j + 1]
+                     : 0.f;
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<float4*>(A + row * kLd + c0 + 4 * i) =
-            make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
+            make_float4(x[2 * i].x, x[2 * i].y, x[2 * i + 1].x, x[2 * i + 1].y);
     }
   }
   before_sync();
@@ -171,57 +183,62 @@ __global__ void __launch_bounds__(kThreads, 1) gd_prepare_kernel(const __grid_co
   __syncthreads();
   lower_blocks<1>(A, inv);
   lower_blocks<2>(A, inv);
+  rows.fetch(v, a.v.st, 0, p.n, 0, a.dv, g.dvt, g.vec);
   lower_blocks<3>(A, inv);
   {  // Tt as parts, in the place of A and of itself
-    float2 v[4][8];
+    float2 x[2][8];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < 2; ++q)
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
-        const int c = half * 64 + q * 16 + 2 * i;
+        const int c = quarter * 32 + q * 16 + 2 * i;
         const float4 f = *reinterpret_cast<const float4*>(inv + row * kLd + c);
-        v[q][i] = make_float2(c <= row ? f.x : 0.f, c + 1 <= row ? f.y : 0.f);
-        v[q][i + 1] = make_float2(c + 2 <= row ? f.z : 0.f, c + 3 <= row ? f.w : 0.f);
+        x[q][i] = make_float2(c <= row ? f.x : 0.f, c + 1 <= row ? f.y : 0.f);
+        x[q][i + 1] = make_float2(c + 2 <= row ? f.z : 0.f, c + 3 <= row ? f.w : 0.f);
       }
     __syncthreads();
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int c0 = half * 64 + q * 16;
-      put16<kP>(smem, 2 * kTile, row, c0, v[q]);
-      if (keep_inverse) store_quads(g.inv + p.at * C * C, C, row, c0, v[q]);
+    for (int q = 0; q < 2; ++q) {
+      const int c0 = quarter * 32 + q * 16;
+      put16<kP>(smem, 2 * kTile, row, c0, x[q]);
+      if (keep_inverse) store_quads(g.inv + p.at * C * C, C, row, c0, x[q]);
     }
   }
   const Operand Tt = k_major(base, 2 * kTile, kTile);
-  const T* v = rows_of<T>(a.v, p.t0, p.b, p.h);
-  const uint32_t vpart = g.dvt * kTile;
-  for (int vt = 0; vt < g.dvt; ++vt)
-    load_data<T, DP>(smem + kPrepRight + vt * kTile, vpart, v, a.v.st, 0, C, p.n, vt * 64, a.dv, g.vec, nullptr);
+  rows.template place<DP>(smem + kPrepRight, vpart, kTile);
   steps.run([&] {
     product<kP, DP>(tmem, Tt, mn_major(base + kPrepRight, vpart, kTile), 8, id_of(64 * g.dvt, false, true), false);
   });
+  rows.fetch(k, a.k.st, 0, p.n, 0, a.dk, g.dkt, g.vec);
   steps.wait();
-  for (int ct = 0; ct < g.dkt; ++ct)
-    load_data<T, kP>(smem + kPrepRight + ct * kTile, part, k, a.k.st, 0, C, p.n, ct * 64, a.dk, g.vec, tab.gates.up);
+  rows.template place<kP>(smem + kPrepRight, part, kTile, tab.gates.up);
   steps.run([&] {
     product<kP, kP>(tmem + 128, Tt, mn_major(base + kPrepRight, part, kTile), 8, id_of(64 * g.dkt, false, true), false);
   });
   float* E = g.E + p.at * C * 64 * g.dvt;
 #pragma unroll 1
-  for (int q = 0; q < 2 * g.dvt; ++q) {
-    const int c0 = (half * 2 * g.dvt + q) * 16;
+  for (int q = 0; q < g.dvt; ++q) {
+    const int c0 = (quarter * g.dvt + q) * 16;
     float2 f[8];
     read16(mine + c0, f);
     store_quads(E, C, row, c0, f);
   }
   steps.wait();
+  // W as tiles [dkt][parts] in the place of its right operand, and from there to the walk's copy
 #pragma unroll 1
-  for (int q = 0; q < 2 * g.dkt; ++q) {
-    const int c0 = (half * 2 * g.dkt + q) * 16;
+  for (int q = 0; q < g.dkt; ++q) {
+    const int c0 = (quarter * g.dkt + q) * 16;
     float2 f[8];
     read16(mine + 128 + c0, f);
-    // tiles [dkt][parts]
-    unsigned char* img = g.wimg + ((p.at * g.dkt + (c0 >> 6)) * kP) * kTile;
-    put16<kP>(img, kTile, row, c0 & 63, f);
+    put16<kP>(smem + kPrepRight + (c0 >> 6) * kP * kTile, kTile, row, c0 & 63, f);
+  }
+  to_async();
+  before_sync();
+  __syncthreads();
+  if (tid == 0) {
+    bulk_store(g.wimg + p.at * g.dkt * kP * kTile, base + kPrepRight, g.dkt * kP * kTile);
+    bulk_commit();
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   finish(tmem, 256, steps.ok, g.status);
 }
@@ -484,11 +501,12 @@ struct OutTab {
   uint32_t tmem;
 };
 
+constexpr int kOutThreads = 256;
 template <typename T>
-__global__ void __launch_bounds__(kThreads, kData<T> == 3 ? 1 : 2)
+__global__ void __launch_bounds__(kOutThreads, kData<T> == 3 ? 1 : 2)
     gd_outputs_kernel(const __grid_constant__ Args g, bool out_vec) {
   using K = OutCfg<T>;
-  constexpr int DP = K::DP, PC = K::PC;
+  constexpr int DP = K::DP, PC = K::PC, NT = kOutThreads;
   extern __shared__ __align__(1024) unsigned char smem[];
   OutTab& tab = *reinterpret_cast<OutTab*>(smem + K::kTab);
   const GdArgs& a = g.a;
@@ -496,27 +514,29 @@ __global__ void __launch_bounds__(kThreads, kData<T> == 3 ? 1 : 2)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = (warp & 3) * 32 + lane, half = warp >> 2;
   T* o = static_cast<T*>(a.o) + p.b * a.ob + p.h * a.oh;
   const int live = (int)(a.T - p.t0 < C ? a.T - p.t0 : C);  // rows of the tensor
-  for (int i = tid; i < (live - p.n) * a.dv; i += kThreads)  // zeros past the length
+  for (int i = tid; i < (live - p.n) * a.dv; i += NT)       // zeros past the length
     o[(p.t0 + p.n + i / a.dv) * a.ot + i % a.dv] = from_f32<T>(0.f);
   if (p.n == 0) return;
-  if (!begin(&tab.bar, &tab.tmem, 256, smem, g.status)) return;
-  Steps steps{&tab.bar};
-  const uint32_t tmem = tab.tmem, mine = tmem + ((uint32_t)((warp & 3) * 32) << 16), base = smem_u32(smem);
-  {
-    const float* from = reinterpret_cast<const float*>(g.gates + p.at);
-    float* to = reinterpret_cast<float*>(&tab.gates);
-    for (int i = tid; i < (int)(sizeof(Gates) / 4); i += kThreads) to[i] = from[i];
-  }
   const int rows = 64 * g.dkt, cols = 64 * g.dvt;
   const float* S = g.S + p.slot * rows * cols;
   const T *q = rows_of<T>(a.q, p.t0, p.b, p.hq), *k = rows_of<T>(a.k, p.t0, p.b, p.hq);
+  DataRows<T, C, 1, NT> qs, ks;
+  QuadRows<64, 2, NT> ss;
+  auto fetch = [&](int ct) {
+    qs.fetch(q, a.q.st, 0, p.n, ct * 64, a.dk, 1, g.vec);
+    ks.fetch(k, a.k.st, 0, p.n, ct * 64, a.dk, 1, g.vec);
+    ss.fetch(S + ct * 64 * 4, rows, 64, g.dvt);
+  };
+  fetch(0);
+  if (!begin(&tab.bar, &tab.tmem, 256, smem, g.status)) return;
+  Steps steps{&tab.bar};
+  const uint32_t tmem = tab.tmem, mine = tmem + ((uint32_t)((warp & 3) * 32) << 16), base = smem_u32(smem);
+  copy_gates<NT>(tab.gates, g.gates + p.at);
   for (int ct = 0; ct < g.dkt; ++ct) {
-    if (ct > 0) steps.wait();
-    load_data<T, DP>(smem, kTile, q, a.q.st, 0, C, p.n, ct * 64, a.dk, g.vec, nullptr);
-    load_data<T, DP>(smem + K::kK, kTile, k, a.k.st, 0, C, p.n, ct * 64, a.dk, g.vec, nullptr);
+    qs.template place<DP>(smem, kTile, kTile);
+    ks.template place<DP>(smem + K::kK, kTile, kTile);
     // 64 rows of the state: tiles [parts][dvt][64][64]
-    for (int vt = 0; vt < g.dvt; ++vt)
-      load_quads<PC>(smem + K::kS + vt * (kTile / 2), g.dvt * (kTile / 2), S + ct * 64 * 4, rows, 64, vt * 64, nullptr);
+    ss.template place<PC>(smem + K::kS, g.dvt * (kTile / 2), kTile / 2, 64, g.dvt);
     steps.run([&] {
       const Operand Q = k_major(base, kTile, kTile);
       const int n = min(4, (a.dk - 64 * ct + 15) / 16);
@@ -524,8 +544,12 @@ __global__ void __launch_bounds__(kThreads, kData<T> == 3 ? 1 : 2)
       product<DP, PC>(tmem + 128, Q, mn_major(base + K::kS, g.dvt * (kTile / 2), kTile / 2), n,
                       id_of(cols, false, true), ct > 0);
     });
+    if (ct + 1 < g.dkt) fetch(ct + 1);
+    steps.wait();
   }
-  steps.wait();
+  QuadRows<C, 1, NT> es;
+  const float* E = g.E + p.at * C * cols;
+  es.fetch(E, C, C, 1);
   {
     const float hi = tab.gates.hi[row], lo = tab.gates.lo[row];
 #pragma unroll 1
@@ -542,14 +566,14 @@ __global__ void __launch_bounds__(kThreads, kData<T> == 3 ? 1 : 2)
       put16<PC>(smem, 2 * kTile, row, c0, v);
     }
   }
-  const float* E = g.E + p.at * C * cols;
   const float up = tab.gates.up[row];
   for (int vt = 0; vt < g.dvt; ++vt) {
-    load_quads<PC>(smem + K::kU, kTile, E, C, C, vt * 64, tab.gates.beta);
+    es.template place<PC>(smem + K::kU, kTile, kTile, C, 1, tab.gates.beta);
     steps.run([&] {
       product<PC, PC>(tmem, k_major(base, 2 * kTile, kTile), mn_major(base + K::kU, kTile, kTile), 8,
                       id_of(64, false, true), false);
     });
+    if (vt + 1 < g.dvt) es.fetch(E + (size_t)(vt + 1) * 16 * C * 4, C, C, 1);
     steps.wait();
 #pragma unroll 1
     for (int x = 0; x < 2; ++x) {
@@ -577,7 +601,7 @@ cudaError_t launch_prepare(const Args& g, bool keep_inverse, cudaStream_t s) {
     constexpr uint32_t smem = kPrepTab + sizeof(PrepTab);
     const cudaError_t e = allow(gd_prepare_kernel<T>, smem);
     if (e != cudaSuccess) return e;
-    gd_prepare_kernel<T><<<(unsigned)(g.nbh * g.chunks), kThreads, smem, s>>>(g, keep_inverse);
+    gd_prepare_kernel<T><<<(unsigned)(g.nbh * g.chunks), kPrepThreads, smem, s>>>(g, keep_inverse);
   });
   return cudaGetLastError();
 }
@@ -603,7 +627,7 @@ cudaError_t launch_outputs(const Args& g, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
     const bool vec = (reinterpret_cast<uintptr_t>(g.a.o) & 15) == 0 && (g.a.T == 1 || g.a.ot % V == 0) &&
                      (g.a.B == 1 || g.a.ob % V == 0) && (g.a.H == 1 || g.a.oh % V == 0);
-    gd_outputs_kernel<T><<<(unsigned)(g.nbh * g.chunks), kThreads, smem, s>>>(g, vec);
+    gd_outputs_kernel<T><<<(unsigned)(g.nbh * g.chunks), kOutThreads, smem, s>>>(g, vec);
   });
   return cudaGetLastError();
 }

@@ -18,6 +18,9 @@
 // whole are left out, all sums are fp32.  bf16 has fp32's range, so nothing is scaled to fit.  Log-decays are
 // summed in 64 bits and kept as two fp32 values, so that differences of distant sums keep their bits; one below
 // -1000 counts as -1000 (exp is 0 from -104), which keeps those differences finite.
+//
+// Blocks of the side-by-side kernels work in step: place operands, multiply, read.  What a step loads is requested
+// before the wait for the products of the step before it.
 #pragma once
 
 #include "gated_delta.h"
@@ -29,13 +32,13 @@ namespace gd {
 using namespace tc;
 using bf16 = __nv_bfloat16;
 
-constexpr int C = 128, kThreads = 256, kP = 3;        // tokens per chunk; threads; parts of computed values
+constexpr int C = 128, kP = 3;                        // tokens per chunk; parts of computed values
 constexpr uint32_t kTile = 16384;                     // [128][64] bf16, 128-byte swizzled
 template <typename T>
 constexpr int kData = std::is_same<T, float>::value ? 3 : (std::is_same<T, __half>::value ? 2 : 1);
 
-// Per chunk and head, fp32 [128] each: sums of log-decays in two parts, their exponentials, those to the
-// chunk's end, betas.
+// Per chunk and head, fp32 [128] each: sums of log-decays (to the base 2) in two parts, their exponentials, those to
+// the chunk's end, betas.
 struct Gates {
   float hi[C], lo[C], up[C], down[C], beta[C];
 };
@@ -90,7 +93,7 @@ __device__ __forceinline__ const T* rows_of(const LaSeq& x, long long t0, int b,
 
 // exp(G_i - G_j).
 __device__ __forceinline__ float decay_between(float hi_i, float lo_i, float hi_j, float lo_j) {
-  return expf((hi_i - hi_j) + (lo_i - lo_j));
+  return exp2f((hi_i - hi_j) + (lo_i - lo_j));
 }
 
 // 8 values of row r, columns 8 chunk ..., as P parts into tiles `stride` bytes apart.
@@ -108,67 +111,91 @@ __device__ __forceinline__ void put8(unsigned char* tile, uint32_t stride, int r
   }
 }
 
-// 8 values from p, of which the first m count.
+// 8 values from p, of which the first m count, the others zero.
 template <typename T>
-__device__ __forceinline__ void get8(const T* p, int m, bool vec, float2 (&v)[4]) {
+__device__ __forceinline__ Pack<T, 8> get8(const T* p, int m, bool vec) {
+  Pack<T, 8> r;
   if (vec && m >= 8) {
-    if constexpr (sizeof(T) == 2) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-      v[0] = unpack<T>(u.x);
-      v[1] = unpack<T>(u.y);
-      v[2] = unpack<T>(u.z);
-      v[3] = unpack<T>(u.w);
-    } else {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-      v[0] = make_float2(a.x, a.y);
-      v[1] = make_float2(a.z, a.w);
-      v[2] = make_float2(b.x, b.y);
-      v[3] = make_float2(b.z, b.w);
-    }
+    const uint4* u = reinterpret_cast<const uint4*>(p);
+    uint4* to = reinterpret_cast<uint4*>(&r);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) to[i] = __ldg(u + i);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] = make_float2(2 * i < m ? to_f32(p[2 * i]) : 0.f, 2 * i + 1 < m ? to_f32(p[2 * i + 1]) : 0.f);
+    for (int i = 0; i < 8; ++i) r.v[i] = i < m ? p[i] : from_f32<T>(0.f);
   }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void pairs_of(const Pack<T, 8>& r, float2 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = pair_of<T, 8>(r, i);
 }
 
-// Rows [r0, r0 + rows) of a data tensor (from its row of token 0 of the chunk), columns [c0, c0 + 64) of d, as P parts
-// into a tile of `rows` rows; zeros past n rows and d columns.  Each row times scale[row] where that is given.  Eight
-// neighbouring threads take a row.  img: a copy of the tile in device memory, parts kTile apart.
-template <typename T, int P>
-__device__ __forceinline__ void load_data(unsigned char* tile, uint32_t stride, const T* x, long long st, int r0,
-                                          int rows, int n, int c0, int d, bool vec, const float* scale,
-                                          unsigned char* img = nullptr) {
-  for (int u = threadIdx.x; u < rows * 8; u += kThreads) {
-    const int r = r0 + (u >> 3), chunk = u & 7, c = c0 + chunk * 8;
-    float2 v[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
-    if (r < n && c < d) get8<T>(x + r * st + c, d - c, vec, v);
-    if (scale) {
+// ROWS rows of a data tensor (from its row of the chunk's token 0), TILES tiles of 64 columns at most, requested by
+// NT threads at once and later placed as P parts: rows past n and columns past d are zeros.
+template <typename T, int ROWS, int TILES, int NT>
+struct DataRows {
+  static constexpr int N = ROWS * 8 * TILES / NT;
+  Pack<T, 8> raw[N];
+  int shift;  // neighbouring threads take a row's pieces of 8 columns
+  __device__ __forceinline__ void fetch(const T* x, long long st, int r0, int n, int c0, int d, int tiles, bool vec) {
+    shift = TILES == 2 && tiles == 2 ? 4 : 3;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = r < n ? mul2(v[i], both(scale[r])) : both(0.f);
+    for (int i = 0; i < N; ++i) {
+      const int u = i * NT + threadIdx.x, r = r0 + (u >> shift), c = c0 + (u & ((1 << shift) - 1)) * 8;
+      const bool in = (u >> shift) < ROWS && r < n && c < d;
+      raw[i] = get8<T>(x + (in ? r * st + c : 0), in ? d - c : 0, vec);
     }
-    float2 w[4] = {v[0], v[1], v[2], v[3]};
-    put8<P>(tile, stride, u >> 3, chunk, v);
-    if (img) put8<P>(img, kTile, r, chunk, w);
   }
-}
-// The same from an fp32 matrix of R rows in quads; a row per lane.
-template <int P>
-__device__ __forceinline__ void load_quads(unsigned char* tile, uint32_t stride, const float* m, int R, int rows, int c0,
-                                           const float* scale) {
-  for (int u = threadIdx.x; u < rows * 8; u += kThreads) {
-    const int r = u % rows, chunk = u / rows;
-    const float4* q = reinterpret_cast<const float4*>(m) + ((size_t)(c0 / 4 + 2 * chunk) * R + r);
-    const float4 a = q[0], b = q[R];
-    float2 v[4] = {make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)};
-    if (scale) {
-      const float2 f = both(scale[r]);
+  // Tiles `tile` bytes apart, parts `part` apart; each row times scale[row] where that is given.
+  template <int P>
+  __device__ __forceinline__ void place(unsigned char* to, uint32_t part, uint32_t tile, const float* scale = nullptr) const {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], f);
+    for (int i = 0; i < N; ++i) {
+      const int u = i * NT + threadIdx.x, r = u >> shift, piece = u & ((1 << shift) - 1);
+      if (r >= ROWS) continue;
+      float2 v[4];
+      pairs_of<T>(raw[i], v);
+      if (scale)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], both(scale[r]));
+      put8<P>(to + (piece >> 3) * tile, part, r, piece & 7, v);
     }
-    put8<P>(tile, stride, r, chunk, v);
   }
-}
+};
+// The same for an fp32 matrix of R <= ROWS rows in quads of columns; a row per lane.
+template <int ROWS, int TILES, int NT>
+struct QuadRows {
+  static constexpr int N = ROWS * 8 * TILES / NT;
+  float4 a[N], b[N];
+  __device__ __forceinline__ void fetch(const float* m, int R, int rows, int tiles) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int u = i * NT + threadIdx.x, r = u % ROWS, piece = u / ROWS;
+      if (r < rows && piece < 8 * tiles) {
+        const float4* q = reinterpret_cast<const float4*>(m) + ((size_t)(2 * piece) * R + r);
+        a[i] = q[0];
+        b[i] = q[R];
+      }
+    }
+  }
+  template <int P>
+  __device__ __forceinline__ void place(unsigned char* to, uint32_t part, uint32_t tile, int rows, int tiles,
+                                        const float* scale = nullptr) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int u = i * NT + threadIdx.x, r = u % ROWS, piece = u / ROWS;
+      if (r >= rows || piece >= 8 * tiles) continue;
+      float2 v[4] = {make_float2(a[i].x, a[i].y), make_float2(a[i].z, a[i].w), make_float2(b[i].x, b[i].y),
+                     make_float2(b[i].z, b[i].w)};
+      if (scale)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], both(scale[r]));
+      put8<P>(to + (piece >> 3) * tile, part, r, piece & 7, v);
+    }
+  }
+};
 
 // An operand: descriptor of its first part, bytes from one part to the next, and of its steps of 16 along K.
 struct Operand {
@@ -202,6 +229,12 @@ __device__ __forceinline__ void product(uint32_t d, const Operand& a, const Oper
 }
 __device__ __forceinline__ uint32_t id_of(int n, bool a_mn, bool b_mn) {
   return bf16_idesc(128, n) | (a_mn ? kAMn : 0u) | (b_mn ? kBMn : 0u);
+}
+
+template <int NT>
+__device__ __forceinline__ void copy_gates(Gates& to, const Gates* from) {
+  for (int i = threadIdx.x; i < (int)(sizeof(Gates) / 4); i += NT)
+    reinterpret_cast<float*>(&to)[i] = reinterpret_cast<const float*>(from)[i];
 }
 
 // Blocks that work in step: operands are placed by all threads, one thread issues the products, all wait for them.

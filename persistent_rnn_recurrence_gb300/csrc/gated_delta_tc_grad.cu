@@ -7,38 +7,58 @@ namespace prnn {
 namespace gd {
 namespace {
 
+constexpr int kThreads = 512;
 // Two operands of [128][128] in three parts, and a third by pieces of 64 columns and as many tokens as fit.
 constexpr uint32_t kMatrix = kP * 2 * kTile, kOne = 0, kTwo = kMatrix, kThree = 2 * kMatrix, kPiece = 24 * 1024,
                    kTab = kThree + kPiece;
 struct Tab {
   Gates gates;
-  float rows[2][3][C];   // per half of the columns: q . dq, v . dv, and dbeta's sum
-  float leaves[8];
+  float rows[4][3][C];   // per quarter of the columns: q . dq, v . dv, and dbeta's sum
+  float leaves[kThreads / 32];
   uint64_t bar;
   uint32_t tmem;
 };
 static_assert(kTab + sizeof(Tab) <= 227 * 1024, "shared memory");
 
-__device__ __forceinline__ void copy_gates(Gates& to, const Gates* from) {
-  for (int i = threadIdx.x; i < (int)(sizeof(Gates) / 4); i += kThreads)
-    reinterpret_cast<float*>(&to)[i] = reinterpret_cast<const float*>(from)[i];
-}
-
 // A product over the chunk's tokens with a data tensor x (its rows tokens, MN-major) as the right operand,
-// d += left x, or twice with two left operands, piece by piece.  The left one has PA parts.
-template <typename T, typename F>
-__device__ __forceinline__ void over_tokens(Steps& steps, unsigned char* smem, const T* x, long long st, int n, int d,
-                                            int tiles, bool vec, F&& issue) {
-  constexpr int DP = kData<T>, ROWS = DP * kTile <= kPiece ? C : C / 2;
-  for (int ct = 0; ct < tiles; ++ct)
-    for (int r0 = 0; r0 < C && r0 < n; r0 += ROWS) {
-      load_data<T, DP>(smem + kThree, ROWS * 128, x, st, r0, ROWS, n, ct * 64, d, vec, nullptr);
+// piece by piece; `issue` gets the piece's tile of columns, its first step of 16 tokens, the operand, its steps
+// and whether it adds to what earlier tokens left.  The first piece has been requested by `first`.
+template <typename T>
+struct Pieces {
+  static constexpr int DP = kData<T>, ROWS = DP * kTile <= kPiece ? C : C / 2;
+  DataRows<T, ROWS, 1, kThreads> rows;
+  const T* x;
+  long long st;
+  int n, d, tiles;
+  bool vec;
+  __device__ __forceinline__ void fetch(int ct, int r0) { rows.fetch(x, st, r0, n, ct * 64, d, 1, vec); }
+  __device__ __forceinline__ void first(const T* x_, long long st_, int n_, int d_, int tiles_, bool vec_) {
+    x = x_;
+    st = st_;
+    n = n_;
+    d = d_;
+    tiles = tiles_;
+    vec = vec_;
+    fetch(0, 0);
+  }
+  template <typename F>
+  __device__ __forceinline__ void multiply(Steps& steps, unsigned char* smem, F&& issue) {
+    int ct = 0, r0 = 0;
+    while (ct < tiles) {
+      rows.template place<DP>(smem + kThree, ROWS * 128, ROWS * 128);
       steps.run([&] {
         issue(ct, r0 / 16, mn_major(smem_u32(smem) + kThree, ROWS * 128, ROWS * 128), ROWS / 16, r0 > 0);
       });
+      r0 += ROWS;
+      if (r0 >= n || r0 >= C) {
+        r0 = 0;
+        ++ct;
+      }
+      if (ct < tiles) fetch(ct, r0);
       steps.wait();
     }
-}
+  }
+};
 // The left operand of such a product from its step of 16 tokens on.
 __device__ __forceinline__ Operand from_step(Operand o, int k) {
   o.desc += o.tile ? (k >> 2) * o.tile + (k & 3) * 2 : k * 128;
@@ -54,29 +74,32 @@ __global__ void __launch_bounds__(kThreads, 1) gd_before_reverse_kernel(const __
   const GdArgs& a = g.a;
   const Place p = place_of(g);
   if (p.n == 0) return;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = (warp & 3) * 32 + lane, half = warp >> 2;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = (warp & 3) * 32 + lane, quarter = warp >> 2;
+  const T *q = rows_of<T>(a.q, p.t0, p.b, p.hq), *k = rows_of<T>(a.k, p.t0, p.b, p.hq),
+          *d_o = rows_of<T>(a.d_o, p.t0, p.b, p.h);
+  DataRows<T, C, 2, kThreads> qs, ks;
+  qs.fetch(q, a.q.st, 0, p.n, 0, a.dk, g.dkt, g.vec);
+  ks.fetch(k, a.k.st, 0, p.n, 0, a.dk, g.dkt, g.vec);
   if (!begin(&tab.bar, &tab.tmem, 512, smem, g.status)) return;
   Steps steps{&tab.bar};
   const uint32_t tmem = tab.tmem, mine = tmem + ((uint32_t)((warp & 3) * 32) << 16), base = smem_u32(smem);
-  copy_gates(tab.gates, g.gates + p.at);
+  copy_gates<kThreads>(tab.gates, g.gates + p.at);
   const int rows = 64 * g.dkt, cols = 64 * g.dvt;
   const uint32_t part = g.dkt * kTile;
-  const T *q = rows_of<T>(a.q, p.t0, p.b, p.hq), *k = rows_of<T>(a.k, p.t0, p.b, p.hq),
-          *d_o = rows_of<T>(a.d_o, p.t0, p.b, p.h);
-  for (int ct = 0; ct < g.dkt; ++ct) {
-    load_data<T, DP>(smem + kOne + ct * kTile, part, q, a.q.st, 0, C, p.n, ct * 64, a.dk, g.vec, nullptr);
-    load_data<T, DP>(smem + kTwo + ct * kTile, part, k, a.k.st, 0, C, p.n, ct * 64, a.dk, g.vec, nullptr);
-  }
+  qs.template place<DP>(smem + kOne, part, kTile);
+  ks.template place<DP>(smem + kTwo, part, kTile);
   steps.run([&] {
     product<DP, DP>(tmem, k_major(base + kOne, part, kTile), k_major(base + kTwo, part, kTile), (a.dk + 15) / 16,
                     id_of(128, false, false), false);
   });
+  Pieces<T> dos;
+  dos.first(d_o, a.d_o.st, p.n, a.dv, g.dvt, g.vec);
   steps.wait();
   if (tid < C) tab.rows[0][0][tid] = a.scale * tab.gates.up[tid];
   const float hi = tab.gates.hi[row], lo = tab.gates.lo[row];
 #pragma unroll 1
-  for (int x = 0; x < 4; ++x) {
-    const int c0 = half * 64 + x * 16;
+  for (int x = 0; x < 2; ++x) {
+    const int c0 = quarter * 32 + x * 16;
     float2 v[8];
     read16(mine + c0, v);
 #pragma unroll
@@ -88,18 +111,16 @@ __global__ void __launch_bounds__(kThreads, 1) gd_before_reverse_kernel(const __
     put16<kP>(smem + kTwo, 2 * kTile, row, c0, v);
   }
   __syncthreads();
-  for (int ct = 0; ct < g.dkt; ++ct)
-    load_data<T, kP>(smem + kOne + ct * kTile, part, q, a.q.st, 0, C, p.n, ct * 64, a.dk, g.vec, tab.rows[0][0]);
+  qs.template place<kP>(smem + kOne, part, kTile, tab.rows[0][0]);
   const Operand P = mn_major(base + kTwo, 2 * kTile, kTile), Q = mn_major(base + kOne, part, kTile);
-  over_tokens<T>(steps, smem, d_o, a.d_o.st, p.n, a.dv, g.dvt, g.vec,
-                 [&](int ct, int k0, const Operand& right, int n, bool add) {
+  dos.multiply(steps, smem, [&](int ct, int k0, const Operand& right, int n, bool add) {
     product<kP, DP>(tmem + 128 + 64 * ct, from_step(P, k0), right, n, id_of(64, true, true), add);
     product<kP, DP>(tmem + 256 + 64 * ct, from_step(Q, k0), right, n, id_of(64, true, true), add);
   });
   float *X = g.X + p.at * C * cols, *Z0 = g.Z0 + p.at * rows * cols;
 #pragma unroll 1
-  for (int x = 0; x < 2 * g.dvt; ++x) {
-    const int c0 = (half * 2 * g.dvt + x) * 16;
+  for (int x = 0; x < g.dvt; ++x) {
+    const int c0 = (quarter * g.dvt + x) * 16;
     float2 v[8];
     read16(mine + 128 + c0, v);
     store_quads(X, C, row, c0, v);
@@ -118,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
   Tab& tab = *reinterpret_cast<Tab*>(smem + kTab);
   const GdArgs& a = g.a;
   const Place p = place_of(g);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = (warp & 3) * 32 + lane, half = warp >> 2;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = (warp & 3) * 32 + lane, quarter = warp >> 2;
   // where this head's rows of gradients go: the tensors themselves, or fp32 parts that are summed over heads later
   const bool parts = a.dq_part != nullptr;
   auto zero_rows = [&](auto* x, long long st, int d, int live) {
@@ -148,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
   Steps steps{&tab.bar};
   const uint32_t tmem = tab.tmem, mine = tmem + ((uint32_t)((warp & 3) * 32) << 16), base = smem_u32(smem);
   const uint32_t D0 = 0, D1 = 128, D2 = 256, D3 = 384;
-  copy_gates(tab.gates, g.gates + p.at);
+  copy_gates<kThreads>(tab.gates, g.gates + p.at);
   __syncthreads();
   const int rows = 64 * g.dkt, cols = 64 * g.dvt;
   const uint32_t kpart = g.dkt * kTile, vpart = g.dvt * kTile;
@@ -159,16 +180,17 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
   const float hi = tab.gates.hi[row], lo = tab.gates.lo[row], up = tab.gates.up[row], down = tab.gates.down[row],
               beta = tab.gates.beta[row];
   const bool mine_live = row < p.n;
-  auto quads = [&](uint32_t where, const float* m, int R_, int rows_, int tiles, const float* scale) {
-    for (int t = 0; t < tiles; ++t) load_quads<kP>(smem + where + t * kTile, tiles * kTile, m, R_, rows_, t * 64, scale);
-  };
+  QuadRows<C, 2, kThreads> fp;
+  DataRows<T, C, 2, kThreads> data;
+  Pieces<T> pieces;
   // this row's 16 values at columns c0 of a data tensor's row times v, summed
   auto dot_row = [&](const T* x, int c0, int d, const float2 (&f)[8]) {
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      float2 y[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
-      if (c0 + 8 * j < d) get8<T>(x + c0 + 8 * j, d - c0 - 8 * j, g.vec, y);
+      if (c0 + 8 * j >= d) continue;
+      float2 y[4];
+      pairs_of<T>(get8<T>(x + c0 + 8 * j, d - c0 - 8 * j, g.vec), y);
 #pragma unroll
       for (int i = 0; i < 4; ++i) s = fmaf(y[i].x, f[4 * j + i].x, fmaf(y[i].y, f[4 * j + i].y, s));
     }
@@ -176,8 +198,10 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
   };
 
   // dV = Tt^T (beta X)
-  quads(kOne, inv, C, C, 2, nullptr);
-  quads(kTwo, X, C, C, g.dvt, tab.gates.beta);
+  fp.fetch(inv, C, C, 2);
+  fp.template place<kP>(smem + kOne, 2 * kTile, kTile, C, 2);
+  fp.fetch(X, C, C, g.dvt);
+  fp.template place<kP>(smem + kTwo, vpart, kTile, C, g.dvt, tab.gates.beta);
   steps.run([&] {
     product<kP, kP>(tmem + D0, mn_major(base + kOne, 2 * kTile, kTile), mn_major(base + kTwo, vpart, kTile), 8,
                     id_of(cols, true, true), false);
@@ -188,17 +212,18 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
   const bool any_tiny = __syncthreads_or(tiny && mine_live);
   float es = 0.f;  // e . x or e . dv
   if (any_tiny)
-    for (int c = half * 32 * g.dvt; c < (half + 1) * 32 * g.dvt; c += 4) {
+    for (int c = quarter * 16 * g.dvt; c < (quarter + 1) * 16 * g.dvt; c += 4) {
       const size_t i = (size_t)(c / 4) * C + row;
       const float4 e = reinterpret_cast<const float4*>(E)[i], x = reinterpret_cast<const float4*>(X)[i];
       es = fmaf(e.x, x.x, fmaf(e.y, x.y, fmaf(e.z, x.z, fmaf(e.w, x.w, es))));
     }
+  fp.fetch(E, C, C, g.dvt);
   steps.wait();
   {
     float s = 0.f, ev = 0.f;
 #pragma unroll 1
-    for (int x = 0; x < 2 * g.dvt; ++x) {
-      const int c0 = (half * 2 * g.dvt + x) * 16;
+    for (int x = 0; x < g.dvt; ++x) {
+      const int c0 = (quarter * g.dvt + x) * 16;
       float2 f[8];
       read16(mine + D0 + c0, f);
       if (mine_live) {
@@ -212,21 +237,22 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
       }
       put16<kP>(smem + kTwo, vpart, row, c0, f);
     }
-    tab.rows[half][1][row] = s;
+    tab.rows[quarter][1][row] = s;
     if (!tiny) es = ev / beta;
   }
   // dV E^T, E dV^T, and K K^T where a beta is 0
-  quads(kOne, E, C, C, g.dvt, nullptr);
+  fp.template place<kP>(smem + kOne, vpart, kTile, C, g.dvt);
   const Operand one_v = k_major(base + kOne, vpart, kTile), two_v = k_major(base + kTwo, vpart, kTile);
   const int vsteps = (a.dv + 15) / 16, ksteps = (a.dk + 15) / 16;
   steps.run([&] {
     product<kP, kP>(tmem + D0, two_v, one_v, vsteps, id_of(128, false, false), false);
     product<kP, kP>(tmem + D1, one_v, two_v, vsteps, id_of(128, false, false), false);
   });
+  pieces.first(k, a.k.st, p.n, a.dk, g.dkt, g.vec);
   steps.wait();
   if (any_tiny) {
-    for (int ct = 0; ct < g.dkt; ++ct)
-      load_data<T, DP>(smem + kOne + ct * kTile, kpart, k, a.k.st, 0, C, p.n, ct * 64, a.dk, g.vec, nullptr);
+    data.fetch(k, a.k.st, 0, p.n, 0, a.dk, g.dkt, g.vec);
+    data.template place<DP>(smem + kOne, kpart, kTile);
     steps.run([&] {
       const Operand K = k_major(base + kOne, kpart, kTile);
       product<DP, DP>(tmem + D2, K, K, ksteps, id_of(128, false, false), false);
@@ -236,8 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
   {  // -(Y + Y^T) as the next left operand, dbeta
     float s = es;
 #pragma unroll 1
-    for (int x = 0; x < 4; ++x) {
-      const int c0 = half * 64 + x * 16;
+    for (int x = 0; x < 2; ++x) {
+      const int c0 = quarter * 32 + x * 16;
       float2 y1[8], y2[8], kk[8] = {};
       read16(mine + D0 + c0, y1);
       read16(mine + D1 + c0, y2);
@@ -261,33 +287,35 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
       }
       put16<kP>(smem + kOne, 2 * kTile, row, c0, y1);
     }
-    tab.rows[half][2][row] = s;
+    tab.rows[quarter][2][row] = s;
   }
   before_sync();
   __syncthreads();
   after_sync();
   // D3 = -(Y + Y^T) K
   const Operand one_t = k_major(base + kOne, 2 * kTile, kTile);
-  over_tokens<T>(steps, smem, k, a.k.st, p.n, a.dk, g.dkt, g.vec,
-                 [&](int ct, int k0, const Operand& right, int n, bool add) {
+  pieces.multiply(steps, smem, [&](int ct, int k0, const Operand& right, int n, bool add) {
     product<kP, DP>(tmem + D3 + 64 * ct, from_step(one_t, k0), right, n, id_of(64, false, true), add);
   });
   // D0 = dV S0^T
-  quads(kOne, S, rows, rows, g.dvt, nullptr);
+  fp.fetch(S, rows, rows, g.dvt);
+  fp.template place<kP>(smem + kOne, vpart, kTile, rows, g.dvt);
   steps.run([&] { product<kP, kP>(tmem + D0, two_v, one_v, vsteps, id_of(rows, false, false), false); });
+  data.fetch(d_o, a.d_o.st, 0, p.n, 0, a.dv, g.dvt, g.vec);
   steps.wait();
   // D1 = dO S0^T
-  for (int vt = 0; vt < g.dvt; ++vt)
-    load_data<T, DP>(smem + kTwo + vt * kTile, vpart, d_o, a.d_o.st, 0, C, p.n, vt * 64, a.dv, g.vec, nullptr);
+  data.template place<DP>(smem + kTwo, vpart, kTile);
   steps.run([&] { product<DP, kP>(tmem + D1, two_v, one_v, vsteps, id_of(rows, false, false), false); });
+  fp.fetch(E, C, C, g.dvt);
   steps.wait();
   // D2 = dO U^T
-  quads(kOne, E, C, C, g.dvt, tab.gates.beta);
+  fp.template place<kP>(smem + kOne, vpart, kTile, C, g.dvt, tab.gates.beta);
   steps.run([&] { product<DP, kP>(tmem + D2, two_v, one_v, vsteps, id_of(128, false, false), false); });
+  pieces.first(k, a.k.st, p.n, a.dk, g.dkt, g.vec);
   steps.wait();
 #pragma unroll 1
-  for (int x = 0; x < 4; ++x) {
-    const int c0 = half * 64 + x * 16;
+  for (int x = 0; x < 2; ++x) {
+    const int c0 = quarter * 32 + x * 16;
     float2 f[8];
     read16(mine + D2 + c0, f);
 #pragma unroll
@@ -303,16 +331,16 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
   after_sync();
   // D2 = Z K
   const Operand two_t = k_major(base + kTwo, 2 * kTile, kTile), two_tt = mn_major(base + kTwo, 2 * kTile, kTile);
-  over_tokens<T>(steps, smem, k, a.k.st, p.n, a.dk, g.dkt, g.vec,
-                 [&](int ct, int k0, const Operand& right, int n, bool add) {
+  pieces.multiply(steps, smem, [&](int ct, int k0, const Operand& right, int n, bool add) {
     product<kP, DP>(tmem + D2 + 64 * ct, from_step(two_t, k0), right, n, id_of(64, false, true), add);
   });
+  pieces.first(q, a.q.st, p.n, a.dk, g.dkt, g.vec);
   {
     float s = 0.f;
     const float f0 = a.scale * up;
 #pragma unroll 1
-    for (int x = 0; x < 2 * g.dkt; ++x) {
-      const int c0 = (half * 2 * g.dkt + x) * 16;
+    for (int x = 0; x < g.dkt; ++x) {
+      const int c0 = (quarter * g.dkt + x) * 16;
       float2 f[8], h[8];
       read16(mine + D1 + c0, f);
       read16(mine + D2 + c0, h);
@@ -324,18 +352,18 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
         else if (a.dq_out) store16<T>(dq + (p.t0 + row) * a.dqt + c0, a.dk - c0, dq_vec, f);
       }
     }
-    tab.rows[half][0][row] = s;
+    tab.rows[quarter][0][row] = s;
   }
   before_sync();
   __syncthreads();
   after_sync();
   // D3 += Z^T Q
-  over_tokens<T>(steps, smem, q, a.q.st, p.n, a.dk, g.dkt, g.vec,
-                 [&](int ct, int k0, const Operand& right, int n, bool) {
+  pieces.multiply(steps, smem, [&](int ct, int k0, const Operand& right, int n, bool) {
     product<kP, DP>(tmem + D3 + 64 * ct, from_step(two_tt, k0), right, n, id_of(64, true, true), true);
   });
   // D1 = U R^T
-  quads(kTwo, R, rows, rows, g.dvt, nullptr);
+  fp.fetch(R, rows, rows, g.dvt);
+  fp.template place<kP>(smem + kTwo, vpart, kTile, rows, g.dvt);
   steps.run([&] { product<kP, kP>(tmem + D1, one_v, two_v, vsteps, id_of(rows, false, false), false); });
   // <S, R> where the chunk ends
   float leave = 0.f;
@@ -347,8 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
   if (lane == 0) tab.leaves[warp] = leave;
   steps.wait();
 #pragma unroll 1
-  for (int x = 0; x < 2 * g.dkt; ++x) {
-    const int c0 = (half * 2 * g.dkt + x) * 16;
+  for (int x = 0; x < g.dkt; ++x) {
+    const int c0 = (quarter * g.dkt + x) * 16;
     float2 f[8], h[8];
     read16(mine + D3 + c0, f);
     read16(mine + D0 + c0, h);
@@ -364,15 +392,17 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
   }
   __syncthreads();
   if (warp == 0) {  // the gates: a lane has 4 tokens, summed from the chunk's end
+    auto all = [&](int what, int r) {
+      return (tab.rows[0][what][r] + tab.rows[1][what][r]) + (tab.rows[2][what][r] + tab.rows[3][what][r]);
+    };
     float base_ = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) base_ += tab.leaves[i];
+    for (int i = 0; i < kThreads / 32; ++i) base_ += tab.leaves[i];
     float s[4], run = 0.f;
 #pragma unroll
     for (int i = 3; i >= 0; --i) {
       const int r = lane * 4 + i;
-      const float dqq = tab.rows[0][0][r] + tab.rows[1][0][r], dvv = tab.rows[0][1][r] + tab.rows[1][1][r];
-      s[i] = run += r < p.n ? dqq - dvv : 0.f;
+      s[i] = run += r < p.n ? all(0, r) - all(1, r) : 0.f;
     }
     float after = run;
 #pragma unroll
@@ -388,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
       if (r >= p.n) continue;
       if (a.dg) a.dg[(p.t0 + r) * a.dgt + p.b * a.dgb + p.h * a.dgh] = s[i] + after + base_;
       if (a.dbeta)
-        a.dbeta[(p.t0 + r) * a.dbt + p.b * a.dbb + p.h * a.dbh] = tab.rows[0][2][r] + tab.rows[1][2][r];
+        a.dbeta[(p.t0 + r) * a.dbt + p.b * a.dbb + p.h * a.dbh] = all(2, r);
     }
   }
   finish(tmem, 512, steps.ok, g.status);
