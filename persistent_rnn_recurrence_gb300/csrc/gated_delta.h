@@ -26,8 +26,12 @@ struct GdArgs {
   long long dgt, dgb, dgh, dbt, dbb, dbh;
   float* d_state;               // may be null
   // scratch, fp32: [T][B][H][dv] e (null: not kept) and du, [T][B][H][dk] gradients before shared heads are summed,
-  // (tensor cores: null where no heads share theirs), the states at the ends of blocks [blocks][B*H][dk][dv] and their products with the gradients [blocks][B*H][dk]
+  // the states at the ends of blocks [blocks][B*H][dk][dv] and their products with the gradients [blocks][B*H][dk]
   float *e, *du, *dq_part, *dk_part, *marks, *leaves;
+  // tensor cores: rows rounded up to 8 values, and fp32 parts [T][B][H][dkp or dvp] of results that the kernels do not
+  // write in place (dq_part and dk_part as well)
+  int dkp, dvp;
+  float *o_part, *dv_part;
 };
 
 cudaError_t launch_gd_walk_forward(const GdArgs& a, cudaStream_t s);
@@ -36,8 +40,8 @@ cudaError_t launch_gd_walk_backward(const GdArgs& a, cudaStream_t s);
 // On the tensor cores, in chunks, for dk and dv up to 128: whether it serves a call, its scratch, the call.
 constexpr int kGdTcLeast = 32;  // tokens
 bool gd_tc_serves(prnn_dtype_t dtype, int T, int dk, int dv);
-size_t gd_tc_workspace(prnn_dtype_t dtype, int T, int B, int H, int dk, int dv, bool backward);
-cudaError_t launch_gd_tc(const GdArgs& a, void* scratch, bool backward, cudaStream_t s);
+size_t gd_tc_workspace(const GdArgs& a, bool backward);
+cudaError_t launch_gd_tc(GdArgs a, void* scratch, bool backward, cudaStream_t s);
 
 struct GdStepArgs {
   prnn_dtype_t dtype;

@@ -91,7 +91,7 @@ Parts walk_parts(const Call* a) {
 
 bool on_tensor_cores(const Call* a) { return gd_tc_serves(a->dtype, a->T, a->dk, a->dv); }
 
-GdArgs common(const Call* a) {
+GdArgs args_of(const Call* a) {
   GdArgs g{};
   g.dtype = a->dtype;
   g.T = a->T;
@@ -114,6 +114,34 @@ GdArgs common(const Call* a) {
   g.k = in(a->k, share);
   g.v = in(a->v, 1);
   g.state = a->state;
+  g.o = a->o.data;
+  g.ot = a->o.stride_t;
+  g.ob = a->o.stride_b;
+  g.oh = a->o.stride_h;
+  g.state_out = a->state_out;
+  g.d_o = in(a->d_o, 1);
+  g.d_state_out = a->d_state_out;
+  g.d_state = a->d_state;
+  g.dq_out = a->d_q.data;
+  g.dqt = a->d_q.stride_t;
+  g.dqb = a->d_q.stride_b;
+  g.dqh = a->d_q.stride_h;
+  g.dk_out = a->d_k.data;
+  g.dkt = a->d_k.stride_t;
+  g.dkb = a->d_k.stride_b;
+  g.dkh = a->d_k.stride_h;
+  g.dv_out = a->d_v.data;
+  g.dvt = a->d_v.stride_t;
+  g.dvb = a->d_v.stride_b;
+  g.dvh = a->d_v.stride_h;
+  g.dg = static_cast<float*>(a->d_log_decay.data);
+  g.dgt = a->d_log_decay.stride_t;
+  g.dgb = a->d_log_decay.stride_b;
+  g.dgh = a->d_log_decay.stride_h;
+  g.dbeta = static_cast<float*>(a->d_beta.data);
+  g.dbt = a->d_beta.stride_t;
+  g.dbb = a->d_beta.stride_b;
+  g.dbh = a->d_beta.stride_h;
   return g;
 }
 
@@ -127,12 +155,8 @@ prnn_status_t prnn_gated_delta_workspace(const prnn_gated_delta_t* a, int backwa
   if (!shape_ok(a, &why)) return why;
   *bytes = 0;
   if (a->T == 0 || a->B == 0) return PRNN_OK;
-  if (on_tensor_cores(a)) {
-    *bytes = gd_tc_workspace(a->dtype, a->T, a->B, a->heads, a->dk, a->dv, backward != 0);
-    if (backward && a->heads > a->qk_heads) *bytes += 2 * walk_parts(a).dq;
-  } else if (backward) {
-    *bytes = walk_parts(a).total;
-  }
+  if (on_tensor_cores(a)) *bytes = gd_tc_workspace(args_of(a), backward != 0);
+  else if (backward) *bytes = walk_parts(a).total;
   return PRNN_OK;
 }
 
@@ -160,12 +184,7 @@ prnn_status_t prnn_gated_delta_forward(const prnn_gated_delta_t* a, void* stream
   all.array(a->lens, 4ull * a->B, false);
   if (need) all.array(a->workspace, need, true);
   if (!all.good()) return PRNN_ERR_INVALID_ARG;
-  GdArgs g = common(a);
-  g.o = a->o.data;
-  g.ot = a->o.stride_t;
-  g.ob = a->o.stride_b;
-  g.oh = a->o.stride_h;
-  g.state_out = a->state_out;
+  GdArgs g = args_of(a);
   return cuda_status(on_tensor_cores(a) ? launch_gd_tc(g, a->workspace, false, s) : launch_gd_walk_forward(g, s));
 }
 
@@ -200,30 +219,8 @@ prnn_status_t prnn_gated_delta_backward(const prnn_gated_delta_t* a, void* strea
   all.array(a->lens, 4ull * B, false);
   all.array(a->workspace, need, true);
   if (!all.good()) return PRNN_ERR_INVALID_ARG;
-  GdArgs g = common(a);
-  g.d_o = in(a->d_o, 1);
-  g.d_state_out = a->d_state_out;
-  g.d_state = a->d_state;
-  g.dq_out = a->d_q.data;
-  g.dqt = a->d_q.stride_t;
-  g.dqb = a->d_q.stride_b;
-  g.dqh = a->d_q.stride_h;
-  g.dk_out = a->d_k.data;
-  g.dkt = a->d_k.stride_t;
-  g.dkb = a->d_k.stride_b;
-  g.dkh = a->d_k.stride_h;
-  g.dv_out = a->d_v.data;
-  g.dvt = a->d_v.stride_t;
-  g.dvb = a->d_v.stride_b;
-  g.dvh = a->d_v.stride_h;
-  g.dg = static_cast<float*>(a->d_log_decay.data);
-  g.dgt = a->d_log_decay.stride_t;
-  g.dgb = a->d_log_decay.stride_b;
-  g.dgh = a->d_log_decay.stride_h;
-  g.dbeta = static_cast<float*>(a->d_beta.data);
-  g.dbt = a->d_beta.stride_t;
-  g.dbb = a->d_beta.stride_b;
-  g.dbh = a->d_beta.stride_h;
+  GdArgs g = args_of(a);
+  if (on_tensor_cores(a)) return cuda_status(launch_gd_tc(g, a->workspace, true, s));
   const Parts p = walk_parts(a);
   char* w = static_cast<char*>(a->workspace);
   auto take = [&](size_t n) {
@@ -231,21 +228,13 @@ prnn_status_t prnn_gated_delta_backward(const prnn_gated_delta_t* a, void* strea
     w += n;
     return at;
   };
-  const bool tc = on_tensor_cores(a);
-  if (!tc || H > Hq) {
-    g.dq_part = take(p.dq);
-    g.dk_part = take(p.dq);
-  }
-  if (tc) {
-    PRNN_TRY(launch_gd_tc(g, w, true, s));
-    if (H == Hq) return PRNN_OK;
-  } else {
-    g.e = take(p.e);
-    g.du = take(p.e);
-    g.marks = take(p.marks);
-    g.leaves = take(p.leaves);
-    PRNN_TRY(launch_gd_walk_backward(g, s));
-  }
+  g.e = take(p.e);
+  g.du = take(p.e);
+  g.dq_part = take(p.dq);
+  g.dk_part = take(p.dq);
+  g.marks = take(p.marks);
+  g.leaves = take(p.leaves);
+  PRNN_TRY(launch_gd_walk_backward(g, s));
   const prnn_seq_t* out[] = {&a->d_q, &a->d_k};
   const float* part[] = {g.dq_part, g.dk_part};
   for (int i = 0; i < 2; ++i)
@@ -270,7 +259,7 @@ prnn_status_t prnn_gated_delta_step(const prnn_gated_delta_t* a, float* state_po
   all.array(state_pool, sizeof(float) * (size_t)n_slots * a->heads * a->dk * a->dv, true);
   all.array(slots, 4ull * a->B, false);
   if (!all.good()) return PRNN_ERR_INVALID_ARG;
-  const GdArgs g = common(&one);
+  const GdArgs g = args_of(&one);
   GdStepArgs r{a->dtype, a->B, a->heads, a->dk, a->dv, a->scale, g.g, g.beta, g.gb, g.gh, g.bb, g.bh, g.q, g.k, g.v,
                one.o.data, one.o.stride_b, one.o.stride_h, state_pool, n_slots, slots};
   return cuda_status(launch_gd_step(r, static_cast<cudaStream_t>(stream)));

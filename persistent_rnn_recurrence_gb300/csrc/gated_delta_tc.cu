@@ -8,60 +8,53 @@ namespace prnn {
 namespace gd {
 namespace {
 
-// ---- before the states: gates, Tt, Tt V, W, for a chunk of a head per block ------------------------------
+// ---- before the states: gates, Tt, Tt V, W, for a chunk of a head at a time --------------------------------
 //
-// Tt, the inverse of a unit lower triangular matrix, is made in fp32: the four diagonal blocks of 32 by
-// substitution, a column per lane, then the blocks below by T_ij = -T_ii sum_m A_im T_mj, diagonal by diagonal.
-constexpr int kLd = 132;  // floats of a row: 16-byte aligned, rows of a quad of banks apart
+// Tt is the inverse of I + A, A strictly lower triangular.  The diagonal blocks of 32 go by substitution, a column per
+// lane; those of 64 from them by T_10 = -T_11 A_10 T_00 in fp32; and the last block of 64 by the same formula
+// on the tensor cores, T's rows and columns being where the products with V and K want them anyway.
+constexpr int kLd = 68, kPrepThreads = 512;  // floats of a row of 64: 16-byte aligned, rows a quad of banks apart
 struct PrepTab {
   Gates gates;
   double part[4];
   uint64_t bar;
   uint32_t tmem;
 };
-constexpr uint32_t kPrepRight = 96 * 1024, kPrepTab = 192 * 1024;
-static_assert(2 * C * kLd * sizeof(float) <= kPrepTab && kPrepTab + sizeof(PrepTab) <= 227 * 1024, "shared memory");
+// Tt as parts, its diagonal blocks of 64 in fp32 with A's before them, A_10 as parts and A_10 T_00; the right operands lie
+// over the latter three.
+constexpr uint32_t kPrepA = 96 * 1024, kPrepT = kPrepA + 2 * 64 * kLd * 4, kPrepLow = 168 * 1024,
+                   kPrepRight = kPrepA, kPrepTab = 216 * 1024;
+static_assert(kPrepT + 2 * 64 * kLd * 4 <= kPrepLow && kPrepLow + kP * kTile <= kPrepTab &&
+                  kPrepRight + kP * 2 * kTile <= kPrepTab && kPrepTab + sizeof(PrepTab) <= 227 * 1024,
+              "shared memory");
 
-// A's and T's blocks of 32: block (i, j) of T <- -T_ii (sum_{m=j}^{i-1} A_im T_mj), the sum kept in T's unused block
-// (j, i).  Q threads share a block, X x W values each.
-template <int GAP>
+// T_10 <- -T_11 (A_10 T_00) of 2 x 2 blocks of 32, for two diagonal blocks of 64; the product in brackets is kept in
+// T's unused block (0, 1).
 __device__ __forceinline__ void lower_blocks(const float* A, float* T) {
-  constexpr int BLOCKS = 4 - GAP, Q = GAP == 1 ? 128 : (GAP == 2 ? 256 : 512), W = GAP == 3 ? 1 : 2, X = 1024 / Q / W;
-  const int j = threadIdx.x / Q, q = threadIdx.x % Q, i = j + GAP;
-  const int r = q / (32 / W) * X, c = q % (32 / W) * W;
+  const int q = threadIdx.x & 255, r = (q >> 4) * 2, c = (q & 15) * 2;
+  A += (threadIdx.x >> 8) * 64 * kLd;
+  T += (threadIdx.x >> 8) * 64 * kLd;
 #pragma unroll
   for (int pass = 0; pass < 2; ++pass) {
-    if (j < BLOCKS) {
-      float s[X][W];
+    const float* left = pass == 0 ? A + (32 + r) * kLd : T + (32 + r) * kLd + 32;
+    const float* right = pass == 0 ? T + c : T + 32 + c;
+    float2 s[2] = {both(0.f), both(0.f)};
 #pragma unroll
-      for (int x = 0; x < X; ++x)
+    for (int m = 0; m < 32; m += 4) {
+      float4 l[2];
+      float2 f[4];
 #pragma unroll
-        for (int y = 0; y < W; ++y) s[x][y] = 0.f;
-      // pass 0: A[i][j .. i-1] T[j .. i-1][j]; pass 1: T[i][i] times that
-      const float* left = pass == 0 ? A + (32 * i + r) * kLd + 32 * j : T + (32 * i + r) * kLd + 32 * i;
-      const float* right = pass == 0 ? T + 32 * j * kLd + 32 * j + c : T + 32 * j * kLd + 32 * i + c;
-      const int depth = pass == 0 ? 32 * GAP : 32;
-#pragma unroll 2
-      for (int m = 0; m < depth; m += 4) {
-        float4 l[X];
-        Pack<float, W> f[4];
+      for (int x = 0; x < 2; ++x) l[x] = *reinterpret_cast<const float4*>(left + x * kLd + m);
 #pragma unroll
-        for (int x = 0; x < X; ++x) l[x] = *reinterpret_cast<const float4*>(left + x * kLd + m);
+      for (int k = 0; k < 4; ++k) f[k] = *reinterpret_cast<const float2*>(right + (m + k) * kLd);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) f[k] = load_pack<float, W>(right + (m + k) * kLd);
-#pragma unroll
-        for (int x = 0; x < X; ++x)
-#pragma unroll
-          for (int y = 0; y < W; ++y)
-            s[x][y] = fmaf(l[x].w, f[3].v[y], fmaf(l[x].z, f[2].v[y], fmaf(l[x].y, f[1].v[y],
-                                                                        fmaf(l[x].x, f[0].v[y], s[x][y]))));
-      }
-      float* to = pass == 0 ? T + (32 * j + r) * kLd + 32 * i + c : T + (32 * i + r) * kLd + 32 * j + c;
-#pragma unroll
-      for (int x = 0; x < X; ++x)
-#pragma unroll
-        for (int y = 0; y < W; ++y) to[x * kLd + y] = pass == 0 ? s[x][y] : -s[x][y];
+      for (int x = 0; x < 2; ++x)
+        s[x] = fma2(both(l[x].w), f[3], fma2(both(l[x].z), f[2], fma2(both(l[x].y), f[1], fma2(both(l[x].x), f[0], s[x]))));
     }
+    float* to = pass == 0 ? T + r * kLd + 32 + c : T + (32 + r) * kLd + c;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      *reinterpret_cast<float2*>(to + x * kLd) = pass == 0 ? s[x] : mul2(s[x], both(-1.f));
     __syncthreads();
   }
 }
@@ -71,174 +64,201 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 
-constexpr int kPrepThreads = 512;
 template <typename T>
 __global__ void __launch_bounds__(kPrepThreads, 1) gd_prepare_kernel(const __grid_constant__ Args g, int keep_inverse) {
   constexpr int DP = kData<T>, NT = kPrepThreads;
   extern __shared__ __align__(1024) unsigned char smem[];
   PrepTab& tab = *reinterpret_cast<PrepTab*>(smem + kPrepTab);
   const GdArgs& a = g.a;
-  const Place p = place_of(g);
+  int index = blockIdx.x;
+  Place p = next_place(g, index);
   if (p.n == 0) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = (warp & 3) * 32 + lane, quarter = warp >> 2;
-  const T *k = rows_of<T>(a.k, p.t0, p.b, p.hq), *v = rows_of<T>(a.v, p.t0, p.b, p.h);
+  auto keys = [&](const Place& at) { return rows_of<T>(a.k, at.t0, at.b, at.hq); };
   DataRows<T, C, 2, NT> rows;
-  rows.fetch(k, a.k.st, 0, p.n, 0, a.dk, g.dkt, g.vec);
+  rows.fetch(keys(p), a.k.st, 0, p.n, 0, a.dk, g.dkt);
   if (!begin(&tab.bar, &tab.tmem, 256, smem, g.status)) return;
   Steps steps{&tab.bar};
   const uint32_t tmem = tab.tmem, mine = tmem + ((uint32_t)((warp & 3) * 32) << 16), base = smem_u32(smem);
   const uint32_t part = g.dkt * kTile, vpart = g.dvt * kTile;
-  double G = 0;
-  if (tid < C) {
-    if (tid < p.n) {
-      const long long t = p.t0 + tid;
-      float x = a.g[t * a.gt + p.b * a.gb + p.h * a.gh];
-      if (x < -1000.f) x = -1000.f;
-      G = x * 1.4426950408889634;
-      tab.gates.beta[tid] = a.beta[t * a.bt + p.b * a.bb + p.h * a.bh];
-    } else {
-      tab.gates.beta[tid] = 0.f;
-    }
+  const Operand Tt = k_major(base, 2 * kTile, kTile);
+  float *A = reinterpret_cast<float*>(smem + kPrepA), *inv = reinterpret_cast<float*>(smem + kPrepT);
+  while (p.n > 0) {
+    const Place at = p;
+    double G = 0;
+    if (tid < C) {
+      if (tid < at.n) {
+        const long long t = at.t0 + tid;
+        float x = a.g[t * a.gt + at.b * a.gb + at.h * a.gh];
+        if (x < -1000.f) x = -1000.f;
+        G = x * 1.4426950408889634;
+        tab.gates.beta[tid] = a.beta[t * a.bt + at.b * a.bb + at.h * a.bh];
+      } else {
+        tab.gates.beta[tid] = 0.f;
+      }
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double x = __shfl_up_sync(0xffffffffu, G, o);
-      if (lane >= o) G += x;
+      for (int o = 1; o < 32; o <<= 1) {
+        const double x = __shfl_up_sync(0xffffffffu, G, o);
+        if (lane >= o) G += x;
+      }
+      if (lane == 31) tab.part[warp] = G;
     }
-    if (lane == 31) tab.part[warp] = G;
-  }
-  rows.template place<DP>(smem, part, kTile);
-  __syncthreads();
-  if (tid < C) {
-    double all = 0;
+    // K's operand lies where Tt will
+    rows.template place<DP>(smem, part, kTile);
+    __syncthreads();
+    if (tid < C) {
+      double all = 0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      if (w < warp) G += tab.part[w];
-      all += tab.part[w];
+      for (int w = 0; w < 4; ++w) {
+        if (w < warp) G += tab.part[w];
+        all += tab.part[w];
+      }
+      const double last = __shfl_sync(0xffffffffu, G, lane | 15), first = __shfl_sync(0xffffffffu, G, lane & 16);
+      const float hi = (float)G;
+      tab.gates.sum[tid] = make_float2(hi, (float)(G - hi));
+      tab.gates.up[tid] = exp2f(hi);
+      tab.gates.down[tid] = exp2f((float)(all - G));
+      tab.gates.to_last[tid] = exp2f((float)(last - G));
+      tab.gates.from_first[tid] = exp2f((float)(G - first));
     }
-    const float hi = (float)G;
-    tab.gates.hi[tid] = hi;
-    tab.gates.lo[tid] = hi == hi ? (float)(G - hi) : hi;
-    tab.gates.up[tid] = exp2f(hi);
-    tab.gates.down[tid] = exp2f((float)(all - G));
-  }
-  const Operand K = k_major(base, part, kTile);
-  steps.run([&] { product<DP, DP>(tmem, K, K, (a.dk + 15) / 16, id_of(128, false, false), false); });
-  if (tid == 0) {  // the walk's copy of K
-    for (int ct = 0; ct < g.dkt; ++ct)
-      for (int q = 0; q < DP; ++q)
-        bulk_store(g.kimg + ((p.at * g.dkt + ct) * DP + q) * kTile, base + q * part + ct * kTile, kTile);
-    bulk_commit();
-  }
-  {
-    const float* from = reinterpret_cast<const float*>(&tab.gates);
-    float* to = reinterpret_cast<float*>(g.gates + p.at);
-    for (int i = tid; i < (int)(sizeof(Gates) / 4); i += NT) to[i] = from[i];
-  }
-  if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-  steps.wait();
-  __syncthreads();  // K's place may be written again
-  float* A = reinterpret_cast<float*>(smem);
-  float* inv = A + C * kLd;
-  {  // A_ij = (k_i . k_j) D_ij beta_j below the diagonal
-    const float hi = tab.gates.hi[row], lo = tab.gates.lo[row];
+    const Operand K = k_major(base, part, kTile);
+    steps.run([&] { product<DP, DP>(tmem, K, K, (a.dk + 15) / 16, id_of(128, false, false), false); });
+    if (tid == 0) {  // the walk's copy of K
+      for (int ct = 0; ct < g.dkt; ++ct)
+        for (int q = 0; q < DP; ++q)
+          bulk_store(g.kimg + ((at.at * g.dkt + ct) * DP + q) * kTile, base + q * part + ct * kTile, kTile);
+      bulk_commit();
+    }
+    {
+      const float* from = reinterpret_cast<const float*>(&tab.gates);
+      float* to = reinterpret_cast<float*>(g.gates + at.at);
+      for (int i = tid; i < (int)(sizeof(Gates) / 4); i += NT) to[i] = from[i];
+    }
+    steps.wait();
 #pragma unroll 1
-    for (int q = 0; q < 2; ++q) {
+    for (int q = 0; q < 2; ++q) {  // A_ij = (k_i . k_j) D_ij beta_j below the diagonal
       const int c0 = quarter * 32 + q * 16;
+      if ((c0 >> 5) > (warp & 3)) continue;  // behind all of the warp's rows
       float2 x[8];
       read16(mine + c0, x);
+      decayed<true>(x, row, c0, tab.gates);
+      times16(x, tab.gates.beta + c0);
+      if (row >= 64 && c0 < 64) {
+        put16<kP>(smem + kPrepLow, kTile, row, c0, x);
+      } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int j = c0 + 2 * i;
-        x[i].x = j < row ? x[i].x * decay_between(hi, lo, tab.gates.hi[j], tab.gates.lo[j]) * tab.gates.beta[j] : 0.f;
-        x[i].y = j + 1 < row
-                     ? x[i].y * decay_between(hi, lo, tab.gates.hi[j + 1], tab.gates.lo[j + 1]) * tab.gates.beta[j + 1]
-                     : 0.f;
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4*>(A + row * kLd + (c0 & 63) + 4 * i) =
+              make_float4(x[2 * i].x, x[2 * i].y, x[2 * i + 1].x, x[2 * i + 1].y);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<float4*>(A + row * kLd + c0 + 4 * i) =
-            make_float4(x[2 * i].x, x[2 * i].y, x[2 * i + 1].x, x[2 * i + 1].y);
     }
-  }
-  before_sync();
-  __syncthreads();
-  if (warp < 4) {
-    float x[32];
-    const float* D = A + 32 * warp * kLd + 32 * warp;
-#pragma unroll
-    for (int r = 0; r < 32; ++r) {
-      float s[4] = {r == lane ? 1.f : 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int m = 0; m < r; m += 4) {
-        const float4 l = *reinterpret_cast<const float4*>(D + r * kLd + m);
-        s[0] = fmaf(-l.x, x[m], s[0]);
-        if (m + 1 < r) s[1] = fmaf(-l.y, x[m + 1], s[1]);
-        if (m + 2 < r) s[2] = fmaf(-l.z, x[m + 2], s[2]);
-        if (m + 3 < r) s[3] = fmaf(-l.w, x[m + 3], s[3]);
-      }
-      x[r] = (s[0] + s[1]) + (s[2] + s[3]);
-      inv[(32 * warp + r) * kLd + 32 * warp + lane] = x[r];
-    }
-  }
-  __syncthreads();
-  lower_blocks<1>(A, inv);
-  lower_blocks<2>(A, inv);
-  rows.fetch(v, a.v.st, 0, p.n, 0, a.dv, g.dvt, g.vec);
-  lower_blocks<3>(A, inv);
-  {  // Tt as parts, in the place of A and of itself
-    float2 x[2][8];
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const int c = quarter * 32 + q * 16 + 2 * i;
-        const float4 f = *reinterpret_cast<const float4*>(inv + row * kLd + c);
-        x[q][i] = make_float2(c <= row ? f.x : 0.f, c + 1 <= row ? f.y : 0.f);
-        x[q][i + 1] = make_float2(c + 2 <= row ? f.z : 0.f, c + 3 <= row ? f.w : 0.f);
-      }
+    before_sync();
     __syncthreads();
+    if (warp < 4) {
+      float x[32];
+      const int r0 = 32 * warp, c0 = 32 * (warp & 1);
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int c0 = quarter * 32 + q * 16;
-      put16<kP>(smem, 2 * kTile, row, c0, x[q]);
-      if (keep_inverse) store_quads(g.inv + p.at * C * C, C, row, c0, x[q]);
+      for (int r = 0; r < 32; ++r) {
+        float s[4] = {r == lane ? 1.f : 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int m = 0; m < r; m += 4) {
+          const float4 l = *reinterpret_cast<const float4*>(A + (r0 + r) * kLd + c0 + m);
+          s[0] = fmaf(-l.x, x[m], s[0]);
+          if (m + 1 < r) s[1] = fmaf(-l.y, x[m + 1], s[1]);
+          if (m + 2 < r) s[2] = fmaf(-l.z, x[m + 2], s[2]);
+          if (m + 3 < r) s[3] = fmaf(-l.w, x[m + 3], s[3]);
+        }
+        x[r] = (s[0] + s[1]) + (s[2] + s[3]);
+        inv[(r0 + r) * kLd + c0 + lane] = x[r];
+      }
     }
-  }
-  const Operand Tt = k_major(base, 2 * kTile, kTile);
-  rows.template place<DP>(smem + kPrepRight, vpart, kTile);
-  steps.run([&] {
-    product<kP, DP>(tmem, Tt, mn_major(base + kPrepRight, vpart, kTile), 8, id_of(64 * g.dvt, false, true), false);
-  });
-  rows.fetch(k, a.k.st, 0, p.n, 0, a.dk, g.dkt, g.vec);
-  steps.wait();
-  rows.template place<kP>(smem + kPrepRight, part, kTile, tab.gates.up);
-  steps.run([&] {
-    product<kP, kP>(tmem + 128, Tt, mn_major(base + kPrepRight, part, kTile), 8, id_of(64 * g.dkt, false, true), false);
-  });
-  float* E = g.E + p.at * C * 64 * g.dvt;
+    if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncthreads();
+    lower_blocks(A, inv);
+    rows.fetch(rows_of<T>(a.v, at.t0, at.b, at.h), a.v.st, 0, at.n, 0, a.dv, g.dvt);
+    {  // the diagonal blocks of 64 and the zeros right of them as parts
+      float2 x[2][8];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int c0 = quarter * 32 + q * 16;
+        if (row >= 64 && c0 < 64) continue;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const int c = c0 + 2 * i;
+          const float4 f = *reinterpret_cast<const float4*>(inv + row * kLd + (c & 63));
+          x[q][i] = make_float2(c <= row ? f.x : 0.f, c + 1 <= row ? f.y : 0.f);
+          x[q][i + 1] = make_float2(c + 2 <= row ? f.z : 0.f, c + 3 <= row ? f.w : 0.f);
+        }
+        put16<kP>(smem, 2 * kTile, row, c0, x[q]);
+        if (keep_inverse) store_quads(g.inv + at.at * C * C, C, row, c0, x[q]);
+      }
+    }
+    // A_10 T_00, of which rows 64 ... count
+    steps.run([&] {
+      product<kP, kP>(tmem + 128, k_major(base + kPrepLow, kTile, kTile), mn_major(base, 2 * kTile, kTile), 4,
+                      id_of(64, false, true), false);
+    });
+    steps.wait();
+    unsigned char* mid = smem + kPrepA;  // [3][64][64], rows 64 ...
+    if (row >= 64) {
+      const int c0 = quarter * 16;
+      float2 x[8];
+      read16(mine + 128 + c0, x);
+      put16<kP>(mid, kTile / 2, row - 64, c0, x);
+    }
+    steps.run([&] {
+      Operand left = Tt;
+      left.desc += kTile >> 4;  // columns 64 ...
+      product<kP, kP>(tmem + 192, left, mn_major(base + kPrepA, kTile / 2, kTile / 2), 4, id_of(64, false, true), false);
+    });
+    steps.wait();
+    if (row >= 64) {
+      const int c0 = quarter * 16;
+      float2 x[8];
+      read16(mine + 192 + c0, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], both(-1.f));
+      put16<kP>(smem, 2 * kTile, row, c0, x);
+      if (keep_inverse) store_quads(g.inv + at.at * C * C, C, row, c0, x);
+    }
+    rows.template place<DP>(smem + kPrepRight, vpart, kTile);
+    steps.run([&] {
+      product<kP, DP>(tmem, Tt, mn_major(base + kPrepRight, vpart, kTile), 8, id_of(64 * g.dvt, false, true), false);
+    });
+    rows.fetch(keys(at), a.k.st, 0, at.n, 0, a.dk, g.dkt);
+    steps.wait();
+    rows.template place<kP>(smem + kPrepRight, part, kTile, tab.gates.up);
+    steps.run([&] {
+      product<kP, kP>(tmem + 128, Tt, mn_major(base + kPrepRight, part, kTile), 8, id_of(64 * g.dkt, false, true), false);
+    });
+    index += gridDim.x;
+    p = next_place(g, index);
+    if (p.n > 0) rows.fetch(keys(p), a.k.st, 0, p.n, 0, a.dk, g.dkt);
+    float* E = g.E + at.at * C * 64 * g.dvt;
 #pragma unroll 1
-  for (int q = 0; q < g.dvt; ++q) {
-    const int c0 = (quarter * g.dvt + q) * 16;
-    float2 f[8];
-    read16(mine + c0, f);
-    store_quads(E, C, row, c0, f);
-  }
-  steps.wait();
-  // W as tiles [dkt][parts] in the place of its right operand, and from there to the walk's copy
+    for (int q = 0; q < g.dvt; ++q) {
+      const int c0 = (quarter * g.dvt + q) * 16;
+      float2 f[8];
+      read16(mine + c0, f);
+      store_quads(E, C, row, c0, f);
+    }
+    steps.wait();
+    // W as tiles [dkt][parts] in the place of its right operand, and from there to the walk's copy
 #pragma unroll 1
-  for (int q = 0; q < g.dkt; ++q) {
-    const int c0 = (quarter * g.dkt + q) * 16;
-    float2 f[8];
-    read16(mine + 128 + c0, f);
-    put16<kP>(smem + kPrepRight + (c0 >> 6) * kP * kTile, kTile, row, c0 & 63, f);
-  }
-  to_async();
-  before_sync();
-  __syncthreads();
-  if (tid == 0) {
-    bulk_store(g.wimg + p.at * g.dkt * kP * kTile, base + kPrepRight, g.dkt * kP * kTile);
-    bulk_commit();
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    for (int q = 0; q < g.dkt; ++q) {
+      const int c0 = (quarter * g.dkt + q) * 16;
+      float2 f[8];
+      read16(mine + 128 + c0, f);
+      put16<kP>(smem + kPrepRight + (c0 >> 6) * kP * kTile, kTile, row, c0 & 63, f);
+    }
+    to_async();
+    before_sync();
+    __syncthreads();
+    if (tid == 0) {
+      bulk_store(g.wimg + at.at * g.dkt * kP * kTile, base + kPrepRight, g.dkt * kP * kTile);
+      bulk_commit();
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    }
   }
   finish(tmem, 256, steps.ok, g.status);
 }
@@ -504,18 +524,23 @@ struct OutTab {
 constexpr int kOutThreads = 256;
 template <typename T>
 __global__ void __launch_bounds__(kOutThreads, kData<T> == 3 ? 1 : 2)
-    gd_outputs_kernel(const __grid_constant__ Args g, bool out_vec) {
+    gd_outputs_kernel(const __grid_constant__ Args g) {
   using K = OutCfg<T>;
   constexpr int DP = K::DP, PC = K::PC, NT = kOutThreads;
   extern __shared__ __align__(1024) unsigned char smem[];
   OutTab& tab = *reinterpret_cast<OutTab*>(smem + K::kTab);
   const GdArgs& a = g.a;
-  const Place p = place_of(g);
+  const Place p = place_of(g, blockIdx.x);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = (warp & 3) * 32 + lane, half = warp >> 2;
   T* o = static_cast<T*>(a.o) + p.b * a.ob + p.h * a.oh;
+  float* o_part = a.o_part ? a.o_part + ((long long)p.b * a.H + p.h) * a.dvp : nullptr;
+  const long long part_t = (long long)a.B * a.H * a.dvp;
   const int live = (int)(a.T - p.t0 < C ? a.T - p.t0 : C);  // rows of the tensor
-  for (int i = tid; i < (live - p.n) * a.dv; i += NT)       // zeros past the length
-    o[(p.t0 + p.n + i / a.dv) * a.ot + i % a.dv] = from_f32<T>(0.f);
+  for (int i = tid; i < (live - p.n) * a.dvp; i += NT) {    // zeros past the length
+    const long long t = p.t0 + p.n + i / a.dvp;
+    if (o_part) o_part[t * part_t + i % a.dvp] = 0.f;
+    else o[t * a.ot + i % a.dvp] = from_f32<T>(0.f);
+  }
   if (p.n == 0) return;
   const int rows = 64 * g.dkt, cols = 64 * g.dvt;
   const float* S = g.S + p.slot * rows * cols;
@@ -523,8 +548,8 @@ __global__ void __launch_bounds__(kOutThreads, kData<T> == 3 ? 1 : 2)
   DataRows<T, C, 1, NT> qs, ks;
   QuadRows<64, 2, NT> ss;
   auto fetch = [&](int ct) {
-    qs.fetch(q, a.q.st, 0, p.n, ct * 64, a.dk, 1, g.vec);
-    ks.fetch(k, a.k.st, 0, p.n, ct * 64, a.dk, 1, g.vec);
+    qs.fetch(q, a.q.st, 0, p.n, ct * 64, a.dk, 1);
+    ks.fetch(k, a.k.st, 0, p.n, ct * 64, a.dk, 1);
     ss.fetch(S + ct * 64 * 4, rows, 64, g.dvt);
   };
   fetch(0);
@@ -551,18 +576,12 @@ __global__ void __launch_bounds__(kOutThreads, kData<T> == 3 ? 1 : 2)
   const float* E = g.E + p.at * C * cols;
   es.fetch(E, C, C, 1);
   {
-    const float hi = tab.gates.hi[row], lo = tab.gates.lo[row];
 #pragma unroll 1
     for (int x = 0; x < 4; ++x) {
       const int c0 = half * 64 + x * 16;
       float2 v[8];
-      read16(mine + c0, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int j = c0 + 2 * i;
-        v[i].x = j <= row ? v[i].x * decay_between(hi, lo, tab.gates.hi[j], tab.gates.lo[j]) : 0.f;
-        v[i].y = j < row ? v[i].y * decay_between(hi, lo, tab.gates.hi[j + 1], tab.gates.lo[j + 1]) : 0.f;
-      }
+      if ((c0 >> 5) <= (warp & 3)) read16(mine + c0, v);
+      decayed<false>(v, row, c0, tab.gates);
       put16<PC>(smem, 2 * kTile, row, c0, v);
     }
   }
@@ -583,7 +602,9 @@ __global__ void __launch_bounds__(kOutThreads, kData<T> == 3 ? 1 : 2)
       read16(mine + 128 + c0, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = mul2(fma2(both(up), w[i], v[i]), both(a.scale));
-      if (row < p.n) store16<T>(o + (p.t0 + row) * a.ot + c0, a.dv - c0, out_vec, v);
+      if (row >= p.n) continue;
+      if (o_part) store16<float>(o_part + (p.t0 + row) * part_t + c0, a.dvp - c0, v);
+      else store16<T>(o + (p.t0 + row) * a.ot + c0, a.dvp - c0, v);
     }
   }
   finish(tmem, 256, steps.ok, g.status);
@@ -601,7 +622,7 @@ cudaError_t launch_prepare(const Args& g, bool keep_inverse, cudaStream_t s) {
     constexpr uint32_t smem = kPrepTab + sizeof(PrepTab);
     const cudaError_t e = allow(gd_prepare_kernel<T>, smem);
     if (e != cudaSuccess) return e;
-    gd_prepare_kernel<T><<<(unsigned)(g.nbh * g.chunks), kPrepThreads, smem, s>>>(g, keep_inverse);
+    gd_prepare_kernel<T><<<grid_of(g), kPrepThreads, smem, s>>>(g, keep_inverse);
   });
   return cudaGetLastError();
 }
@@ -624,10 +645,7 @@ cudaError_t launch_outputs(const Args& g, cudaStream_t s) {
     constexpr uint32_t smem = OutCfg<T>::kTab + sizeof(OutTab);
     const cudaError_t e = allow(gd_outputs_kernel<T>, smem);
     if (e != cudaSuccess) return e;
-    constexpr int V = 16 / sizeof(T);
-    const bool vec = (reinterpret_cast<uintptr_t>(g.a.o) & 15) == 0 && (g.a.T == 1 || g.a.ot % V == 0) &&
-                     (g.a.B == 1 || g.a.ob % V == 0) && (g.a.H == 1 || g.a.oh % V == 0);
-    gd_outputs_kernel<T><<<(unsigned)(g.nbh * g.chunks), kOutThreads, smem, s>>>(g, vec);
+    gd_outputs_kernel<T><<<(unsigned)(g.nbh * g.chunks), kOutThreads, smem, s>>>(g);
   });
   return cudaGetLastError();
 }
@@ -671,32 +689,107 @@ Plan plan_of(prnn_dtype_t dtype, int T, int B, int H, int dk, int dv, bool backw
   return p;
 }
 
-bool seq_vec(const LaSeq& s, const GdArgs& a, int d, int heads) {
-  const int v = a.dtype == PRNN_F32 ? 4 : 8;
-  return (reinterpret_cast<uintptr_t>(s.p) & 15) == 0 && d % 8 == 0 && (a.T == 1 || s.st % v == 0) &&
-         (a.B == 1 || s.sb % v == 0) && (heads == 1 || s.sh % v == 0);
+// A row of a head's values per warp: x [T][B][heads][d] with any strides into rows of dp >= d values, zeros behind d.
+template <typename T>
+__global__ void __launch_bounds__(256) gd_copy_kernel(const T* x, long long st, long long sb, long long sh, int B, int heads,
+                                                      int d, int dp, long long rows, T* out) {
+  const int lane = threadIdx.x & 31;
+  for (long long row = blockIdx.x * 8LL + (threadIdx.x >> 5); row < rows; row += gridDim.x * 8LL) {
+    const long long tb = row / heads, t = tb / B;
+    const T* from = x + t * st + (tb - t * B) * sb + (row - tb * heads) * sh;
+    for (int k = lane; k < dp; k += 32) out[row * dp + k] = k < d ? from[k] : from_f32<T>(0.f);
+  }
+}
+// out[t][b][hq][0 .. d) = sum of the `group` heads of part [T][B][H][dp] that share hq.
+template <typename T>
+__global__ void __launch_bounds__(256) gd_join_kernel(const float* part, T* out, long long ot, long long ob, long long oh,
+                                                      int B, int heads, int group, int d, int dp, long long rows) {
+  const int lane = threadIdx.x & 31;
+  for (long long row = blockIdx.x * 8LL + (threadIdx.x >> 5); row < rows; row += gridDim.x * 8LL) {
+    const long long tb = row / heads, t = tb / B;
+    T* to = out + t * ot + (tb - t * B) * ob + (row - tb * heads) * oh;
+    const float* from = part + row * group * dp;
+    for (int k = lane; k < d; k += 32) {
+      float s = 0.f;
+      for (int j = 0; j < group; ++j) s += from[(long long)j * dp + k];
+      to[k] = from_f32<T>(s);
+    }
+  }
+}
+
+int up8(int d) { return (d + 7) / 8 * 8; }
+// Rows of d values that 16-byte accesses fit.
+bool packs(prnn_dtype_t dtype, const void* p, int d, int T, int B, int heads, long long t, long long b, long long h) {
+  const int v = dtype == PRNN_F32 ? 4 : 8;
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && d % 8 == 0 && (T == 1 || t % v == 0) && (B == 1 || b % v == 0) &&
+         (heads == 1 || h % v == 0);
+}
+
+// Tensors that the kernels cannot read or write in place: copies of the data, fp32 parts of the results.
+struct Moves {
+  struct In {
+    LaSeq GdArgs::*seq;
+    int heads, d;
+    size_t bytes;
+  } in[4];
+  struct Out {
+    void* out;
+    long long t, b, h;
+    int group, d;
+    float* GdArgs::*part;
+    size_t bytes;
+  } out[3];
+  int ins = 0, outs = 0;
+  size_t total = 0;
+};
+Moves moves_of(const GdArgs& a, bool backward) {
+  Moves m;
+  const int hq = a.H / a.q.share;
+  const size_t esz = a.dtype == PRNN_F32 ? 4 : 2, tokens = (size_t)a.T * a.B;
+  auto in = [&](LaSeq GdArgs::*seq, int heads, int d) {
+    const LaSeq& x = a.*seq;
+    if (packs(a.dtype, x.p, d, a.T, a.B, heads, x.st, x.sb, x.sh)) return;
+    m.in[m.ins++] = {seq, heads, d, up16(tokens * heads * up8(d) * esz)};
+    m.total += m.in[m.ins - 1].bytes;
+  };
+  auto out = [&](void* p, long long t, long long b, long long h, int group, int d, float* GdArgs::*part) {
+    if (!p || (group == 1 && packs(a.dtype, p, d, a.T, a.B, a.H, t, b, h))) return;
+    m.out[m.outs++] = {p, t, b, h, group, d, part, up16(tokens * a.H * up8(d) * 4)};
+    m.total += m.out[m.outs - 1].bytes;
+  };
+  in(&GdArgs::q, hq, a.dk);
+  in(&GdArgs::k, hq, a.dk);
+  in(&GdArgs::v, a.H, a.dv);
+  if (!backward) {
+    out(a.o, a.ot, a.ob, a.oh, 1, a.dv, &GdArgs::o_part);
+    return m;
+  }
+  in(&GdArgs::d_o, a.H, a.dv);
+  out(a.dq_out, a.dqt, a.dqb, a.dqh, a.q.share, a.dk, &GdArgs::dq_part);
+  out(a.dk_out, a.dkt, a.dkb, a.dkh, a.q.share, a.dk, &GdArgs::dk_part);
+  out(a.dv_out, a.dvt, a.dvb, a.dvh, 1, a.dv, &GdArgs::dv_part);
+  return m;
+}
+unsigned blocks_for(long long rows) {
+  return (unsigned)std::max(1LL, std::min((rows + 7) / 8, 16LL * seq_sm_count()));
 }
 
 }  // namespace
 
 bool gd_tc_serves(prnn_dtype_t, int T, int dk, int dv) { return dk <= 128 && dv <= 128 && T >= kGdTcLeast; }
 
-size_t gd_tc_workspace(prnn_dtype_t dtype, int T, int B, int H, int dk, int dv, bool backward) {
-  return plan_of(dtype, T, B, H, dk, dv, backward).total;
+size_t gd_tc_workspace(const GdArgs& a, bool backward) {
+  return plan_of(a.dtype, a.T, a.B, a.H, a.dk, a.dv, backward).total + moves_of(a, backward).total;
 }
 
-cudaError_t launch_gd_tc(const GdArgs& a, void* scratch, bool backward, cudaStream_t s) {
+cudaError_t launch_gd_tc(GdArgs a, void* scratch, bool backward, cudaStream_t s) {
   const Plan p = plan_of(a.dtype, a.T, a.B, a.H, a.dk, a.dv, backward);
   Args g{};
-  g.a = a;
   g.chunks = p.chunks;
   g.dkt = p.dkt;
   g.dvt = p.dvt;
   g.status = seq_status_word();
   if (!g.status) return cudaErrorUnknown;
-  const int hq = a.H / a.q.share;
-  g.vec = seq_vec(a.q, a, a.dk, hq) && seq_vec(a.k, a, a.dk, hq) && seq_vec(a.v, a, a.dv, a.H) &&
-          (!backward || seq_vec(a.d_o, a, a.dv, a.H));
   char* at = static_cast<char*>(scratch);
   auto take = [&](size_t n) {
     char* here = at;
@@ -712,6 +805,24 @@ cudaError_t launch_gd_tc(const GdArgs& a, void* scratch, bool backward, cudaStre
   g.X = take(p.X);
   g.Z0 = take(p.Z0);
   g.R = take(p.R);
+  const Moves m = moves_of(a, backward);
+  a.dkp = up8(a.dk);
+  a.dvp = up8(a.dv);
+  a.o_part = a.dq_part = a.dk_part = a.dv_part = nullptr;
+  for (int i = 0; i < m.ins; ++i) {
+    const Moves::In& in = m.in[i];
+    LaSeq& x = a.*in.seq;
+    const int dp = up8(in.d);
+    const long long n = (long long)a.T * a.B * in.heads;
+    void* to = take(in.bytes);
+    PRNN_BY_DTYPE(a.dtype, T, (gd_copy_kernel<T><<<blocks_for(n), 256, 0, s>>>(
+        static_cast<const T*>(x.p), x.st, x.sb, x.sh, a.B, in.heads, in.d, dp, n, static_cast<T*>(to))));
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    x = {to, (long long)a.B * in.heads * dp, (long long)in.heads * dp, dp, x.share};
+  }
+  for (int i = 0; i < m.outs; ++i) a.*m.out[i].part = take(m.out[i].bytes);
+  g.a = a;
   for (g.bh0 = 0; g.bh0 < a.B * a.H; g.bh0 += p.nbh) {
     g.nbh = std::min(p.nbh, a.B * a.H - g.bh0);
     cudaError_t e = launch_prepare(g, backward, s);
@@ -720,6 +831,14 @@ cudaError_t launch_gd_tc(const GdArgs& a, void* scratch, bool backward, cudaStre
     if (e == cudaSuccess && backward) e = launch_before_reverse(g, s);
     if (e == cudaSuccess && backward) e = launch_chain(g, true, s);
     if (e == cudaSuccess && backward) e = launch_gradients(g, s);
+    if (e != cudaSuccess) return e;
+  }
+  for (int i = 0; i < m.outs; ++i) {
+    const Moves::Out& o = m.out[i];
+    const long long n = (long long)a.T * a.B * (a.H / o.group);
+    PRNN_BY_DTYPE(a.dtype, T, (gd_join_kernel<T><<<blocks_for(n), 256, 0, s>>>(
+        a.*o.part, static_cast<T*>(o.out), o.t, o.b, o.h, a.B, a.H / o.group, o.group, o.d, up8(o.d), n)));
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -19,8 +19,10 @@
 // summed in 64 bits and kept as two fp32 values, so that differences of distant sums keep their bits; one below
 // -1000 counts as -1000 (exp is 0 from -104), which keeps those differences finite.
 //
-// Blocks of the side-by-side kernels work in step: place operands, multiply, read.  What a step loads is requested
-// before the wait for the products of the step before it.
+// Blocks of the side-by-side kernels work in step: place operands, multiply, read.  Each runs through its code once a
+// chunk, so code that is fetched costs as much as code that works: what many steps share is a function of its own
+// (noinline), and data that 16-byte loads do not fit is copied beforehand (the gradients kernel of 210 KB of code took
+// 550 us for T = 2048, 4 sequences of 16 heads of 128 x 128 bf16).
 #pragma once
 
 #include "gated_delta.h"
@@ -37,17 +39,18 @@ constexpr uint32_t kTile = 16384;                     // [128][64] bf16, 128-byt
 template <typename T>
 constexpr int kData = std::is_same<T, float>::value ? 3 : (std::is_same<T, __half>::value ? 2 : 1);
 
-// Per chunk and head, fp32 [128] each: sums of log-decays (to the base 2) in two parts, their exponentials, those to
-// the chunk's end, betas.
+// Per chunk and head, fp32 [128] each: sums G of log-decays (to the base 2) as a value and the rest of it, their exponentials, those to
+// the chunk's end, betas; and decays within blocks of 16 tokens: from token j to its block's last, from its block's
+// first to j.
 struct Gates {
-  float hi[C], lo[C], up[C], down[C], beta[C];
+  float2 sum[C];
+  float up[C], down[C], beta[C], to_last[C], from_first[C];
 };
 
 struct Args {
   GdArgs a;
   int chunks, bh0, nbh;        // chunks of T; the heads of this launch: bh0 ... bh0 + nbh
   int dkt, dvt;                // tiles of 64 columns
-  bool vec;                    // data tensors allow 16-byte loads
   int* status;
   // scratch per (head, chunk): W and K as operand tiles [dkt][parts][128][64]; fp32 matrices in quads of
   // columns, [cols / 4][rows][4]: E and X [128][64 dvt], states (a slot more per head) and their gradients
@@ -70,10 +73,10 @@ struct Place {  // of one block: a head's chunk
   size_t at, slot;  // index of the chunk's scratch, of its state
   long long t0;
 };
-__device__ __forceinline__ Place place_of(const Args& g) {
+__device__ __forceinline__ Place place_of(const Args& g, int index) {
   Place p;
-  const int local = blockIdx.x / g.chunks;
-  p.c = blockIdx.x % g.chunks;
+  const int local = index / g.chunks;
+  p.c = index % g.chunks;
   p.bh = g.bh0 + local;
   p.b = p.bh / g.a.H;
   p.h = p.bh % g.a.H;
@@ -86,14 +89,59 @@ __device__ __forceinline__ Place place_of(const Args& g) {
   p.slot = (size_t)local * (g.chunks + 1) + p.c;
   return p;
 }
+// The next of a block's chunks, from `index` in steps of the grid, that has tokens; n = 0 where there is none.
+__device__ __forceinline__ Place next_place(const Args& g, int& index) {
+  Place p{};
+  for (; index < g.nbh * g.chunks; index += gridDim.x) {
+    p = place_of(g, index);
+    if (p.n > 0) return p;
+  }
+  p.n = 0;
+  return p;
+}
 template <typename T>
 __device__ __forceinline__ const T* rows_of(const LaSeq& x, long long t0, int b, int head) {
   return static_cast<const T*>(x.p) + t0 * x.st + b * x.sb + head * x.sh;
 }
 
 // exp(G_i - G_j).
-__device__ __forceinline__ float decay_between(float hi_i, float lo_i, float hi_j, float lo_j) {
-  return exp2f((hi_i - hi_j) + (lo_i - lo_j));
+__device__ __forceinline__ float exp2_of(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float decay_between(float2 i, float2 j) { return exp2_of((i.x - j.x) + (i.y - j.y)); }
+__device__ __forceinline__ float decay_between(const Gates& g, int i, int j) { return decay_between(g.sum[i], g.sum[j]); }
+__device__ __forceinline__ float at_of16(const float2 (&v)[8], int i) { return i & 1 ? v[i / 2].y : v[i / 2].x; }
+__device__ __forceinline__ void set16(float2 (&v)[8], int i, float f) {
+  if (i & 1) v[i / 2].y = f;
+  else v[i / 2].x = f;
+}
+// Columns c0 ... c0 + 15 of row `row`, both within one chunk, times D_ij: zeros where j > row (or j == row if STRICT).
+// A warp's rows are 32 w ...  Blocks of columns before those take one exponential a row, since a way over the block's last
+// token has two factors that are decays themselves; the diagonal ones one for each value.
+template <bool STRICT>
+__device__ __forceinline__ void decayed(float2 (&v)[8], int row, int c0, const Gates& g) {
+  const int w = row >> 5, cw = c0 >> 5;
+  if (cw > w) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = both(0.f);
+  } else if (cw < w) {
+    const float2 f = both(decay_between(g, row, c0 + 15));
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float4 t = *reinterpret_cast<const float4*>(g.to_last + c0 + 2 * i);
+      v[i] = mul2(v[i], mul2(f, make_float2(t.x, t.y)));
+      v[i + 1] = mul2(v[i + 1], mul2(f, make_float2(t.z, t.w)));
+    }
+  } else {
+    const float2 mine = g.sum[row];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float f = at_of16(v, i) * decay_between(mine, g.sum[c0 + i]);
+      set16(v, i, (STRICT ? c0 + i < row : c0 + i <= row) ? f : 0.f);
+    }
+  }
 }
 
 // 8 values of row r, columns 8 chunk ..., as P parts into tiles `stride` bytes apart.
@@ -111,19 +159,19 @@ __device__ __forceinline__ void put8(unsigned char* tile, uint32_t stride, int r
   }
 }
 
-// 8 values from p, of which the first m count, the others zero.
+// 8 values from a multiple of 16 bytes.
 template <typename T>
-__device__ __forceinline__ Pack<T, 8> get8(const T* p, int m, bool vec) {
+__device__ __forceinline__ Pack<T, 8> get8(const T* p) {
   Pack<T, 8> r;
-  if (vec && m >= 8) {
-    const uint4* u = reinterpret_cast<const uint4*>(p);
-    uint4* to = reinterpret_cast<uint4*>(&r);
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) to[i] = __ldg(u + i);
-  } else {
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(&r)[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ Pack<T, 8> zeros8() {
+  Pack<T, 8> r;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r.v[i] = i < m ? p[i] : from_f32<T>(0.f);
-  }
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(&r)[i] = make_uint4(0, 0, 0, 0);
   return r;
 }
 template <typename T>
@@ -139,13 +187,12 @@ struct DataRows {
   static constexpr int N = ROWS * 8 * TILES / NT;
   Pack<T, 8> raw[N];
   int shift;  // neighbouring threads take a row's pieces of 8 columns
-  __device__ __forceinline__ void fetch(const T* x, long long st, int r0, int n, int c0, int d, int tiles, bool vec) {
+  __device__ __forceinline__ void fetch(const T* x, long long st, int r0, int n, int c0, int d, int tiles) {
     shift = TILES == 2 && tiles == 2 ? 4 : 3;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int u = i * NT + threadIdx.x, r = r0 + (u >> shift), c = c0 + (u & ((1 << shift) - 1)) * 8;
-      const bool in = (u >> shift) < ROWS && r < n && c < d;
-      raw[i] = get8<T>(x + (in ? r * st + c : 0), in ? d - c : 0, vec);
+      raw[i] = (u >> shift) < ROWS && r < n && c < d ? get8<T>(x + r * st + c) : zeros8<T>();
     }
   }
   // Tiles `tile` bytes apart, parts `part` apart; each row times scale[row] where that is given.
@@ -197,6 +244,15 @@ struct QuadRows {
   }
 };
 
+// The whole of that, for operands that are not worth their registers earlier.
+template <int P, int NT>
+__device__ __noinline__ void load_quads(unsigned char* to, uint32_t part, const float* m, int rows, int tiles,
+                                        const float* scale) {
+  QuadRows<C, 2, NT> q;
+  q.fetch(m, rows, rows, tiles);
+  q.template place<P>(to, part, kTile, rows, tiles, scale);
+}
+
 // An operand: descriptor of its first part, bytes from one part to the next, and of its steps of 16 along K.
 struct Operand {
   uint64_t desc;
@@ -212,20 +268,22 @@ __device__ __forceinline__ Operand mn_major(uint32_t addr, uint32_t part, uint32
   return {mn_desc(addr, tile), part >> 4, 0};
 }
 // D (+)= A B over `steps` steps of 16: every pair of parts whose places add up to less than three, small ones first.
-template <int PA, int PB>
-__device__ __forceinline__ void product(uint32_t d, const Operand& a, const Operand& b, int steps, uint32_t id,
-                                        bool add) {
-  uint32_t acc = add;
-#pragma unroll
-  for (int s = PA + PB - 2 < 2 ? PA + PB - 2 : 2; s >= 0; --s)
-#pragma unroll
-    for (int p = 0; p < PA; ++p) {
-      if (s - p < 0 || s - p >= PB) continue;
+static __device__ __noinline__ void product_of(int pa, int pb, uint32_t d, Operand a, Operand b, int steps, uint32_t id,
+                                        uint32_t acc) {
+#pragma unroll 1
+  for (int s = min(pa + pb - 2, 2); s >= 0; --s)
+#pragma unroll 1
+    for (int p = max(0, s - pb + 1); p < min(pa, s + 1); ++p)
+#pragma unroll 1
       for (int k = 0; k < steps; ++k) {
         umma_f16(d, a.at(p, k), b.at(s - p, k), id, acc);
         acc = 1;
       }
-    }
+}
+template <int PA, int PB>
+__device__ __forceinline__ void product(uint32_t d, const Operand& a, const Operand& b, int steps, uint32_t id,
+                                        bool add) {
+  product_of(PA, PB, d, a, b, steps, id, add);
 }
 __device__ __forceinline__ uint32_t id_of(int n, bool a_mn, bool b_mn) {
   return bf16_idesc(128, n) | (a_mn ? kAMn : 0u) | (b_mn ? kBMn : 0u);
@@ -318,23 +376,33 @@ __device__ __forceinline__ void put16(unsigned char* tiles, uint32_t stride, int
     put8<P>(tiles + (c0 >> 6) * kTile, stride, r, ((c0 & 63) >> 3) + j, w);
   }
 }
-// 16 values of one row at p, of which the first m are the output's.
+// 16 values of one row at p, of which the first m, a multiple of 8, are the output's.
 template <typename T>
-__device__ __forceinline__ void store16(T* p, int m, bool vec, const float2 (&v)[8]) {
+__device__ __forceinline__ void store16(T* p, int m, const float2 (&v)[8]) {
   constexpr int V = 16 / sizeof(T);
-  if (vec && m >= 16) {
 #pragma unroll
-    for (int i = 0; i < 16 / V; ++i) {
-      Pack<T, V> o;
+  for (int i = 0; i < 16 / V; ++i) {
+    if (i * V >= m) continue;
+    Pack<T, V> o;
 #pragma unroll
-      for (int j = 0; j < V / 2; ++j) set_pair<T, V>(o, j, v[i * V / 2 + j]);
-      store_pack<T, V>(p + i * V, o);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < m) p[i] = from_f32<T>(i & 1 ? v[i / 2].y : v[i / 2].x);
+    for (int j = 0; j < V / 2; ++j) set_pair<T, V>(o, j, v[i * V / 2 + j]);
+    store_pack<T, V>(p + i * V, o);
   }
+}
+
+__device__ __forceinline__ void times16(float2 (&v)[8], const float* f) {  // f: 16 floats, 16-byte aligned
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float4 t = *reinterpret_cast<const float4*>(f + 2 * i);
+    v[i] = mul2(v[i], make_float2(t.x, t.y));
+    v[i + 1] = mul2(v[i + 1], make_float2(t.z, t.w));
+  }
+}
+
+// A block per SM where each has chunks enough to go on with the next, else one for every chunk.
+inline unsigned grid_of(const Args& g) {
+  const long long n = (long long)g.nbh * g.chunks, sms = seq_sm_count();
+  return (unsigned)(n < 4 * sms ? n : sms);
 }
 
 cudaError_t launch_prepare(const Args& g, bool keep_inverse, cudaStream_t s);

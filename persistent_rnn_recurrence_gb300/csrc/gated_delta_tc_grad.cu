@@ -30,15 +30,13 @@ struct Pieces {
   const T* x;
   long long st;
   int n, d, tiles;
-  bool vec;
-  __device__ __forceinline__ void fetch(int ct, int r0) { rows.fetch(x, st, r0, n, ct * 64, d, 1, vec); }
-  __device__ __forceinline__ void first(const T* x_, long long st_, int n_, int d_, int tiles_, bool vec_) {
+  __device__ __forceinline__ void fetch(int ct, int r0) { rows.fetch(x, st, r0, n, ct * 64, d, 1); }
+  __device__ __forceinline__ void first(const T* x_, long long st_, int n_, int d_, int tiles_) {
     x = x_;
     st = st_;
     n = n_;
     d = d_;
     tiles = tiles_;
-    vec = vec_;
     fetch(0, 0);
   }
   template <typename F>
@@ -72,14 +70,14 @@ __global__ void __launch_bounds__(kThreads, 1) gd_before_reverse_kernel(const __
   extern __shared__ __align__(1024) unsigned char smem[];
   Tab& tab = *reinterpret_cast<Tab*>(smem + kTab);
   const GdArgs& a = g.a;
-  const Place p = place_of(g);
+  const Place p = place_of(g, blockIdx.x);
   if (p.n == 0) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = (warp & 3) * 32 + lane, quarter = warp >> 2;
   const T *q = rows_of<T>(a.q, p.t0, p.b, p.hq), *k = rows_of<T>(a.k, p.t0, p.b, p.hq),
           *d_o = rows_of<T>(a.d_o, p.t0, p.b, p.h);
   DataRows<T, C, 2, kThreads> qs, ks;
-  qs.fetch(q, a.q.st, 0, p.n, 0, a.dk, g.dkt, g.vec);
-  ks.fetch(k, a.k.st, 0, p.n, 0, a.dk, g.dkt, g.vec);
+  qs.fetch(q, a.q.st, 0, p.n, 0, a.dk, g.dkt);
+  ks.fetch(k, a.k.st, 0, p.n, 0, a.dk, g.dkt);
   if (!begin(&tab.bar, &tab.tmem, 512, smem, g.status)) return;
   Steps steps{&tab.bar};
   const uint32_t tmem = tab.tmem, mine = tmem + ((uint32_t)((warp & 3) * 32) << 16), base = smem_u32(smem);
@@ -93,21 +91,17 @@ __global__ void __launch_bounds__(kThreads, 1) gd_before_reverse_kernel(const __
                     id_of(128, false, false), false);
   });
   Pieces<T> dos;
-  dos.first(d_o, a.d_o.st, p.n, a.dv, g.dvt, g.vec);
+  dos.first(d_o, a.d_o.st, p.n, a.dv, g.dvt);
   steps.wait();
   if (tid < C) tab.rows[0][0][tid] = a.scale * tab.gates.up[tid];
-  const float hi = tab.gates.hi[row], lo = tab.gates.lo[row];
 #pragma unroll 1
   for (int x = 0; x < 2; ++x) {
     const int c0 = quarter * 32 + x * 16;
     float2 v[8];
-    read16(mine + c0, v);
+    if (quarter <= (warp & 3)) read16(mine + c0, v);
+    decayed<false>(v, row, c0, tab.gates);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int j = c0 + 2 * i;
-      v[i].x = j <= row ? a.scale * v[i].x * decay_between(hi, lo, tab.gates.hi[j], tab.gates.lo[j]) : 0.f;
-      v[i].y = j < row ? a.scale * v[i].y * decay_between(hi, lo, tab.gates.hi[j + 1], tab.gates.lo[j + 1]) : 0.f;
-    }
+    for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], both(a.scale));
     put16<kP>(smem + kTwo, 2 * kTile, row, c0, v);
   }
   __syncthreads();
@@ -132,36 +126,45 @@ __global__ void __launch_bounds__(kThreads, 1) gd_before_reverse_kernel(const __
 
 // ---- the gradients of a chunk ----------------------------------------------------------------------------
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_constant__ Args g, bool dq_vec,
-                                                                   bool dk_vec, bool dv_vec) {
+__global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_constant__ Args g) {
   constexpr int DP = kData<T>;
   extern __shared__ __align__(1024) unsigned char smem[];
   Tab& tab = *reinterpret_cast<Tab*>(smem + kTab);
   const GdArgs& a = g.a;
-  const Place p = place_of(g);
+  const Place p = place_of(g, blockIdx.x);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = (warp & 3) * 32 + lane, quarter = warp >> 2;
-  // where this head's rows of gradients go: the tensors themselves, or fp32 parts that are summed over heads later
-  const bool parts = a.dq_part != nullptr;
-  auto zero_rows = [&](auto* x, long long st, int d, int live) {
-    using E = std::remove_reference_t<decltype(*x)>;
-    for (int i = tid; i < (live - p.n) * d; i += kThreads) x[(p.t0 + p.n + i / d) * st + i % d] = from_f32<E>(0.f);
-  };
-  const int live = (int)(a.T - p.t0 < C ? a.T - p.t0 : C);
-  const long long part_t = (long long)a.B * a.H * a.dk, part_at = ((long long)p.b * a.H + p.h) * a.dk;
-  T *dq = static_cast<T*>(a.dq_out) + p.b * a.dqb + p.h * a.dqh, *dk = static_cast<T*>(a.dk_out) + p.b * a.dkb + p.h * a.dkh,
-    *dv = static_cast<T*>(a.dv_out) + p.b * a.dvb + p.h * a.dvh;
-  if (p.n < live) {
-    if (parts) {
-      zero_rows(a.dq_part + part_at, part_t, a.dk, live);
-      zero_rows(a.dk_part + part_at, part_t, a.dk, live);
-    } else {
-      if (a.dq_out) zero_rows(dq, a.dqt, a.dk, live);
-      if (a.dk_out) zero_rows(dk, a.dkt, a.dk, live);
+  // Where this head's rows of a gradient go: the tensor itself, or fp32 parts that are joined later.
+  struct Rows {
+    T* out;
+    float* part;
+    long long st, part_st;
+    int d;
+    __device__ __forceinline__ void store(long long t, int c0, const float2 (&v)[8]) const {
+      if (part) store16<float>(part + t * part_st + c0, d - c0, v);
+      else if (out) store16<T>(out + t * st + c0, d - c0, v);
     }
-    if (a.dv_out) zero_rows(dv, a.dvt, a.dv, live);
-    for (int i = p.n + tid; i < live; i += kThreads) {
-      if (a.dg) a.dg[(p.t0 + i) * a.dgt + p.b * a.dgb + p.h * a.dgh] = 0.f;
-      if (a.dbeta) a.dbeta[(p.t0 + i) * a.dbt + p.b * a.dbb + p.h * a.dbh] = 0.f;
+    __device__ __forceinline__ void zero(long long t, int c) const {
+      if (part) part[t * part_st + c] = 0.f;
+      else if (out) out[t * st + c] = from_f32<T>(0.f);
+    }
+  };
+  auto rows_to = [&](void* out, float* part, long long st, long long sb, long long sh, int d) {
+    return Rows{out ? static_cast<T*>(out) + p.b * sb + p.h * sh : nullptr,
+                part ? part + ((long long)p.b * a.H + p.h) * d : nullptr, st, (long long)a.B * a.H * d, d};
+  };
+  const Rows dq = rows_to(a.dq_out, a.dq_part, a.dqt, a.dqb, a.dqh, a.dkp),
+             dk = rows_to(a.dk_out, a.dk_part, a.dkt, a.dkb, a.dkh, a.dkp),
+             dv = rows_to(a.dv_out, a.dv_part, a.dvt, a.dvb, a.dvh, a.dvp);
+  const int live = (int)(a.T - p.t0 < C ? a.T - p.t0 : C);  // rows of the tensors
+  for (int r = p.n; r < live; ++r) {                        // zeros past the length
+    if (tid < a.dkp) {
+      dq.zero(p.t0 + r, tid);
+      dk.zero(p.t0 + r, tid);
+    }
+    if (tid < a.dvp) dv.zero(p.t0 + r, tid);
+    if (tid == 0) {
+      if (a.dg) a.dg[(p.t0 + r) * a.dgt + p.b * a.dgb + p.h * a.dgh] = 0.f;
+      if (a.dbeta) a.dbeta[(p.t0 + r) * a.dbt + p.b * a.dbb + p.h * a.dbh] = 0.f;
     }
   }
   if (p.n == 0) return;
@@ -177,31 +180,33 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
               *R = g.R + p.at * rows * cols, *inv = g.inv + p.at * C * C;
   const T *q = rows_of<T>(a.q, p.t0, p.b, p.hq), *k = rows_of<T>(a.k, p.t0, p.b, p.hq),
           *v = rows_of<T>(a.v, p.t0, p.b, p.h), *d_o = rows_of<T>(a.d_o, p.t0, p.b, p.h);
-  const float hi = tab.gates.hi[row], lo = tab.gates.lo[row], up = tab.gates.up[row], down = tab.gates.down[row],
-              beta = tab.gates.beta[row];
+  const float up = tab.gates.up[row], down = tab.gates.down[row], beta = tab.gates.beta[row];
   const bool mine_live = row < p.n;
-  QuadRows<C, 2, kThreads> fp;
   DataRows<T, C, 2, kThreads> data;
   Pieces<T> pieces;
-  // this row's 16 values at columns c0 of a data tensor's row times v, summed
-  auto dot_row = [&](const T* x, int c0, int d, const float2 (&f)[8]) {
+  auto quads = [&](uint32_t where, const float* m, int rows_, int tiles, const float* scale) {
+    load_quads<kP, kThreads>(smem + where, tiles * kTile, m, rows_, tiles, scale);
+  };
+  // this row's 16 values at columns c0 of a data tensor's row times f, summed
+  auto dot_row = [&](const Pack<T, 8> (&x)[2], const float2 (&f)[8]) {
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      if (c0 + 8 * j >= d) continue;
       float2 y[4];
-      pairs_of<T>(get8<T>(x + c0 + 8 * j, d - c0 - 8 * j, g.vec), y);
+      pairs_of<T>(x[j], y);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s = fmaf(y[i].x, f[4 * j + i].x, fmaf(y[i].y, f[4 * j + i].y, s));
+      for (int k = 0; k < 4; ++k) s = fmaf(y[k].x, f[4 * j + k].x, fmaf(y[k].y, f[4 * j + k].y, s));
     }
     return s;
   };
+  auto ask_row = [&](Pack<T, 8> (&x)[2], const T* from, int c0, int d) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) x[j] = mine_live && c0 + 8 * j < d ? get8<T>(from + c0 + 8 * j) : zeros8<T>();
+  };
 
   // dV = Tt^T (beta X)
-  fp.fetch(inv, C, C, 2);
-  fp.template place<kP>(smem + kOne, 2 * kTile, kTile, C, 2);
-  fp.fetch(X, C, C, g.dvt);
-  fp.template place<kP>(smem + kTwo, vpart, kTile, C, g.dvt, tab.gates.beta);
+  quads(kOne, inv, C, 2, nullptr);
+  quads(kTwo, X, C, g.dvt, tab.gates.beta);
   steps.run([&] {
     product<kP, kP>(tmem + D0, mn_major(base + kOne, 2 * kTile, kTile), mn_major(base + kTwo, vpart, kTile), 8,
                     id_of(cols, true, true), false);
@@ -217,7 +222,6 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
       const float4 e = reinterpret_cast<const float4*>(E)[i], x = reinterpret_cast<const float4*>(X)[i];
       es = fmaf(e.x, x.x, fmaf(e.y, x.y, fmaf(e.z, x.z, fmaf(e.w, x.w, es))));
     }
-  fp.fetch(E, C, C, g.dvt);
   steps.wait();
   {
     float s = 0.f, ev = 0.f;
@@ -225,10 +229,12 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
     for (int x = 0; x < g.dvt; ++x) {
       const int c0 = (quarter * g.dvt + x) * 16;
       float2 f[8];
+      Pack<T, 8> vs[2];
+      ask_row(vs, v + row * a.v.st, c0, a.dv);
       read16(mine + D0 + c0, f);
       if (mine_live) {
-        s += dot_row(v + row * a.v.st, c0, a.dv, f);
-        if (a.dv_out) store16<T>(dv + (p.t0 + row) * a.dvt + c0, a.dv - c0, dv_vec, f);
+        s += dot_row(vs, f);
+        dv.store(p.t0 + row, c0, f);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -241,17 +247,17 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
     if (!tiny) es = ev / beta;
   }
   // dV E^T, E dV^T, and K K^T where a beta is 0
-  fp.template place<kP>(smem + kOne, vpart, kTile, C, g.dvt);
+  quads(kOne, E, C, g.dvt, nullptr);
   const Operand one_v = k_major(base + kOne, vpart, kTile), two_v = k_major(base + kTwo, vpart, kTile);
   const int vsteps = (a.dv + 15) / 16, ksteps = (a.dk + 15) / 16;
   steps.run([&] {
     product<kP, kP>(tmem + D0, two_v, one_v, vsteps, id_of(128, false, false), false);
     product<kP, kP>(tmem + D1, one_v, two_v, vsteps, id_of(128, false, false), false);
   });
-  pieces.first(k, a.k.st, p.n, a.dk, g.dkt, g.vec);
+  pieces.first(k, a.k.st, p.n, a.dk, g.dkt);
   steps.wait();
   if (any_tiny) {
-    data.fetch(k, a.k.st, 0, p.n, 0, a.dk, g.dkt, g.vec);
+    data.fetch(k, a.k.st, 0, p.n, 0, a.dk, g.dkt);
     data.template place<DP>(smem + kOne, kpart, kTile);
     steps.run([&] {
       const Operand K = k_major(base + kOne, kpart, kTile);
@@ -264,26 +270,41 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
 #pragma unroll 1
     for (int x = 0; x < 2; ++x) {
       const int c0 = quarter * 32 + x * 16;
-      float2 y1[8], y2[8], kk[8] = {};
-      read16(mine + D0 + c0, y1);
-      read16(mine + D1 + c0, y2);
-      if (any_tiny) read16(mine + D2 + c0, kk);
+      float2 y1[8], y2[8];
+      if (quarter <= (warp & 3)) {
+        read16(mine + D0 + c0, y1);
+        decayed<true>(y1, row, c0, tab.gates);
+        times16(y1, tab.gates.beta + c0);
+      }
+      if (quarter >= (warp & 3)) {  // (e_i . dv_j) D_ji, j behind i
+        read16(mine + D1 + c0, y2);
+        if (quarter > (warp & 3)) {
+          const float2 w = both(decay_between(tab.gates, c0, row));
+          times16(y2, tab.gates.from_first + c0);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int j = c0 + i;
-        const float hj = tab.gates.hi[j], lj = tab.gates.lo[j];
-        const float f1 = i & 1 ? y1[i / 2].y : y1[i / 2].x, f2 = i & 1 ? y2[i / 2].y : y2[i / 2].x,
-                    fk = i & 1 ? kk[i / 2].y : kk[i / 2].x;
-        float y = 0.f;
-        if (j < row) {
-          y = -f1 * tab.gates.beta[j] * decay_between(hi, lo, hj, lj);
-        } else if (j > row) {
-          const float w = f2 * decay_between(hj, lj, hi, lo);
-          y = -w * beta;
-          if (tiny) s = fmaf(-fk, w, s);
+          for (int i = 0; i < 8; ++i) y2[i] = mul2(y2[i], w);
+        } else {
+          const float2 here_ = tab.gates.sum[row];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int j = c0 + i;
+            const float f = at_of16(y2, i) * decay_between(tab.gates.sum[j], here_);
+            set16(y2, i, j > row ? f : 0.f);
+          }
         }
-        if (i & 1) y1[i / 2].y = y;
-        else y1[i / 2].x = y;
+        if (any_tiny) {
+          float2 kk[8];
+          read16(mine + D2 + c0, kk);
+          if (tiny)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s = fmaf(-kk[i].x, y2[i].x, fmaf(-kk[i].y, y2[i].y, s));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (quarter > (warp & 3)) y1[i] = mul2(y2[i], both(-beta));
+        else if (quarter == (warp & 3)) y1[i] = fma2(y2[i], both(-beta), mul2(y1[i], both(-1.f)));
+        else y1[i] = mul2(y1[i], both(-1.f));
       }
       put16<kP>(smem + kOne, 2 * kTile, row, c0, y1);
     }
@@ -298,32 +319,27 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
     product<kP, DP>(tmem + D3 + 64 * ct, from_step(one_t, k0), right, n, id_of(64, false, true), add);
   });
   // D0 = dV S0^T
-  fp.fetch(S, rows, rows, g.dvt);
-  fp.template place<kP>(smem + kOne, vpart, kTile, rows, g.dvt);
+  quads(kOne, S, rows, g.dvt, nullptr);
   steps.run([&] { product<kP, kP>(tmem + D0, two_v, one_v, vsteps, id_of(rows, false, false), false); });
-  data.fetch(d_o, a.d_o.st, 0, p.n, 0, a.dv, g.dvt, g.vec);
+  data.fetch(d_o, a.d_o.st, 0, p.n, 0, a.dv, g.dvt);
   steps.wait();
   // D1 = dO S0^T
   data.template place<DP>(smem + kTwo, vpart, kTile);
   steps.run([&] { product<DP, kP>(tmem + D1, two_v, one_v, vsteps, id_of(rows, false, false), false); });
-  fp.fetch(E, C, C, g.dvt);
   steps.wait();
   // D2 = dO U^T
-  fp.template place<kP>(smem + kOne, vpart, kTile, C, g.dvt, tab.gates.beta);
+  quads(kOne, E, C, g.dvt, tab.gates.beta);
   steps.run([&] { product<DP, kP>(tmem + D2, two_v, one_v, vsteps, id_of(128, false, false), false); });
-  pieces.first(k, a.k.st, p.n, a.dk, g.dkt, g.vec);
+  pieces.first(k, a.k.st, p.n, a.dk, g.dkt);
   steps.wait();
 #pragma unroll 1
   for (int x = 0; x < 2; ++x) {
     const int c0 = quarter * 32 + x * 16;
     float2 f[8];
-    read16(mine + D2 + c0, f);
+    if (quarter <= (warp & 3)) read16(mine + D2 + c0, f);
+    decayed<false>(f, row, c0, tab.gates);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int j = c0 + 2 * i;
-      f[i].x = j <= row ? a.scale * f[i].x * decay_between(hi, lo, tab.gates.hi[j], tab.gates.lo[j]) : 0.f;
-      f[i].y = j < row ? a.scale * f[i].y * decay_between(hi, lo, tab.gates.hi[j + 1], tab.gates.lo[j + 1]) : 0.f;
-    }
+    for (int i = 0; i < 8; ++i) f[i] = mul2(f[i], both(a.scale));
     put16<kP>(smem + kTwo, 2 * kTile, row, c0, f);
   }
   before_sync();
@@ -334,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
   pieces.multiply(steps, smem, [&](int ct, int k0, const Operand& right, int n, bool add) {
     product<kP, DP>(tmem + D2 + 64 * ct, from_step(two_t, k0), right, n, id_of(64, false, true), add);
   });
-  pieces.first(q, a.q.st, p.n, a.dk, g.dkt, g.vec);
+  pieces.first(q, a.q.st, p.n, a.dk, g.dkt);
   {
     float s = 0.f;
     const float f0 = a.scale * up;
@@ -342,14 +358,15 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
     for (int x = 0; x < g.dkt; ++x) {
       const int c0 = (quarter * g.dkt + x) * 16;
       float2 f[8], h[8];
+      Pack<T, 8> qs[2];
+      ask_row(qs, q + row * a.q.st, c0, a.dk);
       read16(mine + D1 + c0, f);
       read16(mine + D2 + c0, h);
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] = fma2(both(f0), f[i], h[i]);
       if (mine_live) {
-        s += dot_row(q + row * a.q.st, c0, a.dk, f);
-        if (parts) store16<float>(a.dq_part + (p.t0 + row) * part_t + part_at + c0, a.dk - c0, dq_vec, f);
-        else if (a.dq_out) store16<T>(dq + (p.t0 + row) * a.dqt + c0, a.dk - c0, dq_vec, f);
+        s += dot_row(qs, f);
+        dq.store(p.t0 + row, c0, f);
       }
     }
     tab.rows[quarter][0][row] = s;
@@ -362,8 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
     product<kP, DP>(tmem + D3 + 64 * ct, from_step(two_tt, k0), right, n, id_of(64, true, true), true);
   });
   // D1 = U R^T
-  fp.fetch(R, rows, rows, g.dvt);
-  fp.template place<kP>(smem + kTwo, vpart, kTile, rows, g.dvt);
+  quads(kTwo, R, rows, g.dvt, nullptr);
   steps.run([&] { product<kP, kP>(tmem + D1, one_v, two_v, vsteps, id_of(rows, false, false), false); });
   // <S, R> where the chunk ends
   float leave = 0.f;
@@ -385,10 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
     read16(mine + D1 + c0, h);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = fma2(both(down), h[i], f[i]);
-    if (mine_live) {
-      if (parts) store16<float>(a.dk_part + (p.t0 + row) * part_t + part_at + c0, a.dk - c0, dk_vec, f);
-      else if (a.dk_out) store16<T>(dk + (p.t0 + row) * a.dkt + c0, a.dk - c0, dk_vec, f);
-    }
+    if (mine_live) dk.store(p.t0 + row, c0, f);
   }
   __syncthreads();
   if (warp == 0) {  // the gates: a lane has 4 tokens, summed from the chunk's end
@@ -424,12 +437,6 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
   finish(tmem, 512, steps.ok, g.status);
 }
 
-bool packs(const GdArgs& a, const void* p, int e, long long t, long long b, long long h) {
-  const int v = 16 / e;
-  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (a.T == 1 || t % v == 0) && (a.B == 1 || b % v == 0) &&
-         (a.H == 1 || h % v == 0);
-}
-
 }  // namespace
 
 cudaError_t launch_before_reverse(const Args& g, cudaStream_t s) {
@@ -450,11 +457,7 @@ cudaError_t launch_gradients(const Args& g, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(gd_gradients_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)smem);
     if (e != cudaSuccess) return e;
-    const bool part = packs(a, a.dq_part, 4, a.dk, a.dk, a.dk);
-    const bool dq = a.dq_part ? part : packs(a, a.dq_out, sizeof(T), a.dqt, a.dqb, a.dqh);
-    const bool dk = a.dq_part ? part : packs(a, a.dk_out, sizeof(T), a.dkt, a.dkb, a.dkh);
-    const bool dv = packs(a, a.dv_out, sizeof(T), a.dvt, a.dvb, a.dvh);
-    gd_gradients_kernel<T><<<(unsigned)(g.nbh * g.chunks), kThreads, smem, s>>>(g, dq, dk, dv);
+    gd_gradients_kernel<T><<<(unsigned)(g.nbh * g.chunks), kThreads, smem, s>>>(g);
   });
   return cudaGetLastError();
 }

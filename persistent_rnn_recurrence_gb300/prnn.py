@@ -1059,13 +1059,18 @@ def gated_delta_rule(q, k, v, log_decay, beta, scale=1.0, state=None, lens=None,
 
 
 def _delta_workspace(head, backward, dev, on):
-    """(tensor, its address, its bytes); it must outlive the call.  The size depends on the sizes alone."""
-    key = ("delta", dev, backward, *head[:7])
+    """(tensor, its address, its bytes); it must outlive the call.  The size depends on the sizes, the strides and
+    the alignment of the tensors, not on where they are."""
+    key = ("delta", dev, backward, *head[:7], *head[10:13], *head[14:17], *head[18:21], *head[31:34], *head[36:39],
+           (head[9] | head[13] | head[17] | head[30] | head[35]) & 15)
     need = _sizes.get(key)
     if need is None:
         if len(_sizes) > 4096:
             _sizes.clear()
-        need = _sizes[key] = prnn_gated_delta_workspace(_GD_PACK(*head, 0, 0), backward)
+        need = prnn_gated_delta_workspace(_GD_PACK(*head, 0, 0), backward)
+        # with a tensor off 16 bytes the size says nothing of the others' alignment
+        if key[-1] == 0:
+            _sizes[key] = need
     if need == 0:
         return None, 0, 0
     ws = _torch.empty(need, dtype=_torch.uint8, device=on)
