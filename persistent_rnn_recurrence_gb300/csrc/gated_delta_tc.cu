@@ -83,19 +83,21 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gd_prepare_kernel(const __gri
   const uint32_t part = g.dkt * kTile, vpart = g.dvt * kTile;
   const Operand Tt = k_major(base, 2 * kTile, kTile);
   float *A = reinterpret_cast<float*>(smem + kPrepA), *inv = reinterpret_cast<float*>(smem + kPrepT);
+  float gate = 0.f, beta = 0.f;
+  auto ask_gates = [&](const Place& at) {
+    const long long t = at.t0 + tid;
+    const bool in = tid < at.n;
+    gate = in ? a.g[t * a.gt + at.b * a.gb + at.h * a.gh] : 0.f;
+    beta = in ? a.beta[t * a.bt + at.b * a.bb + at.h * a.bh] : 0.f;
+  };
+  ask_gates(p);
   while (p.n > 0) {
     const Place at = p;
     double G = 0;
     if (tid < C) {
-      if (tid < at.n) {
-        const long long t = at.t0 + tid;
-        float x = a.g[t * a.gt + at.b * a.gb + at.h * a.gh];
-        if (x < -1000.f) x = -1000.f;
-        G = x * 1.4426950408889634;
-        tab.gates.beta[tid] = a.beta[t * a.bt + at.b * a.bb + at.h * a.bh];
-      } else {
-        tab.gates.beta[tid] = 0.f;
-      }
+      if (gate < -1000.f) gate = -1000.f;
+      G = gate * 1.4426950408889634;
+      tab.gates.beta[tid] = beta;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const double x = __shfl_up_sync(0xffffffffu, G, o);
@@ -105,6 +107,8 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gd_prepare_kernel(const __gri
     }
     // K's operand lies where Tt will
     rows.template place<DP>(smem, part, kTile);
+    rows.fetch(rows_of<T>(a.v, at.t0, at.b, at.h), a.v.st, 0, at.n, 0, a.dv, g.dvt);
+    if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last chunk's W has been read
     __syncthreads();
     if (tid < C) {
       double all = 0;
@@ -175,7 +179,6 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gd_prepare_kernel(const __gri
     if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     __syncthreads();
     lower_blocks(A, inv);
-    rows.fetch(rows_of<T>(a.v, at.t0, at.b, at.h), a.v.st, 0, at.n, 0, a.dv, g.dvt);
     {  // the diagonal blocks of 64 and the zeros right of them as parts
       float2 x[2][8];
 #pragma unroll
@@ -233,7 +236,10 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gd_prepare_kernel(const __gri
     });
     index += gridDim.x;
     p = next_place(g, index);
-    if (p.n > 0) rows.fetch(keys(p), a.k.st, 0, p.n, 0, a.dk, g.dkt);
+    if (p.n > 0) {
+      rows.fetch(keys(p), a.k.st, 0, p.n, 0, a.dk, g.dkt);
+      ask_gates(p);
+    }
     float* E = g.E + at.at * C * 64 * g.dvt;
 #pragma unroll 1
     for (int q = 0; q < g.dvt; ++q) {
@@ -257,9 +263,9 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gd_prepare_kernel(const __gri
     if (tid == 0) {
       bulk_store(g.wimg + at.at * g.dkt * kP * kTile, base + kPrepRight, g.dkt * kP * kTile);
       bulk_commit();
-      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     }
   }
+  if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   finish(tmem, 256, steps.ok, g.status);
 }
 
@@ -553,6 +559,10 @@ __global__ void __launch_bounds__(kOutThreads, kData<T> == 3 ? 1 : 2)
     ss.fetch(S + ct * 64 * 4, rows, 64, g.dvt);
   };
   fetch(0);
+  if (tid == 0) {
+    ask_l2(g.E + p.at * C * cols, C * cols * 4);
+    for (int c4 = 0; g.dkt > 1 && c4 < cols / 4; ++c4) ask_l2(S + (c4 * rows + 64) * 4, 64 * 16);
+  }
   if (!begin(&tab.bar, &tab.tmem, 256, smem, g.status)) return;
   Steps steps{&tab.bar};
   const uint32_t tmem = tab.tmem, mine = tmem + ((uint32_t)((warp & 3) * 32) << 16), base = smem_u32(smem);

@@ -253,6 +253,11 @@ __device__ __noinline__ void load_quads(unsigned char* to, uint32_t part, const 
   q.template place<P>(to, part, kTile, rows, tiles, scale);
 }
 
+// Brings `bytes` bytes from a multiple of 16 into L2.
+__device__ __forceinline__ void ask_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // An operand: descriptor of its first part, bytes from one part to the next, and of its steps of 16 along K.
 struct Operand {
   uint64_t desc;

@@ -180,6 +180,11 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
               *R = g.R + p.at * rows * cols, *inv = g.inv + p.at * C * C;
   const T *q = rows_of<T>(a.q, p.t0, p.b, p.hq), *k = rows_of<T>(a.k, p.t0, p.b, p.hq),
           *v = rows_of<T>(a.v, p.t0, p.b, p.h), *d_o = rows_of<T>(a.d_o, p.t0, p.b, p.h);
+  if (tid == 0) {  // what later steps load
+    ask_l2(E, C * cols * 4);
+    ask_l2(S, rows * cols * 4);
+    ask_l2(R, rows * cols * 4);
+  }
   const float up = tab.gates.up[row], down = tab.gates.down[row], beta = tab.gates.beta[row];
   const bool mine_live = row < p.n;
   DataRows<T, C, 2, kThreads> data;

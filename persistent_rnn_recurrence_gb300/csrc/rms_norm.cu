@@ -48,6 +48,8 @@ __device__ __forceinline__ float block_max(float v, float* part) {
 }
 // A group of zeros has the scale 1.
 __device__ __forceinline__ float scale_of(float top) { return top > 0.f ? top / kE4m3Max : 1.f; }
+// What a value is multiplied by instead of divided by its scale: a rounding of 2^-24 more before that of 2^-4.
+__device__ __forceinline__ float inverse_of(float top) { return top > 0.f ? kE4m3Max / top : 1.f; }
 __device__ __forceinline__ uint8_t to_e4m3(float v) {
   return (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
 }
@@ -102,11 +104,16 @@ __device__ __forceinline__ float top_of(const Pack<float, V>& y) {
   return m;
 }
 template <int V>
-__device__ __forceinline__ void store_e4m3(uint8_t* q, const Pack<float, V>& y, float scale) {
-  Pack<uint8_t, V> o;
+__device__ __forceinline__ void store_e4m3(uint8_t* q, const Pack<float, V>& y, float inverse) {
+  if constexpr (V == 1) {
+    *q = to_e4m3(y.v[0] * inverse);
+  } else {
+    Pack<uint16_t, V / 2> o;
 #pragma unroll
-  for (int i = 0; i < V; ++i) o.v[i] = to_e4m3(y.v[i] / scale);
-  store_pack<uint8_t, V>(q, o);
+    for (int i = 0; i < V / 2; ++i)
+      o.v[i] = (uint16_t)__nv_cvt_float2_to_fp8x2(mul2(pair_of<float, V>(y, i), both(inverse)), __NV_SATFINITE, __NV_E4M3);
+    store_pack<uint16_t, V / 2>(reinterpret_cast<uint16_t*>(q), o);
+  }
 }
 template <typename T, int V>
 __device__ __forceinline__ void store_y(T* y, const Pack<float, V>& f) {
@@ -209,7 +216,7 @@ __device__ __forceinline__ void rms_row(const RmsNormArgs& a, long long r, bool 
     for (int p = 0; p < NV; ++p) {
       const int c = (p * width + t) * V;
       if (live && c < a.cols)
-        store_e4m3<V>(static_cast<uint8_t*>(a.y) + r * a.y_stride + c, y[p], scale_of(top[p]));
+        store_e4m3<V>(static_cast<uint8_t*>(a.y) + r * a.y_stride + c, y[p], inverse_of(top[p]));
     }
   }
 }
@@ -274,20 +281,22 @@ __global__ void __launch_bounds__(1024) rms_long_kernel(RmsNormArgs a) {
             v[i] = c < a.cols ? value(c) : 0.f;
             top = max_nan(top, fabsf(v[i]));
           }
-          const float scale = scale_of(lanes_max<32>(top));
-          if (lane == 0) a.scale[r * groups + g] = scale;
+          top = lanes_max<32>(top);
+          if (lane == 0) a.scale[r * groups + g] = scale_of(top);
+          const float inverse = inverse_of(top);
 #pragma unroll
           for (int i = 0; i < kGroup / 32; ++i) {
             const long long c = g * kGroup + i * 32 + lane;
-            if (c < a.cols) q[c] = to_e4m3(v[i] / scale);
+            if (c < a.cols) q[c] = to_e4m3(v[i] * inverse);
           }
         }
       } else {
         float top = 0.f;
         for (long long c = threadIdx.x; c < a.cols; c += blockDim.x) top = max_nan(top, fabsf(value(c)));
-        const float scale = scale_of(block_max(top, part[1]));
-        if (threadIdx.x == 0) a.scale[r] = scale;
-        for (long long c = threadIdx.x; c < a.cols; c += blockDim.x) q[c] = to_e4m3(value(c) / scale);
+        top = block_max(top, part[1]);
+        if (threadIdx.x == 0) a.scale[r] = scale_of(top);
+        const float inverse = inverse_of(top);
+        for (long long c = threadIdx.x; c < a.cols; c += blockDim.x) q[c] = to_e4m3(value(c) * inverse);
       }
     }
     __syncthreads();
