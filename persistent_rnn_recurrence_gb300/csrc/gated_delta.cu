@@ -110,24 +110,22 @@ __global__ void __launch_bounds__(kThreads) gd_walk_kernel(const __grid_constant
     }
     Z[j] = make_float4(z[0], z[1], z[2], z[3]);
   }
-  auto dot = [&](const float* p) {
+  auto dot = [&](const float4 (&k)[Q]) {
     float2 s0 = both(0.f), s1 = both(0.f);
 #pragma unroll
     for (int j = 0; j < Q; ++j) {
-      const float4 k = *reinterpret_cast<const float4*>(p + (j * kLanes + lane) * 4);
-      s0 = fma2(make_float2(Z[j].x, Z[j].y), make_float2(k.x, k.y), s0);
-      s1 = fma2(make_float2(Z[j].z, Z[j].w), make_float2(k.z, k.w), s1);
+      s0 = fma2(make_float2(Z[j].x, Z[j].y), make_float2(k[j].x, k[j].y), s0);
+      s1 = fma2(make_float2(Z[j].z, Z[j].w), make_float2(k[j].z, k[j].w), s1);
     }
     s0 = add2(s0, s1);
     return lanes8_sum(s0.x + s0.y);
   };
-  auto update = [&](float f, float g, const float* p) {  // Z <- f Z + g p
+  auto update = [&](float f, float g, const float4 (&k)[Q]) {  // Z <- f Z + g k
     const float2 ff = both(f), gg = both(g);
 #pragma unroll
     for (int j = 0; j < Q; ++j) {
-      const float4 k = *reinterpret_cast<const float4*>(p + (j * kLanes + lane) * 4);
-      const float2 lo = fma2(gg, make_float2(k.x, k.y), mul2(ff, make_float2(Z[j].x, Z[j].y)));
-      const float2 hi = fma2(gg, make_float2(k.z, k.w), mul2(ff, make_float2(Z[j].z, Z[j].w)));
+      const float2 lo = fma2(gg, make_float2(k[j].x, k[j].y), mul2(ff, make_float2(Z[j].x, Z[j].y)));
+      const float2 hi = fma2(gg, make_float2(k[j].z, k[j].w), mul2(ff, make_float2(Z[j].z, Z[j].w)));
       Z[j] = make_float4(lo.x, lo.y, hi.x, hi.y);
     }
   };
@@ -185,13 +183,37 @@ __global__ void __launch_bounds__(kThreads) gd_walk_kernel(const __grid_constant
     const float* s0 = col + (blk & 1) * 2 * TB * kCols;
     const float* g0 = gate + (blk & 1) * 2 * TB;
     const int live = min(TB, len - blk * TB);
+    // a token's vectors and scalars, requested while the one before is worked on
+    struct Token {
+      float4 p[NV][Q];
+      float x0, x1, dec, beta;
+    } cur, ahead;
+    constexpr bool kAhead = Q <= 4;  // wider ones have no registers for two
+    auto take = [&](Token& to, int w) {
+      const int t = kRev ? live - 1 - w : w;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < Q; ++j)
+          to.p[v][j] = *reinterpret_cast<const float4*>(v0 + (v * TB + t) * N + (j * kLanes + lane) * 4);
+      to.x0 = s0[t * kCols + mine];
+      to.x1 = s0[(TB + t) * kCols + mine];
+      to.dec = g0[t];
+      to.beta = g0[TB + t];
+    };
+    if (kAhead) take(ahead, 0);
 #pragma unroll 1
     for (int w = 0; w < live; ++w) {
       const int t = kRev ? live - 1 - w : w;
       const long long tt = (long long)blk * TB + t;
-      const float* p0 = v0 + t * N;
-      const float *p1 = p0 + TB * N, *p2 = p1 + TB * N;
-      const float x0 = s0[t * kCols + mine], x1 = s0[(TB + t) * kCols + mine], dec = g0[t], beta = g0[TB + t];
+      if (kAhead) {
+        cur = ahead;
+        if (w + 1 < live) take(ahead, w + 1);
+      } else {
+        take(cur, w);
+      }
+      const float x0 = cur.x0, x1 = cur.x1, dec = cur.dec, beta = cur.beta;
+      const float4 (&p0)[Q] = cur.p[0], (&p1)[Q] = cur.p[1], (&p2)[Q] = cur.p[NV - 1];
       float r0, r1 = 0.f;
       if (WALK == kValues) {
         r0 = fmaf(-dec, dot(p0), x0);

@@ -273,22 +273,28 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gd_prepare_kernel(const __gri
 //
 // Forwards Z = S:  Y = E0 - W Z, kept as E;     Z <- e^G_C Z + K^T (beta e^(G_C-G) Y).
 // Backwards Z = R: Y = X0 + e^(G_C-G) (K Z), kept as X;  Z <- e^G_C Z + Z0 - W^T (beta Y).
-// A block walks the chunks of one head and kSlice of its dv columns; the state is in the registers of 8 warps,
+// A block walks the chunks of one head and SL of its dv columns; the state is in the registers of SL / 4 warps,
 // 16 columns of a row each.  The parts of Z (of Y) stand side by side as columns of one product, which reads the
-// other operand once for each of its own parts.  W and K come as ready tiles in bulk copies through a ring of
-// kStages, a half of an operand per stage: the first product sums over column tiles, the second over halves of
-// the tokens.
+// other operand once for each of its own parts.  W and K come as ready tiles in bulk copies through a ring, a half of
+// an operand per stage: the first product sums over column tiles, the second over halves of the tokens.
 //
 // Bound by the chain of a chunk: two products, each with the way from tensor memory through registers into the next
-// one's operand.
-constexpr int kSlice = 32, kStages = 3, kChainThreads = 320;
-constexpr uint32_t kStage = kP * kTile, kChainZ = kStages * kStage, kChainY = kChainZ + 2 * kTile,
-                   kChainTab = kChainY + 2 * kTile;
+// one's operand.  Slices of 32 columns make it shorter and spread a head over more SMs; slices of 64 take
+// half the blocks, for when those of 32 would not run all at once.
+constexpr uint32_t kStage = kP * kTile;
+template <int SL>
+struct ChainCfg {
+  static constexpr int kStages = SL == 32 ? 3 : 2, kWorkers = SL / 4, kThreads = 32 * (kWorkers + 2);
+  static constexpr uint32_t kOperand = SL == 32 ? 2 * kTile : 3 * kTile;  // parts side by side in tiles of 64 columns
+  static constexpr uint32_t kZ = kStages * kStage, kY = kZ + kOperand, kTab = kY + kOperand;
+  static constexpr uint32_t kCols = SL == 32 ? 256 : 512;                 // of tensor memory: a half for each product
+};
 struct ChainTab {
-  uint64_t full[kStages], empty[kStages], z_ready, y_full, y_ready, z_full;
+  uint64_t full[3], empty[3], z_ready, y_full, y_ready, z_full;
   uint32_t tmem;
 };
-static_assert(kChainTab + sizeof(ChainTab) <= 227 * 1024, "shared memory");
+static_assert(ChainCfg<32>::kTab + sizeof(ChainTab) <= 227 * 1024 && ChainCfg<64>::kTab + sizeof(ChainTab) <= 227 * 1024,
+              "shared memory");
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile(
@@ -298,14 +304,16 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 // PK: parts of K.
-template <int PK, bool REV>
-__global__ void __launch_bounds__(kChainThreads, 1) gd_chain_kernel(const __grid_constant__ Args g) {
+template <int PK, bool REV, int SL>
+__global__ void __launch_bounds__(ChainCfg<SL>::kThreads, 1) gd_chain_kernel(const __grid_constant__ Args g) {
+  using K = ChainCfg<SL>;
+  constexpr int kStages = K::kStages, kWorkers = K::kWorkers;
   constexpr int P1 = REV ? PK : kP, P2 = REV ? kP : PK;  // parts of the two left operands
   extern __shared__ __align__(1024) unsigned char smem[];
-  ChainTab& tab = *reinterpret_cast<ChainTab*>(smem + kChainTab);
+  ChainTab& tab = *reinterpret_cast<ChainTab*>(smem + K::kTab);
   const GdArgs& a = g.a;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int local = blockIdx.x, bh = g.bh0 + local, b = bh / a.H, col0 = blockIdx.y * kSlice;
+  const int local = blockIdx.x, bh = g.bh0 + local, b = bh / a.H, col0 = blockIdx.y * SL;
   const int len = length_of(a, b), chunks = (len + C - 1) / C;
   const uint32_t base = smem_u32(smem);
   if (base & 1023u) {
@@ -317,14 +325,14 @@ __global__ void __launch_bounds__(kChainThreads, 1) gd_chain_kernel(const __grid
       mbar_init(&tab.full[i], 1);
       mbar_init(&tab.empty[i], 1);
     }
-    mbar_init(&tab.z_ready, 8);
+    mbar_init(&tab.z_ready, kWorkers);
     mbar_init(&tab.y_full, 1);
-    mbar_init(&tab.y_ready, 8);
+    mbar_init(&tab.y_ready, kWorkers);
     mbar_init(&tab.z_full, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 9) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tab.tmem)), "r"(256)
+  if (warp == kWorkers + 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tab.tmem)), "r"(K::kCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -337,7 +345,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) gd_chain_kernel(const __grid
   auto tokens_of = [&](int c) { return min(C, len - c * C); };
   auto at_of = [&](int c) { return (size_t)local * g.chunks + c; };
 
-  if (warp == 8) {
+  if (warp == kWorkers) {
     if (elected()) {
       int turn = 0;
       auto stage = [&](uint32_t bytes) {
@@ -370,7 +378,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) gd_chain_kernel(const __grid
         ok = ok && landed;
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == kWorkers + 1) {
     if (elected()) {
       int turn = 0;
       // D = left (PL parts) times the parts of the right side by side: the first part of the left meets all three
@@ -380,10 +388,10 @@ __global__ void __launch_bounds__(kChainThreads, 1) gd_chain_kernel(const __grid
 #pragma unroll
         for (int p = 0; p < PL; ++p)
           for (int k = 0; k < steps; ++k)
-            umma_f16(d, left.at(p, k), right.at(0, k_right + k), bf16_idesc(128, (kP - p) * kSlice) | id,
+            umma_f16(d, left.at(p, k), right.at(0, k_right + k), bf16_idesc(128, (kP - p) * SL) | id,
                      add || p > 0 || k > 0);
       };
-      const Operand Z = mn_major(base + kChainZ, 0, kTile), Y = mn_major(base + kChainY, 0, kTile);
+      const Operand Z = mn_major(base + K::kZ, 0, kTile), Y = mn_major(base + K::kY, 0, kTile);
       for (int i = 0; i < chunks; ++i) {
         const int c = chunk_of(i);
         seq_wait(&tab.z_ready, i & 1, ok);
@@ -401,7 +409,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) gd_chain_kernel(const __grid
         for (int hf = 0; hf * 64 < tokens_of(c); ++hf, ++turn) {
           const int s = turn % kStages;
           seq_wait(&tab.full[s], (turn / kStages) & 1, ok);
-          multiply(std::integral_constant<int, P2>(), tmem + 128,
+          multiply(std::integral_constant<int, P2>(), tmem + K::kCols / 2,
                    mn_major(base + s * kStage, g.dkt * (kTile / 2), kTile / 2), Y, 4 * hf, 4, kAMn | kBMn, hf > 0);
           umma_commit(&tab.empty[s]);
         }
@@ -410,8 +418,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) gd_chain_kernel(const __grid
       // every product has read its operands before the block leaves: the workers wait for the last
     }
   } else {
-    const int row = (warp & 3) * 32 + lane, half = warp >> 2, c0 = col0 + half * 16;
-    const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 16;
+    const int row = (warp & 3) * 32 + lane, part16 = warp >> 2, c0 = col0 + part16 * 16;
+    const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + part16 * 16;
     const int rows = 64 * g.dkt, cols = 64 * g.dvt;
     const size_t head = (size_t)bh * a.dk * a.dv;
     float2 Z[8];
@@ -427,7 +435,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) gd_chain_kernel(const __grid
     auto keep = [&](float* states, size_t slot) {
       if (row < rows) store_quads(states + slot * rows * cols, rows, row, c0, Z);
     };
-    auto publish = [&](uint32_t where, const float2 (&v)[8]) {  // columns [32 p, 32 p + 32) are part p's
+    auto publish = [&](uint32_t where, const float2 (&v)[8]) {  // columns [SL p, SL p + SL) are part p's
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         float2 w[4] = {v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
@@ -438,8 +446,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) gd_chain_kernel(const __grid
           u.y = take<bf16>(w[1]);
           u.z = take<bf16>(w[2]);
           u.w = take<bf16>(w[3]);
-          const int chunk = (p & 1) * 4 + half * 2 + j;
-          *reinterpret_cast<uint4*>(smem + where + (p >> 1) * kTile + row * 128 + ((chunk ^ (row & 7)) << 4)) = u;
+          const int c = p * SL + part16 * 16 + j * 8, chunk = (c & 63) >> 3;
+          *reinterpret_cast<uint4*>(smem + where + (c >> 6) * kTile + row * 128 + ((chunk ^ (row & 7)) << 4)) = u;
         }
       }
       to_async();
@@ -447,8 +455,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) gd_chain_kernel(const __grid
     };
     auto sum = [&](uint32_t at, float2 (&v)[8]) {
       float2 x[8], y[8];
-      read16(at + 2 * kSlice, x);
-      read16(at + kSlice, y);
+      read16(at + 2 * SL, x);
+      read16(at + SL, y);
       read16(at, v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = add2(v[i], add2(y[i], x[i]));
@@ -464,7 +472,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) gd_chain_kernel(const __grid
     };
     for (int i = 0; i < chunks; ++i) {
       const int c = chunk_of(i);
-      publish(kChainZ, Z);
+      publish(K::kZ, Z);
       warp_arrive(&tab.z_ready);
       if (REV) keep(g.R, at_of(c));
       else keep(g.S, (size_t)local * (g.chunks + 1) + c);
@@ -484,13 +492,13 @@ __global__ void __launch_bounds__(kChainThreads, 1) gd_chain_kernel(const __grid
         y[j] = fma2(f, v[j], y[j]);
         v[j] = mul2(w, y[j]);
       }
-      publish(kChainY, v);
+      publish(K::kY, v);
       warp_arrive(&tab.y_ready);
       store_quads(ym, C, row, c0, y);
       seq_wait(&tab.z_full, i & 1, ok);
       __syncwarp();
       after_sync();
-      sum(mine + 128, v);
+      sum(mine + K::kCols / 2, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (REV) v[j] = add2(v[j], z0[j]);
@@ -507,9 +515,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) gd_chain_kernel(const __grid
   if (!ok) atomicExch(g.status, 1);
   before_sync();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kWorkers + 1) {
     after_sync();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(K::kCols) : "memory");
   }
 }
 
@@ -637,17 +645,27 @@ cudaError_t launch_prepare(const Args& g, bool keep_inverse, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+namespace {
+template <int PK, bool REV, int SL>
+cudaError_t chain(const Args& g, cudaStream_t s) {
+  using K = ChainCfg<SL>;
+  constexpr uint32_t smem = K::kTab + sizeof(ChainTab);
+  const cudaError_t e = allow(gd_chain_kernel<PK, REV, SL>, smem);
+  if (e != cudaSuccess) return e;
+  gd_chain_kernel<PK, REV, SL><<<dim3(g.nbh, (g.a.dv + SL - 1) / SL), K::kThreads, smem, s>>>(g);
+  return cudaGetLastError();
+}
+}  // namespace
+
 cudaError_t launch_chain(const Args& g, bool reverse, cudaStream_t s) {
-  constexpr uint32_t smem = kChainTab + sizeof(ChainTab);
-  const dim3 grid(g.nbh, (g.a.dv + kSlice - 1) / kSlice);
+  const bool narrow = g.a.dv <= 32 || (long long)g.nbh * ((g.a.dv + 31) / 32) <= seq_sm_count();
+  cudaError_t e = cudaSuccess;
   PRNN_BY_DTYPE(g.a.dtype, T, {
     constexpr int PK = kData<T>;
-    const cudaError_t e = reverse ? allow(gd_chain_kernel<PK, true>, smem) : allow(gd_chain_kernel<PK, false>, smem);
-    if (e != cudaSuccess) return e;
-    if (reverse) gd_chain_kernel<PK, true><<<grid, kChainThreads, smem, s>>>(g);
-    else gd_chain_kernel<PK, false><<<grid, kChainThreads, smem, s>>>(g);
+    if (reverse) e = narrow ? chain<PK, true, 32>(g, s) : chain<PK, true, 64>(g, s);
+    else e = narrow ? chain<PK, false, 32>(g, s) : chain<PK, false, 64>(g, s);
   });
-  return cudaGetLastError();
+  return e;
 }
 
 cudaError_t launch_outputs(const Args& g, cudaStream_t s) {

@@ -460,21 +460,19 @@ __global__ void __launch_bounds__(256) rms_grad_lanes_kernel(RmsNormGradArgs a) 
   }
 }
 
-__global__ void __launch_bounds__(256) rms_join_kernel(const float* partial, int splits, int cols, float* dweight) {
-  __shared__ float sums[8][33];
+__global__ void __launch_bounds__(1024) rms_join_kernel(const float* partial, int splits, int cols, float* dweight) {
+  __shared__ float sums[32][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   for (long long c0 = 32LL * blockIdx.x; c0 < cols; c0 += 32LL * gridDim.x) {
     const long long c = c0 + tx;
     float s = 0.f;
     if (c < cols)
-      for (int i = ty; i < splits; i += 8) s += partial[(size_t)i * cols + c];
+#pragma unroll 4
+      for (int i = ty; i < splits; i += 32) s += partial[(size_t)i * cols + c];
     sums[ty][tx] = s;
     __syncthreads();
-    if (ty == 0 && c < cols) {
-#pragma unroll
-      for (int i = 1; i < 8; ++i) s += sums[i][tx];
-      dweight[c] = s;
-    }
+    s = warp_sum(sums[tx][ty]);
+    if (tx == 0 && c0 + ty < cols) dweight[c0 + ty] = s;
     __syncthreads();
   }
 }
@@ -554,7 +552,7 @@ cudaError_t launch_backward(RmsNormGradArgs a, int splits, cudaStream_t s) {
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.dweight) return e;
-  rms_join_kernel<<<(unsigned)std::min<long long>((a.cols + 31LL) / 32, 65535), 256, 0, s>>>(a.partial, splits, a.cols,
+  rms_join_kernel<<<(unsigned)std::min<long long>((a.cols + 31LL) / 32, 65535), 1024, 0, s>>>(a.partial, splits, a.cols,
                                                                                              a.dweight);
   return cudaGetLastError();
 }

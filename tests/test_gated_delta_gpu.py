@@ -158,6 +158,20 @@ def test_backward(env, case, dtype):
     check_backward(torch, prnn, dtype, problem(torch, dtype, *case))
 
 
+# more heads than fit the SMs in narrow slices, in every type; ragged, and with heads that share
+MANY = [(200, 10, 16, 16, 64, 64, None, True), (130, 20, 16, 8, 128, 100, [130] * 10 + [0, 1, 127, 128, 129] * 2, False),
+        (32, 3, 64, 64, 40, 33, None, True)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("case", MANY, ids=lambda c: str(c[:6]))
+def test_many_heads(env, case, dtype):
+    torch, prnn = env
+    p = problem(torch, dtype, *case, seed=2)
+    check_forward(torch, prnn, dtype, p)
+    check_backward(torch, prnn, dtype, p)
+
+
 def gates(torch, p, kind):
     """Gates and keys where the recurrence can go wrong."""
     if kind == "no decay":
