@@ -821,7 +821,8 @@ typedef struct {
 
 /* Workspace of prnn_gated_delta_forward (backward == 0) or _backward (1) for the call that `a` describes (the
  * alignment of its pointers and strides counts; they are not followed).  About 2 KB a token and head of 128 x 128
- * forward and 4 KB backward, at most some 8 GB: beyond that, heads are worked on in groups. */
+ * forward and 4 KB backward, at most 8 GB (beyond that, heads are worked on in groups) besides copies of tensors that
+ * are not aligned to 16 bytes and fp32 sums of the gradients of shared heads. */
 prnn_status_t prnn_gated_delta_workspace(const prnn_gated_delta_t* a, int backward, size_t* bytes);
 
 /* All T tokens.  T == 0 copies the state; B == 0 is a no-op. */

@@ -71,29 +71,31 @@ __global__ void __launch_bounds__(kThreads) gd_walk_kernel(const __grid_constant
     return i == 0 ? seq(a.k, hq) : (WALK == kRowsBackward ? seq(a.q, hq) : 0.f);
   };
   const int blocks = (len + TB - 1) / TB;
-  float staged[PER];
+  constexpr int PERC = 2 * TB * kCols / kThreads;
+  float staged[PER], staged_col[PERC], staged_gate;
   auto fetch = [&](int blk) {
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const int i = j * kThreads + tid, x = i % N, t = blk * TB + i / N % TB;
       staged[j] = t < len ? vector(i / (N * TB), t, x) : 0.f;
     }
+#pragma unroll
+    for (int j = 0; j < PERC; ++j) {
+      const int i = j * kThreads + tid, t = blk * TB + i / kCols % TB;
+      staged_col[j] = t < len ? column(i / (TB * kCols), t, c0 + i % kCols) : 0.f;
+    }
+    const long long t = blk * TB + tid % TB;
+    staged_gate = 0.f;
+    if (tid < 2 * TB && t < len)
+      staged_gate = tid < TB ? a.g[t * a.gt + b * a.gb + h * a.gh] : a.beta[t * a.bt + b * a.bb + h * a.bh];
   };
   auto place = [&](int blk) {
     float* to = vec + (blk & 1) * NV * TB * N;
 #pragma unroll
     for (int j = 0; j < PER; ++j) to[j * kThreads + tid] = staged[j];
-    for (int i = tid; i < 2 * TB * kCols; i += kThreads) {
-      const int t = blk * TB + i / kCols % TB;
-      col[(blk & 1) * 2 * TB * kCols + i] = t < len ? column(i / (TB * kCols), t, c0 + i % kCols) : 0.f;
-    }
-    if (tid < 2 * TB) {
-      const long long t = blk * TB + tid % TB;
-      float g = 0.f;
-      if (t < len)
-        g = tid < TB ? expf(a.g[t * a.gt + b * a.gb + h * a.gh]) : a.beta[t * a.bt + b * a.bb + h * a.bh];
-      gate[(blk & 1) * 2 * TB + tid] = g;
-    }
+#pragma unroll
+    for (int j = 0; j < PERC; ++j) col[(blk & 1) * 2 * TB * kCols + j * kThreads + tid] = staged_col[j];
+    if (tid < 2 * TB) gate[(blk & 1) * 2 * TB + tid] = tid < TB ? expf(staged_gate) : staged_gate;
   };
   // the state, transposed for walks over rows: this lane's quads of column (row) c
   float4 Z[Q];

@@ -38,8 +38,7 @@ cudaError_t launch_gd_walk_forward(const GdArgs& a, cudaStream_t s);
 cudaError_t launch_gd_walk_backward(const GdArgs& a, cudaStream_t s);
 
 // On the tensor cores, in chunks, for dk and dv up to 128: whether it serves a call, its scratch, the call.
-constexpr int kGdTcLeast = 32;  // tokens
-bool gd_tc_serves(prnn_dtype_t dtype, int T, int dk, int dv);
+bool gd_tc_serves(int T, int B, int H, int dk, int dv, bool backward);
 size_t gd_tc_workspace(const GdArgs& a, bool backward);
 cudaError_t launch_gd_tc(GdArgs a, void* scratch, bool backward, cudaStream_t s);
 

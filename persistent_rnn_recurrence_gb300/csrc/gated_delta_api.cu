@@ -89,7 +89,9 @@ Parts walk_parts(const Call* a) {
   return p;
 }
 
-bool on_tensor_cores(const Call* a) { return gd_tc_serves(a->dtype, a->T, a->dk, a->dv); }
+bool on_tensor_cores(const Call* a, bool backward) {
+  return gd_tc_serves(a->T, a->B, a->heads, a->dk, a->dv, backward);
+}
 
 GdArgs args_of(const Call* a) {
   GdArgs g{};
@@ -155,7 +157,7 @@ prnn_status_t prnn_gated_delta_workspace(const prnn_gated_delta_t* a, int backwa
   if (!shape_ok(a, &why)) return why;
   *bytes = 0;
   if (a->T == 0 || a->B == 0) return PRNN_OK;
-  if (on_tensor_cores(a)) *bytes = gd_tc_workspace(args_of(a), backward != 0);
+  if (on_tensor_cores(a, backward != 0)) *bytes = gd_tc_workspace(args_of(a), backward != 0);
   else if (backward) *bytes = walk_parts(a).total;
   return PRNN_OK;
 }
@@ -185,7 +187,7 @@ prnn_status_t prnn_gated_delta_forward(const prnn_gated_delta_t* a, void* stream
   if (need) all.array(a->workspace, need, true);
   if (!all.good()) return PRNN_ERR_INVALID_ARG;
   GdArgs g = args_of(a);
-  return cuda_status(on_tensor_cores(a) ? launch_gd_tc(g, a->workspace, false, s) : launch_gd_walk_forward(g, s));
+  return cuda_status(on_tensor_cores(a, false) ? launch_gd_tc(g, a->workspace, false, s) : launch_gd_walk_forward(g, s));
 }
 
 prnn_status_t prnn_gated_delta_backward(const prnn_gated_delta_t* a, void* stream) {
@@ -220,7 +222,7 @@ prnn_status_t prnn_gated_delta_backward(const prnn_gated_delta_t* a, void* strea
   all.array(a->workspace, need, true);
   if (!all.good()) return PRNN_ERR_INVALID_ARG;
   GdArgs g = args_of(a);
-  if (on_tensor_cores(a)) return cuda_status(launch_gd_tc(g, a->workspace, true, s));
+  if (on_tensor_cores(a, true)) return cuda_status(launch_gd_tc(g, a->workspace, true, s));
   const Parts p = walk_parts(a);
   char* w = static_cast<char*>(a->workspace);
   auto take = [&](size_t n) {

@@ -123,29 +123,35 @@ __device__ __forceinline__ void store_y(T* y, const Pack<float, V>& f) {
   store_pack<T, V>(y, o);
 }
 
-// One row.  TPR > 0: TPR neighbouring lanes hold it (no barrier; lanes without a row go along with `live`
-// false); TPR == 0: the whole block does.  Thread t holds the packs t, t + width, ... of V columns.
-template <typename T, int V, int NV, int TPR, bool Q>
-__device__ __forceinline__ void rms_row(const RmsNormArgs& a, long long r, bool live, int t, int width,
-                                        float* part, unsigned* tops) {
-  const T* x = static_cast<const T*>(a.x) + (live ? r * a.x_stride : 0);
-  const T* res = a.residual ? static_cast<const T*>(a.residual) + (live ? r * a.residual_stride : 0) : nullptr;
-  Pack<T, V> h[NV], b[NV];
+// What a thread holds of a row before the residual's addition: the packs t, t + width, ... of V columns.
+template <typename T, int V, int NV>
+struct RowPacks {
+  Pack<T, V> x[NV], res[NV];
+  __device__ __forceinline__ void load(const RmsNormArgs& a, long long r, int t, int width) {
 #pragma unroll
-  for (int p = 0; p < NV; ++p) {
-    const int c = (p * width + t) * V;
-    if (live && c < a.cols) {
-      h[p] = load_once<T, V>(x + c);
-      if (res) b[p] = load_once<T, V>(res + c);
+    for (int p = 0; p < NV; ++p) {
+      const int c = (p * width + t) * V;
+      if (r >= a.rows || c >= a.cols) continue;
+      x[p] = load_once<T, V>(static_cast<const T*>(a.x) + r * a.x_stride + c);
+      if (a.residual) res[p] = load_once<T, V>(static_cast<const T*>(a.residual) + r * a.residual_stride + c);
     }
   }
+};
+
+// One row.  TPR > 0: TPR neighbouring lanes hold it (no barrier; lanes without a row go along with `live`
+// false); TPR == 0: the whole block does.
+template <typename T, int V, int NV, int TPR, bool Q>
+__device__ __forceinline__ void rms_row(const RmsNormArgs& a, RowPacks<T, V, NV>& in, long long r, bool live, int t,
+                                        int width, float* part, unsigned* tops) {
+  const bool res = a.residual != nullptr;
+  Pack<T, V> (&h)[NV] = in.x;
   float s = 0.f;
 #pragma unroll
   for (int p = 0; p < NV; ++p) {
     const int c = (p * width + t) * V;
     if (!live || c >= a.cols) continue;
     if (res) {
-      h[p] = added<T, V>(h[p], b[p]);
+      h[p] = added<T, V>(h[p], in.res[p]);
       store_pack<T, V>(static_cast<T*>(a.h) + r * a.h_stride + c, h[p]);
     }
     s += squares<T, V>(h[p]);
@@ -227,18 +233,25 @@ template <int NV>
 constexpr int kMostThreads = NV == 4 ? 512 : 1024;
 template <typename T, int V, int NV, bool Q>
 __global__ void __launch_bounds__(kMostThreads<NV>) rms_block_kernel(RmsNormArgs a) {
-  __shared__ float part[64];
+  __shared__ float part[2][64];
   __shared__ unsigned tops[Q && V == 1 ? kMostGroups : 1];
-  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    rms_row<T, V, NV, 0, Q>(a, r, true, threadIdx.x, blockDim.x, part, tops);
-    if (r + gridDim.x < a.rows) __syncthreads();
+  RowPacks<T, V, NV> cur, ahead;
+  cur.load(a, blockIdx.x, threadIdx.x, blockDim.x);
+  int turn = 0;
+  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
+    ahead.load(a, r + gridDim.x, threadIdx.x, blockDim.x);
+    rms_row<T, V, NV, 0, Q>(a, cur, r, true, threadIdx.x, blockDim.x, part[turn], tops);
+    if (Q && V == 1) __syncthreads();
+    cur = ahead;
   }
 }
 // A row per TPR lanes.
 template <typename T, int V, int NV, int TPR, bool Q>
 __global__ void __launch_bounds__(256) rms_lanes_kernel(RmsNormArgs a) {
   const long long r = (long long)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
-  rms_row<T, V, NV, TPR, Q>(a, r, r < a.rows, threadIdx.x % TPR, TPR, nullptr, nullptr);
+  RowPacks<T, V, NV> in;
+  in.load(a, r, threadIdx.x % TPR, TPR);
+  rms_row<T, V, NV, TPR, Q>(a, in, r, r < a.rows, threadIdx.x % TPR, TPR, nullptr, nullptr);
 }
 
 // Rows too long for registers: a block per row, which is read again (from L2) for each step.  Columns are counted
@@ -303,30 +316,35 @@ __global__ void __launch_bounds__(1024) rms_long_kernel(RmsNormArgs a) {
   }
 }
 
+constexpr int kRmsResident = 1024, kRmsOne = 128, kRmsTwo = 512;
+
 template <typename T, int V, bool Q>
 void launch_forward(const RmsNormArgs& a, cudaStream_t s) {
   const int packs = (a.cols + V - 1) / V;
   auto lanes = [&](auto kernel, int tpr) {
     kernel<<<(unsigned)((a.rows + 256 / tpr - 1) / (256 / tpr)), 256, 0, s>>>(a);
   };
-  const unsigned blocks = (unsigned)std::min<long long>(a.rows, 0x7fffffff);
   const bool one = (a.rows + 7) / 8 <= 0x7fffffff;  // a grid has as many blocks
   if (one && V > 1 && packs <= 8) return lanes(rms_lanes_kernel<T, V, 1, 8, Q>, 8);
   if (one && V > 1 && packs <= 16) return lanes(rms_lanes_kernel<T, V, 1, 16, Q>, 16);
   if (one && V > 1 && packs <= 32) return lanes(rms_lanes_kernel<T, V, 1, 32, Q>, 32);
   if (one && V == 1 && packs <= 128) return lanes(rms_lanes_kernel<T, V, V == 1 ? 4 : 1, 32, Q>, 32);
-  // With few rows a row is spread over as many threads as it has packs; with many, four packs a thread keep
-  // the loads of a row in flight and more rows on an SM.
-  const int most = a.rows < 4LL * seq_sm_count() ? 1024 : 128;
+  // With few rows a row is spread over as many threads as it has packs; with many, blocks stay and go on to a row a
+  // grid away, whose loads are under way while this one is summed and written.
+  const bool many = a.rows >= 4LL * seq_sm_count();
   auto threads = [&](int nv) { return ((packs + nv - 1) / nv + 31) / 32 * 32; };
-  if (threads(1) <= most) {
-    rms_block_kernel<T, V, 1, Q><<<blocks, threads(1), 0, s>>>(a);
-  } else if (threads(2) <= most) {
-    rms_block_kernel<T, V, 2, Q><<<blocks, threads(2), 0, s>>>(a);
+  auto block = [&](auto kernel, int nv) {
+    const int n = threads(nv), per_sm = std::max(1, kRmsResident / n);
+    kernel<<<(unsigned)std::min<long long>(a.rows, (long long)per_sm * seq_sm_count()), n, 0, s>>>(a);
+  };
+  if (threads(1) <= (many ? kRmsOne : 1024)) {
+    block(rms_block_kernel<T, V, 1, Q>, 1);
+  } else if (threads(2) <= (many ? kRmsTwo : 1024)) {
+    block(rms_block_kernel<T, V, 2, Q>, 2);
   } else if (threads(4) <= kMostThreads<4>) {
-    rms_block_kernel<T, V, 4, Q><<<blocks, threads(4), 0, s>>>(a);
+    block(rms_block_kernel<T, V, 4, Q>, 4);
   } else if (V == 1 && threads(8) <= 1024) {
-    rms_block_kernel<T, V, V == 1 ? 8 : 1, Q><<<blocks, threads(8), 0, s>>>(a);
+    block(rms_block_kernel<T, V, V == 1 ? 8 : 1, Q>, 8);
   } else {
     rms_long_kernel<T, Q><<<(unsigned)std::min<long long>(a.rows, 4LL * seq_sm_count()), 1024, 0, s>>>(a);
   }
