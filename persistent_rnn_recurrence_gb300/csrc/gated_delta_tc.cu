@@ -287,7 +287,9 @@ struct ChainCfg {
   static constexpr int kStages = SL == 32 ? 3 : 2, kWorkers = SL / 4, kThreads = 32 * (kWorkers + 2);
   static constexpr uint32_t kOperand = SL == 32 ? 2 * kTile : 3 * kTile;  // parts side by side in tiles of 64 columns
   static constexpr uint32_t kZ = kStages * kStage, kY = kZ + kOperand, kTab = kY + kOperand;
-  static constexpr uint32_t kCols = SL == 32 ? 256 : 512;                 // of tensor memory: a half for each product
+  // tensor memory, used by both products in turn: the left operand's first part times all of the right one's, and the
+  // small rest, which would lose more to the rounding of each step's sum beside the large ones
+  static constexpr uint32_t kSmall = kP * SL, kCols = SL == 32 ? 256 : 512;
 };
 struct ChainTab {
   uint64_t full[3], empty[3], z_ready, y_full, y_ready, z_full;
@@ -381,15 +383,15 @@ __global__ void __launch_bounds__(ChainCfg<SL>::kThreads, 1) gd_chain_kernel(con
   } else if (warp == kWorkers + 1) {
     if (elected()) {
       int turn = 0;
-      // D = left (PL parts) times the parts of the right side by side: the first part of the left meets all three
-      auto multiply = [&](auto parts, uint32_t d, const Operand& left, const Operand& right, int k_right, int steps,
-                          uint32_t id, bool add) {
+      // left (PL parts) times the parts of the right side by side: the first part of the left meets all three
+      auto multiply = [&](auto parts, const Operand& left, const Operand& right, int k_right, int steps, uint32_t id,
+                          bool add) {
         constexpr int PL = decltype(parts)::value;
 #pragma unroll
         for (int p = 0; p < PL; ++p)
           for (int k = 0; k < steps; ++k)
-            umma_f16(d, left.at(p, k), right.at(0, k_right + k), bf16_idesc(128, (kP - p) * SL) | id,
-                     add || p > 0 || k > 0);
+            umma_f16(tmem + (p > 0 ? K::kSmall : 0), left.at(p, k), right.at(0, k_right + k),
+                     bf16_idesc(128, (kP - p) * SL) | id, add || p > 1 || k > 0);
       };
       const Operand Z = mn_major(base + K::kZ, 0, kTile), Y = mn_major(base + K::kY, 0, kTile);
       for (int i = 0; i < chunks; ++i) {
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(ChainCfg<SL>::kThreads, 1) gd_chain_kernel(con
         for (int ct = 0; ct < g.dkt; ++ct, ++turn) {
           const int s = turn % kStages;
           seq_wait(&tab.full[s], (turn / kStages) & 1, ok);
-          multiply(std::integral_constant<int, P1>(), tmem, k_major(base + s * kStage, kTile, kTile), Z, 4 * ct,
+          multiply(std::integral_constant<int, P1>(), k_major(base + s * kStage, kTile, kTile), Z, 4 * ct,
                    min(4, (a.dk - 64 * ct + 15) / 16), kBMn, ct > 0);
           umma_commit(&tab.empty[s]);
         }
@@ -409,8 +411,7 @@ __global__ void __launch_bounds__(ChainCfg<SL>::kThreads, 1) gd_chain_kernel(con
         for (int hf = 0; hf * 64 < tokens_of(c); ++hf, ++turn) {
           const int s = turn % kStages;
           seq_wait(&tab.full[s], (turn / kStages) & 1, ok);
-          multiply(std::integral_constant<int, P2>(), tmem + K::kCols / 2,
-                   mn_major(base + s * kStage, g.dkt * (kTile / 2), kTile / 2), Y, 4 * hf, 4, kAMn | kBMn, hf > 0);
+          multiply(std::integral_constant<int, P2>(), mn_major(base + s * kStage, g.dkt * (kTile / 2), kTile / 2), Y, 4 * hf, 4, kAMn | kBMn, hf > 0);
           umma_commit(&tab.empty[s]);
         }
         umma_commit(&tab.z_full);
@@ -453,13 +454,24 @@ __global__ void __launch_bounds__(ChainCfg<SL>::kThreads, 1) gd_chain_kernel(con
       to_async();
       before_sync();
     };
-    auto sum = [&](uint32_t at, float2 (&v)[8]) {
+    auto sum = [&](bool small, float2 (&v)[8]) {  // the small ones first
       float2 x[8], y[8];
-      read16(at + 2 * SL, x);
-      read16(at + SL, y);
-      read16(at, v);
+      if (small) {
+        read16(mine + K::kSmall + SL, v);
+        read16(mine + K::kSmall, x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = add2(v[i], add2(y[i], x[i]));
+        for (int i = 0; i < 8; ++i) v[i] = add2(v[i], x[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = both(0.f);
+      }
+      read16(mine + 2 * SL, y);
+      read16(mine + SL, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = add2(v[i], add2(x[i], y[i]));
+      read16(mine, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = add2(v[i], x[i]);
     };
     auto fetch = [&](const float* m, int R, float2 (&v)[8]) {
       const float4* q = reinterpret_cast<const float4*>(m) + ((size_t)(c0 / 4) * R + row);
@@ -485,7 +497,7 @@ __global__ void __launch_bounds__(ChainCfg<SL>::kThreads, 1) gd_chain_kernel(con
       seq_wait(&tab.y_full, i & 1, ok);
       __syncwarp();
       after_sync();
-      sum(mine, v);
+      sum(P1 > 1, v);
       const float2 f = both(REV ? down : -1.f), w = both(REV ? -beta : beta * down);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -498,7 +510,7 @@ __global__ void __launch_bounds__(ChainCfg<SL>::kThreads, 1) gd_chain_kernel(con
       seq_wait(&tab.z_full, i & 1, ok);
       __syncwarp();
       after_sync();
-      sum(mine + K::kCols / 2, v);
+      sum(P2 > 1, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (REV) v[j] = add2(v[j], z0[j]);

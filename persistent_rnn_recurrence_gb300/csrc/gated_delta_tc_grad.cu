@@ -379,9 +379,9 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
   before_sync();
   __syncthreads();
   after_sync();
-  // D3 += Z^T Q
-  pieces.multiply(steps, smem, [&](int ct, int k0, const Operand& right, int n, bool) {
-    product<kP, DP>(tmem + D3 + 64 * ct, from_step(two_tt, k0), right, n, id_of(64, true, true), true);
+  // D2 = Z^T Q
+  pieces.multiply(steps, smem, [&](int ct, int k0, const Operand& right, int n, bool add) {
+    product<kP, DP>(tmem + D2 + 64 * ct, from_step(two_tt, k0), right, n, id_of(64, true, true), add);
   });
   // D1 = U R^T
   quads(kTwo, R, rows, g.dvt, nullptr);
@@ -400,6 +400,9 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
     const int c0 = (quarter * g.dkt + x) * 16;
     float2 f[8], h[8];
     read16(mine + D3 + c0, f);
+    read16(mine + D2 + c0, h);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = add2(f[i], h[i]);
     read16(mine + D0 + c0, h);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = fma2(both(-up), h[i], f[i]);
