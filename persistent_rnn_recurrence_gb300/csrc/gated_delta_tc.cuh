@@ -184,7 +184,7 @@ __device__ __forceinline__ void pairs_of(const Pack<T, 8>& r, float2 (&v)[4]) {
 // NT threads at once and later placed as P parts: rows past n and columns past d are zeros.
 template <typename T, int ROWS, int TILES, int NT>
 struct DataRows {
-  static constexpr int N = ROWS * 8 * TILES / NT;
+  static constexpr int N = (ROWS * 8 * TILES + NT - 1) / NT;
   Pack<T, 8> raw[N];
   int shift;  // neighbouring threads take a row's pieces of 8 columns
   __device__ __forceinline__ void fetch(const T* x, long long st, int r0, int n, int c0, int d, int tiles) {
@@ -214,7 +214,7 @@ struct DataRows {
 // The same for an fp32 matrix of R <= ROWS rows in quads of columns; a row per lane.
 template <int ROWS, int TILES, int NT>
 struct QuadRows {
-  static constexpr int N = ROWS * 8 * TILES / NT;
+  static constexpr int N = (ROWS * 8 * TILES + NT - 1) / NT;
   float4 a[N], b[N];
   __device__ __forceinline__ void fetch(const float* m, int R, int rows, int tiles) {
 #pragma unroll
@@ -275,15 +275,22 @@ __device__ __forceinline__ Operand mn_major(uint32_t addr, uint32_t part, uint32
 // D (+)= A B over `steps` steps of 16: every pair of parts whose places add up to less than three, small ones first.
 static __device__ __noinline__ void product_of(int pa, int pb, uint32_t d, Operand a, Operand b, int steps, uint32_t id,
                                         uint32_t acc) {
+  const uint32_t step_a = a.tile ? 2 : 128, step_b = b.tile ? 2 : 128, tile_a = a.tile ? a.tile : 512,
+                 tile_b = b.tile ? b.tile : 512;
 #pragma unroll 1
   for (int s = min(pa + pb - 2, 2); s >= 0; --s)
 #pragma unroll 1
-    for (int p = max(0, s - pb + 1); p < min(pa, s + 1); ++p)
+    for (int p = max(0, s - pb + 1); p < min(pa, s + 1); ++p) {
+      uint64_t da = a.desc + p * a.part, db = b.desc + (s - p) * b.part;
 #pragma unroll 1
-      for (int k = 0; k < steps; ++k) {
-        umma_f16(d, a.at(p, k), b.at(s - p, k), id, acc);
-        acc = 1;
-      }
+      for (int k = 0; k < steps; k += 4, da += tile_a, db += tile_b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (k + j < steps) {
+            umma_f16(d, da + j * step_a, db + j * step_b, id, acc);
+            acc = 1;
+          }
+    }
 }
 template <int PA, int PB>
 __device__ __forceinline__ void product(uint32_t d, const Operand& a, const Operand& b, int steps, uint32_t id,
@@ -319,6 +326,7 @@ struct Steps {
       __syncwarp();
     }
   }
+  // One warp polls: the others would take its turns to issue the products.
   __device__ __forceinline__ void wait() {
     seq_wait(bar, turn & 1, ok);
     ++turn;

@@ -790,7 +790,11 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None, dx=None, stream=None):
         dxp, dxs = dx.data_ptr(), cols
     else:
         dxp, dxs = _same_rows(dx, h, dev, what + ": dx")
-    need = prnn_rms_norm_workspace(rows, cols)
+    need = _sizes.get(("rms", dev, rows, cols))
+    if need is None:
+        if len(_sizes) > 4096:
+            _sizes.clear()
+        need = _sizes["rms", dev, rows, cols] = prnn_rms_norm_workspace(rows, cols)
     dweight = _torch.empty(cols, dtype=f32, device=on)
     ws = _torch.empty(need, dtype=_torch.uint8, device=on)
     _check(_lib.prnn_rms_norm_backward(code, rows, cols, dyp, dys, h.data_ptr(), hs,
