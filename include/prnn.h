@@ -662,7 +662,7 @@ prnn_status_t prnn_rms_norm_forward(prnn_dtype_t dtype, long long rows, int cols
 
 /*
  * The same with an output in 8 bits, as a product in 8 bits takes it: for every group of columns of a row,
- *     scale = max |y| / 448 (1 where that maximum is 0 or NaN),   q_c = y_c / scale rounded to e4m3.
+ *     scale = max |y| / 448 (1 where that maximum is at most 2^-100, or NaN),   q_c = y_c / scale rounded to e4m3.
  * group: 128 columns (the last of a row may be fewer) or 0, the row.  q [rows] bytes of e4m3 (no infinities; 0x7f
  * and 0xff are NaN), rows q_stride >= cols apart; scale [rows][ceil(cols / group)] fp32 ([rows] for 0).  q overlaps
  * nothing else.

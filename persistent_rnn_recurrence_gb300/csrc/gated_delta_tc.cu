@@ -619,8 +619,8 @@ __global__ void __launch_bounds__(kOutThreads, kData<T> == 3 ? 1 : 2)
   for (int vt = 0; vt < g.dvt; ++vt) {
     es.template place<PC>(smem + K::kU, kTile, kTile, C, 1, tab.gates.beta);
     steps.run([&] {
-      product<PC, PC>(tmem, k_major(base, 2 * kTile, kTile), mn_major(base + K::kU, kTile, kTile), 8,
-                      id_of(64, false, true), false);
+      product<PC, PC, PC - 1>(tmem, k_major(base, 2 * kTile, kTile), mn_major(base + K::kU, kTile, kTile), 8,
+                              id_of(64, false, true), false);
     });
     if (vt + 1 < g.dvt) es.fetch(E + (size_t)(vt + 1) * 16 * C * 4, C, C, 1);
     steps.wait();

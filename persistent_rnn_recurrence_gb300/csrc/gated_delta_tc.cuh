@@ -272,13 +272,13 @@ __device__ __forceinline__ Operand k_major(uint32_t addr, uint32_t part, uint32_
 __device__ __forceinline__ Operand mn_major(uint32_t addr, uint32_t part, uint32_t tile) {
   return {mn_desc(addr, tile), part >> 4, 0};
 }
-// D (+)= A B over `steps` steps of 16: every pair of parts whose places add up to less than three, small ones first.
-static __device__ __noinline__ void product_of(int pa, int pb, uint32_t d, Operand a, Operand b, int steps, uint32_t id,
-                                        uint32_t acc) {
+// D (+)= A B over `steps` steps of 16: every pair of parts whose places add up to MOST at most, small ones first.
+static __device__ __noinline__ void product_of(int pa, int pb, int most, uint32_t d, Operand a, Operand b, int steps,
+                                               uint32_t id, uint32_t acc) {
   const uint32_t step_a = a.tile ? 2 : 128, step_b = b.tile ? 2 : 128, tile_a = a.tile ? a.tile : 512,
                  tile_b = b.tile ? b.tile : 512;
 #pragma unroll 1
-  for (int s = min(pa + pb - 2, 2); s >= 0; --s)
+  for (int s = min(pa + pb - 2, most); s >= 0; --s)
 #pragma unroll 1
     for (int p = max(0, s - pb + 1); p < min(pa, s + 1); ++p) {
       uint64_t da = a.desc + p * a.part, db = b.desc + (s - p) * b.part;
@@ -292,10 +292,10 @@ static __device__ __noinline__ void product_of(int pa, int pb, uint32_t d, Opera
           }
     }
 }
-template <int PA, int PB>
+template <int PA, int PB, int MOST = 2>
 __device__ __forceinline__ void product(uint32_t d, const Operand& a, const Operand& b, int steps, uint32_t id,
                                         bool add) {
-  product_of(PA, PB, d, a, b, steps, id, add);
+  product_of(PA, PB, MOST, d, a, b, steps, id, add);
 }
 __device__ __forceinline__ uint32_t id_of(int n, bool a_mn, bool b_mn) {
   return bf16_idesc(128, n) | (a_mn ? kAMn : 0u) | (b_mn ? kBMn : 0u);

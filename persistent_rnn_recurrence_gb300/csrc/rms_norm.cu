@@ -3,7 +3,12 @@
 //
 // Bound by memory: 5 to 9 flops per element against 4 to 16 bytes.  A row is read once and kept packed in
 // registers, in its own type, between the sum of squares and the output: the stream is normalised as it is
-// stored, so the packed form loses nothing and takes half the registers of fp32 values.
+// stored, so the packed form loses nothing and takes half the registers of fp32 values.  Blocks stay and request their
+// next row while one is summed and written; two packs a thread measured best (8192 x 5760 bf16 into e4m3 83 us, with one
+// pack 92, with four 112).  Measured on GB300, against the copy rate of 6.78 TB/s: 8192 x 4096 bf16 with residual 40 us (0.98),
+// 8192 x 5760 bf16 with residual into e4m3 83 (0.59: some 16 instructions a value, at 24 warps an SM), gradient of 8192 x 2304 fp32
+// with the stream's 65 (0.69: a row's reduction stands between its loads and its store).  Rows that 16-byte accesses do not
+// fit go value by value: 8192 x 2001 bf16 70, into e4m3 120.
 #include <algorithm>
 
 #include <cuda_fp8.h>
@@ -46,10 +51,11 @@ __device__ __forceinline__ float block_max(float v, float* part) {
   for (int w = 1; w < warps; ++w) m = max_nan(m, part[w]);
   return m;
 }
-// A group of zeros has the scale 1.
-__device__ __forceinline__ float scale_of(float top) { return top > 0.f ? top / kE4m3Max : 1.f; }
+// A group of zeros has the scale 1, and so has one so small that its scale's inverse leaves fp32's range.
+constexpr float kLeastTop = 7.888609e-31f;  // 2^-100
+__device__ __forceinline__ float scale_of(float top) { return top > kLeastTop ? top * (1.f / kE4m3Max) : 1.f; }
 // What a value is multiplied by instead of divided by its scale: a rounding of 2^-24 more before that of 2^-4.
-__device__ __forceinline__ float inverse_of(float top) { return top > 0.f ? kE4m3Max / top : 1.f; }
+__device__ __forceinline__ float inverse_of(float top) { return top > kLeastTop ? kE4m3Max / top : 1.f; }
 __device__ __forceinline__ uint8_t to_e4m3(float v) {
   return (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
 }

@@ -193,6 +193,25 @@ def test_rows_of_zeros_infinities_and_nan(env, dtype, cols):
         assert bool(q[[0, 2, 5]].float().isfinite().all())
 
 
+@pytest.mark.parametrize("cols", [100, 256, 301, 40000])
+def test_values_too_small_for_a_scale(env, cols):
+    """Outputs whose largest is 2^-100 and below become zeros with the scale 1, not infinities or NaN; just above that they
+    keep their bits."""
+    torch, prnn = env
+    x = normal(torch, (3, cols), torch.float32, 80)
+    x[:, ::7] = 0
+    for power, zero in ((-140, True), (-125, True), (-110, True), (-97, False), (120, False)):
+        w = torch.full((cols,), 2.0 ** power, device="cuda")
+        want, _, _ = reference(torch, x, w, 1e-6, None)
+        for group in (0, 128):
+            q, scale, _, _ = prnn.rms_norm_e4m3(x, w, 1e-6, group=group)
+            assert bool(q.float().isfinite().all())
+            if zero:
+                assert bool((q.float() == 0).all()) and bool((scale == 1).all())
+            else:
+                check_e4m3(torch, q, scale, want, group, f"2^{power}")
+
+
 def test_empty_and_single(env):
     torch, prnn = env
     x = torch.zeros(0, 64, device="cuda", dtype=torch.bfloat16)
