@@ -793,8 +793,8 @@ prnn_status_t prnn_linear_attention_step(const prnn_linear_attention_t* a, float
  * prnn_rms_norm over the last axis with weight dk^-1/2 makes them so) and beta in 0 .. 2: with longer keys the state
  * grows without bound, and so do its results.  fp32 sums, states and gates throughout; one rounding at each
  * 16-bit output.  An infinity or NaN in a token within the length may reach, as NaN, the
- * outputs and gradients of its own sequence and head up to 127 tokens before it and everywhere behind it.  Tokens
- * past the length reach nothing, whatever they hold.
+ * outputs of its own sequence and head up to 127 tokens before it and everywhere behind it, and all of that
+ * head's gradients there.  Tokens past the length reach nothing, whatever they hold.
  */
 typedef struct {
   prnn_dtype_t dtype;         /* of q, k, v, o and their gradients                               */
