@@ -12,48 +12,51 @@ namespace {
 //
 // Tt is the inverse of I + A, A strictly lower triangular.  The diagonal blocks of 32 go by substitution, a column per
 // lane; those of 64 from them by T_10 = -T_11 A_10 T_00 in fp32; and the last block of 64 by the same formula
-// on the tensor cores, T's rows and columns being where the products with V and K want them anyway.
-constexpr int kLd = 68, kPrepThreads = 512;  // floats of a row of 64: 16-byte aligned, rows a quad of banks apart
+// on the tensor cores.
+//
+// The steps stand one behind another, so two blocks share an SM and fill each other's waits.  That fits because Tt is kept
+// without its zero quarter: its columns 64 ... have rows 64 ... only, as the left operand of a sum of their own that
+// counts in those rows alone (the 64 rows before them, which the product reads as well, hold anything); and
+// because right operands come in pieces of 64 tokens.
+constexpr int kLd = 68, kPrepThreads = 256;  // floats of a row of 64: 16-byte aligned, rows a quad of banks apart
 struct PrepTab {
   Gates gates;
   double part[4];
   uint64_t bar;
   uint32_t tmem;
 };
-// Tt as parts, its diagonal blocks of 64 in fp32 with A's before them, A_10 as parts and A_10 T_00; the right operands lie
-// over the latter three.
-constexpr uint32_t kPrepA = 96 * 1024, kPrepT = kPrepA + 2 * 64 * kLd * 4, kPrepLow = 168 * 1024,
-                   kPrepRight = kPrepA, kPrepTab = 216 * 1024;
-static_assert(kPrepT + 2 * 64 * kLd * 4 <= kPrepLow && kPrepLow + kP * kTile <= kPrepTab &&
-                  kPrepRight + kP * 2 * kTile <= kPrepTab && kPrepTab + sizeof(PrepTab) <= 227 * 1024,
-              "shared memory");
+// Tt's columns 0 ... and 64 ... as parts, a right operand.  Before them, in the same place: K; A and T in fp32 with A_10 as
+// parts.  After them: W.
+constexpr uint32_t kHalf = kTile / 2, kTt1 = kP * kTile, kPrepT = 2 * 64 * kLd * 4, kPrepRight = kTt1 + kP * kHalf,
+                   kPrepTab = kPrepRight + kP * kHalf;
+static_assert(2 * kPrepT <= kPrepRight && 2 * kP * kTile <= kPrepTab && 2 * (kPrepTab + sizeof(PrepTab) + 1024) <= 228 * 1024,
+              "shared memory of two blocks");
 
 // T_10 <- -T_11 (A_10 T_00) of 2 x 2 blocks of 32, for two diagonal blocks of 64; the product in brackets is kept in
 // T's unused block (0, 1).
 __device__ __forceinline__ void lower_blocks(const float* A, float* T) {
-  const int q = threadIdx.x & 255, r = (q >> 4) * 2, c = (q & 15) * 2;
-  A += (threadIdx.x >> 8) * 64 * kLd;
-  T += (threadIdx.x >> 8) * 64 * kLd;
-#pragma unroll
+  const int q = threadIdx.x & 127, r = (q >> 4) * 4, c = (q & 15) * 2;
+  A += (threadIdx.x >> 7) * 64 * kLd;
+  T += (threadIdx.x >> 7) * 64 * kLd;
+#pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     const float* left = pass == 0 ? A + (32 + r) * kLd : T + (32 + r) * kLd + 32;
     const float* right = pass == 0 ? T + c : T + 32 + c;
-    float2 s[2] = {both(0.f), both(0.f)};
-#pragma unroll
+    float2 s[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
+#pragma unroll 4
     for (int m = 0; m < 32; m += 4) {
-      float4 l[2];
       float2 f[4];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) l[x] = *reinterpret_cast<const float4*>(left + x * kLd + m);
 #pragma unroll
       for (int k = 0; k < 4; ++k) f[k] = *reinterpret_cast<const float2*>(right + (m + k) * kLd);
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-        s[x] = fma2(both(l[x].w), f[3], fma2(both(l[x].z), f[2], fma2(both(l[x].y), f[1], fma2(both(l[x].x), f[0], s[x]))));
+      for (int x = 0; x < 4; ++x) {
+        const float4 l = *reinterpret_cast<const float4*>(left + x * kLd + m);
+        s[x] = fma2(both(l.w), f[3], fma2(both(l.z), f[2], fma2(both(l.y), f[1], fma2(both(l.x), f[0], s[x]))));
+      }
     }
     float* to = pass == 0 ? T + r * kLd + 32 + c : T + (32 + r) * kLd + c;
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < 4; ++x)
       *reinterpret_cast<float2*>(to + x * kLd) = pass == 0 ? s[x] : mul2(s[x], both(-1.f));
     __syncthreads();
   }
@@ -63,32 +66,46 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// The thread's own stores have read their source.
+__device__ __forceinline__ void bulk_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 template <typename T>
-__global__ void __launch_bounds__(kPrepThreads, 1) gd_prepare_kernel(const __grid_constant__ Args g, int keep_inverse) {
-  constexpr int DP = kData<T>, NT = kPrepThreads;
+__global__ void __launch_bounds__(kPrepThreads, 2) gd_prepare_kernel(const __grid_constant__ Args g, int keep_inverse) {
+  constexpr int DP = kData<T>, NT = kPrepThreads, VT = DP == 1 ? 2 : 1;  // tiles of V in a piece
   extern __shared__ __align__(1024) unsigned char smem[];
   PrepTab& tab = *reinterpret_cast<PrepTab*>(smem + kPrepTab);
   const GdArgs& a = g.a;
   int index = blockIdx.x;
   Place p = next_place(g, index);
   if (p.n == 0) return;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = (warp & 3) * 32 + lane, quarter = warp >> 2;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = (warp & 3) * 32 + lane, half = warp >> 2;
+  const bool low = (warp & 3) >= 2;  // rows 64 ...
   auto keys = [&](const Place& at) { return rows_of<T>(a.k, at.t0, at.b, at.hq); };
   DataRows<T, C, 2, NT> rows;
   rows.fetch(keys(p), a.k.st, 0, p.n, 0, a.dk, g.dkt);
   if (!begin(&tab.bar, &tab.tmem, 256, smem, g.status)) return;
   Steps steps{&tab.bar};
   const uint32_t tmem = tab.tmem, mine = tmem + ((uint32_t)((warp & 3) * 32) << 16), base = smem_u32(smem);
-  const uint32_t part = g.dkt * kTile, vpart = g.dvt * kTile;
-  const Operand Tt = k_major(base, 2 * kTile, kTile);
-  float *A = reinterpret_cast<float*>(smem + kPrepA), *inv = reinterpret_cast<float*>(smem + kPrepT);
+  const uint32_t part = g.dkt * kTile;
+  // Tt's columns 0 ... and, with rows 0 ... 63 that do not count, 64 ...
+  const Operand left0 = k_major(base, kTile, kTile), left1 = k_major(base + kTt1 - kHalf, kHalf, kTile);
+  float *A = reinterpret_cast<float*>(smem), *inv = reinterpret_cast<float*>(smem + kPrepT);
   float gate = 0.f, beta = 0.f;
   auto ask_gates = [&](const Place& at) {
     const long long t = at.t0 + tid;
     const bool in = tid < at.n;
     gate = in ? a.g[t * a.gt + at.b * a.gb + at.h * a.gh] : 0.f;
     beta = in ? a.beta[t * a.bt + at.b * a.bb + at.h * a.bh] : 0.f;
+  };
+  // columns c0 ... of an accumulator whose tokens 64 ... have one of their own, 128 columns on
+  auto read_both = [&](int c0, int n, float2 (&v)[8]) {
+    read16(mine + c0, v);
+    if (low && n > 64) {
+      float2 x[8];
+      read16(mine + 128 + c0, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = add2(v[i], x[i]);
+    }
   };
   ask_gates(p);
   while (p.n > 0) {
@@ -105,11 +122,9 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gd_prepare_kernel(const __gri
       }
       if (lane == 31) tab.part[warp] = G;
     }
-    // K's operand lies where Tt will
-    rows.template place<DP>(smem, part, kTile);
-    rows.fetch(rows_of<T>(a.v, at.t0, at.b, at.h), a.v.st, 0, at.n, 0, a.dv, g.dvt);
-    if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last chunk's W has been read
+    if (tid == 0) bulk_read();  // the last chunk's W
     __syncthreads();
+    rows.template place<DP>(smem, part, kTile);
     if (tid < C) {
       double all = 0;
 #pragma unroll
@@ -117,13 +132,12 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gd_prepare_kernel(const __gri
         if (w < warp) G += tab.part[w];
         all += tab.part[w];
       }
-      const double last = __shfl_sync(0xffffffffu, G, lane | 15), first = __shfl_sync(0xffffffffu, G, lane & 16);
+      const double last = __shfl_sync(0xffffffffu, G, lane | 15);
       const float hi = (float)G;
       tab.gates.sum[tid] = make_float2(hi, (float)(G - hi));
       tab.gates.up[tid] = exp2f(hi);
       tab.gates.down[tid] = exp2f((float)(all - G));
       tab.gates.to_last[tid] = exp2f((float)(last - G));
-      tab.gates.from_first[tid] = exp2f((float)(G - first));
     }
     const Operand K = k_major(base, part, kTile);
     steps.run([&] { product<DP, DP>(tmem, K, K, (a.dk + 15) / 16, id_of(128, false, false), false); });
@@ -138,17 +152,19 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gd_prepare_kernel(const __gri
       float* to = reinterpret_cast<float*>(g.gates + at.at);
       for (int i = tid; i < (int)(sizeof(Gates) / 4); i += NT) to[i] = from[i];
     }
+    if (tid == 0) bulk_read();
     steps.wait();
+    __syncthreads();  // K's place may be written
 #pragma unroll 1
-    for (int q = 0; q < 2; ++q) {  // A_ij = (k_i . k_j) D_ij beta_j below the diagonal
-      const int c0 = quarter * 32 + q * 16;
+    for (int q = 0; q < 4; ++q) {  // A_ij = (k_i . k_j) D_ij beta_j below the diagonal
+      const int c0 = half * 64 + q * 16;
       if ((c0 >> 5) > (warp & 3)) continue;  // behind all of the warp's rows
       float2 x[8];
       read16(mine + c0, x);
       decayed<true>(x, row, c0, tab.gates);
       times16(x, tab.gates.beta + c0);
-      if (row >= 64 && c0 < 64) {
-        put16<kP>(smem + kPrepLow, kTile, row, c0, x);
+      if (low && half == 0) {
+        put16<kP>(smem + kPrepRight, kHalf, row - 64, c0, x);
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -176,96 +192,125 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gd_prepare_kernel(const __gri
         inv[(r0 + r) * kLd + c0 + lane] = x[r];
       }
     }
-    if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     __syncthreads();
     lower_blocks(A, inv);
-    {  // the diagonal blocks of 64 and the zeros right of them as parts
+    {  // the diagonal blocks of 64 as parts, in the place of themselves and A
       float2 x[2][8];
+      const int col0 = (low ? 64 : 0) + half * 32;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int c0 = quarter * 32 + q * 16;
-        if (row >= 64 && c0 < 64) continue;
+      for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-          const int c = c0 + 2 * i;
+          const int c = col0 + q * 16 + 2 * i;
           const float4 f = *reinterpret_cast<const float4*>(inv + row * kLd + (c & 63));
           x[q][i] = make_float2(c <= row ? f.x : 0.f, c + 1 <= row ? f.y : 0.f);
           x[q][i + 1] = make_float2(c + 2 <= row ? f.z : 0.f, c + 3 <= row ? f.w : 0.f);
         }
-        put16<kP>(smem, 2 * kTile, row, c0, x[q]);
-        if (keep_inverse) store_quads(g.inv + at.at * C * C, C, row, c0, x[q]);
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int c0 = col0 + q * 16;
+        if (low) put16<kP>(smem + kTt1, kHalf, row - 64, c0 - 64, x[q]);
+        else put16<kP>(smem, kTile, row, c0, x[q]);
+        if (!keep_inverse) continue;
+        store_quads(g.inv + at.at * C * C, C, row, c0, x[q]);
+        if (low) continue;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[q][i] = both(0.f);
+        store_quads(g.inv + at.at * C * C, C, row, c0 + 64, x[q]);
       }
     }
-    // A_10 T_00, of which rows 64 ... count
+    // T_10: A_10 T_00, whose rows 64 ... count, then T_11 times that
     steps.run([&] {
-      product<kP, kP>(tmem + 128, k_major(base + kPrepLow, kTile, kTile), mn_major(base, 2 * kTile, kTile), 4,
+      product<kP, kP>(tmem + 128, k_major(base + kPrepRight - kHalf, kHalf, kTile), mn_major(base, kTile, kTile), 4,
                       id_of(64, false, true), false);
     });
     steps.wait();
-    unsigned char* mid = smem + kPrepA;  // [3][64][64], rows 64 ...
-    if (row >= 64) {
-      const int c0 = quarter * 16;
-      float2 x[8];
-      read16(mine + 128 + c0, x);
-      put16<kP>(mid, kTile / 2, row - 64, c0, x);
-    }
-    steps.run([&] {
-      Operand left = Tt;
-      left.desc += kTile >> 4;  // columns 64 ...
-      product<kP, kP>(tmem + 192, left, mn_major(base + kPrepA, kTile / 2, kTile / 2), 4, id_of(64, false, true), false);
-    });
+    if (low)
+#pragma unroll 1
+      for (int q = 0; q < 2; ++q) {
+        const int c0 = half * 32 + q * 16;
+        float2 x[8];
+        read16(mine + 128 + c0, x);
+        put16<kP>(smem + kPrepRight, kHalf, row - 64, c0, x);
+      }
+    const Operand right = mn_major(base + kPrepRight, kHalf, kHalf);
+    steps.run([&] { product<kP, kP>(tmem + 192, left1, right, 4, id_of(64, false, true), false); });
+    DataRows<T, 64, VT, NT> vs;
+    const T* v = rows_of<T>(a.v, at.t0, at.b, at.h);
+    vs.fetch(v, a.v.st, 0, at.n, 0, a.dv, VT == 2 ? g.dvt : 1);
     steps.wait();
-    if (row >= 64) {
-      const int c0 = quarter * 16;
-      float2 x[8];
-      read16(mine + 192 + c0, x);
+    if (low)
+#pragma unroll 1
+      for (int q = 0; q < 2; ++q) {
+        const int c0 = half * 32 + q * 16;
+        float2 x[8];
+        read16(mine + 192 + c0, x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], both(-1.f));
-      put16<kP>(smem, 2 * kTile, row, c0, x);
-      if (keep_inverse) store_quads(g.inv + at.at * C * C, C, row, c0, x);
-    }
-    rows.template place<DP>(smem + kPrepRight, vpart, kTile);
-    steps.run([&] {
-      product<kP, DP>(tmem, Tt, mn_major(base + kPrepRight, vpart, kTile), 8, id_of(64 * g.dvt, false, true), false);
-    });
-    rows.fetch(keys(at), a.k.st, 0, at.n, 0, a.dk, g.dkt);
-    steps.wait();
-    rows.template place<kP>(smem + kPrepRight, part, kTile, tab.gates.up);
-    steps.run([&] {
-      product<kP, kP>(tmem + 128, Tt, mn_major(base + kPrepRight, part, kTile), 8, id_of(64 * g.dkt, false, true), false);
-    });
-    index += gridDim.x;
-    p = next_place(g, index);
-    if (p.n > 0) {
-      rows.fetch(keys(p), a.k.st, 0, p.n, 0, a.dk, g.dkt);
-      ask_gates(p);
+        for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], both(-1.f));
+        put16<kP>(smem, kTile, row, c0, x);
+        if (keep_inverse) store_quads(g.inv + at.at * C * C, C, row, c0, x);
+      }
+    // Tt V, tokens 64 ... in columns 128 ...
+    const int vpieces = VT == 2 ? 1 : g.dvt;
+    DataRows<T, 64, 1, NT> ks;
+#pragma unroll 1
+    for (int i = 0; i < 2 * vpieces && i / vpieces * 64 < at.n; ++i) {
+      const int th = i / vpieces, vt = i % vpieces;
+      vs.template place<DP>(smem + kPrepRight, VT == 2 ? 0 : kHalf, kHalf);
+      steps.run([&] {
+        product<kP, DP>(tmem + 128 * th + 64 * vt, th ? left1 : left0, right, 4, id_of(VT == 2 ? 64 * g.dvt : 64, false, true),
+                        false);
+      });
+      const int next = i + 1, nh = next / vpieces;
+      if (nh < 2 && nh * 64 < at.n) vs.fetch(v, a.v.st, nh * 64, at.n, next % vpieces * 64, a.dv, VT == 2 ? g.dvt : 1);
+      else ks.fetch(keys(at), a.k.st, 0, at.n, 0, a.dk, 1);
+      steps.wait();
     }
     float* E = g.E + at.at * C * 64 * g.dvt;
 #pragma unroll 1
-    for (int q = 0; q < g.dvt; ++q) {
-      const int c0 = (quarter * g.dvt + q) * 16;
+    for (int q = 0; q < 2 * g.dvt; ++q) {
+      const int c0 = (half * 2 * g.dvt + q) * 16;
       float2 f[8];
-      read16(mine + c0, f);
+      read_both(c0, at.n, f);
       store_quads(E, C, row, c0, f);
     }
-    steps.wait();
-    // W as tiles [dkt][parts] in the place of its right operand, and from there to the walk's copy
+    // W = Tt (e^G K), likewise
+    index += gridDim.x;
+    p = next_place(g, index);
 #pragma unroll 1
-    for (int q = 0; q < g.dkt; ++q) {
-      const int c0 = (quarter * g.dkt + q) * 16;
+    for (int i = 0; i < 2 * g.dkt && i / g.dkt * 64 < at.n; ++i) {
+      const int th = i / g.dkt, ct = i % g.dkt;
+      ks.template place<kP>(smem + kPrepRight, kHalf, kHalf, tab.gates.up + 64 * th);
+      steps.run([&] {
+        product<kP, kP>(tmem + 128 * th + 64 * ct, th ? left1 : left0, right, 4, id_of(64, false, true), false);
+      });
+      const int next = i + 1, nh = next / g.dkt;
+      if (nh < 2 && nh * 64 < at.n) {
+        ks.fetch(keys(at), a.k.st, nh * 64, at.n, next % g.dkt * 64, a.dk, 1);
+      } else if (p.n > 0) {
+        rows.fetch(keys(p), a.k.st, 0, p.n, 0, a.dk, g.dkt);
+        ask_gates(p);
+      }
+      steps.wait();
+    }
+    // as tiles [dkt][parts], and from there to the walk's copy
+#pragma unroll 1
+    for (int q = 0; q < 2 * g.dkt; ++q) {
+      const int c0 = (half * 2 * g.dkt + q) * 16;
       float2 f[8];
-      read16(mine + 128 + c0, f);
-      put16<kP>(smem + kPrepRight + (c0 >> 6) * kP * kTile, kTile, row, c0 & 63, f);
+      read_both(c0, at.n, f);
+      put16<kP>(smem + (c0 >> 6) * kP * kTile, kTile, row, c0 & 63, f);
     }
     to_async();
     before_sync();
     __syncthreads();
     if (tid == 0) {
-      bulk_store(g.wimg + at.at * g.dkt * kP * kTile, base + kPrepRight, g.dkt * kP * kTile);
+      bulk_store(g.wimg + at.at * g.dkt * kP * kTile, base, g.dkt * kP * kTile);
       bulk_commit();
     }
   }
-  if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  if (tid == 0) bulk_read();
   finish(tmem, 256, steps.ok, g.status);
 }
 
@@ -652,7 +697,7 @@ cudaError_t launch_prepare(const Args& g, bool keep_inverse, cudaStream_t s) {
     constexpr uint32_t smem = kPrepTab + sizeof(PrepTab);
     const cudaError_t e = allow(gd_prepare_kernel<T>, smem);
     if (e != cudaSuccess) return e;
-    gd_prepare_kernel<T><<<grid_of(g), kPrepThreads, smem, s>>>(g, keep_inverse);
+    gd_prepare_kernel<T><<<grid_of(g, 2), kPrepThreads, smem, s>>>(g, keep_inverse);
   });
   return cudaGetLastError();
 }

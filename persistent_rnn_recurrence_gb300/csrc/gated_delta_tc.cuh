@@ -40,11 +40,10 @@ template <typename T>
 constexpr int kData = std::is_same<T, float>::value ? 3 : (std::is_same<T, __half>::value ? 2 : 1);
 
 // Per chunk and head, fp32 [128] each: sums G of log-decays (to the base 2) as a value and the rest of it, their exponentials, those to
-// the chunk's end, betas; and decays within blocks of 16 tokens: from token j to its block's last, from its block's
-// first to j.
+// the chunk's end, betas; and the decays from each token to the last of its block of 16.
 struct Gates {
   float2 sum[C];
-  float up[C], down[C], beta[C], to_last[C], from_first[C];
+  float up[C], down[C], beta[C], to_last[C];
 };
 
 struct Args {
@@ -412,10 +411,10 @@ __device__ __forceinline__ void times16(float2 (&v)[8], const float* f) {  // f:
   }
 }
 
-// A block per SM where each has chunks enough to go on with the next, else one for every chunk.
-inline unsigned grid_of(const Args& g) {
-  const long long n = (long long)g.nbh * g.chunks, sms = seq_sm_count();
-  return (unsigned)(n < 4 * sms ? n : sms);
+// `per_sm` blocks an SM where each has chunks enough to go on with the next, else one for every chunk.
+inline unsigned grid_of(const Args& g, int per_sm) {
+  const long long n = (long long)g.nbh * g.chunks, at_once = (long long)per_sm * seq_sm_count();
+  return (unsigned)(n < 4 * at_once ? n : at_once);
 }
 
 cudaError_t launch_prepare(const Args& g, bool keep_inverse, cudaStream_t s);

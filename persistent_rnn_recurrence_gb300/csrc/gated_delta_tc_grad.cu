@@ -251,17 +251,17 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
     tab.rows[quarter][1][row] = s;
     if (!tiny) es = ev / beta;
   }
-  // dV E^T, E dV^T, and K K^T where a beta is 0
+  // dV E^T, and where a beta is 0, E dV^T and K K^T
   quads(kOne, E, C, g.dvt, nullptr);
   const Operand one_v = k_major(base + kOne, vpart, kTile), two_v = k_major(base + kTwo, vpart, kTile);
   const int vsteps = (a.dv + 15) / 16, ksteps = (a.dk + 15) / 16;
   steps.run([&] {
     product<kP, kP>(tmem + D0, two_v, one_v, vsteps, id_of(128, false, false), false);
-    product<kP, kP>(tmem + D1, one_v, two_v, vsteps, id_of(128, false, false), false);
+    if (any_tiny) product<kP, kP>(tmem + D1, one_v, two_v, vsteps, id_of(128, false, false), false);
   });
   pieces.first(k, a.k.st, p.n, a.dk, g.dkt);
   steps.wait();
-  if (any_tiny) {
+  if (any_tiny) {  // es -= sum over j > i of (k_i . k_j) D_ji (e_i . dv_j)
     data.fetch(k, a.k.st, 0, p.n, 0, a.dk, g.dkt);
     data.template place<DP>(smem + kOne, kpart, kTile);
     steps.run([&] {
@@ -269,59 +269,41 @@ __global__ void __launch_bounds__(kThreads, 1) gd_gradients_kernel(const __grid_
       product<DP, DP>(tmem + D2, K, K, ksteps, id_of(128, false, false), false);
     });
     steps.wait();
-  }
-  {  // -(Y + Y^T) as the next left operand, dbeta
-    float s = es;
 #pragma unroll 1
     for (int x = 0; x < 2; ++x) {
       const int c0 = quarter * 32 + x * 16;
-      float2 y1[8], y2[8];
-      if (quarter <= (warp & 3)) {
-        read16(mine + D0 + c0, y1);
-        decayed<true>(y1, row, c0, tab.gates);
-        times16(y1, tab.gates.beta + c0);
+      if (quarter < (warp & 3)) continue;
+      float2 y[8], kk[8];
+      read16(mine + D1 + c0, y);
+      read16(mine + D2 + c0, kk);
+      const float2 here = tab.gates.sum[row];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float f = at_of16(kk, i) * at_of16(y, i) * decay_between(tab.gates.sum[c0 + i], here);
+        es -= tiny && c0 + i > row ? f : 0.f;
       }
-      if (quarter >= (warp & 3)) {  // (e_i . dv_j) D_ji, j behind i
-        read16(mine + D1 + c0, y2);
-        if (quarter > (warp & 3)) {
-          const float2 w = both(decay_between(tab.gates, c0, row));
-          times16(y2, tab.gates.from_first + c0);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y2[i] = mul2(y2[i], w);
-        } else {
-          const float2 here_ = tab.gates.sum[row];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int j = c0 + i;
-            const float f = at_of16(y2, i) * decay_between(tab.gates.sum[j], here_);
-            set16(y2, i, j > row ? f : 0.f);
-          }
-        }
-        if (any_tiny) {
-          float2 kk[8];
-          read16(mine + D2 + c0, kk);
-          if (tiny)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s = fmaf(-kk[i].x, y2[i].x, fmaf(-kk[i].y, y2[i].y, s));
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (quarter > (warp & 3)) y1[i] = mul2(y2[i], both(-beta));
-        else if (quarter == (warp & 3)) y1[i] = fma2(y2[i], both(-beta), mul2(y1[i], both(-1.f)));
-        else y1[i] = mul2(y1[i], both(-1.f));
-      }
-      put16<kP>(smem + kOne, 2 * kTile, row, c0, y1);
     }
-    tab.rows[quarter][2][row] = s;
+  }
+  tab.rows[quarter][2][row] = es;
+#pragma unroll 1
+  for (int x = 0; x < 2; ++x) {  // -Y as the next left operand
+    const int c0 = quarter * 32 + x * 16;
+    float2 y[8];
+    if (quarter <= (warp & 3)) read16(mine + D0 + c0, y);
+    decayed<true>(y, row, c0, tab.gates);
+    times16(y, tab.gates.beta + c0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = mul2(y[i], both(-1.f));
+    put16<kP>(smem + kOne, 2 * kTile, row, c0, y);
   }
   before_sync();
   __syncthreads();
   after_sync();
-  // D3 = -(Y + Y^T) K
-  const Operand one_t = k_major(base + kOne, 2 * kTile, kTile);
+  // D3 = -(Y + Y^T) K, Y in both majors
+  const Operand one_t = k_major(base + kOne, 2 * kTile, kTile), one_tt = mn_major(base + kOne, 2 * kTile, kTile);
   pieces.multiply(steps, smem, [&](int ct, int k0, const Operand& right, int n, bool add) {
     product<kP, DP>(tmem + D3 + 64 * ct, from_step(one_t, k0), right, n, id_of(64, false, true), add);
+    product<kP, DP>(tmem + D3 + 64 * ct, from_step(one_tt, k0), right, n, id_of(64, true, true), true);
   });
   // D0 = dV S0^T
   quads(kOne, S, rows, g.dvt, nullptr);
