@@ -17,8 +17,10 @@ namespace {
 // The steps stand one behind another, so two blocks share an SM and fill each other's waits.  That fits because Tt is kept
 // without its zero quarter: its columns 64 ... have rows 64 ... only, as the left operand of a sum of their own that
 // counts in those rows alone (the 64 rows before them, which the product reads as well, hold anything); and
-// because right operands come in pieces of 64 tokens.
-constexpr int kLd = 68, kPrepThreads = 256;  // floats of a row of 64: 16-byte aligned, rows a quad of banks apart
+// because right operands come in pieces of 64 tokens.  Where chunks are too few for that, one block of twice the threads and
+// with whole right operands takes a chunk in less time: 180 chunks of fp32, of which a half are empty, 27 us against 41;
+// but 2048 of bf16 264 us against 235.
+constexpr int kLd = 68;  // floats of a row of 64: 16-byte aligned, rows a quad of banks apart
 struct PrepTab {
   Gates gates;
   double part[4];
@@ -27,36 +29,43 @@ struct PrepTab {
 };
 // Tt's columns 0 ... and 64 ... as parts, a right operand.  Before them, in the same place: K; A and T in fp32 with A_10 as
 // parts.  After them: W.
-constexpr uint32_t kHalf = kTile / 2, kTt1 = kP * kTile, kPrepT = 2 * 64 * kLd * 4, kPrepRight = kTt1 + kP * kHalf,
-                   kPrepTab = kPrepRight + kP * kHalf;
-static_assert(2 * kPrepT <= kPrepRight && 2 * kP * kTile <= kPrepTab && 2 * (kPrepTab + sizeof(PrepTab) + 1024) <= 228 * 1024,
-              "shared memory of two blocks");
+constexpr uint32_t kHalf = kTile / 2, kTt1 = kP * kTile, kPrepT = 2 * 64 * kLd * 4, kPrepRight = kTt1 + kP * kHalf;
+template <int NT>
+constexpr uint32_t kPrepTab = kPrepRight + (NT == 512 ? 2 * kP * kTile : kP * kHalf);
+static_assert(2 * kPrepT <= kPrepRight && 2 * kP * kTile <= kPrepTab<256> &&
+                  2 * (kPrepTab<256> + sizeof(PrepTab) + 1024) <= 228 * 1024 &&
+                  kPrepTab<512> + sizeof(PrepTab) <= 227 * 1024,
+              "shared memory of two blocks, and of one");
 
 // T_10 <- -T_11 (A_10 T_00) of 2 x 2 blocks of 32, for two diagonal blocks of 64; the product in brackets is kept in
 // T's unused block (0, 1).
+template <int NT>
 __device__ __forceinline__ void lower_blocks(const float* A, float* T) {
-  const int q = threadIdx.x & 127, r = (q >> 4) * 4, c = (q & 15) * 2;
-  A += (threadIdx.x >> 7) * 64 * kLd;
-  T += (threadIdx.x >> 7) * 64 * kLd;
+  constexpr int Q = NT / 2, X = 512 / Q;  // threads of a block of 64, rows of 2 values each
+  const int q = threadIdx.x % Q, r = (q >> 4) * X, c = (q & 15) * 2;
+  A += threadIdx.x / Q * 64 * kLd;
+  T += threadIdx.x / Q * 64 * kLd;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     const float* left = pass == 0 ? A + (32 + r) * kLd : T + (32 + r) * kLd + 32;
     const float* right = pass == 0 ? T + c : T + 32 + c;
-    float2 s[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
+    float2 s[X];
+#pragma unroll
+    for (int x = 0; x < X; ++x) s[x] = both(0.f);
 #pragma unroll 4
     for (int m = 0; m < 32; m += 4) {
       float2 f[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) f[k] = *reinterpret_cast<const float2*>(right + (m + k) * kLd);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
+      for (int x = 0; x < X; ++x) {
         const float4 l = *reinterpret_cast<const float4*>(left + x * kLd + m);
         s[x] = fma2(both(l.w), f[3], fma2(both(l.z), f[2], fma2(both(l.y), f[1], fma2(both(l.x), f[0], s[x]))));
       }
     }
     float* to = pass == 0 ? T + r * kLd + 32 + c : T + (32 + r) * kLd + c;
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
+    for (int x = 0; x < X; ++x)
       *reinterpret_cast<float2*>(to + x * kLd) = pass == 0 ? s[x] : mul2(s[x], both(-1.f));
     __syncthreads();
   }
@@ -69,16 +78,18 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 // The thread's own stores have read their source.
 __device__ __forceinline__ void bulk_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
-template <typename T>
-__global__ void __launch_bounds__(kPrepThreads, 2) gd_prepare_kernel(const __grid_constant__ Args g, int keep_inverse) {
-  constexpr int DP = kData<T>, NT = kPrepThreads, VT = DP == 1 ? 2 : 1;  // tiles of V in a piece
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT, 512 / NT) gd_prepare_kernel(const __grid_constant__ Args g, int keep_inverse) {
+  constexpr int DP = kData<T>, VT = DP == 1 ? 2 : 1;  // tiles of V in a piece
+  constexpr int GROUPS = NT / C, BLOCKS = 4 / GROUPS;  // groups of columns, blocks of 16 of 64 columns for each
+  constexpr bool kWhole = NT == 512;
   extern __shared__ __align__(1024) unsigned char smem[];
-  PrepTab& tab = *reinterpret_cast<PrepTab*>(smem + kPrepTab);
+  PrepTab& tab = *reinterpret_cast<PrepTab*>(smem + kPrepTab<NT>);
   const GdArgs& a = g.a;
   int index = blockIdx.x;
   Place p = next_place(g, index);
   if (p.n == 0) return;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = (warp & 3) * 32 + lane, half = warp >> 2;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = (warp & 3) * 32 + lane, group = warp >> 2;
   const bool low = (warp & 3) >= 2;  // rows 64 ...
   auto keys = [&](const Place& at) { return rows_of<T>(a.k, at.t0, at.b, at.hq); };
   DataRows<T, C, 2, NT> rows;
@@ -156,14 +167,14 @@ __global__ void __launch_bounds__(kPrepThreads, 2) gd_prepare_kernel(const __gri
     steps.wait();
     __syncthreads();  // K's place may be written
 #pragma unroll 1
-    for (int q = 0; q < 4; ++q) {  // A_ij = (k_i . k_j) D_ij beta_j below the diagonal
-      const int c0 = half * 64 + q * 16;
+    for (int q = 0; q < 2 * BLOCKS; ++q) {  // A_ij = (k_i . k_j) D_ij beta_j below the diagonal
+      const int c0 = (group * 2 * BLOCKS + q) * 16;
       if ((c0 >> 5) > (warp & 3)) continue;  // behind all of the warp's rows
       float2 x[8];
       read16(mine + c0, x);
       decayed<true>(x, row, c0, tab.gates);
       times16(x, tab.gates.beta + c0);
-      if (low && half == 0) {
+      if (low && c0 < 64) {
         put16<kP>(smem + kPrepRight, kHalf, row - 64, c0, x);
       } else {
 #pragma unroll
@@ -193,12 +204,12 @@ __global__ void __launch_bounds__(kPrepThreads, 2) gd_prepare_kernel(const __gri
       }
     }
     __syncthreads();
-    lower_blocks(A, inv);
+    lower_blocks<NT>(A, inv);
     {  // the diagonal blocks of 64 as parts, in the place of themselves and A
-      float2 x[2][8];
-      const int col0 = (low ? 64 : 0) + half * 32;
+      float2 x[BLOCKS][8];
+      const int col0 = (low ? 64 : 0) + group * BLOCKS * 16;
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+      for (int q = 0; q < BLOCKS; ++q)
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
           const int c = col0 + q * 16 + 2 * i;
@@ -208,7 +219,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) gd_prepare_kernel(const __gri
         }
       __syncthreads();
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < BLOCKS; ++q) {
         const int c0 = col0 + q * 16;
         if (low) put16<kP>(smem + kTt1, kHalf, row - 64, c0 - 64, x[q]);
         else put16<kP>(smem, kTile, row, c0, x[q]);
@@ -228,8 +239,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) gd_prepare_kernel(const __gri
     steps.wait();
     if (low)
 #pragma unroll 1
-      for (int q = 0; q < 2; ++q) {
-        const int c0 = half * 32 + q * 16;
+      for (int q = 0; q < BLOCKS; ++q) {
+        const int c0 = (group * BLOCKS + q) * 16;
         float2 x[8];
         read16(mine + 128 + c0, x);
         put16<kP>(smem + kPrepRight, kHalf, row - 64, c0, x);
@@ -238,12 +249,13 @@ __global__ void __launch_bounds__(kPrepThreads, 2) gd_prepare_kernel(const __gri
     steps.run([&] { product<kP, kP>(tmem + 192, left1, right, 4, id_of(64, false, true), false); });
     DataRows<T, 64, VT, NT> vs;
     const T* v = rows_of<T>(a.v, at.t0, at.b, at.h);
-    vs.fetch(v, a.v.st, 0, at.n, 0, a.dv, VT == 2 ? g.dvt : 1);
+    if constexpr (kWhole) rows.fetch(v, a.v.st, 0, at.n, 0, a.dv, g.dvt);
+    else vs.fetch(v, a.v.st, 0, at.n, 0, a.dv, VT == 2 ? g.dvt : 1);
     steps.wait();
     if (low)
 #pragma unroll 1
-      for (int q = 0; q < 2; ++q) {
-        const int c0 = half * 32 + q * 16;
+      for (int q = 0; q < BLOCKS; ++q) {
+        const int c0 = (group * BLOCKS + q) * 16;
         float2 x[8];
         read16(mine + 192 + c0, x);
 #pragma unroll
@@ -254,8 +266,24 @@ __global__ void __launch_bounds__(kPrepThreads, 2) gd_prepare_kernel(const __gri
     // Tt V, tokens 64 ... in columns 128 ...
     const int vpieces = VT == 2 ? 1 : g.dvt;
     DataRows<T, 64, 1, NT> ks;
+    // a whole right operand of `tiles` tiles, its tokens 64 ... for columns 128 ...
+    auto whole = [&](auto parts, int tiles) {
+      constexpr int PR = decltype(parts)::value;
+      steps.run([&] {
+        Operand both_halves = mn_major(base + kPrepRight, tiles * kTile, kTile);
+        product<kP, PR>(tmem, left0, both_halves, 4, id_of(64 * tiles, false, true), false);
+        both_halves.desc += kHalf >> 4;
+        if (at.n > 64) product<kP, PR>(tmem + 128, left1, both_halves, 4, id_of(64 * tiles, false, true), false);
+      });
+    };
+    if constexpr (kWhole) {
+      rows.template place<DP>(smem + kPrepRight, g.dvt * kTile, kTile);
+      whole(std::integral_constant<int, DP>(), g.dvt);
+      rows.fetch(keys(at), a.k.st, 0, at.n, 0, a.dk, g.dkt);
+      steps.wait();
+    }
 #pragma unroll 1
-    for (int i = 0; i < 2 * vpieces && i / vpieces * 64 < at.n; ++i) {
+    for (int i = 0; !kWhole && i < 2 * vpieces && i / vpieces * 64 < at.n; ++i) {
       const int th = i / vpieces, vt = i % vpieces;
       vs.template place<DP>(smem + kPrepRight, VT == 2 ? 0 : kHalf, kHalf);
       steps.run([&] {
@@ -269,8 +297,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) gd_prepare_kernel(const __gri
     }
     float* E = g.E + at.at * C * 64 * g.dvt;
 #pragma unroll 1
-    for (int q = 0; q < 2 * g.dvt; ++q) {
-      const int c0 = (half * 2 * g.dvt + q) * 16;
+    for (int q = 0; q < BLOCKS * g.dvt; ++q) {
+      const int c0 = (group * BLOCKS * g.dvt + q) * 16;
       float2 f[8];
       read_both(c0, at.n, f);
       store_quads(E, C, row, c0, f);
@@ -278,8 +306,17 @@ __global__ void __launch_bounds__(kPrepThreads, 2) gd_prepare_kernel(const __gri
     // W = Tt (e^G K), likewise
     index += gridDim.x;
     p = next_place(g, index);
+    if constexpr (kWhole) {
+      rows.template place<kP>(smem + kPrepRight, part, kTile, tab.gates.up);
+      whole(std::integral_constant<int, kP>(), g.dkt);
+      if (p.n > 0) {
+        rows.fetch(keys(p), a.k.st, 0, p.n, 0, a.dk, g.dkt);
+        ask_gates(p);
+      }
+      steps.wait();
+    }
 #pragma unroll 1
-    for (int i = 0; i < 2 * g.dkt && i / g.dkt * 64 < at.n; ++i) {
+    for (int i = 0; !kWhole && i < 2 * g.dkt && i / g.dkt * 64 < at.n; ++i) {
       const int th = i / g.dkt, ct = i % g.dkt;
       ks.template place<kP>(smem + kPrepRight, kHalf, kHalf, tab.gates.up + 64 * th);
       steps.run([&] {
@@ -296,8 +333,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) gd_prepare_kernel(const __gri
     }
     // as tiles [dkt][parts], and from there to the walk's copy
 #pragma unroll 1
-    for (int q = 0; q < 2 * g.dkt; ++q) {
-      const int c0 = (half * 2 * g.dkt + q) * 16;
+    for (int q = 0; q < BLOCKS * g.dkt; ++q) {
+      const int c0 = (group * BLOCKS * g.dkt + q) * 16;
       float2 f[8];
       read_both(c0, at.n, f);
       put16<kP>(smem + (c0 >> 6) * kP * kTile, kTile, row, c0 & 63, f);
@@ -692,14 +729,22 @@ cudaError_t allow(K kernel, uint32_t smem) {
 
 }  // namespace
 
-cudaError_t launch_prepare(const Args& g, bool keep_inverse, cudaStream_t s) {
-  PRNN_BY_DTYPE(g.a.dtype, T, {
-    constexpr uint32_t smem = kPrepTab + sizeof(PrepTab);
-    const cudaError_t e = allow(gd_prepare_kernel<T>, smem);
-    if (e != cudaSuccess) return e;
-    gd_prepare_kernel<T><<<grid_of(g, 2), kPrepThreads, smem, s>>>(g, keep_inverse);
-  });
+namespace {
+template <typename T, int NT>
+cudaError_t prepare(const Args& g, bool keep_inverse, cudaStream_t s) {
+  constexpr uint32_t smem = kPrepTab<NT> + sizeof(PrepTab);
+  const cudaError_t e = allow(gd_prepare_kernel<T, NT>, smem);
+  if (e != cudaSuccess) return e;
+  gd_prepare_kernel<T, NT><<<grid_of(g, 512 / NT), NT, smem, s>>>(g, keep_inverse);
   return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_prepare(const Args& g, bool keep_inverse, cudaStream_t s) {
+  const bool few = 4LL * g.nbh * g.chunks <= 5LL * seq_sm_count();
+  cudaError_t e = cudaSuccess;
+  PRNN_BY_DTYPE(g.a.dtype, T, e = (few ? prepare<T, 512>(g, keep_inverse, s) : prepare<T, 256>(g, keep_inverse, s)));
+  return e;
 }
 
 namespace {
