@@ -363,22 +363,27 @@ __global__ void __launch_bounds__(NT, 512 / NT) gd_prepare_kernel(const __grid_c
 // Bound by the chain of a chunk: two products, each with the way from tensor memory through registers into the next
 // one's operand.  Slices of 32 columns make it shorter and spread a head over more SMs; slices of 64 take
 // half the blocks, for when those of 32 would not run all at once.
+//
+// Where the halves of both operands fit side by side each has a place of its own, and the next chunk's is requested as
+// soon as the product with this one's has read it; else they share a ring (fp32, and fp16 in slices of 64).  What the
+// workers read, Y0 and Z0, is brought into L2 a chunk ahead.
 constexpr uint32_t kStage = kP * kTile;
-template <int SL>
+template <int SL, int PK, bool REV>
 struct ChainCfg {
-  static constexpr int kStages = SL == 32 ? 3 : 2, kWorkers = SL / 4, kThreads = 32 * (kWorkers + 2);
+  static constexpr bool kOwn = PK <= (SL == 32 ? 2 : 1);
+  static constexpr int kRing = SL == 32 ? 3 : 2, kWorkers = SL / 4, kThreads = 32 * (kWorkers + 2);
+  static constexpr int P1 = REV ? PK : kP, P2 = REV ? kP : PK;           // parts of the two left operands
+  static constexpr uint32_t kLoads = kOwn ? 2 * (kP + PK) * kTile : kRing * kStage;
   static constexpr uint32_t kOperand = SL == 32 ? 2 * kTile : 3 * kTile;  // parts side by side in tiles of 64 columns
-  static constexpr uint32_t kZ = kStages * kStage, kY = kZ + kOperand, kTab = kY + kOperand;
+  static constexpr uint32_t kZ = kLoads, kY = kZ + kOperand, kTab = kY + kOperand;
   // tensor memory, used by both products in turn: the left operand's first part times all of the right one's, and the
   // small rest, which would lose more to the rounding of each step's sum beside the large ones
   static constexpr uint32_t kSmall = kP * SL, kCols = SL == 32 ? 256 : 512;
 };
 struct ChainTab {
-  uint64_t full[3], empty[3], z_ready, y_full, y_ready, z_full;
+  uint64_t full[4], empty[4], z_ready, y_full, y_ready, z_full;
   uint32_t tmem;
 };
-static_assert(ChainCfg<32>::kTab + sizeof(ChainTab) <= 227 * 1024 && ChainCfg<64>::kTab + sizeof(ChainTab) <= 227 * 1024,
-              "shared memory");
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile(
@@ -389,10 +394,10 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 
 // PK: parts of K.
 template <int PK, bool REV, int SL>
-__global__ void __launch_bounds__(ChainCfg<SL>::kThreads, 1) gd_chain_kernel(const __grid_constant__ Args g) {
-  using K = ChainCfg<SL>;
-  constexpr int kStages = K::kStages, kWorkers = K::kWorkers;
-  constexpr int P1 = REV ? PK : kP, P2 = REV ? kP : PK;  // parts of the two left operands
+__global__ void __launch_bounds__((ChainCfg<SL, PK, REV>::kThreads), 1) gd_chain_kernel(const __grid_constant__ Args g) {
+  using K = ChainCfg<SL, PK, REV>;
+  static_assert(K::kTab + sizeof(ChainTab) <= 227 * 1024, "shared memory");
+  constexpr int kWorkers = K::kWorkers, P1 = K::P1, P2 = K::P2;
   extern __shared__ __align__(1024) unsigned char smem[];
   ChainTab& tab = *reinterpret_cast<ChainTab*>(smem + K::kTab);
   const GdArgs& a = g.a;
@@ -405,7 +410,7 @@ __global__ void __launch_bounds__(ChainCfg<SL>::kThreads, 1) gd_chain_kernel(con
     return;
   }
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&tab.full[i], 1);
       mbar_init(&tab.empty[i], 1);
     }
@@ -429,37 +434,74 @@ __global__ void __launch_bounds__(ChainCfg<SL>::kThreads, 1) gd_chain_kernel(con
   auto tokens_of = [&](int c) { return min(C, len - c * C); };
   auto at_of = [&](int c) { return (size_t)local * g.chunks + c; };
 
+  // The place of half `half` of the first or second left operand of the i-th chunk, and how many it has held before;
+  // `turn` counts the ring's.
+  struct Slot {
+    int s, n;
+    uint32_t at;
+  };
+  const bool short_last = chunks > 0 && tokens_of(chunks - 1) <= 64;
+  auto slot = [&](int second, int half, int i, int& turn) {
+    if constexpr (K::kOwn) {
+      const int s = 2 * second + half;
+      // the last chunk may have no second half of tokens; backwards it comes first
+      return Slot{s, i - (REV && s == 3 && short_last ? 1 : 0), second ? (2 * P1 + half * P2) * kTile : half * P1 * kTile};
+    } else {
+      const Slot at{turn % K::kRing, turn / K::kRing, turn % K::kRing * kStage};
+      ++turn;
+      return at;
+    }
+  };
+
   if (warp == kWorkers) {
     if (elected()) {
       int turn = 0;
-      auto stage = [&](uint32_t bytes) {
-        const int s = turn % kStages;
-        if (turn >= kStages) seq_wait(&tab.empty[s], (turn / kStages - 1) & 1, ok);
-        mbar_arrive_expect_tx(&tab.full[s], bytes);
-        ++turn;
-        return s;
+      auto request = [&](const Slot& at, uint32_t bytes) {
+        if (at.n > 0) seq_wait(&tab.empty[at.s], (at.n - 1) & 1, ok);
+        mbar_arrive_expect_tx(&tab.full[at.s], bytes);
       };
+      const int rows = 64 * g.dkt, cols = 64 * g.dvt, wide = min(SL, cols - col0);
+      auto ahead = [&](int i) {
+        if (i >= chunks) return;
+        const size_t at = at_of(chunk_of(i));
+        ask_l2((REV ? g.X : g.E) + at * C * cols + (size_t)col0 * C, wide * C * 4);
+        if (REV) ask_l2(g.Z0 + at * rows * cols + (size_t)col0 * rows, wide * rows * 4);
+      };
+      ahead(0);
       for (int i = 0; i < chunks; ++i) {
         const int c = chunk_of(i);
         const unsigned char* w = g.wimg + at_of(c) * g.dkt * kP * kTile;
         const unsigned char* k = g.kimg + at_of(c) * g.dkt * PK * kTile;
         const unsigned char *first = REV ? k : w, *second = REV ? w : k;
+        ahead(i + 1);
         for (int ct = 0; ct < g.dkt; ++ct) {
-          const int s = stage(P1 * kTile);
-          bulk_load(base + s * kStage, first + ct * P1 * kTile, P1 * kTile, &tab.full[s]);
+          const Slot at = slot(0, ct, i, turn);
+          request(at, P1 * kTile);
+          bulk_load(base + at.at, first + ct * P1 * kTile, P1 * kTile, &tab.full[at.s]);
         }
         for (int hf = 0; hf * 64 < tokens_of(c); ++hf) {
-          const int s = stage(P2 * g.dkt * kTile / 2);
+          const Slot at = slot(1, hf, i, turn);
+          request(at, P2 * g.dkt * kTile / 2);
           for (int p = 0; p < P2; ++p)
             for (int ct = 0; ct < g.dkt; ++ct)
-              bulk_load(base + s * kStage + (p * g.dkt + ct) * (kTile / 2),
-                        second + (ct * P2 + p) * kTile + hf * (kTile / 2), kTile / 2, &tab.full[s]);
+              bulk_load(base + at.at + (p * g.dkt + ct) * (kTile / 2),
+                        second + (ct * P2 + p) * kTile + hf * (kTile / 2), kTile / 2, &tab.full[at.s]);
         }
       }
-      for (int i = max(0, turn - kStages); i < turn; ++i) {  // every load lands before the block leaves
+      // every load lands before the block leaves
+      auto land = [&](int s, int n) {
+        if (n < 0) return;
         bool landed = true;
-        seq_wait(&tab.full[i % kStages], (i / kStages) & 1, landed);
+        seq_wait(&tab.full[s], n & 1, landed);
         ok = ok && landed;
+      };
+      if constexpr (K::kOwn) {
+        land(0, chunks - 1);
+        land(1, g.dkt > 1 ? chunks - 1 : -1);
+        land(2, chunks - 1);
+        land(3, chunks - 1 - (short_last ? 1 : 0));
+      } else {
+        for (int i = max(0, turn - K::kRing); i < turn; ++i) land(i % K::kRing, i / K::kRing);
       }
     }
   } else if (warp == kWorkers + 1) {
@@ -471,30 +513,33 @@ __global__ void __launch_bounds__(ChainCfg<SL>::kThreads, 1) gd_chain_kernel(con
         constexpr int PL = decltype(parts)::value;
 #pragma unroll
         for (int p = 0; p < PL; ++p)
-          for (int k = 0; k < steps; ++k)
-            umma_f16(tmem + (p > 0 ? K::kSmall : 0), left.at(p, k), right.at(0, k_right + k),
-                     bf16_idesc(128, (kP - p) * SL) | id, add || p > 1 || k > 0);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < steps)
+              umma_f16(tmem + (p > 0 ? K::kSmall : 0), left.at(p, k), right.at(0, k_right + k),
+                       bf16_idesc(128, (kP - p) * SL) | id, add || p > 1 || k > 0);
       };
       const Operand Z = mn_major(base + K::kZ, 0, kTile), Y = mn_major(base + K::kY, 0, kTile);
       for (int i = 0; i < chunks; ++i) {
         const int c = chunk_of(i);
         seq_wait(&tab.z_ready, i & 1, ok);
         after_sync();
-        for (int ct = 0; ct < g.dkt; ++ct, ++turn) {
-          const int s = turn % kStages;
-          seq_wait(&tab.full[s], (turn / kStages) & 1, ok);
-          multiply(std::integral_constant<int, P1>(), k_major(base + s * kStage, kTile, kTile), Z, 4 * ct,
+        for (int ct = 0; ct < g.dkt; ++ct) {
+          const Slot at = slot(0, ct, i, turn);
+          seq_wait(&tab.full[at.s], at.n & 1, ok);
+          multiply(std::integral_constant<int, P1>(), k_major(base + at.at, kTile, kTile), Z, 4 * ct,
                    min(4, (a.dk - 64 * ct + 15) / 16), kBMn, ct > 0);
-          umma_commit(&tab.empty[s]);
+          umma_commit(&tab.empty[at.s]);
         }
         umma_commit(&tab.y_full);
         seq_wait(&tab.y_ready, i & 1, ok);
         after_sync();
-        for (int hf = 0; hf * 64 < tokens_of(c); ++hf, ++turn) {
-          const int s = turn % kStages;
-          seq_wait(&tab.full[s], (turn / kStages) & 1, ok);
-          multiply(std::integral_constant<int, P2>(), mn_major(base + s * kStage, g.dkt * (kTile / 2), kTile / 2), Y, 4 * hf, 4, kAMn | kBMn, hf > 0);
-          umma_commit(&tab.empty[s]);
+        for (int hf = 0; hf * 64 < tokens_of(c); ++hf) {
+          const Slot at = slot(1, hf, i, turn);
+          seq_wait(&tab.full[at.s], at.n & 1, ok);
+          multiply(std::integral_constant<int, P2>(), mn_major(base + at.at, g.dkt * (kTile / 2), kTile / 2), Y, 4 * hf, 4,
+                   kAMn | kBMn, hf > 0);
+          umma_commit(&tab.empty[at.s]);
         }
         umma_commit(&tab.z_full);
       }
@@ -537,23 +582,23 @@ __global__ void __launch_bounds__(ChainCfg<SL>::kThreads, 1) gd_chain_kernel(con
       before_sync();
     };
     auto sum = [&](bool small, float2 (&v)[8]) {  // the small ones first
-      float2 x[8], y[8];
+      uint32_t x[16], y[16], z[16];
       if (small) {
-        read16(mine + K::kSmall + SL, v);
-        read16(mine + K::kSmall, x);
+        tmem_ld16(mine + K::kSmall + SL, x);
+        tmem_ld16(mine + K::kSmall, y);
+        wait_ld();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = add2(v[i], x[i]);
+        for (int i = 0; i < 8; ++i) v[i] = add2(pair_at(x, i), pair_at(y, i));
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = both(0.f);
       }
-      read16(mine + 2 * SL, y);
-      read16(mine + SL, x);
+      tmem_ld16(mine + 2 * SL, x);
+      tmem_ld16(mine + SL, y);
+      tmem_ld16(mine, z);
+      wait_ld();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = add2(v[i], add2(x[i], y[i]));
-      read16(mine, x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = add2(v[i], x[i]);
+      for (int i = 0; i < 8; ++i) v[i] = add2(add2(v[i], add2(pair_at(x, i), pair_at(y, i))), pair_at(z, i));
     };
     auto fetch = [&](const float* m, int R, float2 (&v)[8]) {
       const float4* q = reinterpret_cast<const float4*>(m) + ((size_t)(c0 / 4) * R + row);
@@ -575,7 +620,6 @@ __global__ void __launch_bounds__(ChainCfg<SL>::kThreads, 1) gd_chain_kernel(con
       float* ym = (REV ? g.X : g.E) + at_of(c) * C * cols;
       float2 y[8], v[8], z0[8];
       fetch(ym, C, y);
-      if (REV && row < rows) fetch(g.Z0 + at_of(c) * rows * cols, rows, z0);
       seq_wait(&tab.y_full, i & 1, ok);
       __syncwarp();
       after_sync();
@@ -589,6 +633,7 @@ __global__ void __launch_bounds__(ChainCfg<SL>::kThreads, 1) gd_chain_kernel(con
       publish(K::kY, v);
       warp_arrive(&tab.y_ready);
       store_quads(ym, C, row, c0, y);
+      if (REV && row < rows) fetch(g.Z0 + at_of(c) * rows * cols, rows, z0);
       seq_wait(&tab.z_full, i & 1, ok);
       __syncwarp();
       after_sync();
@@ -750,7 +795,7 @@ cudaError_t launch_prepare(const Args& g, bool keep_inverse, cudaStream_t s) {
 namespace {
 template <int PK, bool REV, int SL>
 cudaError_t chain(const Args& g, cudaStream_t s) {
-  using K = ChainCfg<SL>;
+  using K = ChainCfg<SL, PK, REV>;
   constexpr uint32_t smem = K::kTab + sizeof(ChainTab);
   const cudaError_t e = allow(gd_chain_kernel<PK, REV, SL>, smem);
   if (e != cudaSuccess) return e;
