@@ -539,13 +539,20 @@ __global__ void __launch_bounds__(256) rms_dw_long_kernel(RmsNormGradArgs a, int
 template <typename T, int V>
 cudaError_t launch_backward(RmsNormGradArgs a, int splits, cudaStream_t s) {
   const int packs = (a.cols + V - 1) / V;
+  // As many blocks as the SMs hold at once by their registers (some 72 a thread, 128 for more than 8 values): a
+  // part of another wave costs more than it adds (32768 x 1152 bf16: with 5 an SM 67 us, with 8 75, with
+  // 6 90, with 4 124).
+  auto resident = [&](int nv, int threads) { return std::max(1, 65536 / ((nv * V <= 8 ? 72 : 128) * threads)); };
   auto lanes = [&](auto kernel, int tpr) {
     const int rows = 256 / tpr;
-    splits = (int)std::min<long long>(splits, (a.rows + rows - 1) / rows);
+    splits = (int)std::min<long long>({splits, (a.rows + rows - 1) / rows, resident(1, 256) * (long long)seq_sm_count()});
     kernel<<<splits, 256, 0, s>>>(a);
   };
   auto threads = [&](int nv) { return ((packs + nv - 1) / nv + 31) / 32 * 32; };
-  auto block = [&](auto kernel, int nv) { kernel<<<splits, threads(nv), 0, s>>>(a); };
+  auto block = [&](auto kernel, int nv) {
+    splits = std::min(splits, resident(nv, threads(nv)) * seq_sm_count());
+    kernel<<<splits, threads(nv), 0, s>>>(a);
+  };
   if (V > 1 && packs <= 8) {
     lanes(rms_grad_lanes_kernel<T, V, 1, 8>, 8);
   } else if (V > 1 && packs <= 16) {
@@ -599,10 +606,9 @@ cudaError_t launch_rms_norm(const RmsNormArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// Blocks whose parts of dweight are kept apart: enough to fill the SMs with a row each, fewer where the
-// parts themselves would be many bytes.
+// Blocks whose parts of dweight are kept apart, at most: enough for every type's plan.
 int rms_norm_splits(long long rows, int cols) {
-  const long long per_sm = cols <= 1024 ? 8 : (cols <= 4096 ? 4 : 2);
+  const long long per_sm = cols <= 1024 ? 10 : (cols <= 4096 ? 5 : 2);
   return (int)std::max(1LL, std::min(rows, per_sm * seq_sm_count()));
 }
 
