@@ -11,8 +11,9 @@
 // The decays' gradient <S', R'> is taken apart per block of kGdBlock tokens: moving the decay of one token scales all
 // that comes after it, so dlog_decay_t = sum over i >= t of the block of (q_i . dq_i - v_i . dv_i) + <S, R> at its end.
 //
-// Bound by the chain of a token in the first two walks (dot product, three shuffles, update: some 130
-// cycles) where warps are few, by instructions (about 75 a token and warp of 4 columns) where they are many.
+// Bound by the chain of a token in the first two walks (dot product, three shuffles, update) and the blocks' staging where
+// warps are few, by instructions and reads of shared memory where they are many.  Measured on GB300, bf16, us a token
+// forward: 8 heads of 64 x 64 0.30, 16 of 128 x 128 0.41, 128 of 128 x 128 1.8; the gradient's four walks 4.2 times that.
 #include <algorithm>
 
 #include "gated_delta.h"

@@ -1,6 +1,10 @@
 // gated_delta_tc_grad.cu -- the chunks' gradients of the gated delta rule on the 5th-generation tensor cores: what the
 // walk over the states' gradients needs beforehand, and what follows from it.  The algebra and the rounding are in
 // gated_delta_tc.cuh.
+//
+// Two operands in three parts and a piece of a third fill an SM's shared memory, so one block of 16 warps works through its
+// steps one behind another: latency bounds both kernels (T = 2048, 4 sequences of 16 heads of 128 x 128 bf16: 98 and 351 us,
+// 0.25 instructions a cycle and scheduler, DRAM at a fifth of its rate).  32 warps took 466 us, for their registers.
 #include "gated_delta_tc.cuh"
 
 namespace prnn {

@@ -6,9 +6,9 @@
 // stored, so the packed form loses nothing and takes half the registers of fp32 values.  Blocks stay and request their
 // next row while one is summed and written; two packs a thread measured best (8192 x 5760 bf16 into e4m3 83 us, with one
 // pack 92, with four 112).  Measured on GB300, against the copy rate of 6.78 TB/s: 8192 x 4096 bf16 with residual 40 us (0.98),
-// 8192 x 5760 bf16 with residual into e4m3 83 (0.59: some 16 instructions a value, at 24 warps an SM), gradient of 8192 x 2304 fp32
-// with the stream's 65 (0.69: a row's reduction stands between its loads and its store).  Rows that 16-byte accesses do not
-// fit go value by value: 8192 x 2001 bf16 70, into e4m3 120.
+// 8192 x 5760 with residual 63 (0.88) and into e4m3 83 (0.59: some 16 instructions a value, at 24 warps an SM), gradients with the
+// stream's 8192 x 5760 fp32 121 (0.92), 8192 x 2304 fp32 60 (0.74: a row's reduction stands between its loads and its store).
+// Rows that 16-byte accesses do not fit go value by value: 8192 x 2001 bf16 with residual 70, into e4m3 115.
 #include <algorithm>
 
 #include <cuda_fp8.h>
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(1024) rms_long_kernel(RmsNormArgs a) {
   }
 }
 
-constexpr int kRmsResident = 1024, kRmsOne = 128, kRmsTwo = 512;
+constexpr int kRmsOne = 128, kRmsTwo = 512;  // threads of one and two packs each, where rows are many
 
 template <typename T, int V, bool Q>
 void launch_forward(const RmsNormArgs& a, cudaStream_t s) {
@@ -340,7 +340,9 @@ void launch_forward(const RmsNormArgs& a, cudaStream_t s) {
   const bool many = a.rows >= 4LL * seq_sm_count();
   auto threads = [&](int nv) { return ((packs + nv - 1) / nv + 31) / 32 * 32; };
   auto block = [&](auto kernel, int nv) {
-    const int n = threads(nv), per_sm = std::max(1, kRmsResident / n);
+    // as many blocks as an SM holds by their registers, no part of another wave
+    const int regs = V == 1 ? (nv > 4 ? 64 : 48) : (nv == 1 ? 56 : (nv == 4 ? 128 : (V == 8 && !Q ? 56 : 64)));
+    const int n = threads(nv), per_sm = std::max(1, std::min(2048, 65536 / regs) / n);
     kernel<<<(unsigned)std::min<long long>(a.rows, (long long)per_sm * seq_sm_count()), n, 0, s>>>(a);
   };
   if (threads(1) <= (many ? kRmsOne : 1024)) {
