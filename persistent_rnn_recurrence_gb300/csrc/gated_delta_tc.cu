@@ -957,8 +957,9 @@ unsigned blocks_for(long long rows) {
 
 // Short sequences go token by token: that takes about 0.35 us a token and 1.8 ns more for each block of 16 columns, chunks
 // about 40 us for the first (in the gradients four times the one, twice the other).  Measured, tokens by tokens
-// and in chunks, us, bf16: 8 heads of 64 x 64, 64 tokens 24 and 32, 96 tokens 35 and 32; 128 heads of 128 x 128, 16 tokens
-// 34 and 54, 32 tokens 62 and 55; gradients 60 and 66 (32 tokens of 8 heads), 80 and 66 (48).
+// and in chunks, us, bf16: 8 heads of 64 x 64, 64 tokens 22 and 31, 96 tokens 31 and 33, 128 tokens 40 and 33; 16 heads of
+// 128 x 128, 64 tokens 29 and 40, 96 tokens 43 and 42; 128 heads, 16 tokens 32 and 55, 32 tokens 58 and 55; gradients of 8 heads of
+// 64 x 64, 32 tokens 53 and 60, 48 tokens 71 and 60; of 128 heads of 128 x 128, 16 tokens 141 and 96.
 bool gd_tc_serves(int T, int B, int H, int dk, int dv, bool backward) {
   const double blocks = (double)B * H * ((dv + 15) / 16);
   if (dk > 128 || dv > 128 || T * (200.0 + blocks) < (backward ? 11000.0 : 22000.0)) return false;
