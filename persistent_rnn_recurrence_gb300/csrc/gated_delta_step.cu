@@ -4,8 +4,8 @@
 // Bound by memory: the state is read and written once, 8 dk dv bytes per head against 7 dk dv flops.  A block holds
 // all dk rows of 32 columns in registers, so that the state is read once although its product with k comes before
 // its update; S^T q = S'^T q + (k . q) beta e, so both products with S' are summed at once and one
-// exchange serves both.  Measured on GB300: 96 sequences of 16 heads of 128 x 128 36.9 us (0.80 of the copy rate of 6.78 TB/s), one
-// of 8 heads of 64 x 64 3.7 (a launch).
+// exchange serves both.  Measured on GB300: 96 sequences of 16 heads of 128 x 128 36.9 us (0.80 of the copy rate of
+// 6.78 TB/s), one of 8 heads of 64 x 64 3.7 (a launch).
 #include <algorithm>
 
 #include "gated_delta.h"

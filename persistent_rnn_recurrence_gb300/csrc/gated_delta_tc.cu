@@ -287,8 +287,8 @@ __global__ void __launch_bounds__(NT, 512 / NT) gd_prepare_kernel(const __grid_c
       const int th = i / vpieces, vt = i % vpieces;
       vs.template place<DP>(smem + kPrepRight, VT == 2 ? 0 : kHalf, kHalf);
       steps.run([&] {
-        product<kP, DP>(tmem + 128 * th + 64 * vt, th ? left1 : left0, right, 4, id_of(VT == 2 ? 64 * g.dvt : 64, false, true),
-                        false);
+        product<kP, DP>(tmem + 128 * th + 64 * vt, th ? left1 : left0, right, 4,
+                        id_of(VT == 2 ? 64 * g.dvt : 64, false, true), false);
       });
       const int next = i + 1, nh = next / vpieces;
       if (nh < 2 && nh * 64 < at.n) vs.fetch(v, a.v.st, nh * 64, at.n, next % vpieces * 64, a.dv, VT == 2 ? g.dvt : 1);
@@ -357,12 +357,13 @@ __global__ void __launch_bounds__(NT, 512 / NT) gd_prepare_kernel(const __grid_c
 // Backwards Z = R: Y = X0 + e^(G_C-G) (K Z), kept as X;  Z <- e^G_C Z + Z0 - W^T (beta Y).
 // A block walks the chunks of one head and SL of its dv columns; the state is in the registers of SL / 4 warps,
 // 16 columns of a row each.  The parts of Z (of Y) stand side by side as columns of one product, which reads the
-// other operand once for each of its own parts.  W and K come as ready tiles in bulk copies through a ring, a half of
-// an operand per stage: the first product sums over column tiles, the second over halves of the tokens.
+// other operand once for each of its own parts.  W and K come as ready tiles in bulk copies, a half of an operand at a
+// time: the first product sums over column tiles, the second over halves of the tokens.
 //
 // Bound by the chain of a chunk: two products, each with the way from tensor memory through registers into the next
-// one's operand (4600 cycles in slices of 32: T = 8192, 2 sequences of 16 heads of 128 x 128 bf16 155 us).  Slices of 32 columns make it shorter and spread a head over more SMs; slices of 64 take
-// half the blocks, for when those of 32 would not run all at once.
+// one's operand (4600 cycles in slices of 32: T = 8192, 2 sequences of 16 heads of 128 x 128 bf16 155 us).  Slices of 32
+// columns make it shorter and spread a head over more SMs; slices of 64 take half the blocks, for when those of 32 would
+// not run all at once (T = 2048, 4 sequences: forward 65 us against 91, backwards 78 against 129 before it read Z0 late).
 //
 // Where the halves of both operands fit side by side each has a place of its own, and the next chunk's is requested as
 // soon as the product with this one's has read it; else they share a ring (fp32, and fp16 in slices of 64).  What the
@@ -445,7 +446,8 @@ __global__ void __launch_bounds__((ChainCfg<SL, PK, REV>::kThreads), 1) gd_chain
     if constexpr (K::kOwn) {
       const int s = 2 * second + half;
       // the last chunk may have no second half of tokens; backwards it comes first
-      return Slot{s, i - (REV && s == 3 && short_last ? 1 : 0), second ? (2 * P1 + half * P2) * kTile : half * P1 * kTile};
+      return Slot{s, i - (REV && s == 3 && short_last ? 1 : 0),
+                  second ? (2 * P1 + half * P2) * kTile : half * P1 * kTile};
     } else {
       const Slot at{turn % K::kRing, turn / K::kRing, turn % K::kRing * kStage};
       ++turn;
