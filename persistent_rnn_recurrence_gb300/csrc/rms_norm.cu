@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(1024) rms_join_kernel(const float* partial, in
   }
 }
 
-// Rows too long for registers: dx by rows, then the columns' sums a thread each.
+// Rows too long for registers: the columns' sums a thread each, then dx by rows.  Both read dy.
 template <typename T>
 __global__ void __launch_bounds__(1024) rms_dx_long_kernel(RmsNormGradArgs a) {
   __shared__ float part[32];
@@ -576,12 +576,12 @@ cudaError_t launch_backward(RmsNormGradArgs a, int splits, cudaStream_t s) {
   } else if (V == 1 && threads(16) <= 512) {
     block(rms_grad_block_kernel<T, V, V == 1 ? 16 : 1>, 16);
   } else {
-    if (a.dx)
-      rms_dx_long_kernel<T><<<(unsigned)std::min<long long>(a.rows, 4LL * seq_sm_count()), 1024, 0, s>>>(a);
-    if (a.dweight) {
+    if (a.dweight) {  // before dx, which may be written over dy
       const unsigned gx = (unsigned)std::min<long long>((a.cols + 255LL) / 256, 65535);
       rms_dw_long_kernel<T><<<dim3(gx, splits), 256, 0, s>>>(a, splits);
     }
+    if (a.dx)
+      rms_dx_long_kernel<T><<<(unsigned)std::min<long long>(a.rows, 4LL * seq_sm_count()), 1024, 0, s>>>(a);
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.dweight) return e;
