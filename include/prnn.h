@@ -830,7 +830,8 @@ prnn_status_t prnn_gated_delta_forward(const prnn_gated_delta_t* a, void* stream
 
 /*
  * Gradients of the forward call with the same inputs, for the loss whose gradient is d_o with respect to o and
- * d_state_out with respect to state_out.  From the last token, with R = d_state_out:
+ * d_state_out with respect to state_out.  o and state_out themselves are neither read nor written here, so one
+ * descriptor may serve both calls; `state` must still hold what the forward call began with.  From the last token, with R = d_state_out:
  *     R += scale q_t do_t^T;  du = R^T k_t;  dv_t = beta_t du;  dbeta_t = e_t . du;  dq_t = scale S_t do_t;
  *     dk_t = R (beta_t e_t) - S' dv_t;  R <- R - k_t dv_t^T;  dlog_decay_t = sum of S' * R;  R <- a R,
  * d_state = R at the end; dq and dk are summed over the heads that share them.

@@ -222,6 +222,10 @@ prnn_status_t prnn_gated_delta_backward(const prnn_gated_delta_t* a, void* strea
   all.array(a->workspace, need, true);
   if (!all.good()) return PRNN_ERR_INVALID_ARG;
   GdArgs g = args_of(a);
+  // the forward call's outputs, which a descriptor of both passes still names: the kernels of the forward pass, which run
+  // again here, write them where they are given
+  g.o = nullptr;
+  g.state_out = nullptr;
   if (on_tensor_cores(a, true)) return cuda_status(launch_gd_tc(g, a->workspace, true, s));
   const Parts p = walk_parts(a);
   char* w = static_cast<char*>(a->workspace);
