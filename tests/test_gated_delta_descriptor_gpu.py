@@ -1,5 +1,6 @@
 """The gated delta rule's C calls with one descriptor for both passes, as a C program keeps it: the forward call's outputs
-are still named in it when the backward call runs.  Sizes that go token by token and in chunks.  Compared bit for bit with calls that name nothing besides."""
+are still named in it when the backward call runs, and the state is updated in place.  Sizes that go token by token
+and in chunks.  Compared bit for bit with calls that name nothing besides."""
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -53,6 +54,20 @@ def call(torch, prnn, a, backward):
         bytes(a), torch.cuda.current_stream().cuda_stream)
     torch.cuda.synchronize()
     assert prnn.prnn_sequence_status() == prnn.PRNN_OK
+
+
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_state_in_place(env, case, dtype):
+    """state_out == state; a sequence of no tokens keeps its state's bits."""
+    torch, prnn = env
+    dt = getattr(torch, dtype)
+    p = inputs(torch, case, dt)
+    want, end = prnn.gated_delta_rule(p["q"], p["k"], p["v"], p["log_decay"], p["beta"], 0.2, p["state"], p["lens"])
+    state, o = p["state"].clone(), torch.full_like(p["v"], 7.0)
+    ins = {n: p[n] for n in ("q", "k", "v", "log_decay", "beta", "lens")}
+    call(torch, prnn, descriptor(torch, prnn, case, dt, {**ins, "state": state, "state_out": state, "o": o}), 0)
+    assert torch.equal(o, want) and torch.equal(state, end) and torch.equal(state[1], p["state"][1])
 
 
 @pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
