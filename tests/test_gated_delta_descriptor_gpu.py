@@ -93,3 +93,19 @@ def test_backward_leaves_the_forward_outputs(env, case, dtype):
         for n, m in names.items():
             assert torch.equal(outs[n], want[m]), (n, same)
         assert torch.equal(o, before[0]) and torch.equal(state_out, before[1]), same
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_each_gradient_alone(env, case, dtype):
+    """Gradients whose data is NULL are not computed; the others do not need them."""
+    torch, prnn = env
+    dt = getattr(torch, dtype)
+    p = inputs(torch, case, dt)
+    want = prnn.gated_delta_rule_backward(p["d_o"], p["q"], p["k"], p["v"], p["log_decay"], p["beta"], 0.2, p["state"],
+                                          p["lens"], p["d_state_out"])
+    for n, m in {"d_q": "dq", "d_k": "dk", "d_v": "dv", "d_log_decay": "dlog_decay", "d_beta": "dbeta",
+                 "d_state": "dstate"}.items():
+        out = torch.full_like(want[m], 3.0)
+        call(torch, prnn, descriptor(torch, prnn, case, dt, {**p, n: out}), 1)
+        assert torch.equal(out, want[m]), n

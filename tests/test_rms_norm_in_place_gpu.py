@@ -87,3 +87,24 @@ def test_backward_in_a_joint_tensor(env):
     got, dw2 = prnn.rms_norm_backward(place[:, 3:8503], h, w, rstd, dx=place[:, 3:8503])
     assert torch.equal(got, dx) and torch.equal(dw2, dw)
     assert torch.equal(place[:, :3], wide[:, :3]) and torch.equal(place[:, 8503:], wide[:, 8503:])
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("shape", [(700, 40), (33, 301), (700, 2304), *SHAPES], ids=str)
+def test_one_gradient_alone(env, shape, dtype):
+    """dx with dweight NULL and no workspace, over dy; dweight with dx NULL."""
+    torch, prnn = env
+    dt = getattr(torch, dtype)
+    code = {torch.float32: prnn.PRNN_F32, torch.bfloat16: prnn.PRNN_BF16}[dt]
+    (rows, cols), st = shape, torch.cuda.current_stream().cuda_stream
+    h, dy, dh = (normal(torch, shape, dt, 11 + i) for i in range(3))
+    w = normal(torch, (cols,), torch.float32, 14)
+    _, _, rstd = prnn.rms_norm(h, w)
+    dx, dw = prnn.rms_norm_backward(dy, h, w, rstd, dh)
+    place = dy.clone()
+    prnn.prnn_rms_norm_backward(code, rows, cols, place, cols, h, cols, w, rstd, dh, cols, place, cols, None, None, 0, st)
+    assert torch.equal(place, dx)
+    n = prnn.prnn_rms_norm_workspace(rows, cols)
+    out, ws = torch.full_like(dw, 7.0), torch.empty(n, dtype=torch.uint8, device="cuda")
+    prnn.prnn_rms_norm_backward(code, rows, cols, dy, cols, h, cols, w, rstd, dh, cols, None, 0, out, ws, n, st)
+    assert torch.equal(out, dw)
