@@ -595,8 +595,8 @@ prnn_status_t prnn_stack_destroy(prnn_stack_t s);
  * normalisation, dropout with the residual, and linear attention with a decay
  * per head, each with its gradient.  They need no handle.  Device pointers
  * throughout; data in fp32, fp16 or bf16 (`dtype`), arithmetic, statistics and
- * states in fp32, one rounding at each 16-bit output (what linear attention rounds between its
- * products of 16-bit data is stated there).  Asynchronous on `stream`;
+ * states in fp32, one rounding at each 16-bit output (what linear attention and the gated delta
+ * rule round between their products is stated there).  Asynchronous on `stream`;
  * a call allocates nothing: what scratch it needs is the caller's `workspace`,
  * 16-byte aligned, of the size its *_workspace query gives, used by the call
  * on its stream only (give overlapping calls their own).  Results do not depend on the
@@ -653,7 +653,9 @@ prnn_status_t prnn_layer_norm_backward(prnn_dtype_t dtype, long long rows, int c
  * at multiples of their strides (elements, >= cols).  h may be x or residual itself, y may be x or residual
  * itself (same stride); y and h must not overlap.  weight [cols] fp32, NULL: 1.  rstd [rows] fp32 is for the
  * backward pass and may be NULL.  rows == 0 is a no-op; eps >= 0.  Over the last axis of queries and keys
- * [T][B][heads][d] with weight d^-1/2 it makes them of length one (but for eps).
+ * [T][B][heads][d] with weight d^-1/2 it makes them of length one (but for eps).  The squares are summed in fp32: a row
+ * with a value of 2^64 or more has rstd 0 and zeros as y, and with eps 0 a row whose squares all vanish (values
+ * below 2^-75) has an infinite rstd.
  */
 prnn_status_t prnn_rms_norm_forward(prnn_dtype_t dtype, long long rows, int cols, const void* x, long long x_stride,
                                     const void* residual, long long residual_stride, const float* weight, float eps,
@@ -791,8 +793,11 @@ prnn_status_t prnn_linear_attention_step(const prnn_linear_attention_t* a, float
  *     S' = a S_{t-1},   e_t = v_t - S'^T k_t,   S_t = S' + k_t (beta_t e_t)^T  [dk][dv],   o_t = scale * S_t^T q_t.
  * Tensors, shared heads, lengths and states are as in linear attention.  Keys are meant to be of length one (a
  * prnn_rms_norm over the last axis with weight dk^-1/2 makes them so) and beta in 0 .. 2: with longer keys the state
- * grows without bound, and so do its results.  fp32 sums, states and gates throughout; one rounding at each
- * 16-bit output.  An infinity or NaN in a token within the length may reach, as NaN, the
+ * grows without bound, and so do its results.  fp32 sums, states and gates throughout.  Long calls with dk and dv up to
+ * 128 go in chunks of tokens, whose products take their operands as sums of bf16 parts: the data exactly, what is
+ * computed in between to 24 bits; but to 16 bits where only a 16-bit o follows, which is then off by some 2e-6 of
+ * scale |q| |S| (S the column of the state) before its own rounding, against 3e-7 in fp32.  All other calls multiply
+ * in fp32.  An infinity or NaN in a token within the length may reach, as NaN, the
  * outputs of its own sequence and head up to 127 tokens before it and everywhere behind it, and all of that
  * head's gradients there.  Tokens past the length reach nothing, whatever they hold.
  */
@@ -820,9 +825,11 @@ typedef struct {
 } prnn_gated_delta_t;
 
 /* Workspace of prnn_gated_delta_forward (backward == 0) or _backward (1) for the call that `a` describes (the
- * alignment of its pointers and strides counts; they are not followed).  About 2 KB a token and head of 128 x 128
- * forward and 4 KB backward, at most 8 GB (beyond that, heads are worked on in groups) besides copies of tensors that
- * are not aligned to 16 bytes and fp32 sums of the gradients of shared heads. */
+ * alignment of its pointers and strides counts; they are not followed).  In chunks about 2 KB a token and head of 128 x
+ * 128 forward and 4 KB backward, at most 8 GB (beyond that, heads are worked on in groups) besides copies of tensors
+ * whose rows are not whole groups of 8 values on 16 bytes and fp32 sums of the gradients of shared heads.  Calls that go
+ * token by token (short ones, and those with dk or dv above 128) take nothing forward and 8 (dk + dv) + dk dv / 32 bytes
+ * a token and head backward, without that limit: 6 KB for 256 x 256. */
 prnn_status_t prnn_gated_delta_workspace(const prnn_gated_delta_t* a, int backward, size_t* bytes);
 
 /* All T tokens.  T == 0 copies the state; B == 0 is a no-op. */
@@ -834,14 +841,17 @@ prnn_status_t prnn_gated_delta_forward(const prnn_gated_delta_t* a, void* stream
  * descriptor may serve both calls; `state` must still hold what the forward call began with.  From the last token, with R = d_state_out:
  *     R += scale q_t do_t^T;  du = R^T k_t;  dv_t = beta_t du;  dbeta_t = e_t . du;  dq_t = scale S_t do_t;
  *     dk_t = R (beta_t e_t) - S' dv_t;  R <- R - k_t dv_t^T;  dlog_decay_t = sum of S' * R;  R <- a R,
- * d_state = R at the end; dq and dk are summed over the heads that share them.
+ * d_state = R at the end; dq and dk are summed over the heads that share them.  dlog_decay is computed as a difference of
+ * sums over up to 128 tokens, of o . d_o and of v . dv, and <S, R> at their end, and is off by some 1e-6 of the
+ * magnitudes of these: where they cancel (strong decays; exactly 0 at the first token without a state) what is
+ * left is their rounding.
  */
 prnn_status_t prnn_gated_delta_backward(const prnn_gated_delta_t* a, void* stream);
 
 /*
  * One token for each of B sequences (decoding), states in `state_pool` [n_slots][heads][dk][dv] fp32 updated in
- * place through `slots`, as prnn_linear_attention_step: a->T, lens and the strides over t are not used.  No
- * workspace.
+ * place through `slots`, as prnn_linear_attention_step (live slots must differ from one another): lens and the
+ * strides over t are not used, nor is a valid T.  No workspace.
  */
 prnn_status_t prnn_gated_delta_step(const prnn_gated_delta_t* a, float* state_pool, int n_slots,
                                     const int32_t* slots, void* stream);

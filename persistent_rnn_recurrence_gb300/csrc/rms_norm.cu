@@ -6,8 +6,9 @@
 // stored, so the packed form loses nothing and takes half the registers of fp32 values.  Blocks stay and request their
 // next row while one is summed and written; two packs a thread measured best (8192 x 5760 bf16 into e4m3 83 us, with one
 // pack 92, with four 112).  Measured on GB300, against the copy rate of 6.78 TB/s: 8192 x 4096 bf16 with residual 40 us (0.98),
-// 8192 x 5760 with residual 63 (0.88) and into e4m3 83 (0.59: some 16 instructions a value, at 24 warps an SM), gradients with the
-// stream's 8192 x 5760 fp32 121 (0.92), 8192 x 2304 fp32 60 (0.74: a row's reduction stands between its loads and its store).
+// 8192 x 5760 with residual 63 (0.88) and into e4m3 81 (0.60: some 40 instructions a value where the other output takes 27, at
+// 24 warps an SM), gradients with the stream's 8192 x 5760 fp32 121 (0.92), 8192 x 2304 fp32 58 and 7 to join dweight (0.68: a
+// row's reduction stands between its loads and its store, and its blocks are one and a half waves, as said at their launch).
 // Rows that 16-byte accesses do not fit go value by value: 8192 x 2001 bf16 with residual 70, into e4m3 115.
 #include <algorithm>
 
@@ -340,7 +341,7 @@ void launch_forward(const RmsNormArgs& a, cudaStream_t s) {
   const bool many = a.rows >= 4LL * seq_sm_count();
   auto threads = [&](int nv) { return ((packs + nv - 1) / nv + 31) / 32 * 32; };
   auto block = [&](auto kernel, int nv) {
-    // as many blocks as an SM holds by their registers, no part of another wave
+    // as many blocks as an SM holds by (a bound on) their registers, no part of another wave
     const int regs = V == 1 ? (nv > 4 ? 64 : 48) : (nv == 1 ? 56 : (nv == 4 ? 128 : (V == 8 && !Q ? 56 : 64)));
     const int n = threads(nv), per_sm = std::max(1, std::min(2048, 65536 / regs) / n);
     kernel<<<(unsigned)std::min<long long>(a.rows, (long long)per_sm * seq_sm_count()), n, 0, s>>>(a);
@@ -541,9 +542,12 @@ __global__ void __launch_bounds__(256) rms_dw_long_kernel(RmsNormGradArgs a, int
 template <typename T, int V>
 cudaError_t launch_backward(RmsNormGradArgs a, int splits, cudaStream_t s) {
   const int packs = (a.cols + V - 1) / V;
-  // As many blocks as the SMs hold at once by their registers (some 72 a thread, 128 for more than 8 values): a
-  // part of another wave costs more than it adds (32768 x 1152 bf16: with 5 an SM 67 us, with 8 75, with
-  // 6 90, with 4 124).
+  // As many blocks as the SMs hold at once by their registers: up to 72 a thread in most kernels of up to 8 values, 80 in
+  // blocks of 256 threads, which are three an SM either way, and 128 for more values.  A part of another wave costs more
+  // than it adds (32768 x 1152 bf16: with 5 an SM 67 us, with 8 75, with 6 90, with 4 124).  Two kernels hold more than
+  // is taken here, and some widths get up to twice the blocks that fit: fp32 in two packs of four (110 registers, 1025 to 3584
+  // columns; 2304 columns are three blocks of 288 threads an SM where two fit), and four single values a thread (78 in bf16
+  // and 84 in fp32, widths among 1025 to 1792).
   auto resident = [&](int nv, int threads) { return std::max(1, 65536 / ((nv * V <= 8 ? 72 : 128) * threads)); };
   auto lanes = [&](auto kernel, int tpr) {
     const int rows = 256 / tpr;

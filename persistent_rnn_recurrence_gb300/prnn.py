@@ -1123,8 +1123,8 @@ def gated_delta_rule_backward(do, q, k, v, log_decay, beta, scale=1.0, state=Non
 def gated_delta_rule_step(q, k, v, log_decay, beta, state, scale=1.0, slots=None, o=None, stream=None):
     """One token of the gated delta rule for each sequence (prnn_gated_delta_step): q, k [B, qk_heads, dk],
     v [B, heads, dv], log_decay and beta fp32 [B, heads]; state fp32 [n, heads, dk, dv], updated in place:
-    sequence b's is state[slots[b]] (int32 on the device; outside 0 .. n-1 marks a padding row), or state[b].
-    Returns o [B, heads, dv]."""
+    sequence b's is state[slots[b]] (int32 on the device, live ones different from one another; outside 0 .. n-1
+    marks a padding row), or state[b].  Returns o [B, heads, dv]."""
     if stream is not None:
         import torch
         with torch.cuda.stream(stream):
